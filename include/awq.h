@@ -401,6 +401,87 @@ awq_status awq_gemm_splitk_noalloc(const void* x, const void* qweight, const voi
                                    const void* zeros, void* y, int M, int N, int K, int bits,
                                    int group_size, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Operators beside the packed products in a decoder block.
+ * ------------------------------------------------------------------------ */
+
+/* 16-bit element type of the operators below that name a dtype. */
+typedef enum { AWQ_F16 = 0, AWQ_BF16 = 1 } awq_dtype;
+
+typedef enum {
+    AWQ_NORM_RMS = 0,         /* v / sqrt(mean(v^2) + eps) * weight (+ bias) */
+    AWQ_NORM_LAYER = 1        /* the same of v - mean(v)                     */
+} awq_norm_kind;
+
+/*
+ * awq_norm_gate_residual -- the norm after a block, its gate, the scaled
+ * residual and the norm before the next block, in one pass over the rows:
+ *   t  = post(block)                         (block itself without post_weight)
+ *   r' = residual_scale * residual + gate * t     (gate = 1 without one)
+ *   h  = pre(r')                             (from the fp32 r')
+ *   block, residual  dtype [T][H];  post_weight, post_bias, pre_weight,
+ *   pre_bias  dtype [H], all but pre_weight may be NULL (post_bias needs
+ *   post_weight);  gate  dtype [gate_rows][H] or NULL: row t of the T rows
+ *   takes gate row t / (T / gate_rows), gate_rows divides T (1: one gate for
+ *   all; ignored without a gate)
+ *   kind     awq_norm_kind of both norms;  eps >= 0, added to the mean square
+ *   residual_out  dtype [T][H] out: r', rounded once (may be `residual`)
+ *   h        out: dtype [T][H] rounded once; or, with h_scales, int8 [T][H]
+ *   h_scales NULL, or fp32 [T] out: h is then written as the codes of
+ *            awq_quantize_rows of the fp32 h, ready for awq_gemm_w8a8
+ *   H a multiple of 8, at most 32768 (else AWQ_ERR_SHAPE).  All arithmetic is
+ *   fp32.  T == 0 is a valid empty call.
+ */
+awq_status awq_norm_gate_residual(const void* block, const void* residual,
+                                  const void* post_weight, const void* post_bias,
+                                  const void* gate, int gate_rows, float residual_scale,
+                                  const void* pre_weight, const void* pre_bias, int kind,
+                                  float eps, int T, int H, int dtype, void* residual_out,
+                                  void* h, float* h_scales, hipStream_t stream);
+
+/*
+ * awq_quantize_rows -- 8-bit codes with one scale per row (a token of
+ * activations, or an output channel of weights):
+ *   scale[m] = max_k |x[m][k]| / 127;  q[m][k] = rint(127 x[m][k] / max|x[m]|)
+ *   (exact quotient, ties to even; a row of zeros has scale 0 and codes 0; a
+ *   row holding an infinity or a NaN gets that as its scale)
+ *   x  dtype [M][K] in, K a multiple of 16 and < 2^17 (else AWQ_ERR_SHAPE);
+ *   q  int8 [M][K] out;  scales  fp32 [M] out.
+ */
+awq_status awq_quantize_rows(const void* x, int M, int K, int dtype, void* q, float* scales,
+                             hipStream_t stream);
+
+/*
+ * awq_gemm_w8a8 -- product in 8-bit integers with a scale for each token and
+ * each channel, for any M >= 1:
+ *   y[m][n] = x_scales[m] * weight_scales[n] * sum_k x[m][k] weight[n][k] + bias[n]
+ *   x  int8 [M][K], x_scales fp32 [M], weight int8 [N][K], weight_scales fp32
+ *   [N]: as awq_quantize_rows writes them;  bias  fp32 [N] or NULL;
+ *   y  dtype [M][N] out.  The sum is exact in int32: K a multiple of 16 and
+ *   < 2^17 (else AWQ_ERR_SHAPE); M * N < 2^40.
+ *   workspace / workspace_bytes: device scratch of at least
+ *   awq_gemm_w8a8_workspace_bytes(M, N, K) bytes (may be NULL when that is 0;
+ *   else too small is AWQ_ERR_WORKSPACE): int32 partial sums of the K splits
+ *   that products with few output tiles are cut into.  The size depends on
+ *   the current device.
+ */
+size_t awq_gemm_w8a8_workspace_bytes(int M, int N, int K);
+awq_status awq_gemm_w8a8(const void* x, const float* x_scales, const void* weight,
+                         const float* weight_scales, const float* bias, void* y, int M, int N,
+                         int K, int dtype, void* workspace, size_t workspace_bytes,
+                         hipStream_t stream);
+
+/*
+ * awq_linear_w8a8 -- awq_quantize_rows and awq_gemm_w8a8 in one call: x is
+ * dtype [M][K], its codes and scales are the same.  A few short rows (decode)
+ * are quantized inside the product's launch.  Workspace as above, of
+ * awq_linear_w8a8_workspace_bytes(M, N, K) bytes.
+ */
+size_t awq_linear_w8a8_workspace_bytes(int M, int N, int K);
+awq_status awq_linear_w8a8(const void* x, const void* weight, const float* weight_scales,
+                           const float* bias, void* y, int M, int N, int K, int dtype,
+                           void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

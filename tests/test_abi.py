@@ -355,3 +355,54 @@ def test_binding_refuses_when_library_missing(monkeypatch, tmp_path):
     monkeypatch.setattr(B, "_lib", None)
     with pytest.raises(B.AwqError):
         B.load_library()
+
+
+def test_norm_gate_residual_validation(lib):
+    def call(block=P, residual=P2, post=NUL, post_b=NUL, gate=NUL, gate_rows=0, alpha=1.0, pre=P3, pre_b=NUL,
+             kind=0, eps=1e-6, T=4, H=64, dtype=0, r_out=P4, h=P5, h_scales=NUL):
+        return lib.awq_norm_gate_residual(block, residual, post, post_b, gate, gate_rows, alpha, pre, pre_b, kind,
+                                          eps, T, H, dtype, r_out, h, h_scales, NUL)
+    for bad in (dict(block=NUL), dict(residual=NUL), dict(pre=NUL), dict(r_out=NUL), dict(h=NUL), dict(post_b=P)):
+        assert call(**bad) == NULL, bad
+    for bad in (dict(block=MIS), dict(residual=MIS), dict(pre=MIS), dict(r_out=MIS), dict(h=MIS), dict(post=MIS),
+                dict(post=P, post_b=MIS), dict(gate=MIS, gate_rows=1), dict(pre_b=MIS), dict(h_scales=MIS)):
+        assert call(**bad) == ALIGN, bad
+    for bad in (dict(T=-1), dict(H=0), dict(H=-8), dict(H=60), dict(H=32776), dict(gate=P, gate_rows=0),
+                dict(gate=P, gate_rows=3)):
+        assert call(**bad) == SHAPE, bad
+    for bad in (dict(dtype=2), dict(dtype=-1), dict(kind=2), dict(eps=-1.0), dict(eps=float("nan"))):
+        assert call(**bad) == UNSUP, bad
+    assert call(T=0, block=NUL) == OK
+
+
+def test_w8a8_validation(lib):
+    assert lib.awq_quantize_rows(NUL, 4, 64, 0, P, P2, NUL) == NULL
+    assert lib.awq_quantize_rows(P, 4, 64, 0, MIS, P2, NUL) == ALIGN
+    for M, K in ((-1, 64), (4, 0), (4, 72), (4, 1 << 17)):
+        assert lib.awq_quantize_rows(P, M, K, 0, P2, P3, NUL) == SHAPE
+    assert lib.awq_quantize_rows(P, 4, 64, 5, P2, P3, NUL) == UNSUP
+    assert lib.awq_quantize_rows(NUL, 0, 64, 0, NUL, NUL, NUL) == OK
+
+    def gemm(x=P, sx=P2, w=P3, sw=P4, bias=NUL, y=P5, M=4, N=8192, K=64, dtype=0, ws=NUL, ws_bytes=0):
+        return lib.awq_gemm_w8a8(x, sx, w, sw, bias, y, M, N, K, dtype, ws, ws_bytes, NUL)
+
+    def linear(x=P, w=P3, sw=P4, bias=NUL, y=P5, M=4, N=8192, K=64, dtype=0, ws=NUL, ws_bytes=0):
+        return lib.awq_linear_w8a8(x, w, sw, bias, y, M, N, K, dtype, ws, ws_bytes, NUL)
+
+    for call, names in ((gemm, ("x", "sx", "w", "sw", "y")), (linear, ("x", "w", "sw", "y"))):
+        for name in names:
+            assert call(**{name: NUL}) == NULL, name
+            assert call(**{name: MIS}) == ALIGN, name
+        assert call(bias=MIS) == ALIGN
+        for bad in (dict(M=-1), dict(N=-1), dict(K=0), dict(K=24), dict(K=1 << 17), dict(M=1 << 21, N=1 << 20)):
+            assert call(**bad) == SHAPE, bad
+        assert call(dtype=3) == UNSUP
+        assert call(M=0, w=NUL) == OK and call(N=0, w=NUL) == OK
+    for size, call in ((lib.awq_gemm_w8a8_workspace_bytes, gemm), (lib.awq_linear_w8a8_workspace_bytes, linear)):
+        assert size(0, 64, 64) == size(4, 64, 24) == size(4, -1, 64) == 0
+        need = size(100, 64, 28672)                       # few output tiles, long rows: split
+        assert need > 0
+        shape = dict(M=100, N=64, K=28672)
+        assert call(**shape) == NULL
+        assert call(**shape, ws=MIS, ws_bytes=need) == ALIGN
+        assert call(**shape, ws=P, ws_bytes=need - 1) == WS

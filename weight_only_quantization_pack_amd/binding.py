@@ -17,6 +17,7 @@ LIB_NAME = "libawq.so"
 _c_void_p = ctypes.c_void_p
 _c_int = ctypes.c_int
 _c_size_t = ctypes.c_size_t
+_c_float = ctypes.c_float
 
 # (name, restype, argtypes) for every exported symbol of include/awq.h
 SIGNATURES = [
@@ -59,6 +60,16 @@ SIGNATURES = [
     ("awq_gemm_splitk_noalloc_max_bytes", _c_size_t, []),
     ("awq_gemm_splitk_noalloc", _c_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
                                          _c_int, _c_int, _c_int, _c_int, _c_int, _c_void_p]),
+    ("awq_norm_gate_residual", _c_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_int,
+                                        _c_float, _c_void_p, _c_void_p, _c_int, _c_float, _c_int, _c_int,
+                                        _c_int, _c_void_p, _c_void_p, _c_void_p, _c_void_p]),
+    ("awq_quantize_rows", _c_int, [_c_void_p, _c_int, _c_int, _c_int, _c_void_p, _c_void_p, _c_void_p]),
+    ("awq_gemm_w8a8_workspace_bytes", _c_size_t, [_c_int, _c_int, _c_int]),
+    ("awq_gemm_w8a8", _c_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_int,
+                               _c_int, _c_int, _c_int, _c_void_p, _c_size_t, _c_void_p]),
+    ("awq_linear_w8a8_workspace_bytes", _c_size_t, [_c_int, _c_int, _c_int]),
+    ("awq_linear_w8a8", _c_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_int, _c_int,
+                                 _c_int, _c_int, _c_void_p, _c_size_t, _c_void_p]),
 ]
 
 STATUS = {0: "AWQ_OK", 1: "AWQ_ERR_NULL", 2: "AWQ_ERR_SHAPE", 3: "AWQ_ERR_UNSUPPORTED",
@@ -455,3 +466,191 @@ def gemm(x, qweight, scales, zeros, N: int, bits: int = 4, group_size: int = GRO
             return _matmul("awq_gemm_splitk", x, qweight, scales, zeros, N, bits, group_size, out,
                            workspace)
     return _matmul("awq_gemm", x, qweight, scales, zeros, N, bits, group_size, out)
+
+
+# ---------------------------------------------------------------------------
+# operators beside the packed products in a decoder block
+# ---------------------------------------------------------------------------
+NORM_KINDS = {"rms": 0, "layer": 1}
+
+
+def _dtype_code(dtype, name):
+    """awq_dtype of a 16-bit torch dtype."""
+    torch = _torch()
+    if dtype == torch.float16:
+        return 0
+    if dtype == torch.bfloat16:
+        return 1
+    raise TypeError(f"{name} must be torch.float16 or torch.bfloat16, got {dtype}")
+
+
+def _rows2d(t, name):
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions, got shape {tuple(t.shape)}")
+    return t.shape
+
+
+def _need_optional(t, dtype, shape, name):
+    if t is not None:
+        _need(t, dtype, shape, name)
+
+
+def _same_device(first, **others):
+    """Every tensor on the first one's GPU (whose stream the call goes to)."""
+    dev = first.device
+    for name, t in others.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+
+
+def _workspace(workspace, need, device):
+    """(tensor kept alive, pointer, bytes) of a call's scratch memory."""
+    if need == 0:
+        return None, None, 0
+    if workspace is None:
+        workspace = _torch().empty(need, dtype=_torch().uint8, device=device)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def norm_gate_residual(block, residual, pre_weight, post_weight=None, gate=None, residual_scale: float = 1.0,
+                       kind: str = "rms", pre_bias=None, post_bias=None, eps: float = 1e-6,
+                       quantize: bool = False, out=None):
+    """Norms before and after a block with its gate and the scaled residual
+    (awq_norm_gate_residual), one launch:
+
+        t  = post(block)                            (block itself without post_weight)
+        r' = residual_scale * residual + gate * t
+        h  = pre(r')
+
+    block, residual: fp16 or bf16 [T][H], contiguous, H a multiple of 8, at
+    most 32768; weights and biases [H] and gate [H] or [B][H] (B divides T: one
+    gate row for each T / B rows) of the same type.  kind "rms" or "layer" for
+    both norms.  Returns (r', h), or with quantize=True (r', codes int8 [T][H],
+    scales fp32 [T]) for gemm_w8a8.  out: the tensors to write, in that order;
+    the first may be `residual`.
+    """
+    torch = _torch()
+    lib = load_library()
+    T, H = _rows2d(block, "block")
+    dtype = block.dtype
+    code = _dtype_code(dtype, "block")
+    _need(block, dtype, (T, H), "block")
+    _need(residual, dtype, (T, H), "residual")
+    for t, name in ((pre_weight, "pre_weight"), (post_weight, "post_weight"), (pre_bias, "pre_bias"),
+                    (post_bias, "post_bias")):
+        if t is not None or name == "pre_weight":
+            _need(t, dtype, (H,), name)
+    if post_bias is not None and post_weight is None:
+        raise ValueError("post_bias needs post_weight")
+    if kind not in NORM_KINDS:
+        raise ValueError(f"kind must be one of {sorted(NORM_KINDS)}, got {kind!r}")
+    gate_rows = 0
+    if gate is not None:
+        gate_rows = 1 if gate.dim() == 1 else gate.shape[0]
+        _need(gate, dtype, (H,) if gate.dim() == 1 else (gate_rows, H), "gate")
+        if gate_rows == 0 or T % gate_rows:
+            raise ValueError(f"gate rows ({gate_rows}) must divide the rows of block ({T})")
+    _same_device(block, residual=residual, pre_weight=pre_weight, post_weight=post_weight, gate=gate,
+                 pre_bias=pre_bias, post_bias=post_bias)
+    if out is None:
+        r = torch.empty_like(residual)
+        h = torch.empty((T, H), dtype=torch.int8 if quantize else dtype, device=block.device)
+        scales = torch.empty(T, dtype=torch.float32, device=block.device) if quantize else None
+    else:
+        r, h, scales = out if quantize else (*out, None)
+        _need(r, dtype, (T, H), "out[0]")
+        _need(h, torch.int8 if quantize else dtype, (T, H), "out[1]")
+        _need_optional(scales, torch.float32, (T,), "out[2]")
+        _same_device(block, **{"out[0]": r, "out[1]": h, "out[2]": scales})
+    st = lib.awq_norm_gate_residual(_ptr(block), _ptr(residual), _ptr(post_weight), _ptr(post_bias), _ptr(gate),
+                                    gate_rows, residual_scale, _ptr(pre_weight), _ptr(pre_bias),
+                                    NORM_KINDS[kind], eps, T, H, code, _ptr(r), _ptr(h), _ptr(scales),
+                                    _stream_ptr(block))
+    _check(st, "awq_norm_gate_residual")
+    return (r, h, scales) if quantize else (r, h)
+
+
+def quantize_rows(x, out=None):
+    """8-bit codes with one scale per row (awq_quantize_rows): (int8 [M][K],
+    fp32 [M]) with scale = max|row| / 127 and q = rint(127 x / max|row|).  Rows
+    are tokens of activations or output channels of weights; x fp16 or bf16, K
+    a multiple of 16."""
+    torch = _torch()
+    lib = load_library()
+    M, K = _rows2d(x, "x")
+    code = _dtype_code(x.dtype, "x")
+    _need(x, x.dtype, (M, K), "x")
+    if out is None:
+        q = torch.empty((M, K), dtype=torch.int8, device=x.device)
+        scales = torch.empty(M, dtype=torch.float32, device=x.device)
+    else:
+        q, scales = out
+        _need(q, torch.int8, (M, K), "out[0]")
+        _need(scales, torch.float32, (M,), "out[1]")
+        _same_device(x, **{"out[0]": q, "out[1]": scales})
+    st = lib.awq_quantize_rows(_ptr(x), M, K, code, _ptr(q), _ptr(scales), _stream_ptr(x))
+    _check(st, "awq_quantize_rows")
+    return q, scales
+
+
+def gemm_w8a8_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(load_library().awq_gemm_w8a8_workspace_bytes(M, N, K))
+
+
+def linear_w8a8_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(load_library().awq_linear_w8a8_workspace_bytes(M, N, K))
+
+
+def _w8a8_operands(x, M, K, weight, weight_scales, bias, dtype, out):
+    """Checks of the product's weight side; (N, out)."""
+    torch = _torch()
+    N, _ = _rows2d(weight, "weight")
+    _need(weight, torch.int8, (N, K), "weight")
+    _need(weight_scales, torch.float32, (N,), "weight_scales")
+    _need_optional(bias, torch.float32, (N,), "bias")
+    if out is None:
+        out = torch.empty((M, N), dtype=dtype, device=x.device)
+    else:
+        _need(out, dtype, (M, N), "out")
+    _same_device(x, weight=weight, weight_scales=weight_scales, bias=bias, out=out)
+    return N, out
+
+
+def gemm_w8a8(q, q_scales, weight, weight_scales, bias=None, dtype=None, out=None, workspace=None):
+    """y = q_scales[m] * weight_scales[n] * (q . weight^T) + bias in 8-bit
+    integers (awq_gemm_w8a8): q int8 [M][K] and weight int8 [N][K] with their
+    fp32 scales, as quantize_rows gives them; bias fp32 [N].  y is fp16 or bf16
+    [M][N]: dtype (default torch.float16), or out's."""
+    torch = _torch()
+    lib = load_library()
+    M, K = _rows2d(q, "q")
+    _need(q, torch.int8, (M, K), "q")
+    _need(q_scales, torch.float32, (M,), "q_scales")
+    if dtype is None:
+        dtype = torch.float16 if out is None else out.dtype
+    code = _dtype_code(dtype, "dtype")
+    _same_device(q, q_scales=q_scales)
+    N, out = _w8a8_operands(q, M, K, weight, weight_scales, bias, dtype, out)
+    keep, ws, ws_bytes = _workspace(workspace, int(lib.awq_gemm_w8a8_workspace_bytes(M, N, K)), q.device)
+    st = lib.awq_gemm_w8a8(_ptr(q), _ptr(q_scales), _ptr(weight), _ptr(weight_scales), _ptr(bias), _ptr(out),
+                           M, N, K, code, ws, ws_bytes, _stream_ptr(q))
+    _check(st, "awq_gemm_w8a8")
+    return out
+
+
+def linear_w8a8(x, weight, weight_scales, bias=None, out=None, workspace=None):
+    """gemm_w8a8 of the quantized rows of x (awq_linear_w8a8): x fp16 or bf16
+    [M][K], y of the same type.  One call: short decode rows are quantized
+    inside the product's launch."""
+    lib = load_library()
+    M, K = _rows2d(x, "x")
+    code = _dtype_code(x.dtype, "x")
+    _need(x, x.dtype, (M, K), "x")
+    N, out = _w8a8_operands(x, M, K, weight, weight_scales, bias, x.dtype, out)
+    keep, ws, ws_bytes = _workspace(workspace, int(lib.awq_linear_w8a8_workspace_bytes(M, N, K)), x.device)
+    st = lib.awq_linear_w8a8(_ptr(x), _ptr(weight), _ptr(weight_scales), _ptr(bias), _ptr(out), M, N, K, code,
+                             ws, ws_bytes, _stream_ptr(x))
+    _check(st, "awq_linear_w8a8")
+    return out

@@ -382,3 +382,105 @@ awq_status awq_gemm_splitk_noalloc(const void* x, const void* qweight, const voi
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------------------
+// operators beside the packed products
+// ---------------------------------------------------------------------------
+namespace {
+constexpr int kMaxNormWidth = 32768;      // a row lives in one workgroup's registers
+constexpr int kMaxW8a8K = 1 << 17;        // 128 * 128 * K < 2^31: exact int32 sums
+
+int check_dtype(int dtype) { return dtype == AWQ_F16 || dtype == AWQ_BF16 ? AWQ_OK : AWQ_ERR_UNSUPPORTED; }
+
+// null pointers pass
+int check_optional(std::initializer_list<const void*> ps) {
+    for (const void* p : ps)
+        if (p != nullptr && check_ptr(p) != AWQ_OK) return AWQ_ERR_ALIGN;
+    return AWQ_OK;
+}
+
+int check_w8a8(int M, int N, int K, int dtype) {
+    if (int st = check_dtype(dtype)) return st;
+    if (M < 0 || N < 0 || K <= 0 || K % 16 != 0 || K >= kMaxW8a8K) return AWQ_ERR_SHAPE;
+    if ((long long)M * N >= (1LL << 40)) return AWQ_ERR_SHAPE;
+    return AWQ_OK;
+}
+
+int check_workspace(const void* workspace, size_t bytes, size_t need) {
+    if (need == 0) return AWQ_OK;
+    if (workspace == nullptr) return AWQ_ERR_NULL;
+    if (int st = check_ptr(workspace)) return st;
+    return bytes < need ? AWQ_ERR_WORKSPACE : AWQ_OK;
+}
+}  // namespace
+
+extern "C" {
+
+awq_status awq_norm_gate_residual(const void* block, const void* residual, const void* post_weight,
+                                  const void* post_bias, const void* gate, int gate_rows,
+                                  float residual_scale, const void* pre_weight, const void* pre_bias,
+                                  int kind, float eps, int T, int H, int dtype, void* residual_out,
+                                  void* h, float* h_scales, hipStream_t stream) {
+    int st = check_dtype(dtype);
+    if (st) return as_status(st);
+    if (kind != AWQ_NORM_RMS && kind != AWQ_NORM_LAYER) return AWQ_ERR_UNSUPPORTED;
+    if (!(eps >= 0.0f)) return AWQ_ERR_UNSUPPORTED;
+    if (T < 0 || H <= 0 || H % 8 != 0 || H > kMaxNormWidth) return AWQ_ERR_SHAPE;
+    if (gate != nullptr && (gate_rows <= 0 || T % gate_rows != 0)) return AWQ_ERR_SHAPE;
+    if (T == 0) return AWQ_OK;
+    if ((st = check_ptrs({block, residual, pre_weight, residual_out, h}))) return as_status(st);
+    if (post_bias != nullptr && post_weight == nullptr) return AWQ_ERR_NULL;
+    if ((st = check_optional({post_weight, post_bias, gate, pre_bias, h_scales}))) return as_status(st);
+    awq::NormProblem p{block, residual, post_weight, post_bias, gate, pre_weight, pre_bias, residual_out, h,
+                       h_scales, residual_scale, eps, gate_rows, kind, T, H, dtype};
+    return hip_status(awq::launch_norm(p, stream));
+}
+
+awq_status awq_quantize_rows(const void* x, int M, int K, int dtype, void* q, float* scales,
+                             hipStream_t stream) {
+    int st = check_w8a8(M, 0, K, dtype);
+    if (st) return as_status(st);
+    if (M == 0) return AWQ_OK;
+    if ((st = check_ptrs({x, q, scales}))) return as_status(st);
+    return hip_status(awq::launch_quantize_rows(x, M, K, dtype, q, scales, stream));
+}
+
+size_t awq_gemm_w8a8_workspace_bytes(int M, int N, int K) {
+    if (M <= 0 || N <= 0 || check_w8a8(M, N, K, AWQ_F16) != AWQ_OK) return 0;
+    return awq::w8a8_workspace_bytes(M, N, K);
+}
+
+size_t awq_linear_w8a8_workspace_bytes(int M, int N, int K) {
+    if (M <= 0 || N <= 0 || check_w8a8(M, N, K, AWQ_F16) != AWQ_OK) return 0;
+    return awq::linear_w8a8_workspace_bytes(M, N, K);
+}
+
+awq_status awq_gemm_w8a8(const void* x, const float* x_scales, const void* weight,
+                         const float* weight_scales, const float* bias, void* y, int M, int N, int K,
+                         int dtype, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    int st = check_w8a8(M, N, K, dtype);
+    if (st) return as_status(st);
+    if (M == 0 || N == 0) return AWQ_OK;
+    if ((st = check_ptrs({x, x_scales, weight, weight_scales, y}))) return as_status(st);
+    if ((st = check_optional({bias}))) return as_status(st);
+    if ((st = check_workspace(workspace, workspace_bytes, awq::w8a8_workspace_bytes(M, N, K))))
+        return as_status(st);
+    awq::W8a8Problem p{x, nullptr, weight, x_scales, weight_scales, bias, y, M, N, K, dtype};
+    return hip_status(awq::launch_w8a8(p, workspace, stream));
+}
+
+awq_status awq_linear_w8a8(const void* x, const void* weight, const float* weight_scales, const float* bias,
+                           void* y, int M, int N, int K, int dtype, void* workspace,
+                           size_t workspace_bytes, hipStream_t stream) {
+    int st = check_w8a8(M, N, K, dtype);
+    if (st) return as_status(st);
+    if (M == 0 || N == 0) return AWQ_OK;
+    if ((st = check_ptrs({x, weight, weight_scales, y}))) return as_status(st);
+    if ((st = check_optional({bias}))) return as_status(st);
+    if ((st = check_workspace(workspace, workspace_bytes, awq::linear_w8a8_workspace_bytes(M, N, K))))
+        return as_status(st);
+    awq::W8a8Problem p{nullptr, x, weight, nullptr, weight_scales, bias, y, M, N, K, dtype};
+    return hip_status(awq::launch_w8a8(p, workspace, stream));
+}
+
+}  // extern "C"

@@ -264,4 +264,28 @@ int launch_search(const void* const* Ws, const int* Ns, int n_layers, const void
                   float* s_out, float* loss_out, int* best_out, void* workspace, bool fused,
                   hipStream_t st);
 
+
+// norms around a block with its gate and the scaled residual (the C ABI's
+// arguments; gate_rows divides T)
+struct NormProblem {
+    const void *block, *residual, *post_weight, *post_bias, *gate, *pre_weight, *pre_bias;
+    void *residual_out, *h;
+    float* h_scales;                     // non-null: h as int8 codes
+    float residual_scale, eps;
+    int gate_rows, kind, T, H, dtype;
+};
+int launch_norm(const NormProblem& p, hipStream_t st);
+int launch_quantize_rows(const void* x, int M, int K, int dtype, void* q, float* scales, hipStream_t st);
+
+// 8-bit product; either codes and their scales (x, x_scales) or 16-bit rows
+struct W8a8Problem {
+    const void *x, *rows, *weight;
+    const float *x_scales, *weight_scales, *bias;
+    void* y;
+    int M, N, K, dtype;
+};
+size_t w8a8_workspace_bytes(int M, int N, int K);
+size_t linear_w8a8_workspace_bytes(int M, int N, int K);
+int launch_w8a8(const W8a8Problem& p, void* workspace, hipStream_t st);
+
 }  // namespace awq

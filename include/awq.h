@@ -482,6 +482,37 @@ awq_status awq_linear_w8a8(const void* x, const void* weight, const float* weigh
                            const float* bias, void* y, int M, int N, int K, int dtype,
                            void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/*
+ * awq_moe -- a whole mixture-of-experts layer for a few tokens over packed
+ * experts (gate, up and down of each as in awq_gemv_gate_up / awq_gemv):
+ *   l[m][e] = sum_k x[m][k] router[e][k]                     (fp32 sums)
+ *   chosen(m) = the top_k experts with the largest l[m][e], ties to the lowest e
+ *   p[m][j] = exp(l_j) / sum of exp(l) over chosen(m) (renormalize = 1) or
+ *             over all experts (0)
+ *   y[m] = sum_j p[m][j] * down_j(SiLU(gate_j x'[m]) * up_j x'[m])
+ *   x' = x * inv_s, or x when inv_s is NULL (the router reads x)
+ *   x  fp16 [M][K];  inv_s  fp32 [K] or NULL;  router  fp16 [E][K]
+ *   gate_*, up_*  E layers of I x K, down_*  E layers of K x I, one after the
+ *   other, each as awq_quantize_pack writes it (same bits and group_size):
+ *   qweight [E][awq_packed_words], scales and zeros fp16 [E][ceil(N/16)][G][16]
+ *   y  fp16 [M][K] out, rounded once: products take the exact (q - z), sums
+ *   and group scales are fp32, and SiLU(gate) * up goes on as two fp16 numbers
+ *   (22 bits).  It must stay below the fp16 maximum, as in awq_gemv_gate_up.
+ *   0 <= M <= 64, 1 <= top_k <= min(E, 16), E <= 512 (else
+ *   AWQ_ERR_UNSUPPORTED); K and I multiples of 128, one expert's layer < 2^31
+ *   bytes packed (else AWQ_ERR_SHAPE).
+ *   workspace / workspace_bytes: device scratch of at least
+ *   awq_moe_workspace_bytes(M, K, I, E, top_k) bytes, 16-byte aligned.
+ *   The same inputs give the same bits.
+ */
+size_t awq_moe_workspace_bytes(int M, int K, int I, int E, int top_k);
+awq_status awq_moe(const void* x, const float* inv_s, const void* router,
+                   const void* gate_qweight, const void* gate_scales, const void* gate_zeros,
+                   const void* up_qweight, const void* up_scales, const void* up_zeros,
+                   const void* down_qweight, const void* down_scales, const void* down_zeros,
+                   void* y, int M, int K, int I, int E, int top_k, int bits, int group_size,
+                   int renormalize, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

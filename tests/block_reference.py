@@ -45,3 +45,23 @@ UNIT = {"float16": 2.0 ** -11, "bfloat16": 2.0 ** -8}
 
 def unit(dtype):
     return UNIT[str(dtype).replace("torch.", "")]
+
+
+def route(logits, top_k, renormalize):
+    """(ids [M][top_k], weights) in 64 bits, ties to the lowest index."""
+    ids = np.argsort(-logits, axis=1, kind="stable")[:, :top_k]
+    e = np.exp(logits - logits.max(1, keepdims=True))
+    chosen = np.take_along_axis(e, ids, 1)
+    return ids, chosen / (chosen if renormalize else e).sum(1, keepdims=True)
+
+
+def moe(x, router, gate, up, down, top_k, renormalize=True, inv_s=None):
+    """gate, up, down: lists of dequantized float64 layers."""
+    ids, p = route(x @ router.T, top_k, renormalize)
+    xs = x if inv_s is None else x * inv_s
+    y = np.zeros_like(x)
+    for m in range(x.shape[0]):
+        for e, w in zip(ids[m], p[m]):
+            g, u = gate[e] @ xs[m], up[e] @ xs[m]
+            y[m] += w * (down[e] @ (g / (1 + np.exp(-g)) * u))
+    return y

@@ -406,3 +406,23 @@ def test_w8a8_validation(lib):
         assert call(**shape) == NULL
         assert call(**shape, ws=MIS, ws_bytes=need) == ALIGN
         assert call(**shape, ws=P, ws_bytes=need - 1) == WS
+
+
+def test_moe_validation(lib):
+    def call(ptrs=None, inv_s=NUL, M=4, K=256, I=128, E=8, top_k=2, bits=4, gs=128, renorm=1, ws=P5, ws_bytes=1 << 30):
+        p = dict(x=P, router=P2, gq=P3, gs_=P3, gz=P3, uq=P4, us=P4, uz=P4, dq=P5, ds=P5, dz=P5, y=P)
+        p.update(ptrs or {})
+        return lib.awq_moe(p["x"], inv_s, *list(p.values())[1:], M, K, I, E, top_k, bits, gs, renorm, ws, ws_bytes, NUL)
+    for name in ("x", "router", "gq", "gs_", "gz", "uq", "us", "uz", "dq", "ds", "dz", "y"):
+        assert call({name: NUL}) == NULL, name
+        assert call({name: MIS}) == ALIGN, name
+    assert call(inv_s=MIS) == ALIGN and call(ws=NUL) == NULL and call(ws=MIS) == ALIGN
+    need = lib.awq_moe_workspace_bytes(4, 256, 128, 8, 2)
+    assert need > 0 and call(ws_bytes=need - 1) == WS
+    for bad in (dict(bits=5), dict(gs=32), dict(renorm=2), dict(M=65), dict(top_k=0), dict(top_k=9), dict(E=513),
+                dict(E=32, top_k=17), dict(E=0)):
+        assert call(**bad) == UNSUP, bad
+    for bad in (dict(M=-1), dict(K=0), dict(K=192), dict(I=-128), dict(I=64), dict(K=1 << 16, I=1 << 16)):
+        assert call(**bad) == SHAPE, bad
+    assert call({"x": NUL}, M=0) == OK
+    assert lib.awq_moe_workspace_bytes(0, 256, 128, 8, 2) == lib.awq_moe_workspace_bytes(4, 256, 100, 8, 2) == 0

@@ -12,7 +12,7 @@ from .binding import (AwqError, quantize_pack, search_scale, search_scale_shared
                       gemm_splitk_noalloc, gemm_splitk_noalloc_max_bytes,
                       fake_quantize,
                       norm_gate_residual, quantize_rows, gemm_w8a8, linear_w8a8,
-                      gemm_w8a8_workspace_bytes, linear_w8a8_workspace_bytes,
+                      gemm_w8a8_workspace_bytes, linear_w8a8_workspace_bytes, moe, moe_workspace_bytes,
                       library_path,
                       load_library,
                       pack_format_version, packed_words_per_row, packed_words)
@@ -22,5 +22,5 @@ __all__ = ["AwqError", "quantize_pack", "search_scale", "search_scale_shared", "
            "gemv", "gemv_gate_up", "gemm", "gemm_splitk_workspace_bytes",
            "gemm_splitk_noalloc", "gemm_splitk_noalloc_max_bytes", "scale_activations", "fake_quantize", "library_path", "load_library",
            "norm_gate_residual", "quantize_rows", "gemm_w8a8", "linear_w8a8",
-           "gemm_w8a8_workspace_bytes", "linear_w8a8_workspace_bytes",
+           "gemm_w8a8_workspace_bytes", "linear_w8a8_workspace_bytes", "moe", "moe_workspace_bytes",
            "pack_format_version", "packed_words_per_row", "packed_words"]

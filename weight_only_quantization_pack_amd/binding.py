@@ -70,6 +70,8 @@ SIGNATURES = [
     ("awq_linear_w8a8_workspace_bytes", _c_size_t, [_c_int, _c_int, _c_int]),
     ("awq_linear_w8a8", _c_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_int, _c_int,
                                  _c_int, _c_int, _c_void_p, _c_size_t, _c_void_p]),
+    ("awq_moe_workspace_bytes", _c_size_t, [_c_int] * 5),
+    ("awq_moe", _c_int, [_c_void_p] * 13 + [_c_int] * 8 + [_c_void_p, _c_size_t, _c_void_p]),
 ]
 
 STATUS = {0: "AWQ_OK", 1: "AWQ_ERR_NULL", 2: "AWQ_ERR_SHAPE", 3: "AWQ_ERR_UNSUPPORTED",
@@ -653,4 +655,54 @@ def linear_w8a8(x, weight, weight_scales, bias=None, out=None, workspace=None):
     st = lib.awq_linear_w8a8(_ptr(x), _ptr(weight), _ptr(weight_scales), _ptr(bias), _ptr(out), M, N, K, code,
                              ws, ws_bytes, _stream_ptr(x))
     _check(st, "awq_linear_w8a8")
+    return out
+
+
+def moe_workspace_bytes(M: int, K: int, I: int, E: int, top_k: int) -> int:
+    """Workspace bytes of moe for M tokens of K channels, E experts of I channels."""
+    return int(load_library().awq_moe_workspace_bytes(M, K, I, E, top_k))
+
+
+def _need_experts(layer, E, N, K, bits, group_size, what):
+    torch = _torch()
+    words = int(load_library().awq_packed_words(N, K, bits))
+    G = K // group_size if group_size > 0 else 0
+    params = (E, (N + 15) // 16, G, 16)
+    qweight, scales, zeros = layer
+    _need(qweight, torch.int32, (E, words), what + " qweight")
+    _need(scales, torch.float16, params, what + " scales")
+    _need(zeros, torch.float16, params, what + " zeros")
+
+
+def moe(x, router, gate, up, down, inter: int, top_k: int, bits: int = 4, group_size: int = GROUP_SIZE,
+        renormalize: bool = True, inv_s=None, out=None, workspace=None):
+    """A whole mixture-of-experts layer for a few tokens over packed experts
+    (awq_moe): y[m] = sum_j p_j down_j(SiLU(gate_j x') * up_j x') over the top_k
+    experts of x . router^T.
+
+    x fp16 [M][K], M <= 64; router fp16 [E][K]; gate, up: (qweight int32
+    [E][packed_words(inter, K, bits)], scales, zeros fp16
+    [E][ceil(inter / 16)][K / group_size][16]) -- the E layers of quantize_pack,
+    stacked; down the same of K x inter layers.  p = softmax over the chosen
+    experts (renormalize) or over all.  inv_s (fp32 [K], the reciprocal of the
+    AWQ scale of gate and up): x' = x * inv_s; the router reads x.
+    """
+    torch = _torch()
+    lib = load_library()
+    M, K = _rows2d(x, "x")
+    E, _ = _rows2d(router, "router")
+    _need(x, torch.float16, (M, K), "x")
+    _need(router, torch.float16, (E, K), "router")
+    _need_experts(gate, E, inter, K, bits, group_size, "gate")
+    _need_experts(up, E, inter, K, bits, group_size, "up")
+    _need_experts(down, E, K, inter, bits, group_size, "down")
+    _need_optional(inv_s, torch.float32, (K,), "inv_s")
+    out = _out(out, M, K, x.device)
+    _same_device(x, router=router, inv_s=inv_s, out=out,
+                 **{f"{n}[{i}]": t for n, l in (("gate", gate), ("up", up), ("down", down)) for i, t in enumerate(l)})
+    keep, ws, ws_bytes = _workspace(workspace, int(lib.awq_moe_workspace_bytes(M, K, inter, E, top_k)), x.device)
+    st = lib.awq_moe(_ptr(x), _ptr(inv_s), _ptr(router), _ptr(gate[0]), _ptr(gate[1]), _ptr(gate[2]), _ptr(up[0]),
+                     _ptr(up[1]), _ptr(up[2]), _ptr(down[0]), _ptr(down[1]), _ptr(down[2]), _ptr(out), M, K, inter,
+                     E, top_k, bits, group_size, int(renormalize), ws, ws_bytes, _stream_ptr(x))
+    _check(st, "awq_moe")
     return out

@@ -483,4 +483,43 @@ awq_status awq_linear_w8a8(const void* x, const void* weight, const float* weigh
     return hip_status(awq::launch_w8a8(p, workspace, stream));
 }
 
+namespace {
+int check_moe(int M, int K, int I, int E, int top_k) {
+    if (M > awq::kMoeMaxTokens || E > awq::kMoeMaxExperts || top_k < 1 || top_k > awq::kMoeMaxTopK || top_k > E)
+        return AWQ_ERR_UNSUPPORTED;
+    if (M < 0 || K <= 0 || I <= 0 || K % awq::kGroup != 0 || I % awq::kGroup != 0) return AWQ_ERR_SHAPE;
+    // the kernels address one expert's packed tiles with 32-bit offsets
+    if ((long long)K * I / 2 >= (1LL << 31)) return AWQ_ERR_SHAPE;
+    return AWQ_OK;
+}
+}  // namespace
+
+size_t awq_moe_workspace_bytes(int M, int K, int I, int E, int top_k) {
+    if (M <= 0 || check_moe(M, K, I, E, top_k) != AWQ_OK) return 0;
+    return awq::moe_workspace_bytes(M, K, I, E, top_k);
+}
+
+awq_status awq_moe(const void* x, const float* inv_s, const void* router, const void* gate_qweight,
+                   const void* gate_scales, const void* gate_zeros, const void* up_qweight,
+                   const void* up_scales, const void* up_zeros, const void* down_qweight,
+                   const void* down_scales, const void* down_zeros, void* y, int M, int K, int I, int E,
+                   int top_k, int bits, int group_size, int renormalize, void* workspace,
+                   size_t workspace_bytes, hipStream_t stream) {
+    int st = check_quant_params(bits, group_size, 1);
+    if (st) return as_status(st);
+    if (renormalize != 0 && renormalize != 1) return AWQ_ERR_UNSUPPORTED;
+    if ((st = check_moe(M, K, I, E, top_k))) return as_status(st);
+    if (M == 0) return AWQ_OK;
+    if ((st = check_ptrs({x, router, gate_qweight, gate_scales, gate_zeros, up_qweight, up_scales, up_zeros,
+                          down_qweight, down_scales, down_zeros, y})))
+        return as_status(st);
+    if ((st = check_optional({inv_s}))) return as_status(st);
+    if ((st = check_workspace(workspace, workspace_bytes, awq::moe_workspace_bytes(M, K, I, E, top_k))))
+        return as_status(st);
+    awq::MoeProblem p{x, router, inv_s, {gate_qweight, up_qweight, down_qweight},
+                      {gate_scales, up_scales, down_scales}, {gate_zeros, up_zeros, down_zeros}, y, M, K, I, E,
+                      top_k, bits, group_size, renormalize};
+    return hip_status(awq::launch_moe(p, workspace, stream));
+}
+
 }  // extern "C"

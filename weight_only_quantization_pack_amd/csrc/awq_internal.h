@@ -288,4 +288,16 @@ size_t w8a8_workspace_bytes(int M, int N, int K);
 size_t linear_w8a8_workspace_bytes(int M, int N, int K);
 int launch_w8a8(const W8a8Problem& p, void* workspace, hipStream_t st);
 
+// mixture-of-experts layer for a few tokens
+constexpr int kMoeMaxTokens = 64, kMoeMaxTopK = 16, kMoeMaxExperts = 512;
+struct MoeProblem {
+    const void *x, *router;
+    const float* inv_s;                  // or nullptr
+    const void *qweight[3], *scales[3], *zeros[3];   // gate, up (I x K), down (K x I)
+    void* y;
+    int M, K, I, E, top_k, bits, group_size, renormalize;
+};
+size_t moe_workspace_bytes(int M, int K, int I, int E, int top_k);
+int launch_moe(const MoeProblem& p, void* workspace, hipStream_t st);
+
 }  // namespace awq

@@ -499,8 +499,8 @@ awq_status awq_linear_w8a8(const void* x, const void* weight, const float* weigh
  *   and group scales are fp32, and SiLU(gate) * up goes on as two fp16 numbers
  *   (22 bits).  It must stay below the fp16 maximum, as in awq_gemv_gate_up.
  *   0 <= M <= 64, 1 <= top_k <= min(E, 16), E <= 512 (else
- *   AWQ_ERR_UNSUPPORTED); K and I multiples of 128, one expert's layer < 2^31
- *   bytes packed (else AWQ_ERR_SHAPE).
+ *   AWQ_ERR_UNSUPPORTED); K and I multiples of 128, at most 32768 (else
+ *   AWQ_ERR_SHAPE).
  *   workspace / workspace_bytes: device scratch of at least
  *   awq_moe_workspace_bytes(M, K, I, E, top_k) bytes, 16-byte aligned.
  *   The same inputs give the same bits.

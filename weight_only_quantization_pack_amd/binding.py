@@ -120,9 +120,15 @@ def _check(status: int, what: str):
         raise AwqError(f"{what} failed: {name}", status)
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream_ptr(t):
@@ -472,47 +478,68 @@ def gemm(x, qweight, scales, zeros, N: int, bits: int = 4, group_size: int = GRO
 
 # ---------------------------------------------------------------------------
 # operators beside the packed products in a decoder block
+#
+# A decode step calls these per token, so their checks are kept short: _arg
+# accepts a right argument with one chain of comparisons and gives its address;
+# only a wrong one goes on to the checks that name what is wrong with it.
 # ---------------------------------------------------------------------------
 NORM_KINDS = {"rms": 0, "layer": 1}
+
+
+def _arg(t, dtype, shape, device, name):
+    """The address of t, a contiguous tensor of this type and shape on GPU
+    `device` (its index); None passes through as NULL."""
+    if t is None:
+        return None
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _need(t, dtype, shape, name)
+    raise ValueError(f"{name} must be on GPU {device}, got {t.device}")
+
+
+def _required(t, name):
+    if t is None:
+        raise TypeError(f"{name} must be a torch.Tensor")
 
 
 def _dtype_code(dtype, name):
     """awq_dtype of a 16-bit torch dtype."""
     torch = _torch()
-    if dtype == torch.float16:
+    if dtype is torch.float16:
         return 0
-    if dtype == torch.bfloat16:
+    if dtype is torch.bfloat16:
         return 1
     raise TypeError(f"{name} must be torch.float16 or torch.bfloat16, got {dtype}")
 
 
 def _rows2d(t, name):
+    """(shape, GPU index) of a 2-dimensional GPU tensor."""
     if not isinstance(t, _torch().Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dim() != 2:
         raise ValueError(f"{name} must have 2 dimensions, got shape {tuple(t.shape)}")
-    return t.shape
+    device = t.get_device()
+    if device < 0:
+        raise ValueError(f"{name} must be on the GPU")
+    return t.shape, device
 
 
-def _need_optional(t, dtype, shape, name):
-    if t is not None:
-        _need(t, dtype, shape, name)
+def _raw_stream(device):
+    """The current stream of GPU `device` as an integer handle."""
+    return _torch()._C._cuda_getCurrentRawStream(device)
 
 
-def _same_device(first, **others):
-    """Every tensor on the first one's GPU (whose stream the call goes to)."""
-    dev = first.device
-    for name, t in others.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} must be on {dev}, got {t.device}")
-
-
-def _workspace(workspace, need, device):
-    """(tensor kept alive, pointer, bytes) of a call's scratch memory."""
+def _workspace(workspace, need, like):
+    """(tensor kept alive, address, bytes) of a call's scratch memory."""
     if need == 0:
         return None, None, 0
     if workspace is None:
-        workspace = _torch().empty(need, dtype=_torch().uint8, device=device)
+        workspace = like.new_empty(need, dtype=_torch().uint8)
+    elif workspace.get_device() != like.get_device() or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {like.device}")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -535,41 +562,47 @@ def norm_gate_residual(block, residual, pre_weight, post_weight=None, gate=None,
     """
     torch = _torch()
     lib = load_library()
-    T, H = _rows2d(block, "block")
+    shape, dev = _rows2d(block, "block")
+    T, H = shape
     dtype = block.dtype
     code = _dtype_code(dtype, "block")
-    _need(block, dtype, (T, H), "block")
-    _need(residual, dtype, (T, H), "residual")
-    for t, name in ((pre_weight, "pre_weight"), (post_weight, "post_weight"), (pre_bias, "pre_bias"),
-                    (post_bias, "post_bias")):
-        if t is not None or name == "pre_weight":
-            _need(t, dtype, (H,), name)
+    row = shape[1:]
+    _required(residual, "residual")
+    _required(pre_weight, "pre_weight")
     if post_bias is not None and post_weight is None:
         raise ValueError("post_bias needs post_weight")
     if kind not in NORM_KINDS:
         raise ValueError(f"kind must be one of {sorted(NORM_KINDS)}, got {kind!r}")
-    gate_rows = 0
+    gate_rows, gate_shape = 0, row
     if gate is not None:
-        gate_rows = 1 if gate.dim() == 1 else gate.shape[0]
-        _need(gate, dtype, (H,) if gate.dim() == 1 else (gate_rows, H), "gate")
-        if gate_rows == 0 or T % gate_rows:
-            raise ValueError(f"gate rows ({gate_rows}) must divide the rows of block ({T})")
-    _same_device(block, residual=residual, pre_weight=pre_weight, post_weight=post_weight, gate=gate,
-                 pre_bias=pre_bias, post_bias=post_bias)
+        gate_rows = 1
+        if gate.dim() != 1:
+            gate_rows = gate.shape[0]
+            gate_shape = (gate_rows, H)
+            if gate_rows == 0 or T % gate_rows:
+                raise ValueError(f"gate rows ({gate_rows}) must divide the rows of block ({T})")
+    h_type = torch.int8 if quantize else dtype
+    scales = None
     if out is None:
         r = torch.empty_like(residual)
-        h = torch.empty((T, H), dtype=torch.int8 if quantize else dtype, device=block.device)
-        scales = torch.empty(T, dtype=torch.float32, device=block.device) if quantize else None
+        h = block.new_empty(shape, dtype=h_type)
+        if quantize:
+            scales = block.new_empty(T, dtype=torch.float32)
+    elif quantize:
+        r, h, scales = out
     else:
-        r, h, scales = out if quantize else (*out, None)
-        _need(r, dtype, (T, H), "out[0]")
-        _need(h, torch.int8 if quantize else dtype, (T, H), "out[1]")
-        _need_optional(scales, torch.float32, (T,), "out[2]")
-        _same_device(block, **{"out[0]": r, "out[1]": h, "out[2]": scales})
-    st = lib.awq_norm_gate_residual(_ptr(block), _ptr(residual), _ptr(post_weight), _ptr(post_bias), _ptr(gate),
-                                    gate_rows, residual_scale, _ptr(pre_weight), _ptr(pre_bias),
-                                    NORM_KINDS[kind], eps, T, H, code, _ptr(r), _ptr(h), _ptr(scales),
-                                    _stream_ptr(block))
+        r, h = out
+    _required(r, "out[0]")
+    _required(h, "out[1]")
+    if quantize:
+        _required(scales, "out[2]")
+    st = lib.awq_norm_gate_residual(
+        _arg(block, dtype, shape, dev, "block"), _arg(residual, dtype, shape, dev, "residual"),
+        _arg(post_weight, dtype, row, dev, "post_weight"), _arg(post_bias, dtype, row, dev, "post_bias"),
+        _arg(gate, dtype, gate_shape, dev, "gate"), gate_rows, residual_scale,
+        _arg(pre_weight, dtype, row, dev, "pre_weight"), _arg(pre_bias, dtype, row, dev, "pre_bias"),
+        NORM_KINDS[kind], eps, T, H, code, _arg(r, dtype, shape, dev, "out[0]"), _arg(h, h_type, shape, dev, "out[1]"),
+        _arg(scales, torch.float32, shape[:1], dev, "out[2]"), _raw_stream(dev))
     _check(st, "awq_norm_gate_residual")
     return (r, h, scales) if quantize else (r, h)
 
@@ -581,43 +614,30 @@ def quantize_rows(x, out=None):
     a multiple of 16."""
     torch = _torch()
     lib = load_library()
-    M, K = _rows2d(x, "x")
+    shape, dev = _rows2d(x, "x")
     code = _dtype_code(x.dtype, "x")
-    _need(x, x.dtype, (M, K), "x")
     if out is None:
-        q = torch.empty((M, K), dtype=torch.int8, device=x.device)
-        scales = torch.empty(M, dtype=torch.float32, device=x.device)
+        q = x.new_empty(shape, dtype=torch.int8)
+        scales = x.new_empty(shape[0], dtype=torch.float32)
     else:
         q, scales = out
-        _need(q, torch.int8, (M, K), "out[0]")
-        _need(scales, torch.float32, (M,), "out[1]")
-        _same_device(x, **{"out[0]": q, "out[1]": scales})
-    st = lib.awq_quantize_rows(_ptr(x), M, K, code, _ptr(q), _ptr(scales), _stream_ptr(x))
+        _required(q, "out[0]")
+        _required(scales, "out[1]")
+    st = lib.awq_quantize_rows(_arg(x, x.dtype, shape, dev, "x"), shape[0], shape[1], code,
+                               _arg(q, torch.int8, shape, dev, "out[0]"),
+                               _arg(scales, torch.float32, shape[:1], dev, "out[1]"), _raw_stream(dev))
     _check(st, "awq_quantize_rows")
     return q, scales
 
 
 def gemm_w8a8_workspace_bytes(M: int, N: int, K: int) -> int:
+    """Workspace bytes of gemm_w8a8 (0: none) on the current device."""
     return int(load_library().awq_gemm_w8a8_workspace_bytes(M, N, K))
 
 
 def linear_w8a8_workspace_bytes(M: int, N: int, K: int) -> int:
+    """Workspace bytes of linear_w8a8 (0: none) on the current device."""
     return int(load_library().awq_linear_w8a8_workspace_bytes(M, N, K))
-
-
-def _w8a8_operands(x, M, K, weight, weight_scales, bias, dtype, out):
-    """Checks of the product's weight side; (N, out)."""
-    torch = _torch()
-    N, _ = _rows2d(weight, "weight")
-    _need(weight, torch.int8, (N, K), "weight")
-    _need(weight_scales, torch.float32, (N,), "weight_scales")
-    _need_optional(bias, torch.float32, (N,), "bias")
-    if out is None:
-        out = torch.empty((M, N), dtype=dtype, device=x.device)
-    else:
-        _need(out, dtype, (M, N), "out")
-    _same_device(x, weight=weight, weight_scales=weight_scales, bias=bias, out=out)
-    return N, out
 
 
 def gemm_w8a8(q, q_scales, weight, weight_scales, bias=None, dtype=None, out=None, workspace=None):
@@ -627,17 +647,21 @@ def gemm_w8a8(q, q_scales, weight, weight_scales, bias=None, dtype=None, out=Non
     [M][N]: dtype (default torch.float16), or out's."""
     torch = _torch()
     lib = load_library()
-    M, K = _rows2d(q, "q")
-    _need(q, torch.int8, (M, K), "q")
-    _need(q_scales, torch.float32, (M,), "q_scales")
+    (M, K), dev = _rows2d(q, "q")
+    N = _rows2d(weight, "weight")[0][0]
+    _required(q_scales, "q_scales")
+    _required(weight_scales, "weight_scales")
     if dtype is None:
         dtype = torch.float16 if out is None else out.dtype
     code = _dtype_code(dtype, "dtype")
-    _same_device(q, q_scales=q_scales)
-    N, out = _w8a8_operands(q, M, K, weight, weight_scales, bias, dtype, out)
-    keep, ws, ws_bytes = _workspace(workspace, int(lib.awq_gemm_w8a8_workspace_bytes(M, N, K)), q.device)
-    st = lib.awq_gemm_w8a8(_ptr(q), _ptr(q_scales), _ptr(weight), _ptr(weight_scales), _ptr(bias), _ptr(out),
-                           M, N, K, code, ws, ws_bytes, _stream_ptr(q))
+    if out is None:
+        out = q.new_empty((M, N), dtype=dtype)
+    keep, ws, ws_bytes = _workspace(workspace, lib.awq_gemm_w8a8_workspace_bytes(M, N, K), q)
+    st = lib.awq_gemm_w8a8(_arg(q, torch.int8, (M, K), dev, "q"), _arg(q_scales, torch.float32, (M,), dev, "q_scales"),
+                           _arg(weight, torch.int8, (N, K), dev, "weight"),
+                           _arg(weight_scales, torch.float32, (N,), dev, "weight_scales"),
+                           _arg(bias, torch.float32, (N,), dev, "bias"), _arg(out, dtype, (M, N), dev, "out"),
+                           M, N, K, code, ws, ws_bytes, _raw_stream(dev))
     _check(st, "awq_gemm_w8a8")
     return out
 
@@ -646,14 +670,20 @@ def linear_w8a8(x, weight, weight_scales, bias=None, out=None, workspace=None):
     """gemm_w8a8 of the quantized rows of x (awq_linear_w8a8): x fp16 or bf16
     [M][K], y of the same type.  One call: short decode rows are quantized
     inside the product's launch."""
+    torch = _torch()
     lib = load_library()
-    M, K = _rows2d(x, "x")
-    code = _dtype_code(x.dtype, "x")
-    _need(x, x.dtype, (M, K), "x")
-    N, out = _w8a8_operands(x, M, K, weight, weight_scales, bias, x.dtype, out)
-    keep, ws, ws_bytes = _workspace(workspace, int(lib.awq_linear_w8a8_workspace_bytes(M, N, K)), x.device)
-    st = lib.awq_linear_w8a8(_ptr(x), _ptr(weight), _ptr(weight_scales), _ptr(bias), _ptr(out), M, N, K, code,
-                             ws, ws_bytes, _stream_ptr(x))
+    (M, K), dev = _rows2d(x, "x")
+    dtype = x.dtype
+    code = _dtype_code(dtype, "x")
+    N = _rows2d(weight, "weight")[0][0]
+    _required(weight_scales, "weight_scales")
+    if out is None:
+        out = x.new_empty((M, N))
+    keep, ws, ws_bytes = _workspace(workspace, lib.awq_linear_w8a8_workspace_bytes(M, N, K), x)
+    st = lib.awq_linear_w8a8(_arg(x, dtype, (M, K), dev, "x"), _arg(weight, torch.int8, (N, K), dev, "weight"),
+                             _arg(weight_scales, torch.float32, (N,), dev, "weight_scales"),
+                             _arg(bias, torch.float32, (N,), dev, "bias"), _arg(out, dtype, (M, N), dev, "out"),
+                             M, N, K, code, ws, ws_bytes, _raw_stream(dev))
     _check(st, "awq_linear_w8a8")
     return out
 
@@ -661,17 +691,6 @@ def linear_w8a8(x, weight, weight_scales, bias=None, out=None, workspace=None):
 def moe_workspace_bytes(M: int, K: int, I: int, E: int, top_k: int) -> int:
     """Workspace bytes of moe for M tokens of K channels, E experts of I channels."""
     return int(load_library().awq_moe_workspace_bytes(M, K, I, E, top_k))
-
-
-def _need_experts(layer, E, N, K, bits, group_size, what):
-    torch = _torch()
-    words = int(load_library().awq_packed_words(N, K, bits))
-    G = K // group_size if group_size > 0 else 0
-    params = (E, (N + 15) // 16, G, 16)
-    qweight, scales, zeros = layer
-    _need(qweight, torch.int32, (E, words), what + " qweight")
-    _need(scales, torch.float16, params, what + " scales")
-    _need(zeros, torch.float16, params, what + " zeros")
 
 
 def moe(x, router, gate, up, down, inter: int, top_k: int, bits: int = 4, group_size: int = GROUP_SIZE,
@@ -689,20 +708,27 @@ def moe(x, router, gate, up, down, inter: int, top_k: int, bits: int = 4, group_
     """
     torch = _torch()
     lib = load_library()
-    M, K = _rows2d(x, "x")
-    E, _ = _rows2d(router, "router")
-    _need(x, torch.float16, (M, K), "x")
-    _need(router, torch.float16, (E, K), "router")
-    _need_experts(gate, E, inter, K, bits, group_size, "gate")
-    _need_experts(up, E, inter, K, bits, group_size, "up")
-    _need_experts(down, E, K, inter, bits, group_size, "down")
-    _need_optional(inv_s, torch.float32, (K,), "inv_s")
-    out = _out(out, M, K, x.device)
-    _same_device(x, router=router, inv_s=inv_s, out=out,
-                 **{f"{n}[{i}]": t for n, l in (("gate", gate), ("up", up), ("down", down)) for i, t in enumerate(l)})
-    keep, ws, ws_bytes = _workspace(workspace, int(lib.awq_moe_workspace_bytes(M, K, inter, E, top_k)), x.device)
-    st = lib.awq_moe(_ptr(x), _ptr(inv_s), _ptr(router), _ptr(gate[0]), _ptr(gate[1]), _ptr(gate[2]), _ptr(up[0]),
-                     _ptr(up[1]), _ptr(up[2]), _ptr(down[0]), _ptr(down[1]), _ptr(down[2]), _ptr(out), M, K, inter,
-                     E, top_k, bits, group_size, int(renormalize), ws, ws_bytes, _stream_ptr(x))
+    shape, dev = _rows2d(x, "x")
+    M, K = shape
+    E = _rows2d(router, "router")[0][0]
+    half, I = torch.float16, inter
+    if bits not in (3, 4) or group_size not in (64, 128):
+        _check(3, "awq_moe")                                 # AWQ_ERR_UNSUPPORTED
+    if out is None:
+        out = torch.empty_like(x)
+    keep, ws, ws_bytes = _workspace(workspace, lib.awq_moe_workspace_bytes(M, K, I, E, top_k), x)
+    args = [_arg(x, half, shape, dev, "x"), _arg(inv_s, torch.float32, shape[1:], dev, "inv_s"),
+            _arg(router, half, (E, K), dev, "router")]
+    for layer, n, k, name in ((gate, I, K, "gate"), (up, I, K, "up"), (down, K, I, "down")):
+        qweight, scales, zeros = layer
+        _required(qweight, name + " qweight")
+        _required(scales, name + " scales")
+        _required(zeros, name + " zeros")
+        blocks = (n + 15) // 16
+        params = (E, blocks, k // group_size, 16)
+        args += [_arg(qweight, torch.int32, (E, blocks * 16 * (k // 32 * bits)), dev, name + " qweight"),
+                 _arg(scales, half, params, dev, name + " scales"), _arg(zeros, half, params, dev, name + " zeros")]
+    st = lib.awq_moe(*args, _arg(out, half, shape, dev, "out"), M, K, I, E, top_k, bits, group_size,
+                     int(renormalize), ws, ws_bytes, _raw_stream(dev))
     _check(st, "awq_moe")
     return out

@@ -488,8 +488,8 @@ int check_moe(int M, int K, int I, int E, int top_k) {
     if (M > awq::kMoeMaxTokens || E > awq::kMoeMaxExperts || top_k < 1 || top_k > awq::kMoeMaxTopK || top_k > E)
         return AWQ_ERR_UNSUPPORTED;
     if (M < 0 || K <= 0 || I <= 0 || K % awq::kGroup != 0 || I % awq::kGroup != 0) return AWQ_ERR_SHAPE;
-    // the kernels address one expert's packed tiles with 32-bit offsets
-    if ((long long)K * I / 2 >= (1LL << 31)) return AWQ_ERR_SHAPE;
+    // a token's operand row is held in LDS (as two fp16 planes)
+    if (K > awq::kMoeMaxWidth || I > awq::kMoeMaxWidth) return AWQ_ERR_SHAPE;
     return AWQ_OK;
 }
 }  // namespace

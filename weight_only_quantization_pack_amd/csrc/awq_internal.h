@@ -289,7 +289,7 @@ size_t linear_w8a8_workspace_bytes(int M, int N, int K);
 int launch_w8a8(const W8a8Problem& p, void* workspace, hipStream_t st);
 
 // mixture-of-experts layer for a few tokens
-constexpr int kMoeMaxTokens = 64, kMoeMaxTopK = 16, kMoeMaxExperts = 512;
+constexpr int kMoeMaxTokens = 64, kMoeMaxTopK = 16, kMoeMaxExperts = 512, kMoeMaxWidth = 32768;
 struct MoeProblem {
     const void *x, *router;
     const float* inv_s;                  // or nullptr

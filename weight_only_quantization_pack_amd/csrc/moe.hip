@@ -4,20 +4,18 @@
 //   y = sum_j p_j down_j(SiLU(gate_j x') * up_j x'),  x' = x * inv_s or x
 //
 // HBM-bound: every packed byte of an expert that some token takes is read
-// once, by whichever tokens take it.  Launches:
-//   k_moe_router  the logits (fp16 MFMA, fp32 sums); x' where there is a scale
-//   k_moe_experts the chosen experts and, for each, its gate and up
-//                 projections over its tokens: h = SiLU(g) * u
-//   k_moe_experts the down projections of h, one fp32 row per (token, choice)
-//   k_moe_join    y = sum over the choices, in their order, rounded once
+// once, by whichever tokens take it.  Three launches:
+//   k_moe_route   one workgroup per token: its logits, choices and weights
+//   gate and up   h = SiLU(g) * u of every (token, choice)
+//   down          the projections of h; the workgroup that ends last on a
+//                 block of columns sums the choices there and writes y
+// Both expert products run as k_moe_token (one token) or k_moe_tile (more).
 //
-// One kernel serves both expert products.  A work item is a block of 16 output
-// rows of one chosen expert; WK waves take its k tiles in turn.  The weights
-// are the B operand of v_mfma_f32_16x16x32_f16 (lane slot = operand, as
-// packed), always the exact (q - z), and the group scale multiplies the fp32
-// group sums, so the only roundings on the way are those of fp32 sums.  The
-// 16 operand rows of A hold more than one row per token where that keeps the
-// products exact:
+// The weights are the B operand of v_mfma_f32_16x16x32_f16 (lane slot =
+// operand, as packed), always the exact (q - z), and the group scale
+// multiplies the fp32 group sums, so the only roundings on the way are those
+// of fp32 sums.  The 16 rows of the A operand hold more than one row per token
+// where that keeps the products exact:
 //   - an operand that is not an fp16 number (h, and x' = x * inv_s) is split
 //     into hi = fp16(v) and lo = fp16((v - hi) * 2^11), two rows whose sums
 //     are added as hi + lo / 2^11: 22 bits of v, for matrix time that is free
@@ -32,16 +30,18 @@
 namespace awq {
 namespace {
 
-constexpr int kMoeWaves = 8;                       // waves of an expert workgroup
 constexpr int kMaxAssign = kMoeMaxTokens * kMoeMaxTopK;
+constexpr int kMoeTileBlocks = 8;                  // waves, and blocks of 16 rows, of a k_moe_tile workgroup
 constexpr uint32_t kOutOfRange = 0x80000000u;      // > every buffer's size: loads return zero
 constexpr float kLoScale = 2048.0f;                // of the lo plane
+constexpr int kNonTemporal = 2;                    // weights: each byte is read once
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t moe_rsrc(const void* p, uint32_t bytes) {
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t moe_rsrc(const void* p, size_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)bytes, 0x00020000);
 }
-__device__ __forceinline__ half8_t load_half8(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-    return __builtin_bit_cast(half8_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+__device__ __forceinline__ void load16_lds(__amdgpu_buffer_rsrc_t r, unsigned char* lds, uint32_t voff,
+                                           uint32_t soff) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)lds, 16, voff, soff, 0, 0);
 }
 
 __device__ __forceinline__ void split_hi_lo(float v, _Float16& hi, _Float16& lo) {
@@ -49,101 +49,28 @@ __device__ __forceinline__ void split_hi_lo(float v, _Float16& hi, _Float16& lo)
     lo = (_Float16)((v - (float)hi) * kLoScale);
 }
 
+// Values that another workgroup of the same launch reads: written through to
+// and read from the point where all compute units see the same memory.
+__device__ __forceinline__ void store_shared(float* p, float v) {
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float load_shared(const float* p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 // ---------------------------------------------------------------------------
-// router: one workgroup per 16 experts x 16 tokens, its 16 waves take the k32
-// steps in turn
+// router and choices: one workgroup of 16 waves per token
 // ---------------------------------------------------------------------------
-struct RouterArgs {
+struct RouteArgs {
     const _Float16 *x, *router;
     const float* inv_s;                            // or nullptr
-    float* logits;                                 // [M][E]
+    int* ids;                                      // [M][top_k]
+    float* weights;
     _Float16* scaled;                              // x' hi plane [M][K], then the lo plane (inv_s only)
-    int M, E, K;
+    int* arrived;                                  // the down product's counters, cleared here
+    int n_arrived;
+    int M, E, K, top_k, renorm;
 };
-
-__global__ __launch_bounds__(1024) void k_moe_router(RouterArgs a) {
-    __shared__ float4_t red[16][64];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int j = lane & 15, h = lane >> 4;
-    const int e0 = blockIdx.x * 16, m0 = blockIdx.y * 16;
-    const int mrows = min(16, a.M - m0);
-    const uint32_t row = (uint32_t)a.K * 2u;
-    const __amdgpu_buffer_rsrc_t rx = moe_rsrc(a.x + (size_t)m0 * a.K, (uint32_t)mrows * row);
-    const __amdgpu_buffer_rsrc_t rr = moe_rsrc(a.router + (size_t)e0 * a.K, (uint32_t)min(16, a.E - e0) * row);
-    float4_t acc = {0.f, 0.f, 0.f, 0.f};
-    const int steps = a.K / 32;
-    for (int s = wave; s < steps; s += 16) {
-        const uint32_t off = (uint32_t)j * row + (uint32_t)s * 64u + 16u * h;
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(load_half8(rx, off), load_half8(rr, off), acc, 0, 0, 0);
-    }
-    red[wave][lane] = acc;
-    __syncthreads();
-    if (wave == 0) {
-        float4_t sum = red[0][lane];
-        for (int w = 1; w < 16; ++w) {
-            const float4_t o = red[w][lane];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) sum[r] += o[r];
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            if (4 * h + r < mrows && e0 + j < a.E) a.logits[(size_t)(m0 + 4 * h + r) * a.E + e0 + j] = sum[r];
-    }
-    if (a.inv_s && blockIdx.x == 0) {
-        const size_t plane = (size_t)a.M * a.K;
-        for (int i = tid; i < mrows * a.K; i += 1024) {
-            const int m = i / a.K, k = i - m * a.K;
-            const size_t at = (size_t)(m0 + m) * a.K + k;
-            split_hi_lo((float)a.x[at] * a.inv_s[k], a.scaled[at], a.scaled[plane + at]);
-        }
-    }
-}
-
-// ---------------------------------------------------------------------------
-// routing of all tokens, by every expert workgroup for itself
-// ---------------------------------------------------------------------------
-struct Lists {
-    int ids[kMaxAssign];                           // expert of assignment token * top_k + choice
-    int order[kMaxAssign];                         // assignments grouped by expert (any order within one)
-    int count[kMoeMaxExperts], start[kMoeMaxExperts], cursor[kMoeMaxExperts];
-    int active[kMoeMaxExperts];                    // experts with tokens, ascending
-    int n_active, most;                            // how many, and the largest count
-};
-
-// From ids: counts, starts, the grouped order and the active experts.  Called
-// by a whole workgroup after ids are written and visible.
-__device__ void build_lists(Lists& L, int assigned, int E) {
-    const int tid = threadIdx.x, lane = tid & 63;
-    for (int e = tid; e < E; e += 64 * kMoeWaves) L.count[e] = 0;
-    __syncthreads();
-    for (int i = tid; i < assigned; i += 64 * kMoeWaves) atomicAdd(&L.count[L.ids[i]], 1);
-    __syncthreads();
-    if (tid < 64) {                                // wave 0: prefix over the experts, 64 at a time
-        int base = 0, act = 0, most = 0;
-        for (int e0 = 0; e0 < E; e0 += 64) {
-            const int e = e0 + lane;
-            const int c = e < E ? L.count[e] : 0;
-            int incl = c;
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const int o = __shfl_up(incl, d);
-                if (lane >= d) incl += o;
-            }
-            const uint64_t on = __builtin_amdgcn_ballot_w64(c > 0);
-            if (e < E) {
-                L.start[e] = L.cursor[e] = base + incl - c;
-                if (c > 0) L.active[act + __popcll(on & ((1ull << lane) - 1))] = e;
-            }
-            base += __shfl(incl, 63);
-            act += __popcll(on);
-            most = max(most, (int)wave_reduce((uint32_t)c, MaxU32()));
-        }
-        if (lane == 0) { L.n_active = act; L.most = most; }
-    }
-    __syncthreads();
-    for (int i = tid; i < assigned; i += 64 * kMoeWaves) L.order[atomicAdd(&L.cursor[L.ids[i]], 1)] = i;
-    __syncthreads();
-}
 
 // One wave picks a token's experts from its logits.  The keys order the logits
 // as integers; a NaN comes below every number and a taken expert below a NaN,
@@ -160,38 +87,97 @@ __device__ void route_token(const float* logits, int E, int top_k, bool renorm, 
         const uint32_t b = __builtin_bit_cast(uint32_t, v[i] + 0.0f);      // -0 as 0: they tie
         key[i] = e >= E ? 0u : v[i] != v[i] ? 1u : b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
     }
-    float top = 0.0f, chosen = 0.0f, mine = 0.0f;  // mine: lane j keeps choice j's exp
+    float mine = 0.0f;                             // lane c keeps choice c
+    int id = 0;
     for (int c = 0; c < top_k; ++c) {
         uint32_t best = 0;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) best = max(best, key[i]);
+        for (int i = 0; i < PER; ++i)
+            if (64 * i < E) best = max(best, key[i]);
         best = wave_reduce(best, MaxU32());
-        int pick = -1;                             // lowest index with that key
-        float l = 0.0f;
+        bool found = false;                        // lowest index with that key
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
+            if (64 * i >= E || found) continue;    // wave-uniform
             const uint64_t on = __builtin_amdgcn_ballot_w64(key[i] == best);
-            if (pick < 0 && on) {
+            if (on) {
+                found = true;
                 const int at = __ffsll((unsigned long long)on) - 1;
-                pick = 64 * i + at;
-                l = __shfl(v[i], at);
+                const float l = __builtin_bit_cast(
+                    float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v[i]), at));
+                if (lane == c) { mine = l; id = 64 * i + at; }
                 if (lane == at) key[i] = 0u;
             }
         }
-        if (c == 0) top = l;
-        const float p = expf(l - top);
-        chosen += p;
-        if (lane == c) { mine = p; ids[c] = pick; }
     }
-    float sum = chosen;
+    const float top = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, mine), 0));
+    const float p = lane < top_k ? expf(mine - top) : 0.0f;
+    float s = p;
     if (!renorm) {
-        float s = 0.0f;
+        s = 0.0f;
 #pragma unroll
         for (int i = 0; i < PER; ++i)
             if (lane + 64 * i < E) s += expf(v[i] - top);
-        sum = __builtin_bit_cast(float, wave_reduce(__builtin_bit_cast(uint32_t, s), SumF32()));
     }
-    if (lane < top_k) weights[lane] = mine / sum;
+    const float sum = __builtin_bit_cast(float, wave_reduce(__builtin_bit_cast(uint32_t, s), SumF32()));
+    if (lane < top_k) {
+        ids[lane] = id;
+        weights[lane] = p / sum;
+    }
+}
+
+// A wave takes kRouteRows experts at a time, each lane 8 k of every 512: the
+// router's rows are all in flight while x comes from LDS.
+constexpr int kRouteRows = 4;
+
+__global__ __launch_bounds__(1024) void k_moe_route(RouteArgs a) {
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+    __shared__ float logits[kMoeMaxExperts];
+    uint4* xs = reinterpret_cast<uint4*>(smem);
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int chunks = a.K / 8;
+    const size_t m = blockIdx.x;
+    const uint4* x = reinterpret_cast<const uint4*>(a.x) + m * chunks;
+    for (int i = tid; i < chunks; i += 1024) xs[i] = x[i];
+    if (m == 0)
+        for (int i = tid; i < a.n_arrived; i += 1024) a.arrived[i] = 0;
+    __syncthreads();
+    for (int e0 = wave * kRouteRows; e0 < a.E; e0 += 16 * kRouteRows) {
+        float sum[kRouteRows] = {};
+        const uint4* r[kRouteRows];
+#pragma unroll
+        for (int q = 0; q < kRouteRows; ++q)
+            r[q] = reinterpret_cast<const uint4*>(a.router) + (size_t)min(e0 + q, a.E - 1) * chunks;
+#pragma unroll 2
+        for (int i = lane; i < chunks; i += 64) {
+            uint4 rv[kRouteRows];
+#pragma unroll
+            for (int q = 0; q < kRouteRows; ++q) rv[q] = r[q][i];
+            const uint4 xv = xs[i];
+            const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+#pragma unroll
+            for (int q = 0; q < kRouteRows; ++q) {
+                const uint32_t rw[4] = {rv[q].x, rv[q].y, rv[q].z, rv[q].w};
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+                    sum[q] = __builtin_amdgcn_fdot2(__builtin_bit_cast(half2_t, xw[w]),
+                                                    __builtin_bit_cast(half2_t, rw[w]), sum[q], false);
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < kRouteRows; ++q) {
+            const float l = __builtin_bit_cast(float, wave_reduce(__builtin_bit_cast(uint32_t, sum[q]), SumF32()));
+            if (lane == 0 && e0 + q < a.E) logits[e0 + q] = l;
+        }
+    }
+    __syncthreads();
+    if (wave == 0) route_token(logits, a.E, a.top_k, a.renorm, a.ids + m * a.top_k, a.weights + m * a.top_k);
+    if (a.inv_s) {
+        const _Float16* xh = reinterpret_cast<const _Float16*>(smem);
+        const size_t at = m * a.K, plane = (size_t)a.M * a.K;
+        for (int k = tid; k < a.K; k += 1024)
+            split_hi_lo((float)xh[k] * a.inv_s[k], a.scaled[at + k], a.scaled[plane + at + k]);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -200,218 +186,480 @@ __device__ void route_token(const float* logits, int E, int top_k, bool renorm, 
 struct ExpertArgs {
     const uint32_t* q[2];                          // gate and up, or down alone
     const _Float16 *s[2], *z[2];
-    const _Float16 *hi, *lo;                       // operand planes [rows][K]; lo nullptr: hi is exact
-    const float* logits;                           // gate/up
-    int* ids;                                      // [M * top_k]: written by gate/up, read by down
-    float* weights;
-    _Float16* h;                                   // gate/up out: hi plane [assignments][N], then lo
-    float* part;                                   // down out: fp32 [assignments][N]
-    int M, E, top_k, renorm;
+    const _Float16* in;                            // operand: hi plane [rows][K], then (split) the lo plane
+    int split;                                     // the operand has a lo plane
+    int rows;                                      // M (gate/up) or M * top_k (down)
+    const int* ids;                                // [M * top_k]
+    const float* weights;
+    _Float16* h;                                   // gate/up out: hi plane [M * top_k][N], then lo
+    float* part;                                   // down: fp32 [M * top_k][N]
+    int* arrived;                                  // down: workgroups done with a block of columns
+    _Float16* y;                                   // down out [M][N]
+    int M, E, top_k;
     int N, K;                                      // of one expert's layer
 };
 
-template <int BITS, int GS, int WK, int MT, bool GATEUP>
-__global__ __launch_bounds__(64 * kMoeWaves, 2) void k_moe_experts(ExpertArgs a) {
+// How the 16 operand rows of a tile are shared out (see the top of the file)
+template <int GS>
+struct RowMap {
+    static constexpr int HR = GS == 64 ? 8 : 16;   // rows that differ (the rest: the other group)
+    int per_tile;                                  // tokens of a tile
+    bool low;                                      // this lane's row: the lo plane?
+    int slot;                                      // its token
+    bool mine;                                     // its quarter is in the row's group
+    __device__ __forceinline__ RowMap(int split, int j, int hq) {
+        per_tile = split ? HR / 2 : HR;
+        const int jr = j % HR;
+        low = jr >= per_tile;
+        slot = jr % per_tile;
+        mine = GS == 128 || (j >> 3) == (hq >> 1);
+    }
+    // the sums of a lane's four rows with those of the rows that belong to the
+    // same tokens: valid in the lanes whose row 4 hq is below per_tile
+    __device__ __forceinline__ float4_t join(float4_t v) const {
+        if constexpr (GS == 64) v = add(v, 32, 1.0f);
+        if (per_tile < HR) v = add(v, GS == 64 ? 16 : 32, 1.0f / kLoScale);
+        return v;
+    }
+    static __device__ __forceinline__ float4_t add(float4_t v, int lanes, float f) {
+        float4_t o;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o[r] = __builtin_fmaf(__shfl_down(v[r], lanes), f, v[r]);
+        return o;
+    }
+};
+
+// one expert's buffers
+template <int BITS, int GS, int NL>
+struct Weights {
+    static constexpr int WQ = BITS == 4 ? 4 : 3;
+    __amdgpu_buffer_rsrc_t q[NL], s[NL], z[NL];
+    __device__ __forceinline__ Weights(const ExpertArgs& a, int e) {
+        const uint32_t tiles = (uint32_t)((a.N + 15) / 16) * (uint32_t)(a.K / kGroup);
+        const size_t params = (size_t)tiles * (16 * kGroup / GS);
+#pragma unroll
+        for (int l = 0; l < NL; ++l) {
+            q[l] = moe_rsrc(a.q[l] + (size_t)e * tiles * 64 * WQ, (size_t)tiles * 64 * WQ * 4);
+            s[l] = moe_rsrc(a.s[l] + (size_t)e * params, params * 2);
+            z[l] = moe_rsrc(a.z[l] + (size_t)e * params, params * 2);
+        }
+    }
+};
+
+template <int WQ, int NL>
+struct TileRegs {
+    TileSlot<WQ> w[NL];
+    uint32_t d[NL], z[NL];
+};
+
+// tile t of an expert (all layers); tiles that are not there give zero codes
+// and a zero scale
+template <int BITS, int GS, int NL>
+__device__ __forceinline__ void load_tile(const Weights<BITS, GS, NL>& r, uint32_t t, bool ok, int lane,
+                                          TileRegs<(BITS == 4 ? 4 : 3), NL>& o) {
     constexpr int WQ = BITS == 4 ? 4 : 3;
-    constexpr int NL = GATEUP ? 2 : 1;             // layers per item
-    constexpr int SUB = kMoeWaves / WK;            // items of a workgroup at a time
-    constexpr int U = MT == 1 ? 4 : MT == 2 ? 2 : 1;
-    constexpr int HR = GS == 64 ? 8 : 16;          // operand rows that differ (the rest: the other group)
-    __shared__ Lists L;
-    __shared__ float4_t red[SUB][WK][NL][MT][64];
+    const uint32_t j = lane & 15, pgrp = GS == 64 ? (uint32_t)(lane >> 5) : 0u;
+    const uint32_t oq = ok ? (t * 64u + (uint32_t)lane) * (WQ * 4u) : kOutOfRange;
+    const uint32_t op = ok ? ((t * (kGroup / GS) + pgrp) * 16u + (j & ~1u)) * 2u : kOutOfRange;
+#pragma unroll
+    for (int l = 0; l < NL; ++l) {
+        o.w[l] = load_tile_slot<WQ, kNonTemporal>(r.q[l], oq);
+        o.d[l] = __builtin_amdgcn_raw_buffer_load_b32(r.s[l], op, 0, 0);
+        o.z[l] = __builtin_amdgcn_raw_buffer_load_b32(r.z[l], op, 0, 0);
+    }
+}
+
+// acc += d * (x . (q - z)) of one tile and layer for MT operand tiles
+template <int BITS, int WQ, int MT>
+__device__ __forceinline__ void tile_product(const TileSlot<WQ>& w, uint32_t d, uint32_t z, uint32_t psh,
+                                             const half8_t (*x)[MT], float4_t* acc) {
+    half8_t b[4];
+    exact_operands<BITS, WQ>(w, bits_half((uint16_t)(z >> psh)), b);
+    const float df = (float)bits_half((uint16_t)(d >> psh));
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        float4_t g = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) g = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[q][m], b[q], g, 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[m][r] = __builtin_fmaf(df, g[r], acc[m][r]);
+    }
+}
+
+__device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+
+// ---------------------------------------------------------------------------
+// One token.  A work item is a block of 16 output rows of one choice; WK waves
+// take its tiles in turn, each with U tiles in flight, and their sums meet in
+// LDS.  A workgroup is 8 / WK items and ends with them: with several
+// workgroups on a compute unit, one waits for its first tiles while others
+// compute.
+// ---------------------------------------------------------------------------
+template <int BITS, int GS, int WK, bool GATEUP>
+__global__ __launch_bounds__(512, 4) void k_moe_token(ExpertArgs a) {
+    constexpr int WQ = BITS == 4 ? 4 : 3;
+    constexpr int NL = GATEUP ? 2 : 1;
+    constexpr int SUB = 8 / WK;
+    constexpr int U = 4;
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+    __shared__ float4_t red[8][NL][64];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int j = lane & 15, hq = lane >> 4;
     const int sub = wave / WK, wk = wave % WK;
-    const int assigned = a.M * a.top_k;
-
-    if constexpr (GATEUP) {
-        float* weights = reinterpret_cast<float*>(L.order);       // until the lists are built
-        for (int m = wave; m < a.M; m += kMoeWaves)
-            route_token(a.logits + (size_t)m * a.E, a.E, a.top_k, a.renorm, L.ids + m * a.top_k,
-                        weights + m * a.top_k);
-        __syncthreads();
-        if (blockIdx.x == 0)
-            for (int i = tid; i < assigned; i += 64 * kMoeWaves) {
-                a.ids[i] = L.ids[i];
-                a.weights[i] = weights[i];
-            }
-        __syncthreads();
-    } else {
-        for (int i = tid; i < assigned; i += 64 * kMoeWaves) L.ids[i] = a.ids[i];
-        __syncthreads();
-    }
-    build_lists(L, assigned, a.E);
-
     const int G = a.K / kGroup, NB = (a.N + 15) / 16;
-    const int hilo = a.lo ? 2 : 1;
-    const int per_tile = HR / hilo;                // tokens of an operand tile
-    const int nw = wk < G ? (G - wk + WK - 1) / WK : 0;
-    const uint32_t tiles = (uint32_t)NB * (uint32_t)G;
-    const uint32_t psh = 16u * (uint32_t)(j & 1);
-    const uint32_t pgrp = GS == 64 ? (uint32_t)(hq >> 1) : 0u;
-    // this lane's operand row: token slot, plane, and whether its quarter is the row's group
-    const int jr = j % HR, slot = jr % per_tile;
-    const bool low = jr >= per_tile;
-    const bool mine = GS == 128 || (j >> 3) == (hq >> 1);
-    const int total = L.n_active * NB;
-    const int passes = (L.most + MT * per_tile - 1) / (MT * per_tile);
+    const int total = a.top_k * NB;
+    const int item = (int)blockIdx.x * SUB + sub;
+    const bool live = item < total;
+    const int c = live ? item / NB : 0, b = live ? item % NB : 0;
+    const int e = __builtin_amdgcn_readfirstlane(a.ids[c]);
+    const Weights<BITS, GS, NL> rw(a, e);
+    const int nw = live && wk < G ? (G - wk + WK - 1) / WK : 0;
 
-    for (int base = blockIdx.x * SUB; base < total; base += gridDim.x * SUB) {
-        const int item = base + sub;
-        const bool live = item < total;
-        const int e = __builtin_amdgcn_readfirstlane(L.active[live ? item / NB : 0]);
-        const int b = live ? item % NB : 0;
-        const int cnt = __builtin_amdgcn_readfirstlane(L.count[e]), first = L.start[e];
-        __amdgpu_buffer_rsrc_t rq[NL], rs[NL], rz[NL];
+    TileRegs<WQ, NL> ring[U];
+    auto load = [&](int i, int u) {
+        load_tile<BITS, GS, NL>(rw, (uint32_t)b * (uint32_t)G + (uint32_t)(wk + WK * i), i < nw, lane, ring[u]);
+    };
 #pragma unroll
-        for (int l = 0; l < NL; ++l) {
-            const size_t params = (size_t)tiles * (16 * kGroup / GS);
-            rq[l] = moe_rsrc(a.q[l] + (size_t)e * tiles * 64 * WQ, tiles * 64u * WQ * 4u);
-            rs[l] = moe_rsrc(a.s[l] + (size_t)e * params, (uint32_t)(params * 2));
-            rz[l] = moe_rsrc(a.z[l] + (size_t)e * params, (uint32_t)(params * 2));
+    for (int u = 0; u < U; ++u) load(u, u);
+
+    // the operand planes of this item in LDS (gate/up: one token's for all items)
+    const int planes = a.split ? 2 : 1;
+    const int row_bytes = a.K * 2;
+    unsigned char* xs = smem + (GATEUP ? 0 : sub * planes * row_bytes);
+    {
+        const int n = planes * (a.K / 8);
+        const size_t row = GATEUP ? 0 : c;
+        const int t0 = GATEUP ? tid : wk * 64 + lane, step = GATEUP ? 512 : 64 * WK;
+        for (int i = t0; i < n; i += step) {
+            const int p = i >= a.K / 8;
+            const size_t at = (((size_t)p * a.rows + row) * a.K) / 8 + (i - p * (a.K / 8));
+            reinterpret_cast<uint4*>(xs)[i] = reinterpret_cast<const uint4*>(a.in)[at];
         }
-        for (int pass = 0; pass < passes; ++pass) {
-            const int s0 = pass * MT * per_tile;   // first token slot of this pass
-            const bool work = live && s0 < cnt;    // wave-uniform
-            const _Float16* src[MT];
-            bool on[MT];
+    }
+    __syncthreads();
+    const RowMap<GS> map(a.split, j, hq);
+    const unsigned char* xl = xs + (map.low ? row_bytes : 0) + 64 * hq;
+    const uint32_t psh = 16u * (uint32_t)(j & 1);
+
+    float4_t acc[NL][1];
 #pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                const int s = s0 + t * per_tile + slot;
-                on[t] = work && mine && s < cnt;
-                const int as = L.order[first + (s < cnt ? s : 0)];
-                const int row = GATEUP ? as / a.top_k : as;
-                src[t] = (low ? a.lo : a.hi) + (size_t)row * a.K + 32 * hq;
-            }
-            TileSlot<WQ> w[U][NL];
-            uint32_t pd[U][NL], pz[U][NL];
-            half8_t x[U][MT][4];
-            auto load = [&](int i, int u) {
-                const bool ok = work && i < nw;
-                const int g = wk + WK * i;
-                const uint32_t t = (uint32_t)b * (uint32_t)G + (uint32_t)g;
-                const uint32_t oq = ok ? (t * 64u + (uint32_t)lane) * (WQ * 4u) : kOutOfRange;
-                const uint32_t op = ok ? ((t * (kGroup / GS) + pgrp) * 16u + (uint32_t)(j & ~1)) * 2u : kOutOfRange;
+    for (int l = 0; l < NL; ++l) acc[l][0] = (float4_t){0.f, 0.f, 0.f, 0.f};
+    for (int i0 = 0; i0 < nw; i0 += U) {
 #pragma unroll
-                for (int l = 0; l < NL; ++l) {
-                    w[u][l] = load_tile_slot<WQ, 2>(rq[l], oq);
-                    pd[u][l] = __builtin_amdgcn_raw_buffer_load_b32(rs[l], op, 0, 0);
-                    pz[u][l] = __builtin_amdgcn_raw_buffer_load_b32(rz[l], op, 0, 0);
+        for (int u = 0; u < U; ++u) {
+            if (i0 + u < nw) {                     // wave-uniform
+                const unsigned char* xt = xl + (wk + WK * (i0 + u)) * (2 * kGroup);
+                half8_t x[4][1];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    x[q][0] = *reinterpret_cast<const half8_t*>(xt + 16 * q);
+                    if (!map.mine) x[q][0] = (half8_t){};
                 }
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        half8_t v = {};
-                        if (ok && on[m]) v = *reinterpret_cast<const half8_t*>(src[m] + (size_t)g * kGroup + 8 * q);
-                        x[u][m][q] = v;
-                    }
-            };
-            float4_t acc[NL][MT];
-#pragma unroll
-            for (int l = 0; l < NL; ++l)
-#pragma unroll
-                for (int m = 0; m < MT; ++m) acc[l][m] = (float4_t){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int u = 0; u < U; ++u) load(u, u);
-            for (int i0 = 0; i0 < nw; i0 += U) {
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (i0 + u < nw) {             // wave-uniform
-#pragma unroll
-                        for (int l = 0; l < NL; ++l) {
-                            half8_t bop[4];
-                            exact_operands<BITS, WQ>(w[u][l], bits_half((uint16_t)(pz[u][l] >> psh)), bop);
-                            const float d = (float)bits_half((uint16_t)(pd[u][l] >> psh));
-#pragma unroll
-                            for (int m = 0; m < MT; ++m) {
-                                float4_t g = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                                for (int q = 0; q < 4; ++q)
-                                    g = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[u][m][q], bop[q], g, 0, 0, 0);
-#pragma unroll
-                                for (int r = 0; r < 4; ++r) acc[l][m][r] = __builtin_fmaf(d, g[r], acc[l][m][r]);
-                            }
-                        }
-                    }
-                    load(i0 + u + U, u);
-                }
+                for (int l = 0; l < NL; ++l)
+                    tile_product<BITS, WQ, 1>(ring[u].w[l], ring[u].d[l], ring[u].z[l], psh, x, acc[l]);
             }
+            load(i0 + u + U, u);
+        }
+    }
 #pragma unroll
-            for (int l = 0; l < NL; ++l)
+    for (int l = 0; l < NL; ++l) red[wave][l][lane] = acc[l][0];
+    __syncthreads();
+    if (wk != 0 || !live) return;
+    float4_t v[NL];
 #pragma unroll
-                for (int m = 0; m < MT; ++m) red[sub][wk][l][m][lane] = acc[l][m];
-            __syncthreads();
-            // token slot ts, column c: its operand rows over the WK waves, in a fixed order
-            if (work) {
-                const int n_here = min(MT * per_tile, cnt - s0);
-                for (int i = wk * 64 + lane; i < n_here * 16; i += 64 * WK) {
-                    const int ts = i >> 4, c = i & 15;
-                    const int m = ts / per_tile, r0 = ts % per_tile;
-                    float v[NL];
+    for (int l = 0; l < NL; ++l) {
+        v[l] = red[wave][l][lane];
 #pragma unroll
-                    for (int l = 0; l < NL; ++l) {
-                        float part[2] = {0.f, 0.f};                // hi, lo
-                        for (int p = 0; p < hilo; ++p)
-                            for (int g = 0; g < kGroup / GS; ++g) {
-                                const int row = g * HR + p * per_tile + r0;
-                                for (int q = 0; q < WK; ++q)
-                                    part[p] += red[sub][q][l][m][(row >> 2) * 16 + c][row & 3];
-                            }
-                        v[l] = part[0] + part[1] * (1.0f / kLoScale);
-                    }
-                    const int n = 16 * b + c;
-                    const size_t at = (size_t)L.order[first + s0 + ts] * a.N + n;
-                    if constexpr (GATEUP) {
-                        const float hv = v[0] / (1.0f + expf(-v[0])) * v[1];
-                        split_hi_lo(hv, a.h[at], a.h[(size_t)assigned * a.N + at]);
-                    } else {
-                        a.part[at] = v[0];
-                    }
-                }
-            }
-            __syncthreads();
+        for (int q = 1; q < WK; ++q) {
+            const float4_t o = red[wave + q][l][lane];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[l][r] += o[r];
+        }
+        v[l] = map.join(v[l]);
+    }
+    const int n = 16 * b + j;                      // row 0 is the token: lanes 0..15
+    if constexpr (GATEUP) {
+        if (lane < 16) {
+            const size_t at = (size_t)c * a.N + n;
+            split_hi_lo(silu_mul(v[0][0], v[NL - 1][0]), a.h[at], a.h[(size_t)a.top_k * a.N + at]);
+        }
+    } else {
+        if (lane < 16) store_shared(a.part + (size_t)c * a.N + n, v[0][0]);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        int before = 0;
+        if (lane == 0) before = __hip_atomic_fetch_add(a.arrived + b, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (__builtin_amdgcn_readfirstlane(before) != a.top_k - 1) return;
+        if (lane < 16) {                           // every choice's sums are there
+            float sum = 0.0f;
+            for (int q = 0; q < a.top_k; ++q)
+                sum = __builtin_fmaf(a.weights[q], load_shared(a.part + (size_t)q * a.N + n), sum);
+            a.y[n] = (_Float16)sum;
         }
     }
 }
 
-__global__ __launch_bounds__(256) void k_moe_join(const float* part, const float* weights, _Float16* y, int top_k,
-                                                  int K) {
-    const int k = blockIdx.x * 256 + threadIdx.x;
-    const size_t m = blockIdx.y;
-    if (k >= K) return;
-    float sum = 0.0f;
-    for (int c = 0; c < top_k; ++c)
-        sum = __builtin_fmaf(weights[m * top_k + c], part[(m * top_k + c) * K + k], sum);
-    y[m * K + k] = (_Float16)sum;
+// ---------------------------------------------------------------------------
+// More tokens.  A workgroup of WV waves owns one expert and WV blocks of 16
+// output rows, one per wave over the whole K; the operand rows of the expert's
+// tokens go through LDS for all of them.  S steps of KT tiles are in flight:
+// operand rows direct to LDS, weights to registers.
+// ---------------------------------------------------------------------------
+struct Lists {
+    int ids[kMaxAssign];                           // expert of assignment token * top_k + choice
+    int order[kMaxAssign];                         // assignments grouped by expert (any order within one)
+    int count[kMoeMaxExperts], start[kMoeMaxExperts], cursor[kMoeMaxExperts];
+    int active[kMoeMaxExperts];                    // experts with tokens, ascending
+    int n_active;
+};
+
+// From the choices: counts, starts, the grouped order and the active experts
+template <int NT>
+__device__ __forceinline__ void build_lists(Lists& L, const int* ids, int assigned, int E) {
+    const int tid = threadIdx.x, lane = tid & 63;
+    for (int e = tid; e < E; e += NT) L.count[e] = 0;
+    for (int i = tid; i < assigned; i += NT) L.ids[i] = ids[i];
+    __syncthreads();
+    for (int i = tid; i < assigned; i += NT) atomicAdd(&L.count[L.ids[i]], 1);
+    __syncthreads();
+    if (tid < 64) {                                // wave 0: prefix over the experts, 64 at a time
+        int base = 0, act = 0;
+        for (int e0 = 0; e0 < E; e0 += 64) {
+            const int e = e0 + lane;
+            const int c = e < E ? L.count[e] : 0;
+            int incl = c;
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const int o = __shfl_up(incl, d);
+                if (lane >= d) incl += o;
+            }
+            const uint64_t on = __builtin_amdgcn_ballot_w64(c > 0);
+            if (e < E) {
+                L.start[e] = L.cursor[e] = base + incl - c;
+                if (c > 0) L.active[act + __popcll(on & ((1ull << lane) - 1))] = e;
+            }
+            base += __shfl(incl, 63);
+            act += __popcll(on);
+        }
+        if (lane == 0) L.n_active = act;
+    }
+    __syncthreads();
+    for (int i = tid; i < assigned; i += NT) L.order[atomicAdd(&L.cursor[L.ids[i]], 1)] = i;
+    __syncthreads();
+}
+
+// The 16-byte chunk of a 256-byte operand row that LDS position p of row r
+// holds is p ^ row_swizzle(r): fragment reads then take distinct banks (the
+// prefill kernel's activation rows, measured there)
+__device__ __forceinline__ int row_swizzle(int r) { return (r & 0xA) | ((r & 1) << 2) | ((r >> 2) & 1); }
+
+template <int BITS, int GS, int MT, int WV, bool GATEUP>
+struct TileShape {
+    static constexpr int NL = GATEUP ? 2 : 1;
+    static constexpr int HR = RowMap<GS>::HR;
+    static constexpr int XR = MT * HR;             // operand rows in LDS
+    // tiles per step: at least one 4-row load for every wave
+    static constexpr int KT = XR / 4 >= WV ? 1 : WV / (XR / 4);
+    static constexpr int XW = XR / 4 * KT / WV;    // its loads per wave
+    static constexpr int BUF = XR * KT * 256;
+    static constexpr int LPS = XW + 3 * NL * KT;   // loads per step and wave
+    // steps in flight: about 8 KB of weights per wave
+    static constexpr int S = KT * NL >= 4 ? 3 : KT * NL == 2 ? 5 : 6;
+    static constexpr size_t LDS = (size_t)S * BUF;
+    static_assert(XW * WV == XR / 4 * KT, "every wave loads the same number of row groups");
+    static_assert(LPS * (S - 2) <= 63, "vmcnt counts to 63");
+};
+
+template <int BITS, int GS, int MT, int WV, bool GATEUP>
+__global__ __launch_bounds__(64 * WV, 1) void k_moe_tile(ExpertArgs a) {
+    using T = TileShape<BITS, GS, MT, WV, GATEUP>;
+    constexpr int WQ = BITS == 4 ? 4 : 3, NL = T::NL, S = T::S, KT = T::KT;
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+    __shared__ Lists L;
+    __shared__ int last;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int j = lane & 15, hq = lane >> 4;
+    const int G = a.K / kGroup, NB = (a.N + 15) / 16, NG = (NB + WV - 1) / WV;
+    const int assigned = a.M * a.top_k;
+    const int which = (int)blockIdx.x / NG, bg = (int)blockIdx.x % NG;
+    build_lists<64 * WV>(L, a.ids, assigned, a.E);
+    if (which >= L.n_active) return;
+    const int e = __builtin_amdgcn_readfirstlane(L.active[which]);
+    const int cnt = __builtin_amdgcn_readfirstlane(L.count[e]);
+    const int first = __builtin_amdgcn_readfirstlane(L.start[e]);
+    const int b = bg * WV + wave;
+    const Weights<BITS, GS, NL> rw(a, e);
+    const uint32_t tile0 = (uint32_t)min(b, NB - 1) * (uint32_t)G;
+    const RowMap<GS> map(a.split, j, hq);
+    const uint32_t psh = 16u * (uint32_t)(j & 1);
+    const size_t plane = (size_t)a.rows * a.K * 2;
+    const __amdgpu_buffer_rsrc_t rx = moe_rsrc(a.in, plane * (a.split ? 2 : 1));
+    const int steps = (G + KT - 1) / KT;
+
+    for (int s0 = 0; s0 < cnt; s0 += MT * map.per_tile) {
+        // row group ii = wave * XW + i: tile ii / (XR / 4) of the step, LDS rows 4 rg ..
+        uint32_t xoff[T::XW];
+#pragma unroll
+        for (int i = 0; i < T::XW; ++i) {
+            const int rg = (wave * T::XW + i) % (T::XR / 4);
+            const int r = 4 * rg + (lane >> 4);
+            const int jr = r % T::HR;
+            const int s = s0 + r / T::HR * map.per_tile + jr % map.per_tile;
+            const int as = s < cnt ? L.order[first + s] : 0;
+            const int row = GATEUP ? as / a.top_k : as;
+            xoff[i] = s < cnt ? (uint32_t)((jr >= map.per_tile ? plane : 0) + (size_t)row * a.K * 2) +
+                                    16u * (uint32_t)((lane & 15) ^ row_swizzle(r))
+                              : kOutOfRange;
+        }
+        TileRegs<WQ, NL> ring[S][KT];
+        auto issue = [&](int step, int slot) {
+#pragma unroll
+            for (int i = 0; i < T::XW; ++i) {
+                const int ii = wave * T::XW + i;
+                const int g = step * KT + ii / (T::XR / 4);
+                load16_lds(rx, smem + slot * T::BUF + ii * 1024, g < G ? xoff[i] : kOutOfRange, (uint32_t)g * 256u);
+            }
+#pragma unroll
+            for (int t = 0; t < KT; ++t) {
+                const int g = step * KT + t;
+                load_tile<BITS, GS, NL>(rw, tile0 + (uint32_t)g, g < G, lane, ring[slot][t]);
+            }
+        };
+        float4_t acc[NL][MT];
+#pragma unroll
+        for (int l = 0; l < NL; ++l)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) acc[l][m] = (float4_t){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < S - 1; ++s) {
+            __builtin_amdgcn_sched_barrier(0);
+            issue(s, s);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        int step0 = 0;
+        do {
+#pragma unroll
+            for (int st = 0; st < S; ++st) {
+                const int step = step0 + st;
+                // this wave's part of the step has landed; then everybody's, and
+                // everybody is done with the buffer that is loaded next (a bare
+                // barrier: a fence would also drain the later steps' loads)
+                __builtin_amdgcn_s_waitcnt(vmcnt_imm(T::LPS * (S - 2)));
+                asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+                __builtin_amdgcn_sched_barrier(0);
+                issue(step + S - 1, (st + S - 1) % S);
+                __builtin_amdgcn_sched_barrier(0);
+                if (step < steps) {
+                    const unsigned char* xb = smem + st * T::BUF;
+#pragma unroll
+                    for (int t = 0; t < KT; ++t) {
+                        half8_t x[4][MT];
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) {
+                            const int r = m * T::HR + j % T::HR;
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                x[q][m] = *reinterpret_cast<const half8_t*>(
+                                    xb + t * (T::XR * 256) + r * 256 + (((4 * hq + q) ^ row_swizzle(r)) << 4));
+                                if (!map.mine) x[q][m] = (half8_t){};
+                            }
+                        }
+#pragma unroll
+                        for (int l = 0; l < NL; ++l)
+                            tile_product<BITS, WQ, MT>(ring[st][t].w[l], ring[st][t].d[l], ring[st][t].z[l], psh, x,
+                                                       acc[l]);
+                    }
+                }
+            }
+            step0 += S;
+        } while (step0 < steps);
+
+        const int n = 16 * b + j;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            float4_t v[NL];
+#pragma unroll
+            for (int l = 0; l < NL; ++l) v[l] = map.join(acc[l][m]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int slot = 4 * hq + r, s = s0 + m * map.per_tile + slot;
+                if (slot < map.per_tile && s < cnt && b < NB) {
+                    const size_t at = (size_t)L.order[first + s] * a.N + n;
+                    if constexpr (GATEUP)
+                        split_hi_lo(silu_mul(v[0][r], v[NL - 1][r]), a.h[at], a.h[(size_t)assigned * a.N + at]);
+                    else
+                        store_shared(a.part + at, v[0][r]);
+                }
+            }
+        }
+        // the pass's loads have landed and its LDS reads are done
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    }
+    if constexpr (!GATEUP) {
+        if (tid == 0)
+            last = __hip_atomic_fetch_add(a.arrived + bg, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                   L.n_active - 1;
+        __syncthreads();
+        if (!last) return;
+        const int cols = min(16 * WV, a.N - bg * 16 * WV);
+        for (int i = tid; i < a.M * cols; i += 64 * WV) {
+            const int m = i / cols, n = bg * 16 * WV + i % cols;
+            float sum = 0.0f;
+            for (int q = 0; q < a.top_k; ++q) {
+                const int as = m * a.top_k + q;
+                sum = __builtin_fmaf(a.weights[as], load_shared(a.part + (size_t)as * a.N + n), sum);
+            }
+            a.y[(size_t)m * a.N + n] = (_Float16)sum;
+        }
+    }
 }
 
 using ExpertFn = void (*)(ExpertArgs);
 
-template <int BITS, int GS, bool GATEUP, int WK>
-ExpertFn pick_mt(int mt) {
-    return mt == 1 ? k_moe_experts<BITS, GS, WK, 1, GATEUP>
-                   : mt == 2 ? k_moe_experts<BITS, GS, WK, 2, GATEUP> : k_moe_experts<BITS, GS, WK, 4, GATEUP>;
+int set_lds(ExpertFn kern, size_t lds) {
+    if (lds <= 48 * 1024) return 0;
+    return (int)hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                                    hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+}
+
+// one token: waves of an item -- 8 where each still has 4 tiles, else fewer
+template <int BITS, int GS, bool GATEUP>
+int launch_token(const ExpertArgs& a, hipStream_t st) {
+    const int G = a.K / kGroup, NB = (a.N + 15) / 16;
+    const int wk = G >= 32 ? 8 : G >= 8 ? 4 : 2;
+    ExpertFn kern = wk == 8 ? k_moe_token<BITS, GS, 8, GATEUP>
+                            : wk == 4 ? k_moe_token<BITS, GS, 4, GATEUP> : k_moe_token<BITS, GS, 2, GATEUP>;
+    const int sub = 8 / wk;
+    const size_t lds = (size_t)(GATEUP ? 1 : sub) * (a.split ? 2 : 1) * a.K * 2;
+    if (int e = set_lds(kern, lds)) return e;
+    hipLaunchKernelGGL(kern, dim3((a.top_k * NB + sub - 1) / sub), dim3(512), lds, st, a);
+    return (int)hipGetLastError();
+}
+
+template <int BITS, int GS, bool GATEUP, int MT>
+int launch_tile(const ExpertArgs& a, hipStream_t st) {
+    constexpr int WV = kMoeTileBlocks;
+    using T = TileShape<BITS, GS, MT, WV, GATEUP>;
+    ExpertFn kern = k_moe_tile<BITS, GS, MT, WV, GATEUP>;
+    if (int e = set_lds(kern, T::LDS)) return e;
+    const int NG = ((a.N + 15) / 16 + WV - 1) / WV;
+    hipLaunchKernelGGL(kern, dim3(min(a.M * a.top_k, a.E) * NG), dim3(64 * WV), T::LDS, st, a);
+    return (int)hipGetLastError();
 }
 
 template <int BITS, int GS, bool GATEUP>
 int launch_experts(const ExpertArgs& a, hipStream_t st) {
-    const int G = a.K / kGroup, NB = (a.N + 15) / 16;
-    const int most_active = min(a.M * a.top_k, a.E);
-    const int cus = device_cu_count();
-    // waves of an item: 8 where a wave still has 4 tiles, else fewer
-    const int wk = G >= 32 ? 8 : G >= 8 ? 4 : 1;
+    if (a.M == 1) return launch_token<BITS, GS, GATEUP>(a, st);
     // operand tiles: of an even share of the tokens per expert, twice over
-    const int rows_per_token = (a.lo ? 2 : 1) * (GS == 64 ? 2 : 1);
+    // (an expert with more takes further passes over its weights)
+    const int rows_per_token = (a.split ? 2 : 1) * (GS == 64 ? 2 : 1);
     const int share = min(a.M, 2 * ((a.M * a.top_k + a.E - 1) / a.E));
-    const int mt = share * rows_per_token <= 16 ? 1 : share * rows_per_token <= 32 ? 2 : 4;
-    ExpertFn kern = wk == 8 ? pick_mt<BITS, GS, GATEUP, 8>(mt)
-                            : wk == 4 ? pick_mt<BITS, GS, GATEUP, 4>(mt) : pick_mt<BITS, GS, GATEUP, 1>(mt);
-    const int sub = kMoeWaves / wk;
-    const int grid = min(2 * cus, (most_active * NB + sub - 1) / sub);
-    hipLaunchKernelGGL(kern, dim3(grid), dim3(64 * kMoeWaves), 0, st, a);
-    return (int)hipGetLastError();
+    const int rows = share * rows_per_token;
+    if (rows <= 16) return launch_tile<BITS, GS, GATEUP, 1>(a, st);
+    if (rows <= 32) return launch_tile<BITS, GS, GATEUP, 2>(a, st);
+    return launch_tile<BITS, GS, GATEUP, 4>(a, st);
 }
 
 template <bool GATEUP>
@@ -423,8 +671,8 @@ int launch_experts_any(const ExpertArgs& a, int bits, int group_size, hipStream_
 
 // the workspace's parts, each 256-byte aligned
 struct Workspace {
-    size_t logits, ids, weights, h, part, scaled, bytes;
-    Workspace(int M, int K, int I, int E, int top_k) {
+    size_t ids, weights, arrived, h, part, scaled, bytes;
+    Workspace(int M, int K, int I, int top_k) {
         size_t at = 0;
         auto take = [&](size_t n) {
             const size_t here = at;
@@ -432,9 +680,9 @@ struct Workspace {
             return here;
         };
         const size_t as = (size_t)M * top_k;
-        logits = take((size_t)M * E * 4);
         ids = take(as * 4);
         weights = take(as * 4);
+        arrived = take((size_t)(K / 16) * 4);
         h = take(as * I * 4);
         part = take(as * K * 4);
         scaled = take((size_t)M * K * 4);
@@ -444,44 +692,50 @@ struct Workspace {
 
 }  // namespace
 
-size_t moe_workspace_bytes(int M, int K, int I, int E, int top_k) { return Workspace(M, K, I, E, top_k).bytes; }
+size_t moe_workspace_bytes(int M, int K, int I, int E, int top_k) { return Workspace(M, K, I, top_k).bytes; }
 
 int launch_moe(const MoeProblem& p, void* workspace, hipStream_t st) {
-    const Workspace w(p.M, p.K, p.I, p.E, p.top_k);
+    const Workspace w(p.M, p.K, p.I, p.top_k);
     unsigned char* ws = (unsigned char*)workspace;
     _Float16* scaled = (_Float16*)(ws + w.scaled);
-    const RouterArgs r{(const _Float16*)p.x, (const _Float16*)p.router, p.inv_s, (float*)(ws + w.logits), scaled,
-                       p.M, p.E, p.K};
-    hipLaunchKernelGGL(k_moe_router, dim3((p.E + 15) / 16, (p.M + 15) / 16), dim3(1024), 0, st, r);
+    ExpertArgs a{};
+    a.ids = (int*)(ws + w.ids);
+    a.weights = (float*)(ws + w.weights);
+    a.arrived = (int*)(ws + w.arrived);
+    a.h = (_Float16*)(ws + w.h);
+    a.part = (float*)(ws + w.part);
+    a.y = (_Float16*)p.y;
+    a.M = p.M; a.E = p.E; a.top_k = p.top_k;
+
+    const RouteArgs r{(const _Float16*)p.x, (const _Float16*)p.router, p.inv_s, (int*)(ws + w.ids),
+                      (float*)(ws + w.weights), scaled, a.arrived, p.K / 16, p.M, p.E, p.K, p.top_k, p.renormalize};
+    const size_t lds = (size_t)p.K * 2;
+    if (lds > 48 * 1024)
+        if (int e = (int)hipFuncSetAttribute(reinterpret_cast<const void*>(k_moe_route),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds))
+            return e;
+    hipLaunchKernelGGL(k_moe_route, dim3(p.M), dim3(1024), lds, st, r);
     if (int e = (int)hipGetLastError()) return e;
 
-    ExpertArgs a{};
     for (int l = 0; l < 2; ++l) {
         a.q[l] = (const uint32_t*)p.qweight[l];
         a.s[l] = (const _Float16*)p.scales[l];
         a.z[l] = (const _Float16*)p.zeros[l];
     }
-    a.hi = p.inv_s ? scaled : (const _Float16*)p.x;
-    a.lo = p.inv_s ? scaled + (size_t)p.M * p.K : nullptr;
-    a.logits = r.logits;
-    a.ids = (int*)(ws + w.ids);
-    a.weights = (float*)(ws + w.weights);
-    a.h = (_Float16*)(ws + w.h);
-    a.M = p.M; a.E = p.E; a.top_k = p.top_k; a.renorm = p.renormalize;
+    a.in = p.inv_s ? scaled : (const _Float16*)p.x;
+    a.split = p.inv_s != nullptr;
+    a.rows = p.M;
     a.N = p.I; a.K = p.K;
     if (int e = launch_experts_any<true>(a, p.bits, p.group_size, st)) return e;
 
     a.q[0] = (const uint32_t*)p.qweight[2];
     a.s[0] = (const _Float16*)p.scales[2];
     a.z[0] = (const _Float16*)p.zeros[2];
-    a.hi = a.h;
-    a.lo = a.h + (size_t)p.M * p.top_k * p.I;
-    a.part = (float*)(ws + w.part);
+    a.in = a.h;
+    a.split = 1;
+    a.rows = p.M * p.top_k;
     a.N = p.K; a.K = p.I;
-    if (int e = launch_experts_any<false>(a, p.bits, p.group_size, st)) return e;
-    hipLaunchKernelGGL(k_moe_join, dim3((p.K + 255) / 256, p.M), dim3(256), 0, st, a.part, a.weights,
-                       (_Float16*)p.y, p.top_k, p.K);
-    return (int)hipGetLastError();
+    return launch_experts_any<false>(a, p.bits, p.group_size, st);
 }
 
 }  // namespace awq

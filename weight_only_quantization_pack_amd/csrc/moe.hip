@@ -24,14 +24,24 @@
 //     quarters 0, 1 and 2, 3), so rows 0..7 hold the tokens with quarters 2, 3
 //     zeroed and rows 8..15 the same tokens with quarters 0, 1 zeroed: the
 //     group sums come out in different rows.
+#include <climits>
+#include <type_traits>
+
 #include "packed.h"
 #include "rows.h"
 
+#ifndef AWQ_MOE_OCC
+#define AWQ_MOE_OCC 3
+#define AWQ_MOE_S2 4
+#define AWQ_MOE_S1 6
+#define AWQ_MOE_FILL 4
+#define AWQ_MOE_S64 4
+#define AWQ_MOE_OCC64 4
+#endif
 namespace awq {
 namespace {
 
 constexpr int kMaxAssign = kMoeMaxTokens * kMoeMaxTopK;
-constexpr int kMoeTileBlocks = 8;                  // waves, and blocks of 16 rows, of a k_moe_tile workgroup
 constexpr uint32_t kOutOfRange = 0x80000000u;      // > every buffer's size: loads return zero
 constexpr float kLoScale = 2048.0f;                // of the lo plane
 constexpr int kNonTemporal = 2;                    // weights: each byte is read once
@@ -72,10 +82,12 @@ struct RouteArgs {
     int M, E, K, top_k, renorm;
 };
 
-// One wave picks a token's experts from its logits.  The keys order the logits
+// One wave picks a token's experts from its logits (the sums of their parts, in
+// order).  The keys order the logits
 // as integers; a NaN comes below every number and a taken expert below a NaN,
 // so every pick is a valid expert that was not picked before.
-__device__ void route_token(const float* logits, int E, int top_k, bool renorm, int* ids, float* weights) {
+__device__ void route_token(const float* partial, int slabs, int E, int top_k, bool renorm, int* ids,
+                            float* weights) {
     const int lane = threadIdx.x & 63;
     constexpr int PER = kMoeMaxExperts / 64;
     uint32_t key[PER];
@@ -83,7 +95,8 @@ __device__ void route_token(const float* logits, int E, int top_k, bool renorm, 
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int e = lane + 64 * i;
-        v[i] = e < E ? logits[e] : 0.0f;
+        v[i] = e < E ? partial[e] : 0.0f;
+        for (int p = 1; p < slabs && 64 * i < E; ++p) v[i] += e < E ? partial[p * E + e] : 0.0f;
         const uint32_t b = __builtin_bit_cast(uint32_t, v[i] + 0.0f);      // -0 as 0: they tie
         key[i] = e >= E ? 0u : v[i] != v[i] ? 1u : b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
     }
@@ -126,58 +139,61 @@ __device__ void route_token(const float* logits, int E, int top_k, bool renorm, 
     }
 }
 
-// A wave takes kRouteRows experts at a time, each lane 8 k of every 512: the
-// router's rows are all in flight while x comes from LDS.
-constexpr int kRouteRows = 4;
+// The logits are units of RB experts by kSlab k, taken by the 16 waves in turn:
+// a lane holds 8 k of every 512 of x and of RB router rows, all of them loaded
+// at once.  RB = 4 where that still gives every wave a unit, else 1.
+constexpr int kSlab = 2048;
 
+template <int RB>
 __global__ __launch_bounds__(1024) void k_moe_route(RouteArgs a) {
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-    __shared__ float logits[kMoeMaxExperts];
-    uint4* xs = reinterpret_cast<uint4*>(smem);
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int chunks = a.K / 8;
+    float* partial = reinterpret_cast<float*>(smem);          // [slabs][E]
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const size_t m = blockIdx.x;
-    const uint4* x = reinterpret_cast<const uint4*>(a.x) + m * chunks;
-    for (int i = tid; i < chunks; i += 1024) xs[i] = x[i];
-    if (m == 0)
-        for (int i = tid; i < a.n_arrived; i += 1024) a.arrived[i] = 0;
-    __syncthreads();
-    for (int e0 = wave * kRouteRows; e0 < a.E; e0 += 16 * kRouteRows) {
-        float sum[kRouteRows] = {};
-        const uint4* r[kRouteRows];
+    const int slabs = (a.K + kSlab - 1) / kSlab, groups = (a.E + RB - 1) / RB;
+    const _Float16* x = a.x + m * a.K;
+    const __amdgpu_buffer_rsrc_t rx = moe_rsrc(x, (size_t)a.K * 2);
+    const __amdgpu_buffer_rsrc_t rr = moe_rsrc(a.router, (size_t)a.E * a.K * 2);
+    auto load = [&](const __amdgpu_buffer_rsrc_t& r, uint32_t row, int k) {
+        return __builtin_bit_cast(half8_t, __builtin_amdgcn_raw_buffer_load_b128(
+            r, k < a.K ? (row * (uint32_t)a.K + (uint32_t)k) * 2u : kOutOfRange, 0, 0));
+    };
+    for (int unit = wave; unit < slabs * groups; unit += 16) {
+        const int slab = unit / groups, e0 = unit % groups * RB;
+        half8_t xv[4], rv[4][RB];
 #pragma unroll
-        for (int q = 0; q < kRouteRows; ++q)
-            r[q] = reinterpret_cast<const uint4*>(a.router) + (size_t)min(e0 + q, a.E - 1) * chunks;
-#pragma unroll 2
-        for (int i = lane; i < chunks; i += 64) {
-            uint4 rv[kRouteRows];
+        for (int i = 0; i < 4; ++i) {
+            const int k = slab * kSlab + 512 * i + 8 * lane;
+            xv[i] = load(rx, 0, k);
 #pragma unroll
-            for (int q = 0; q < kRouteRows; ++q) rv[q] = r[q][i];
-            const uint4 xv = xs[i];
-            const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+            for (int q = 0; q < RB; ++q) rv[i][q] = load(rr, (uint32_t)min(e0 + q, a.E - 1), k);
+        }
+        float sum[RB] = {};
 #pragma unroll
-            for (int q = 0; q < kRouteRows; ++q) {
-                const uint32_t rw[4] = {rv[q].x, rv[q].y, rv[q].z, rv[q].w};
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int q = 0; q < RB; ++q)
 #pragma unroll
                 for (int w = 0; w < 4; ++w)
-                    sum[q] = __builtin_amdgcn_fdot2(__builtin_bit_cast(half2_t, xw[w]),
-                                                    __builtin_bit_cast(half2_t, rw[w]), sum[q], false);
-            }
-        }
+                    sum[q] = __builtin_amdgcn_fdot2((half2_t){xv[i][2 * w], xv[i][2 * w + 1]},
+                                                    (half2_t){rv[i][q][2 * w], rv[i][q][2 * w + 1]}, sum[q], false);
 #pragma unroll
-        for (int q = 0; q < kRouteRows; ++q) {
+        for (int q = 0; q < RB; ++q) {
             const float l = __builtin_bit_cast(float, wave_reduce(__builtin_bit_cast(uint32_t, sum[q]), SumF32()));
-            if (lane == 0 && e0 + q < a.E) logits[e0 + q] = l;
+            if (lane == 0 && e0 + q < a.E) partial[slab * a.E + e0 + q] = l;
         }
     }
-    __syncthreads();
-    if (wave == 0) route_token(logits, a.E, a.top_k, a.renorm, a.ids + m * a.top_k, a.weights + m * a.top_k);
+    if (m == 0)
+        for (int i = tid; i < a.n_arrived; i += 1024) a.arrived[i] = 0;
     if (a.inv_s) {
-        const _Float16* xh = reinterpret_cast<const _Float16*>(smem);
         const size_t at = m * a.K, plane = (size_t)a.M * a.K;
         for (int k = tid; k < a.K; k += 1024)
-            split_hi_lo((float)xh[k] * a.inv_s[k], a.scaled[at + k], a.scaled[plane + at + k]);
+            split_hi_lo((float)x[k] * a.inv_s[k], a.scaled[at + k], a.scaled[plane + at + k]);
     }
+    __syncthreads();
+    if (wave == 0)
+        route_token(partial, slabs, a.E, a.top_k, a.renorm, a.ids + m * a.top_k, a.weights + m * a.top_k);
 }
 
 // ---------------------------------------------------------------------------
@@ -192,7 +208,8 @@ struct ExpertArgs {
     const int* ids;                                // [M * top_k]
     const float* weights;
     _Float16* h;                                   // gate/up out: hi plane [M * top_k][N], then lo
-    float* part;                                   // down: fp32 [M * top_k][N]
+    float* part;                                   // down: fp32 [splits][M * top_k][N]
+    int splits, split_tiles;                       // down, more tokens: K in splits of so many tiles
     int* arrived;                                  // down: workgroups done with a block of columns
     _Float16* y;                                   // down out [M][N]
     int M, E, top_k;
@@ -407,52 +424,63 @@ __global__ __launch_bounds__(512, 4) void k_moe_token(ExpertArgs a) {
 // operand rows direct to LDS, weights to registers.
 // ---------------------------------------------------------------------------
 struct Lists {
-    int ids[kMaxAssign];                           // expert of assignment token * top_k + choice
-    int order[kMaxAssign];                         // assignments grouped by expert (any order within one)
-    int count[kMoeMaxExperts], start[kMoeMaxExperts], cursor[kMoeMaxExperts];
-    int active[kMoeMaxExperts];                    // experts with tokens, ascending
-    int n_active;
+    int ids[kMaxAssign];                           // every choice
+    uint32_t present[kMoeMaxExperts / 32];         // experts that some token takes
+    int mine[kMoeMaxTokens];                       // this expert's assignments, ascending
 };
 
-// From the choices: counts, starts, the grouped order and the active experts
+// The expert number `which` (ascending) of those that tokens take and how many
+// assignments it has (listed in L.mine), or -1 for the expert where fewer are
+// taken.  A token takes an expert at most once.
+struct Share { int expert, count; };
+
 template <int NT>
-__device__ __forceinline__ void build_lists(Lists& L, const int* ids, int assigned, int E) {
+__device__ __forceinline__ Share find_share(Lists& L, const int* ids, int assigned, int which) {
+    constexpr int WORDS = kMoeMaxExperts / 32;
     const int tid = threadIdx.x, lane = tid & 63;
-    for (int e = tid; e < E; e += NT) L.count[e] = 0;
-    for (int i = tid; i < assigned; i += NT) L.ids[i] = ids[i];
+    if (tid < WORDS) L.present[tid] = 0;
     __syncthreads();
-    for (int i = tid; i < assigned; i += NT) atomicAdd(&L.count[L.ids[i]], 1);
-    __syncthreads();
-    if (tid < 64) {                                // wave 0: prefix over the experts, 64 at a time
-        int base = 0, act = 0;
-        for (int e0 = 0; e0 < E; e0 += 64) {
-            const int e = e0 + lane;
-            const int c = e < E ? L.count[e] : 0;
-            int incl = c;
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const int o = __shfl_up(incl, d);
-                if (lane >= d) incl += o;
-            }
-            const uint64_t on = __builtin_amdgcn_ballot_w64(c > 0);
-            if (e < E) {
-                L.start[e] = L.cursor[e] = base + incl - c;
-                if (c > 0) L.active[act + __popcll(on & ((1ull << lane) - 1))] = e;
-            }
-            base += __shfl(incl, 63);
-            act += __popcll(on);
-        }
-        if (lane == 0) L.n_active = act;
+    for (int i = tid; i < assigned; i += NT) {
+        const int e = ids[i];
+        L.ids[i] = e;
+        atomicOr(&L.present[e >> 5], 1u << (e & 31));
     }
     __syncthreads();
-    for (int i = tid; i < assigned; i += NT) L.order[atomicAdd(&L.cursor[L.ids[i]], 1)] = i;
+    // lanes 0..15 hold 32 experts each; the word that holds number `which`
+    const uint32_t word = lane < WORDS ? L.present[lane] : 0u;
+    int upto = __builtin_popcount(word);           // experts taken in the words up to this lane's
+#pragma unroll
+    for (int d = 1; d < WORDS; d <<= 1) {
+        const int o = __shfl_up(upto, d);
+        if (lane >= d) upto += o;
+    }
+    const uint64_t past = __builtin_amdgcn_ballot_w64(lane < WORDS && upto > which);
+    if (past == 0) return Share{-1, 0};
+    const int at = __builtin_ctzll(past);
+    uint32_t bits = (uint32_t)__builtin_amdgcn_readlane((int)word, at);
+    for (int skip = which - (__builtin_amdgcn_readlane(upto, at) - __builtin_popcount(bits)); skip > 0; --skip)
+        bits &= bits - 1;
+    Share s{__builtin_amdgcn_readfirstlane(32 * at + __builtin_ctz(bits)), 0};
+    for (int i0 = 0; i0 < assigned; i0 += 64) {    // every wave counts, the first one writes
+        const bool is = i0 + lane < assigned && L.ids[i0 + lane] == s.expert;
+        const uint64_t on = __builtin_amdgcn_ballot_w64(is);
+        if (tid < 64 && is) L.mine[s.count + __popcll(on & ((1ull << lane) - 1))] = i0 + lane;
+        s.count += __popcll(on);
+    }
+    s.count = __builtin_amdgcn_readfirstlane(s.count);
     __syncthreads();
+    return s;
 }
 
-// The 16-byte chunk of a 256-byte operand row that LDS position p of row r
-// holds is p ^ row_swizzle(r): fragment reads then take distinct banks (the
+// The 16-byte chunk of a 256-byte operand row that LDS position p of row r (of
+// its tile) holds is p ^ row_swizzle(r): fragment reads then take distinct banks (the
 // prefill kernel's activation rows, measured there)
 __device__ __forceinline__ int row_swizzle(int r) { return (r & 0xA) | ((r & 1) << 2) | ((r >> 2) & 1); }
+
+// waves per SIMD that k_moe_tile's registers are held to
+constexpr int tile_waves(int GS, int MT, bool gate_up) {
+    return MT >= 4 ? (GS == 128 && !gate_up ? AWQ_MOE_OCC64 : 2) : MT == 2 && gate_up && GS == 64 ? 2 : AWQ_MOE_OCC;
+}
 
 template <int BITS, int GS, int MT, int WV, bool GATEUP>
 struct TileShape {
@@ -462,42 +490,48 @@ struct TileShape {
     // tiles per step: at least one 4-row load for every wave
     static constexpr int KT = XR / 4 >= WV ? 1 : WV / (XR / 4);
     static constexpr int XW = XR / 4 * KT / WV;    // its loads per wave
-    static constexpr int BUF = XR * KT * 256;
+    static constexpr int TB = (XR + (GS == 64)) * 256;     // a tile's rows (and a row of zeros)
+    static constexpr int BUF = TB * KT;
     static constexpr int LPS = XW + 3 * NL * KT;   // loads per step and wave
-    // steps in flight: about 8 KB of weights per wave
-    static constexpr int S = KT * NL >= 4 ? 3 : KT * NL == 2 ? 5 : 6;
+    static constexpr int S = KT * NL >= 4 ? 3 : XR >= 64 ? AWQ_MOE_S64 : KT * NL == 2 ? AWQ_MOE_S2 : AWQ_MOE_S1;
     static constexpr size_t LDS = (size_t)S * BUF;
     static_assert(XW * WV == XR / 4 * KT, "every wave loads the same number of row groups");
     static_assert(LPS * (S - 2) <= 63, "vmcnt counts to 63");
 };
 
 template <int BITS, int GS, int MT, int WV, bool GATEUP>
-__global__ __launch_bounds__(64 * WV, 1) void k_moe_tile(ExpertArgs a) {
+__global__ __launch_bounds__(64 * WV, tile_waves(GS, MT, GATEUP)) void k_moe_tile(ExpertArgs a) {
     using T = TileShape<BITS, GS, MT, WV, GATEUP>;
     constexpr int WQ = BITS == 4 ? 4 : 3, NL = T::NL, S = T::S, KT = T::KT;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     __shared__ Lists L;
-    __shared__ int last;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int j = lane & 15, hq = lane >> 4;
     const int G = a.K / kGroup, NB = (a.N + 15) / 16, NG = (NB + WV - 1) / WV;
     const int assigned = a.M * a.top_k;
-    const int which = (int)blockIdx.x / NG, bg = (int)blockIdx.x % NG;
-    build_lists<64 * WV>(L, a.ids, assigned, a.E);
-    if (which >= L.n_active) return;
-    const int e = __builtin_amdgcn_readfirstlane(L.active[which]);
-    const int cnt = __builtin_amdgcn_readfirstlane(L.count[e]);
-    const int first = __builtin_amdgcn_readfirstlane(L.start[e]);
-    const int b = bg * WV + wave;
-    const Weights<BITS, GS, NL> rw(a, e);
-    const uint32_t tile0 = (uint32_t)min(b, NB - 1) * (uint32_t)G;
+    const int b = (int)blockIdx.x % NG * WV + wave;            // this wave's row block
+    const Share share = find_share<64 * WV>(L, a.ids, assigned, (int)blockIdx.x / NG);
+    if (share.expert < 0) return;
+    const int cnt = share.count;
+    const Weights<BITS, GS, NL> rw(a, share.expert);
     const RowMap<GS> map(a.split, j, hq);
     const uint32_t psh = 16u * (uint32_t)(j & 1);
     const size_t plane = (size_t)a.rows * a.K * 2;
-    const __amdgpu_buffer_rsrc_t rx = moe_rsrc(a.in, plane * (a.split ? 2 : 1));
-    const int steps = (G + KT - 1) / KT;
+    // the size through a scalar register: a descriptor held in vector registers
+    // would cost a loop around every load
+    const __amdgpu_buffer_rsrc_t rx =
+        moe_rsrc(a.in, (size_t)__builtin_amdgcn_readfirstlane((int)(plane << a.split)));
+    // this workgroup's tiles of every row: all, or (down) one split of them
+    const int g0 = GATEUP ? 0 : (int)blockIdx.y * a.split_tiles;
+    const int g1 = GATEUP ? G : min(G, g0 + a.split_tiles);
+    const int steps = (g1 - g0 + KT - 1) / KT;
+    const uint32_t tile0 = (uint32_t)min(b, NB - 1) * (uint32_t)G;
 
+    if constexpr (GS == 64) {                      // the rows of zeros
+        for (int i = tid; i < S * KT * 64; i += 64 * WV)
+            *reinterpret_cast<uint32_t*>(smem + i / 64 * T::TB + T::XR * 256 + i % 64 * 4) = 0;
+    }
     for (int s0 = 0; s0 < cnt; s0 += MT * map.per_tile) {
         // row group ii = wave * XW + i: tile ii / (XR / 4) of the step, LDS rows 4 rg ..
         uint32_t xoff[T::XW];
@@ -507,10 +541,10 @@ __global__ __launch_bounds__(64 * WV, 1) void k_moe_tile(ExpertArgs a) {
             const int r = 4 * rg + (lane >> 4);
             const int jr = r % T::HR;
             const int s = s0 + r / T::HR * map.per_tile + jr % map.per_tile;
-            const int as = s < cnt ? L.order[first + s] : 0;
+            const int as = s < cnt ? L.mine[s] : 0;
             const int row = GATEUP ? as / a.top_k : as;
             xoff[i] = s < cnt ? (uint32_t)((jr >= map.per_tile ? plane : 0) + (size_t)row * a.K * 2) +
-                                    16u * (uint32_t)((lane & 15) ^ row_swizzle(r))
+                                    16u * (uint32_t)((lane & 15) ^ row_swizzle(jr))
                               : kOutOfRange;
         }
         TileRegs<WQ, NL> ring[S][KT];
@@ -518,13 +552,15 @@ __global__ __launch_bounds__(64 * WV, 1) void k_moe_tile(ExpertArgs a) {
 #pragma unroll
             for (int i = 0; i < T::XW; ++i) {
                 const int ii = wave * T::XW + i;
-                const int g = step * KT + ii / (T::XR / 4);
-                load16_lds(rx, smem + slot * T::BUF + ii * 1024, g < G ? xoff[i] : kOutOfRange, (uint32_t)g * 256u);
+                // stated uniform: a scalar offset of the load
+                const int g = __builtin_amdgcn_readfirstlane(g0 + step * KT + ii / (T::XR / 4));
+                load16_lds(rx, smem + slot * T::BUF + ii / (T::XR / 4) * T::TB + ii % (T::XR / 4) * 1024,
+                           g < g1 ? xoff[i] : kOutOfRange, (uint32_t)g * 256u);
             }
 #pragma unroll
             for (int t = 0; t < KT; ++t) {
-                const int g = step * KT + t;
-                load_tile<BITS, GS, NL>(rw, tile0 + (uint32_t)g, g < G, lane, ring[slot][t]);
+                const int g = g0 + step * KT + t;
+                load_tile<BITS, GS, NL>(rw, tile0 + (uint32_t)g, g < g1, lane, ring[slot][t]);
             }
         };
         float4_t acc[NL][MT];
@@ -532,6 +568,30 @@ __global__ __launch_bounds__(64 * WV, 1) void k_moe_tile(ExpertArgs a) {
         for (int l = 0; l < NL; ++l)
 #pragma unroll
             for (int m = 0; m < MT; ++m) acc[l][m] = (float4_t){0.f, 0.f, 0.f, 0.f};
+        const int live = min(MT, (cnt - s0 + map.per_tile - 1) / map.per_tile);
+        // this lane's chunks of its operand row, or (64-wide groups, a row of the
+        // other group) of the row of zeros
+        int xat[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            xat[q] = map.mine ? (j % T::HR) * 256 + (((4 * hq + q) ^ row_swizzle(j % T::HR)) << 4) : T::XR * 256;
+        const int mstep = map.mine ? T::HR * 256 : 0;
+        auto compute = [&](int slot, const TileRegs<WQ, NL>* regs, auto tiles) {
+            constexpr int LM = decltype(tiles)::value;
+            const unsigned char* xb = smem + slot * T::BUF;
+#pragma unroll
+            for (int t = 0; t < KT; ++t) {
+                half8_t x[4][LM];
+#pragma unroll
+                for (int m = 0; m < LM; ++m)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        x[q][m] = *reinterpret_cast<const half8_t*>(xb + t * T::TB + m * mstep + xat[q]);
+#pragma unroll
+                for (int l = 0; l < NL; ++l)
+                    tile_product<BITS, WQ, LM>(regs[t].w[l], regs[t].d[l], regs[t].z[l], psh, x, acc[l]);
+            }
+        };
 #pragma unroll
         for (int s = 0; s < S - 1; ++s) {
             __builtin_amdgcn_sched_barrier(0);
@@ -552,25 +612,11 @@ __global__ __launch_bounds__(64 * WV, 1) void k_moe_tile(ExpertArgs a) {
                 issue(step + S - 1, (st + S - 1) % S);
                 __builtin_amdgcn_sched_barrier(0);
                 if (step < steps) {
-                    const unsigned char* xb = smem + st * T::BUF;
-#pragma unroll
-                    for (int t = 0; t < KT; ++t) {
-                        half8_t x[4][MT];
-#pragma unroll
-                        for (int m = 0; m < MT; ++m) {
-                            const int r = m * T::HR + j % T::HR;
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                x[q][m] = *reinterpret_cast<const half8_t*>(
-                                    xb + t * (T::XR * 256) + r * 256 + (((4 * hq + q) ^ row_swizzle(r)) << 4));
-                                if (!map.mine) x[q][m] = (half8_t){};
-                            }
-                        }
-#pragma unroll
-                        for (int l = 0; l < NL; ++l)
-                            tile_product<BITS, WQ, MT>(ring[st][t].w[l], ring[st][t].d[l], ring[st][t].z[l], psh, x,
-                                                       acc[l]);
-                    }
+                    // the operand tiles that hold tokens (wave-uniform)
+                    if (MT >= 4 && live > 3) compute(st, ring[st], std::integral_constant<int, MT>());
+                    else if (MT >= 4 && live > 2) compute(st, ring[st], std::integral_constant<int, MT >= 4 ? 3 : MT>());
+                    else if (MT >= 2 && live > 1) compute(st, ring[st], std::integral_constant<int, MT >= 2 ? 2 : MT>());
+                    else compute(st, ring[st], std::integral_constant<int, 1>());
                 }
             }
             step0 += S;
@@ -579,6 +625,7 @@ __global__ __launch_bounds__(64 * WV, 1) void k_moe_tile(ExpertArgs a) {
         const int n = 16 * b + j;
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
+            if (m >= live) continue;
             float4_t v[NL];
 #pragma unroll
             for (int l = 0; l < NL; ++l) v[l] = map.join(acc[l][m]);
@@ -586,34 +633,41 @@ __global__ __launch_bounds__(64 * WV, 1) void k_moe_tile(ExpertArgs a) {
             for (int r = 0; r < 4; ++r) {
                 const int slot = 4 * hq + r, s = s0 + m * map.per_tile + slot;
                 if (slot < map.per_tile && s < cnt && b < NB) {
-                    const size_t at = (size_t)L.order[first + s] * a.N + n;
+                    const size_t at = (size_t)L.mine[s] * a.N + n;
                     if constexpr (GATEUP)
                         split_hi_lo(silu_mul(v[0][r], v[NL - 1][r]), a.h[at], a.h[(size_t)assigned * a.N + at]);
                     else
-                        store_shared(a.part + at, v[0][r]);
+                        a.part[(size_t)blockIdx.y * assigned * a.N + at] = v[0][r];
                 }
             }
         }
         // the pass's loads have landed and its LDS reads are done
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     }
-    if constexpr (!GATEUP) {
-        if (tid == 0)
-            last = __hip_atomic_fetch_add(a.arrived + bg, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-                   L.n_active - 1;
-        __syncthreads();
-        if (!last) return;
-        const int cols = min(16 * WV, a.N - bg * 16 * WV);
-        for (int i = tid; i < a.M * cols; i += 64 * WV) {
-            const int m = i / cols, n = bg * 16 * WV + i % cols;
-            float sum = 0.0f;
-            for (int q = 0; q < a.top_k; ++q) {
-                const int as = m * a.top_k + q;
-                sum = __builtin_fmaf(a.weights[as], load_shared(a.part + (size_t)as * a.N + n), sum);
-            }
-            a.y[(size_t)m * a.N + n] = (_Float16)sum;
+}
+
+// y[m] = the choices' rows (the sums of their splits), weighted, in their order;
+// 4 columns a thread
+__global__ __launch_bounds__(256) void k_moe_join(const float* part, const float* weights, _Float16* y, int top_k,
+                                                  int K, int splits) {
+    const int k = (blockIdx.x * 256 + threadIdx.x) * 4;
+    const size_t m = blockIdx.y;
+    if (k >= K) return;
+    float4_t sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int c = 0; c < top_k; ++c) {
+        const float w = weights[m * top_k + c];
+        const float* p = part + (m * top_k + c) * K + k;
+        float4_t v = *reinterpret_cast<const float4_t*>(p);
+        for (int s = 1; s < splits; ++s) {
+            const float4_t o = *reinterpret_cast<const float4_t*>(p + (size_t)s * gridDim.y * top_k * K);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] += o[r];
         }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sum[r] = __builtin_fmaf(w, v[r], sum[r]);
     }
+    *reinterpret_cast<uint2*>(y + m * K + k) = make_uint2(pack2<F16>(sum[0], sum[1]), pack2<F16>(sum[2], sum[3]));
 }
 
 using ExpertFn = void (*)(ExpertArgs);
@@ -640,12 +694,16 @@ int launch_token(const ExpertArgs& a, hipStream_t st) {
 
 template <int BITS, int GS, bool GATEUP, int MT>
 int launch_tile(const ExpertArgs& a, hipStream_t st) {
-    constexpr int WV = kMoeTileBlocks;
+    constexpr int WV = MT * RowMap<GS>::HR >= 64 ? 8 : 4;
     using T = TileShape<BITS, GS, MT, WV, GATEUP>;
-    ExpertFn kern = k_moe_tile<BITS, GS, MT, WV, GATEUP>;
-    if (int e = set_lds(kern, T::LDS)) return e;
+    auto kern = k_moe_tile<BITS, GS, MT, WV, GATEUP>;
+    if (T::LDS > 48 * 1024)
+        if (int e = (int)hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)T::LDS))
+            return e;
     const int NG = ((a.N + 15) / 16 + WV - 1) / WV;
-    hipLaunchKernelGGL(kern, dim3(min(a.M * a.top_k, a.E) * NG), dim3(64 * WV), T::LDS, st, a);
+    const int experts = min(a.M * a.top_k, a.E);
+    hipLaunchKernelGGL(kern, dim3(experts * NG, GATEUP ? 1 : a.splits), dim3(64 * WV), T::LDS, st, a);
     return (int)hipGetLastError();
 }
 
@@ -669,10 +727,19 @@ int launch_experts_any(const ExpertArgs& a, int bits, int group_size, hipStream_
     return bits == 4 ? launch_experts<4, 128, GATEUP>(a, st) : launch_experts<3, 128, GATEUP>(a, st);
 }
 
+// K splits of the down projections of more than one token: as many as bring the
+// expert workgroups (of 4 row blocks) to two per compute unit while a split
+// keeps 16 tiles
+int down_splits(int M, int K, int I, int E, int top_k) {
+    if (M == 1) return 1;
+    const int wgs = min(M * top_k, E) * ((K / 16 + 3) / 4);
+    return max(1, min((I / kGroup) / 16, AWQ_MOE_FILL * device_cu_count() / max(wgs, 1)));
+}
+
 // the workspace's parts, each 256-byte aligned
 struct Workspace {
     size_t ids, weights, arrived, h, part, scaled, bytes;
-    Workspace(int M, int K, int I, int top_k) {
+    Workspace(int M, int K, int I, int E, int top_k) {
         size_t at = 0;
         auto take = [&](size_t n) {
             const size_t here = at;
@@ -684,7 +751,7 @@ struct Workspace {
         weights = take(as * 4);
         arrived = take((size_t)(K / 16) * 4);
         h = take(as * I * 4);
-        part = take(as * K * 4);
+        part = take(as * K * 4 * down_splits(M, K, I, E, top_k));
         scaled = take((size_t)M * K * 4);
         bytes = at;
     }
@@ -692,10 +759,10 @@ struct Workspace {
 
 }  // namespace
 
-size_t moe_workspace_bytes(int M, int K, int I, int E, int top_k) { return Workspace(M, K, I, top_k).bytes; }
+size_t moe_workspace_bytes(int M, int K, int I, int E, int top_k) { return Workspace(M, K, I, E, top_k).bytes; }
 
 int launch_moe(const MoeProblem& p, void* workspace, hipStream_t st) {
-    const Workspace w(p.M, p.K, p.I, p.top_k);
+    const Workspace w(p.M, p.K, p.I, p.E, p.top_k);
     unsigned char* ws = (unsigned char*)workspace;
     _Float16* scaled = (_Float16*)(ws + w.scaled);
     ExpertArgs a{};
@@ -709,12 +776,9 @@ int launch_moe(const MoeProblem& p, void* workspace, hipStream_t st) {
 
     const RouteArgs r{(const _Float16*)p.x, (const _Float16*)p.router, p.inv_s, (int*)(ws + w.ids),
                       (float*)(ws + w.weights), scaled, a.arrived, p.K / 16, p.M, p.E, p.K, p.top_k, p.renormalize};
-    const size_t lds = (size_t)p.K * 2;
-    if (lds > 48 * 1024)
-        if (int e = (int)hipFuncSetAttribute(reinterpret_cast<const void*>(k_moe_route),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds))
-            return e;
-    hipLaunchKernelGGL(k_moe_route, dim3(p.M), dim3(1024), lds, st, r);
+    const int slabs = (p.K + kSlab - 1) / kSlab;
+    auto route = p.E * slabs >= 64 ? k_moe_route<4> : k_moe_route<1>;
+    hipLaunchKernelGGL(route, dim3(p.M), dim3(1024), (size_t)slabs * p.E * 4, st, r);
     if (int e = (int)hipGetLastError()) return e;
 
     for (int l = 0; l < 2; ++l) {
@@ -735,7 +799,14 @@ int launch_moe(const MoeProblem& p, void* workspace, hipStream_t st) {
     a.split = 1;
     a.rows = p.M * p.top_k;
     a.N = p.K; a.K = p.I;
-    return launch_experts_any<false>(a, p.bits, p.group_size, st);
+    const int tiles = p.I / kGroup, splits = down_splits(p.M, p.K, p.I, p.E, p.top_k);
+    a.split_tiles = (tiles + splits - 1) / splits;
+    a.splits = (tiles + a.split_tiles - 1) / a.split_tiles;
+    if (int e = launch_experts_any<false>(a, p.bits, p.group_size, st)) return e;
+    if (p.M == 1) return 0;
+    hipLaunchKernelGGL(k_moe_join, dim3((p.K / 4 + 255) / 256, p.M), dim3(256), 0, st, a.part, a.weights, a.y,
+                       p.top_k, p.K, a.splits);
+    return (int)hipGetLastError();
 }
 
 }  // namespace awq

@@ -23,27 +23,46 @@ __device__ __forceinline__ TileSlot<WQ> load_tile_slot(__amdgpu_buffer_rsrc_t r,
     return s;
 }
 
-// the four exact fp16 operands (q - z) of a lane slot: operand i holds the
-// lane's k = 8 i .. 8 i + 7 (of its 32)
+// The four exact fp16 operands (q - z) of a lane slot: operand i holds the
+// lane's k = 8 i .. 8 i + 7 (of its 32).  A code goes under an exponent whose
+// mantissa step puts it at its place in the word, so that a word needs one
+// shift:
+//   int4: nibbles at bits 0..3 and 4..7 (and 16 above) of w and of w >> 8,
+//         under 2^10 (1024 + q) and 2^6 (64 + q)
+//   int3: fields at bits 0, 3 and 6 of w, 0 and 3 of w >> 9, under 2^10, 2^7
+//         (128 + q) and 2^4 (16 + q); the last pair's bits are gathered from the
+//         three words' bits 15 and 31
+// and subtracting the exponent's value plus z is exact.
 template <int BITS, int WQ>
 __device__ __forceinline__ void exact_operands(const TileSlot<WQ>& w, _Float16 z, half8_t* b) {
-    const _Float16 zb = (_Float16)1024.0f + z, zb16 = (_Float16)64.0f + z;
-    const half2_t zz = {zb, zb}, zz16 = {zb16, zb16};
+    auto pair = [](_Float16 v) { return (half2_t){v, v}; };
+    const half2_t z10 = pair((_Float16)1024.0f + z);
+    auto put = [&](int p, uint32_t bits, half2_t zz) {      // pair p of the slot's 16
+        const half2_t v = __builtin_bit_cast(half2_t, bits) - zz;
+        b[p / 4][2 * (p % 4)] = v[0];
+        b[p / 4][2 * (p % 4) + 1] = v[1];
+    };
+    if constexpr (BITS == 4) {
+        const half2_t z6 = pair((_Float16)64.0f + z);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t pr[4];
-        if constexpr (BITS == 4) {
+        for (int i = 0; i < 4; ++i) {
+            uint32_t pr[4];
             int4_word_pairs(w.w[i], pr);
-        } else {
 #pragma unroll
-            for (int t = 0; t < 4; ++t) pr[t] = int3_pair_bits(w.w, 4 * i + t);
+            for (int t = 0; t < 4; ++t) put(4 * i + t, pr[t], t & 1 ? z6 : z10);
         }
+    } else {
+        const half2_t z7 = pair((_Float16)128.0f + z), z4 = pair((_Float16)16.0f + z);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const half2_t p = __builtin_bit_cast(half2_t, pr[t]) - (BITS == 4 && (t & 1) ? zz16 : zz);
-            b[i][2 * t] = p[0];
-            b[i][2 * t + 1] = p[1];
+        for (int i = 0; i < 3; ++i) {
+            const uint32_t v = w.w[i], v9 = v >> 9;
+            put(5 * i, and_or(v, 0x00070007u, 0x64006400u), z10);
+            put(5 * i + 1, and_or(v, 0x00380038u, 0x58005800u), z7);
+            put(5 * i + 2, and_or(v, 0x01C001C0u, 0x4C004C00u), z4);
+            put(5 * i + 3, and_or(v9, 0x00070007u, 0x64006400u), z10);
+            put(5 * i + 4, and_or(v9, 0x00380038u, 0x58005800u), z7);
         }
+        put(15, int3_pair_bits(w.w, 15), z10);
     }
 }
 

@@ -47,9 +47,15 @@ struct Args {
     int M, N, K, steps;                            // steps of this split (blockIdx.y)
 };
 
+// p[n .. n + 3], entries past the last one repeated
+__device__ __forceinline__ float4_t load4(const float* p, int n, int N) {
+    if (n + 3 < N) return (float4_t){p[n], p[n + 1], p[n + 2], p[n + 3]};
+    return (float4_t){p[min(n, N - 1)], p[min(n + 1, N - 1)], p[min(n + 2, N - 1)], p[min(n + 3, N - 1)]};
+}
+
 // four consecutive outputs n .. n + 3 of row m
 template <class E>
-__device__ __forceinline__ void store4(const Args& a, int m, int n, int4_t acc, float sx) {
+__device__ __forceinline__ void store4(const Args& a, int m, int n, int4_t acc, float sx, float4_t sw, float4_t bias) {
     if (a.part) {
         int* p = a.part + ((size_t)blockIdx.y * a.M + m) * a.N + n;
         if (n + 3 < a.N && (a.N & 3) == 0) {
@@ -63,10 +69,7 @@ __device__ __forceinline__ void store4(const Args& a, int m, int n, int4_t acc, 
     }
     float v[4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int c = min(n + r, a.N - 1);
-        v[r] = (float)acc[r] * (sx * a.sw[c]) + (a.bias ? a.bias[c] : 0.0f);
-    }
+    for (int r = 0; r < 4; ++r) v[r] = (float)acc[r] * (sx * sw[r]) + bias[r];
     uint16_t* p = a.y + (size_t)m * a.N + n;
     if (n + 3 < a.N && (a.N & 3) == 0) {
         *reinterpret_cast<uint2*>(p) = make_uint2(pack2<E>(v[0], v[1]), pack2<E>(v[2], v[3]));
@@ -75,6 +78,20 @@ __device__ __forceinline__ void store4(const Args& a, int m, int n, int4_t acc, 
         for (int r = 0; r < 4; ++r)
             if (n + r < a.N) p[r] = E::store(v[r]);
     }
+}
+
+// Workgroup id -> output tile.  Ids go round-robin over the 8 XCDs: XCD x takes
+// a contiguous run of the tile sequence, which walks column by column through
+// bands of 8 tile rows, so that the tiles an XCD runs at once share operand
+// rows and columns in its L2.
+__device__ __forceinline__ void tile_of(int id, int nTm, int nTn, int& tm, int& tn) {
+    const int nT = nTm * nTn, q = nT / 8, r = nT % 8, xcd = id & 7;
+    const int t = xcd * q + min(xcd, r) + (id >> 3);
+    constexpr int BAND = 8;
+    const int band = t / (BAND * nTn), in = t - band * (BAND * nTn);
+    const int rows = min(BAND, nTm - band * BAND);
+    tm = band * BAND + in % rows;
+    tn = in / rows;
 }
 
 // ---------------------------------------------------------------------------
@@ -223,28 +240,45 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_w8a8_few(Args a) {
 #pragma unroll
             for (int q = 1; q < kWaves; ++q) sum += red[(q * MT * NBW + tile) * 64 + lane];
             const int m = 16 * t + j, n = n0 + 16 * b + 4 * h;
-            if (m < a.M && n < a.N) store4<E>(a, m, n, sum, sx[t]);
+            if (m < a.M && n < a.N)
+                store4<E>(a, m, n, sum, sx[t], load4(a.sw, n, a.N),
+                          a.bias ? load4(a.bias, n, a.N) : (float4_t){0.f, 0.f, 0.f, 0.f});
         }
 }
 
 // ---------------------------------------------------------------------------
-// Many rows: both operands through LDS, TM x TN output tiles.
+// Many rows: TM x TN output tiles, WM x WN waves.  Both operands go through LDS
+// in steps of 64 k (one MFMA deep), S steps in flight as direct-to-LDS loads;
+// a wave reads the fragments of step t + 1 while the MFMAs of step t run.
 // ---------------------------------------------------------------------------
-template <class E, int TM, int TN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN, 1) void k_w8a8_tile(Args a) {
+constexpr int kTileStep = 64;
+
+// XOR of the four 16-byte chunks of row r (of 16) in LDS.  Four rows span the 64
+// banks, and a ds_read_b128 serves lanes 0-3, 12-15, 20-23, 24-27 together (then
+// 4-11, 16-19, 28-31, and the same of the upper half): with rows 0-3, 4-7, 8-11
+// and 12-15 XOR-ed by 0, 2, 3 and 1 each such group of a fragment read takes 16
+// distinct bank quadruples.  XOR by r >> 2 costs 4 conflict cycles per read
+// (SQ_LDS_BANK_CONFLICT).
+__device__ __forceinline__ int chunk_swizzle(int r) { return (((r >> 1) ^ (r >> 2)) & 2) | (r >> 3); }
+
+template <class E, int TM, int TN, int WM, int WN, int S>
+__global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_w8a8_tile(Args a) {
     constexpr int WV = WM * WN;
     constexpr int FM = TM / WM / 16, FN = TN / WN / 16;      // 16-row fragments of a wave
-    constexpr int XI = TM / 8 / WV, WI = TN / 8 / WV;        // 8-row loads of a wave per step
-    constexpr int XB = TM * kStep, BUF = (TM + TN) * kStep;
+    constexpr int XI = TM / 16 / WV, WI = TN / 16 / WV;      // 16-row loads of a wave per step
+    constexpr int XB = TM * kTileStep, BUF = (TM + TN) * kTileStep;
+    constexpr int LPS = XI + WI;
+    static_assert(XI * WV * 16 == TM && WI * WV * 16 == TN, "every wave loads the same number of row groups");
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int j = lane & 15, h = lane >> 4;
     const int wm = wave / WN, wn = wave % WN;
-    const int nTn = (a.N + TN - 1) / TN;
-    const int m0 = (int)blockIdx.x / nTn * TM, n0 = (int)blockIdx.x % nTn * TN;
-    const int total = (a.K + kStep - 1) / kStep;
+    int tm, tn;
+    tile_of(blockIdx.x, (a.M + TM - 1) / TM, (a.N + TN - 1) / TN, tm, tn);
+    const int m0 = tm * TM, n0 = tn * TN;
+    const int total = (a.K + kTileStep - 1) / kTileStep;
     const int k0 = blockIdx.y * a.steps;
     const int steps = min(total - k0, a.steps);
     const size_t K = (size_t)a.K;
@@ -253,21 +287,21 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_w8a8_tile(Args a) {
     const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x + (size_t)m0 * K, (size_t)mrows * K);
     const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.w + (size_t)n0 * K, (size_t)nrows * K);
 
-    // A load instruction fills 8 rows: lane l writes chunk l & 7 of row
-    // l >> 3, which holds the row's global chunk (l & 7) ^ (l >> 3), so that
-    // the fragment reads of 16 rows spread over the banks
-    const int lr = lane >> 3, kc = (lane & 7) ^ lr;
+    // A load instruction fills 16 rows of 64 bytes: lane l writes chunk l & 3 of
+    // row l >> 2, which holds the row's global chunk (l & 3) ^ chunk_swizzle(row)
+    const int lr = lane >> 2, kc = (lane & 3) ^ chunk_swizzle(lr);
     uint32_t xoff[XI], woff[WI];
 #pragma unroll
     for (int i = 0; i < XI; ++i)
-        xoff[i] = (uint32_t)min(8 * (wave * XI + i) + lr, mrows - 1) * (uint32_t)a.K + 16u * kc;
+        xoff[i] = (uint32_t)min(16 * (wave * XI + i) + lr, mrows - 1) * (uint32_t)a.K + 16u * kc;
 #pragma unroll
     for (int i = 0; i < WI; ++i)
-        woff[i] = (uint32_t)min(8 * (wave * WI + i) + lr, nrows - 1) * (uint32_t)a.K + 16u * kc;
-    auto issue = [&](int kt, int buf) {
-        const uint32_t at = (uint32_t)(k0 + kt) * kStep;
-        const bool ok = (int)at + 16 * kc < a.K;
-        unsigned char* xb = smem + buf * BUF;
+        woff[i] = (uint32_t)min(16 * (wave * WI + i) + lr, nrows - 1) * (uint32_t)a.K + 16u * kc;
+    auto issue = [&](int step, int slot) {
+        const uint32_t at = (uint32_t)(k0 + step) * kTileStep;
+        // chunks past K, and all of the steps past the last one, load zeros
+        const bool ok = step < steps && (int)at + 16 * kc < a.K;
+        unsigned char* xb = smem + slot * BUF;
 #pragma unroll
         for (int i = 0; i < XI; ++i)
             load16_lds(rx, xb + (wave * XI + i) * 1024, ok ? xoff[i] : kOutOfRange, at);
@@ -275,46 +309,235 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_w8a8_tile(Args a) {
         for (int i = 0; i < WI; ++i)
             load16_lds(rw, xb + XB + (wave * WI + i) * 1024, ok ? woff[i] : kOutOfRange, at);
     };
+    const int fat = j * kTileStep + ((h ^ chunk_swizzle(j)) << 4);   // this lane's chunk of a fragment
+    const unsigned char* xf = smem + wm * FM * 1024 + fat;
+    const unsigned char* wf = smem + XB + wn * FN * 1024 + fat;
 
     int4_t acc[FM][FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int c = 0; c < FN; ++c) acc[i][c] = (int4_t){0, 0, 0, 0};
+    int4_t xv[2][FM], wv[2][FN];
+    auto fragments = [&](int slot, int f) {
+#pragma unroll
+        for (int c = 0; c < FN; ++c) wv[f][c] = *reinterpret_cast<const int4_t*>(wf + slot * BUF + c * 1024);
+#pragma unroll
+        for (int i = 0; i < FM; ++i) xv[f][i] = *reinterpret_cast<const int4_t*>(xf + slot * BUF + i * 1024);
+    };
 
-    issue(0, 0);
-    for (int kt = 0; kt < steps; ++kt) {
-        const int buf = kt & 1;
-        __builtin_amdgcn_s_waitcnt(0);
-        __syncthreads();                           // step kt is in LDS; the other buffer is free
-        if (kt + 1 < steps) issue(kt + 1, buf ^ 1);
-        const unsigned char* xb = smem + buf * BUF + (wm * FM * 16 + j) * kStep;
-        const unsigned char* wb = smem + buf * BUF + XB + (wn * FN * 16 + j) * kStep;
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int p = ((4 * s + h) ^ (j & 7)) * 16;
-            int4_t wv[FN];
+    for (int s = 0; s < S - 1; ++s) issue(s, s);
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(LPS * (S - 2)));
+    asm volatile("s_barrier" ::: "memory");
+    fragments(0, 0);
+    static_assert(S % 2 == 0, "fragment sets alternate with the steps");
+    int step0 = 0;
+    do {
 #pragma unroll
-            for (int c = 0; c < FN; ++c) wv[c] = *reinterpret_cast<const int4_t*>(wb + c * 16 * kStep + p);
+        for (int st = 0; st < S; ++st) {
+            const int step = step0 + st;
+            // this wave's part of step + 1 has landed and its fragments of step
+            // have been read; then everybody's (a bare barrier: a fence would
+            // drain the loads of the steps after)
+            __builtin_amdgcn_s_waitcnt(vmcnt_imm(LPS * (S - 3)));
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+            issue(step + S - 1, (st + S - 1) % S);
+            fragments((st + 1) % S, (st + 1) & 1);
+            if (step < steps) {
 #pragma unroll
-            for (int i = 0; i < FM; ++i) {
-                const int4_t xv = *reinterpret_cast<const int4_t*>(xb + i * 16 * kStep + p);
+                for (int i = 0; i < FM; ++i)
 #pragma unroll
-                for (int c = 0; c < FN; ++c)
-                    acc[i][c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[c], xv, acc[i][c], 0, 0, 0);
+                    for (int c = 0; c < FN; ++c)
+                        acc[i][c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[st & 1][c], xv[st & 1][i], acc[i][c], 0, 0, 0);
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
-    }
+        step0 += S;
+    } while (step0 < steps);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
+    const int nb = n0 + wn * FN * 16 + 4 * h;
+    float4_t sw[FN], bias[FN];
+#pragma unroll
+    for (int c = 0; c < FN; ++c) {
+        sw[c] = load4(a.sw, nb + 16 * c, a.N);
+        bias[c] = a.bias ? load4(a.bias, nb + 16 * c, a.N) : (float4_t){0.f, 0.f, 0.f, 0.f};
+    }
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
         const int m = m0 + (wm * FM + i) * 16 + j;
         if (m >= a.M) continue;
         const float sx = a.part ? 0.0f : a.sx[m];
 #pragma unroll
-        for (int c = 0; c < FN; ++c) {
-            const int n = n0 + (wn * FN + c) * 16 + 4 * h;
-            if (n < a.N) store4<E>(a, m, n, acc[i][c], sx);
+        for (int c = 0; c < FN; ++c)
+            if (nb + 16 * c < a.N) store4<E>(a, m, nb + 16 * c, acc[i][c], sx, sw[c], bias[c]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// 256 x 256 tiles of the largest products, 8 waves.
+//
+// Steps of 128 k (whole 128-byte lines of every row), two of them in LDS, each
+// as four half tiles of 128 rows: X0, X1, W0, W1.  A wave computes 64 rows of
+// X0 and of X1 against 32 columns of W0 and of W1, in four phases of 16 MFMAs:
+//   phase   reads   multiplies   loads (for step t + 1 or t + 2)
+//     0     X0 W0     X0 W0        X1 (t + 1)
+//     1     W1        X0 W1        X0 (t + 2)
+//     2     X1        X1 W1        W0 (t + 2)
+//     3               X1 W0        W1 (t + 2)
+// Each half tile is read once, so its buffer is loaded again a phase or two
+// later: 5 half tiles (10 loads a wave) are always in flight behind the one a
+// phase waits for, seven phases ahead of its use.
+//
+// A phase is a memory part and a multiply part with a barrier after each.  The
+// waves 4..7 run one barrier behind 0..3 (a SIMD holds one of each): while one
+// multiplies, the other reads, loads and waits.
+// ---------------------------------------------------------------------------
+namespace wide {
+constexpr int T = 256;                             // tile rows and columns
+constexpr int HALF = 128 * kStep;                  // bytes of a half tile
+constexpr int BUF = 4 * HALF;                      // X0 X1 W0 W1 of one step
+constexpr int IN_FLIGHT = 10;                      // loads behind those a phase waits for
+}  // namespace wide
+
+template <class E>
+__global__ __launch_bounds__(512, 2) void k_w8a8_wide(Args a) {
+    using namespace wide;
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int j = lane & 15, h = lane >> 4;
+    const int wm = wave >> 2, wn = wave & 3;
+    int tm, tn;
+    tile_of(blockIdx.x, (a.M + T - 1) / T, (a.N + T - 1) / T, tm, tn);
+    const int m0 = tm * T, n0 = tn * T;
+    const int steps = (a.K + kStep - 1) / kStep;
+    const size_t K = (size_t)a.K;
+    const int mrows = min(T, a.M - m0), nrows = min(T, a.N - n0);
+    const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x + (size_t)m0 * K, (size_t)mrows * K);
+    const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.w + (size_t)n0 * K, (size_t)nrows * K);
+
+    // A load fills 8 rows: lane l writes chunk l & 7 of row l >> 3, which holds
+    // the row's global chunk (l & 7) ^ (row & 6).  A ds_read_b128 serves lanes
+    // 0-3, 12-15, 20-23, 24-27 together (and so on): with that XOR each such
+    // group of a fragment read takes 16 distinct bank quadruples.
+    const int lr = lane >> 3, kc = (lane & 7) ^ (lr & 6);
+    uint32_t off[4][2];                            // of X0 X1 W0 W1: this wave's two row groups
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = (p & 1) * 128 + (wave * 2 + i) * 8 + lr;
+            off[p][i] = (uint32_t)min(r, (p < 2 ? mrows : nrows) - 1) * (uint32_t)a.K + 16u * kc;
+        }
+    auto issue = [&](int part, int step) {
+        const uint32_t at = (uint32_t)step * kStep;
+        // chunks past K, and all of the steps past the last one, load zeros
+        const bool ok = (int)at + 16 * kc < a.K;
+        unsigned char* lds = smem + (step & 1) * BUF + part * HALF + wave * 2048;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            load16_lds(part < 2 ? rx : rw, lds + i * 1024, ok ? off[part][i] : kOutOfRange, at);
+    };
+    const int at0 = ((h ^ (j & 6)) << 4) + j * kStep;        // this lane's chunk, k 0..63 of the step
+    const int at1 = (((4 + h) ^ (j & 6)) << 4) + j * kStep;  // k 64..127
+    int4_t x[4][2], w[2][2][2], acc[2][2][4][2];
+    auto read_x = [&](const unsigned char* half) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[i][0] = *reinterpret_cast<const int4_t*>(half + (wm * 4 + i) * 2048 + at0);
+            x[i][1] = *reinterpret_cast<const int4_t*>(half + (wm * 4 + i) * 2048 + at1);
+        }
+    };
+    auto read_w = [&](const unsigned char* half, int p) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            w[p][c][0] = *reinterpret_cast<const int4_t*>(half + (wn * 2 + c) * 2048 + at0);
+            w[p][c][1] = *reinterpret_cast<const int4_t*>(half + (wn * 2 + c) * 2048 + at1);
+        }
+    };
+    auto multiply = [&](int xp, int wp) {
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    acc[xp][wp][i][c] =
+                        __builtin_amdgcn_mfma_i32_16x16x64_i8(w[wp][c][s], x[i][s], acc[xp][wp][i][c], 0, 0, 0);
+        __builtin_amdgcn_s_setprio(0);
+    };
+    // end of a memory part: its fragments are in registers (their LDS may be
+    // loaded again) and the half tiles of the next part have landed
+    auto ready = [&]() {
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(IN_FLIGHT));
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto next = [&]() {
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) acc[q][p][i][c] = (int4_t){0, 0, 0, 0};
+
+    constexpr int X0 = 0, X1 = 1, W0 = 2, W1 = 3;
+    issue(X0, 0); issue(W0, 0); issue(W1, 0); issue(X1, 0);
+    issue(X0, 1); issue(W0, 1); issue(W1, 1);
+    ready();
+    if (wave >= 4) next();                         // one barrier behind
+    for (int t = 0; t < steps; ++t) {
+        const unsigned char* b = smem + (t & 1) * BUF;
+        read_x(b + X0 * HALF);
+        read_w(b + W0 * HALF, 0);
+        issue(X1, t + 1);
+        ready();
+        multiply(0, 0);
+        next();
+        read_w(b + W1 * HALF, 1);
+        issue(X0, t + 2);
+        ready();
+        multiply(0, 1);
+        next();
+        read_x(b + X1 * HALF);
+        issue(W0, t + 2);
+        ready();
+        multiply(1, 1);
+        next();
+        issue(W1, t + 2);
+        ready();
+        multiply(1, 0);
+        next();
+    }
+    if (wave < 4) next();                          // the same number of barriers for all
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+
+#pragma unroll
+    for (int wp = 0; wp < 2; ++wp) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int n = n0 + wp * 128 + wn * 32 + 16 * c + 4 * h;
+            if (n >= a.N) continue;
+            const float4_t sw = load4(a.sw, n, a.N);
+            const float4_t bias = a.bias ? load4(a.bias, n, a.N) : (float4_t){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int xp = 0; xp < 2; ++xp)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int m = m0 + xp * 128 + wm * 64 + 16 * i + j;
+                    if (m < a.M) store4<E>(a, m, n, acc[xp][wp][i][c], a.sx[m], sw, bias);
+                }
         }
     }
 }
@@ -331,31 +554,37 @@ __global__ __launch_bounds__(256) void k_w8a8_join(Args a, int splits) {
     a.y[i] = E::store(v);
 }
 
-// how a product is cut: the tile kernel and the K splits
+// how a product is cut: the kernel, its tile and the K splits
 struct Plan {
     int few;                                       // k_w8a8_few
     int mt, nbw;                                   // its row tiles and column blocks
+    int tm, tn;                                    // k_w8a8_tile
     int blocks, splits, steps;                     // workgroups per split, splits, steps of each
 };
 
 Plan plan(int M, int N, int K) {
     Plan p{};
     const int cus = device_cu_count();
-    const int total = (K + kStep - 1) / kStep;
+    int total, least;
     p.few = M <= 64;
     if (p.few) {
         p.mt = M <= 16 ? 1 : M <= 32 ? 2 : 4;
         p.nbw = 1;
         p.blocks = (N + 16 * p.nbw - 1) / (16 * p.nbw);
+        total = (K + kStep - 1) / kStep;
+        least = 16;
     } else {
-        p.blocks = ((M + 255) / 256) * ((N + 255) / 256);
+        p.tm = p.tn = 256;
+        if ((long long)((M + 255) / 256) * ((N + 255) / 256) < cus) p.tm = p.tn = 128;
+        p.blocks = ((M + p.tm - 1) / p.tm) * ((N + p.tn - 1) / p.tn);
+        total = (K + kTileStep - 1) / kTileStep;
+        least = 16;
     }
     p.splits = 1;
     p.steps = total;
-    // fewer workgroups than compute units: cut K while a split keeps 16 steps
+    // fewer workgroups than compute units: cut K while a split keeps `least` steps
     if (p.blocks < cus) {
-        int s = cus / p.blocks;
-        s = min(s, total / 16);
+        const int s = min(cus / p.blocks, total / least);
         if (s > 1) {
             p.steps = (total + s - 1) / s;
             p.splits = (total + p.steps - 1) / p.steps;
@@ -378,14 +607,25 @@ int launch_few(const Args& a, const Plan& p, hipStream_t st) {
     return (int)hipGetLastError();
 }
 
-template <class E, int TM, int TN, int WM, int WN>
+template <class E, int TM, int TN, int WM, int WN, int S>
 int launch_tile(const Args& a, const Plan& p, hipStream_t st) {
-    constexpr size_t lds = 2 * (TM + TN) * kStep;
-    auto kern = k_w8a8_tile<E, TM, TN, WM, WN>;
+    constexpr size_t lds = S * (TM + TN) * kTileStep;
+    auto kern = k_w8a8_tile<E, TM, TN, WM, WN, S>;
     if (int e = (int)hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
                                          hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds))
         return e;
     hipLaunchKernelGGL(kern, dim3(p.blocks, p.splits), dim3(64 * WM * WN), lds, st, a);
+    return (int)hipGetLastError();
+}
+
+template <class E>
+int launch_wide(const Args& a, const Plan& p, hipStream_t st) {
+    constexpr size_t lds = 2 * wide::BUF;
+    auto kern = k_w8a8_wide<E>;
+    if (int e = (int)hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                                         hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds))
+        return e;
+    hipLaunchKernelGGL(kern, dim3(p.blocks), dim3(512), lds, st, a);
     return (int)hipGetLastError();
 }
 
@@ -396,7 +636,8 @@ int launch_t(Args a, const Plan& p, hipStream_t st) {
     else if (p.few && p.mt == 1) e = launch_few<E, 1, 1, 4, false>(a, p, st);
     else if (p.few && p.mt == 2) e = launch_few<E, 2, 1, 4, false>(a, p, st);
     else if (p.few) e = launch_few<E, 4, 1, 2, false>(a, p, st);
-    else e = launch_tile<E, 256, 256, 2, 4>(a, p, st);
+    else if (p.tm == 256) e = launch_wide<E>(a, p, st);
+    else e = launch_tile<E, 128, 128, 2, 2, 4>(a, p, st);
     if (e || !a.part) return e;
     const size_t total = (size_t)a.M * a.N;
     hipLaunchKernelGGL((k_w8a8_join<E>), dim3((unsigned)((total + 255) / 256)), dim3(256), 0, st, a, p.splits);

@@ -377,33 +377,41 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_w8a8_tile(Args a)
 }
 
 // ---------------------------------------------------------------------------
-// 256 x 256 tiles of the largest products, 8 waves.
+// 256 x 256 tiles of the largest products, 8 waves, one workgroup per compute
+// unit that takes tile after tile.
 //
 // Steps of 128 k (whole 128-byte lines of every row), two of them in LDS, each
 // as four half tiles of 128 rows: X0, X1, W0, W1.  A wave computes 64 rows of
 // X0 and of X1 against 32 columns of W0 and of W1, in four phases of 16 MFMAs:
-//   phase   reads   multiplies   loads (for step t + 1 or t + 2)
-//     0     X0 W0     X0 W0        X1 (t + 1)
-//     1     W1        X0 W1        X0 (t + 2)
-//     2     X1        X1 W1        W0 (t + 2)
-//     3               X1 W0        W1 (t + 2)
-// Each half tile is read once, so its buffer is loaded again a phase or two
-// later: 5 half tiles (10 loads a wave) are always in flight behind the one a
-// phase waits for, seven phases ahead of its use.
+//   phase   reads (LDS)   multiplies   loads (to LDS)
+//     0     X0 (t)        X0 W0        W0 (t + 2)
+//     1     W1 (t)        X0 W1        X0 (t + 2)
+//     2     X1 (t)        X1 W1        W1 (t + 2)
+//     3     W0 (t + 1)    X1 W0        X1 (t + 2)
+// Each half tile is read once and its buffer is loaded again in the next phase;
+// a phase waits for the one half tile that the next phase reads, with the six
+// after it (12 loads a wave) still in flight.
 //
 // A phase is a memory part and a multiply part with a barrier after each.  The
 // waves 4..7 run one barrier behind 0..3 (a SIMD holds one of each): while one
 // multiplies, the other reads, loads and waits.
+//
+// A tile's results leave while the next tile's first half tiles are loading:
+// each wave turns them in 4 KB of LDS of its own (32 rows of 64 columns) and
+// stores whole 128-byte lines.  For that the 64 columns of a wave are adjacent:
+// row r of half W_p is column 64 (r / 32) + 32 p + r % 32 of the tile.
 // ---------------------------------------------------------------------------
 namespace wide {
 constexpr int T = 256;                             // tile rows and columns
 constexpr int HALF = 128 * kStep;                  // bytes of a half tile
 constexpr int BUF = 4 * HALF;                      // X0 X1 W0 W1 of one step
-constexpr int IN_FLIGHT = 10;                      // loads behind those a phase waits for
+constexpr int IN_FLIGHT = 12;                      // loads behind the half tile a phase waits for
+constexpr int STAGE = 32 * 128;                    // a wave's output rows
+constexpr size_t LDS = 2 * BUF + 8 * STAGE;
 }  // namespace wide
 
 template <class E>
-__global__ __launch_bounds__(512, 2) void k_w8a8_wide(Args a) {
+__global__ __launch_bounds__(512, 2) void k_w8a8_wide(Args a, int tiles) {
     using namespace wide;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     const int tid = threadIdx.x;
@@ -411,40 +419,18 @@ __global__ __launch_bounds__(512, 2) void k_w8a8_wide(Args a) {
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int j = lane & 15, h = lane >> 4;
     const int wm = wave >> 2, wn = wave & 3;
-    int tm, tn;
-    tile_of(blockIdx.x, (a.M + T - 1) / T, (a.N + T - 1) / T, tm, tn);
-    const int m0 = tm * T, n0 = tn * T;
     const int steps = (a.K + kStep - 1) / kStep;
     const size_t K = (size_t)a.K;
-    const int mrows = min(T, a.M - m0), nrows = min(T, a.N - n0);
-    const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x + (size_t)m0 * K, (size_t)mrows * K);
-    const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.w + (size_t)n0 * K, (size_t)nrows * K);
 
     // A load fills 8 rows: lane l writes chunk l & 7 of row l >> 3, which holds
     // the row's global chunk (l & 7) ^ (row & 6).  A ds_read_b128 serves lanes
     // 0-3, 12-15, 20-23, 24-27 together (and so on): with that XOR each such
     // group of a fragment read takes 16 distinct bank quadruples.
     const int lr = lane >> 3, kc = (lane & 7) ^ (lr & 6);
-    uint32_t off[4][2];                            // of X0 X1 W0 W1: this wave's two row groups
-#pragma unroll
-    for (int p = 0; p < 4; ++p)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = (p & 1) * 128 + (wave * 2 + i) * 8 + lr;
-            off[p][i] = (uint32_t)min(r, (p < 2 ? mrows : nrows) - 1) * (uint32_t)a.K + 16u * kc;
-        }
-    auto issue = [&](int part, int step) {
-        const uint32_t at = (uint32_t)step * kStep;
-        // chunks past K, and all of the steps past the last one, load zeros
-        const bool ok = (int)at + 16 * kc < a.K;
-        unsigned char* lds = smem + (step & 1) * BUF + part * HALF + wave * 2048;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            load16_lds(part < 2 ? rx : rw, lds + i * 1024, ok ? off[part][i] : kOutOfRange, at);
-    };
     const int at0 = ((h ^ (j & 6)) << 4) + j * kStep;        // this lane's chunk, k 0..63 of the step
     const int at1 = (((4 + h) ^ (j & 6)) << 4) + j * kStep;  // k 64..127
-    int4_t x[4][2], w[2][2][2], acc[2][2][4][2];
+
+    int4_t x[4][2], w0[2][2][2], w1[2][2], acc[2][2][4][2];
     auto read_x = [&](const unsigned char* half) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -452,14 +438,14 @@ __global__ __launch_bounds__(512, 2) void k_w8a8_wide(Args a) {
             x[i][1] = *reinterpret_cast<const int4_t*>(half + (wm * 4 + i) * 2048 + at1);
         }
     };
-    auto read_w = [&](const unsigned char* half, int p) {
+    auto read_w = [&](const unsigned char* half, int4_t (*w)[2]) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            w[p][c][0] = *reinterpret_cast<const int4_t*>(half + (wn * 2 + c) * 2048 + at0);
-            w[p][c][1] = *reinterpret_cast<const int4_t*>(half + (wn * 2 + c) * 2048 + at1);
+            w[c][0] = *reinterpret_cast<const int4_t*>(half + (wn * 2 + c) * 2048 + at0);
+            w[c][1] = *reinterpret_cast<const int4_t*>(half + (wn * 2 + c) * 2048 + at1);
         }
     };
-    auto multiply = [&](int xp, int wp) {
+    auto multiply = [&](int4_t (*out)[2], const int4_t (*w)[2]) {
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int s = 0; s < 2; ++s)
@@ -467,12 +453,12 @@ __global__ __launch_bounds__(512, 2) void k_w8a8_wide(Args a) {
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
-                    acc[xp][wp][i][c] =
-                        __builtin_amdgcn_mfma_i32_16x16x64_i8(w[wp][c][s], x[i][s], acc[xp][wp][i][c], 0, 0, 0);
+                    out[i][c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[c][s], x[i][s], out[i][c], 0, 0, 0);
         __builtin_amdgcn_s_setprio(0);
     };
     // end of a memory part: its fragments are in registers (their LDS may be
-    // loaded again) and the half tiles of the next part have landed
+    // loaded again) and the half tile of the next part has landed (stores of the
+    // tile before only make the wait stricter)
     auto ready = [&]() {
         __builtin_amdgcn_s_waitcnt(vmcnt_imm(IN_FLIGHT));
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -483,61 +469,153 @@ __global__ __launch_bounds__(512, 2) void k_w8a8_wide(Args a) {
         asm volatile("s_barrier" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
     };
+
+    constexpr int X0 = 0, X1 = 1, W0 = 2, W1 = 3;
+    struct Source { __amdgpu_buffer_rsrc_t rx, rw; uint32_t off[4][2]; };
+    Source src;
+    auto aim = [&](int id) {                       // the loads of a tile
+        int tm, tn;
+        tile_of(id, (a.M + T - 1) / T, (a.N + T - 1) / T, tm, tn);
+        const int mrows = min(T, a.M - tm * T), nrows = min(T, a.N - tn * T);
+        src.rx = make_rsrc(a.x + (size_t)tm * T * K, (size_t)mrows * K);
+        src.rw = make_rsrc(a.w + (size_t)tn * T * K, (size_t)nrows * K);
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
+        for (int p = 0; p < 4; ++p)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = (wave * 2 + i) * 8 + lr;       // of the half tile
+                const int row = p < 2 ? (p & 1) * 128 + r : r / 32 * 64 + (p & 1) * 32 + r % 32;
+                src.off[p][i] = (uint32_t)min(row, (p < 2 ? mrows : nrows) - 1) * (uint32_t)a.K + 16u * kc;
+            }
+    };
+    auto issue = [&](int part, int step) {
+        const uint32_t at = (uint32_t)step * kStep;
+        // chunks past K, and all of the steps past the last one, load zeros
+        const bool ok = (int)at + 16 * kc < a.K;
+        unsigned char* lds = smem + (step & 1) * BUF + part * HALF + wave * 2048;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            load16_lds(part < 2 ? src.rx : src.rw, lds + i * 1024, ok ? src.off[part][i] : kOutOfRange, at);
+    };
+    auto begin = [&]() {
+        issue(W0, 0); issue(X0, 0); issue(W1, 0); issue(X1, 0);
+        issue(W0, 1); issue(X0, 1); issue(W1, 1); issue(X1, 1);
+    };
+    auto step = [&](int t, int odd) {
+        const unsigned char* b = smem + odd * BUF;
+        read_x(b + X0 * HALF);
+        issue(W0, t + 2);
+        ready();
+        multiply(acc[0][0], w0[odd]);
+        next();
+        read_w(b + W1 * HALF, w1);
+        issue(X0, t + 2);
+        ready();
+        multiply(acc[0][1], w1);
+        next();
+        read_x(b + X1 * HALF);
+        issue(W1, t + 2);
+        ready();
+        multiply(acc[1][1], w1);
+        next();
+        read_w(smem + (odd ^ 1) * BUF + W0 * HALF, w0[odd ^ 1]);
+        issue(X1, t + 2);
+        ready();
+        multiply(acc[1][0], w0[odd]);
+        next();
+    };
+
+    aim(blockIdx.x);
+    begin();
+    for (int id = blockIdx.x; id < tiles; id += gridDim.x) {
+        int tm, tn;
+        tile_of(id, (a.M + T - 1) / T, (a.N + T - 1) / T, tm, tn);
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) acc[q][p][i][c] = (int4_t){0, 0, 0, 0};
+        // W0 (0), then X0 (0), have landed for everybody
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(IN_FLIGHT));
+        asm volatile("s_barrier" ::: "memory");
+        read_w(smem + W0 * HALF, w0[0]);
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (wave >= 4) next();                     // one barrier behind
+        for (int t = 0; t < steps; t += 2) {
+            step(t, 0);
+            if (t + 1 < steps) step(t + 1, 1);
+        }
+        if (wave < 4) next();                      // the same number of barriers for all
+        const int nb = tn * T + wn * 64, mb = tm * T + wm * 64;
+        float4_t sw[2][2], bias[2][2];
 #pragma unroll
         for (int p = 0; p < 2; ++p)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int c = 0; c < 2; ++c) {
+                const int n = nb + 32 * p + 16 * c + 4 * h;
+                sw[p][c] = load4(a.sw, n, a.N);
+                bias[p][c] = a.bias ? load4(a.bias, n, a.N) : (float4_t){0.f, 0.f, 0.f, 0.f};
+            }
+        float sx[2][4];
 #pragma unroll
-                for (int c = 0; c < 2; ++c) acc[q][p][i][c] = (int4_t){0, 0, 0, 0};
-
-    constexpr int X0 = 0, X1 = 1, W0 = 2, W1 = 3;
-    issue(X0, 0); issue(W0, 0); issue(W1, 0); issue(X1, 0);
-    issue(X0, 1); issue(W0, 1); issue(W1, 1);
-    ready();
-    if (wave >= 4) next();                         // one barrier behind
-    for (int t = 0; t < steps; ++t) {
-        const unsigned char* b = smem + (t & 1) * BUF;
-        read_x(b + X0 * HALF);
-        read_w(b + W0 * HALF, 0);
-        issue(X1, t + 1);
-        ready();
-        multiply(0, 0);
-        next();
-        read_w(b + W1 * HALF, 1);
-        issue(X0, t + 2);
-        ready();
-        multiply(0, 1);
-        next();
-        read_x(b + X1 * HALF);
-        issue(W0, t + 2);
-        ready();
-        multiply(1, 1);
-        next();
-        issue(W1, t + 2);
-        ready();
-        multiply(1, 0);
-        next();
-    }
-    if (wave < 4) next();                          // the same number of barriers for all
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-
+        for (int q = 0; q < 2; ++q)
 #pragma unroll
-    for (int wp = 0; wp < 2; ++wp) {
+            for (int i = 0; i < 4; ++i) sx[q][i] = a.sx[min(mb + 128 * q + 16 * i + j, a.M - 1)];
+        // The loads past the last step write zeros to LDS: they are done before
+        // the next tile's.  So are the scales': a register load still pending
+        // on entry would be waited for, with all loads behind it, in every step.
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+        asm volatile("s_barrier" ::: "memory");
+        if (id + (int)gridDim.x < tiles) {
+            aim(id + gridDim.x);
+            begin();
+        }
+        if ((a.N & 7) == 0) {
+            unsigned char* stage = smem + 2 * BUF + wave * STAGE;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            const int n = n0 + wp * 128 + wn * 32 + 16 * c + 4 * h;
-            if (n >= a.N) continue;
-            const float4_t sw = load4(a.sw, n, a.N);
-            const float4_t bias = a.bias ? load4(a.bias, n, a.N) : (float4_t){0.f, 0.f, 0.f, 0.f};
+            for (int q = 0; q < 2; ++q)
 #pragma unroll
-            for (int xp = 0; xp < 2; ++xp)
+                for (int i0 = 0; i0 < 4; i0 += 2) {
+                    // row 16 i + j of 128 bytes, its 16-byte chunks XOR-ed by j & 7
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int m = m0 + xp * 128 + wm * 64 + 16 * i + j;
-                    if (m < a.M) store4<E>(a, m, n, acc[xp][wp][i][c], a.sx[m], sw, bias);
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int p = 0; p < 2; ++p)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                float v[4];
+#pragma unroll
+                                for (int r = 0; r < 4; ++r)
+                                    v[r] = (float)acc[q][p][i0 + i][c][r] * (sx[q][i0 + i] * sw[p][c][r]) + bias[p][c][r];
+                                const int chunk = 4 * p + 2 * c + (h >> 1);
+                                *reinterpret_cast<uint2*>(stage + (16 * i + j) * 128 + ((chunk ^ (j & 7)) << 4) +
+                                                          8 * (h & 1)) =
+                                    make_uint2(pack2<E>(v[0], v[1]), pack2<E>(v[2], v[3]));
+                            }
+                    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {  // 8 rows a store, whole lines
+                        const int r = 8 * g + lr, n = nb + 8 * (lane & 7), m = mb + 128 * q + 16 * i0 + r;
+                        const uint4 o = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+                        if (m < a.M && n < a.N) *reinterpret_cast<uint4*>(a.y + (size_t)m * a.N + n) = o;
+                    }
+                    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
                 }
+        } else {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const int m = mb + 128 * q + 16 * i + j, n = nb + 32 * p + 16 * c + 4 * h;
+                            if (m < a.M && n < a.N) store4<E>(a, m, n, acc[q][p][i][c], sx[q][i], sw[p][c], bias[p][c]);
+                        }
         }
     }
 }
@@ -620,12 +698,11 @@ int launch_tile(const Args& a, const Plan& p, hipStream_t st) {
 
 template <class E>
 int launch_wide(const Args& a, const Plan& p, hipStream_t st) {
-    constexpr size_t lds = 2 * wide::BUF;
     auto kern = k_w8a8_wide<E>;
     if (int e = (int)hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                         hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds))
+                                         hipFuncAttributeMaxDynamicSharedMemorySize, (int)wide::LDS))
         return e;
-    hipLaunchKernelGGL(kern, dim3(p.blocks), dim3(512), lds, st, a);
+    hipLaunchKernelGGL(kern, dim3(min(p.blocks, device_cu_count())), dim3(512), wide::LDS, st, a, p.blocks);
     return (int)hipGetLastError();
 }
 

@@ -11,6 +11,13 @@
 // n = 4 h + r, four consecutive outputs.
 #include "rows.h"
 
+#ifndef AWQ_BATCH_S
+#define AWQ_BATCH_S 3
+#define AWQ_BATCH_KT 2
+#define AWQ_BATCH_OCC 4
+#define AWQ_BATCH_WV 4
+#define AWQ_BATCH_FILL 1
+#endif
 namespace awq {
 namespace {
 
@@ -24,10 +31,6 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* p, size_
 
 __device__ __forceinline__ int4_t load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
     return __builtin_bit_cast(int4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
-}
-// weights of a product with few rows are read once: non-temporal
-__device__ __forceinline__ int4_t load16_nt(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-    return __builtin_bit_cast(int4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 2));
 }
 
 // 16 bytes per lane from buffer offset voff + soff to LDS at lds + 16 * lane
@@ -95,57 +98,50 @@ __device__ __forceinline__ void tile_of(int id, int nTm, int nTn, int& tm, int& 
 }
 
 // ---------------------------------------------------------------------------
-// Few rows (M <= 64): HBM-bound on the weights, each read once.  A workgroup
-// of 8 waves owns 16 NBW columns and all rows; its waves take the K steps in
-// turn, each through a ring of U steps in flight, and their exact int32 sums
-// meet in LDS.
+// Few rows (M <= 4): HBM-bound on the weights, each read once.  A workgroup of
+// 4 waves owns 16 columns; its waves take the K steps in turn, each through a
+// ring of U steps in flight, and their exact int32 sums meet in LDS.
 //
-// FUSED (few 16-bit rows that fit in registers): the workgroup quantizes the
-// rows itself, behind its first weight loads, and keeps the codes in LDS.
+// FUSED (16-bit rows that fit in registers): the workgroup quantizes the rows
+// itself, behind its first weight loads, and keeps the codes in LDS.
 // ---------------------------------------------------------------------------
-constexpr int kWaves = 8;
+constexpr int kWaves = 4;
 constexpr int kFusedChunks = 8;                    // 16-byte chunks of x a thread quantizes at most
 
-template <class E, int MT, int NBW, int U, bool FUSED>
-__global__ __launch_bounds__(64 * kWaves, 2) void k_w8a8_few(Args a) {
+template <class E, int U, bool FUSED>
+__global__ __launch_bounds__(64 * kWaves, 4) void k_w8a8_few(Args a) {
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     __shared__ uint32_t slots[kWaves];
+    __shared__ int4_t red[kWaves][64];
     const int tid = threadIdx.x;
     const int lane = tid & 63, wave = tid >> 6;
     const int j = lane & 15, h = lane >> 4;
-    const int n0 = blockIdx.x * 16 * NBW;
+    const int n0 = blockIdx.x * 16;
     const int total = (a.K + kStep - 1) / kStep;
     const int k0 = blockIdx.y * a.steps;
     const int mine = min(total - k0, a.steps);     // steps of this split
     const int nw = wave < mine ? (mine - wave + kWaves - 1) / kWaves : 0;
     const size_t K = (size_t)a.K;
-
-    const __amdgpu_buffer_rsrc_t rw =
-        make_rsrc(a.w + (size_t)n0 * K, (size_t)min(16 * NBW, a.N - n0) * K);
+    const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.w + (size_t)n0 * K, (size_t)min(16, a.N - n0) * K);
     const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x, FUSED ? 0 : (size_t)a.M * K);
 
-    int4_t w[U][NBW][2], x[FUSED ? 1 : U][MT][2];
+    int4_t w[U][2], x[FUSED ? 1 : U][2];
     auto load = [&](int i, int u) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             const int k = (k0 + wave + kWaves * i) * kStep + 64 * s + 16 * h;
-            const bool ok = i < nw && k < a.K;
-#pragma unroll
-            for (int b = 0; b < NBW; ++b)          // rows past N are past the buffer's end
-                w[u][b][s] = load16_nt(rw, ok ? (uint32_t)(16 * b + j) * (uint32_t)a.K + (uint32_t)k : kOutOfRange);
-            if constexpr (!FUSED) {
-#pragma unroll
-                for (int t = 0; t < MT; ++t)       // as are rows past M
-                    x[u][t][s] = load16(rx, ok ? (uint32_t)(16 * t + j) * (uint32_t)a.K + (uint32_t)k : kOutOfRange);
-            }
+            // rows past N or M are past the buffers' ends
+            const uint32_t off = i < nw && k < a.K ? (uint32_t)j * (uint32_t)a.K + (uint32_t)k : kOutOfRange;
+            w[u][s] = load16(rw, off);
+            if constexpr (!FUSED) x[u][s] = load16(rx, off);
         }
     };
 #pragma unroll
     for (int u = 0; u < U; ++u) load(u, u);
 
-    // FUSED: 1, 2 or 4 rows (MP), 8 / MP waves a row
+    // FUSED: 1, 2 or 4 rows (MP), kWaves / MP waves a row
     float* sxs = reinterpret_cast<float*>(slots);
-    const int xstride = (a.K + kStep - 1) / kStep * kStep + 16;
+    const int xstride = total * kStep + 16;
     if constexpr (FUSED) {
         const int MP = a.M > 2 ? 4 : a.M;
         const int per = 64 * kWaves / MP;          // threads per row
@@ -176,8 +172,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_w8a8_few(Args a) {
 #pragma unroll
         for (int c = 0; c < kFusedChunks; ++c) {
             const int i = t + per * c;
-            // steps end past K: the chunks there are zero
-            if (row < a.M && i < (xstride - 16) / 8) {
+            // the last step ends past K: the chunks there are zero
+            if (row < a.M && i < total * (kStep / 8)) {
                 unpack8<E>(r[c], v);
                 *reinterpret_cast<uint2*>(xr + 8 * i) = pack_codes8(v, s);
             }
@@ -186,64 +182,148 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_w8a8_few(Args a) {
         if (t == 0) sxs[row] = s.scale();
     }
 
-    int4_t acc[MT][NBW];
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int b = 0; b < NBW; ++b) acc[t][b] = (int4_t){0, 0, 0, 0};
-
+    int4_t acc = {0, 0, 0, 0};
     for (int i0 = 0; i0 < nw; i0 += U) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (i0 + u < nw) {                     // wave-uniform
 #pragma unroll
-                for (int s = 0; s < 2; ++s)
-#pragma unroll
-                    for (int t = 0; t < MT; ++t) {
-                        int4_t xv;
-                        if constexpr (FUSED)
-                            xv = *reinterpret_cast<const int4_t*>(
-                                smem + (j < a.M ? j : 0) * xstride + (k0 + wave + kWaves * (i0 + u)) * kStep +
-                                64 * s + 16 * h);
-                        else
-                            xv = x[u][t][s];
-#pragma unroll
-                        for (int b = 0; b < NBW; ++b)
-                            acc[t][b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[u][b][s], xv, acc[t][b], 0, 0, 0);
-                    }
+                for (int s = 0; s < 2; ++s) {
+                    int4_t xv;
+                    if constexpr (FUSED)
+                        xv = *reinterpret_cast<const int4_t*>(
+                            smem + (j < a.M ? j : 0) * xstride + (wave + kWaves * (i0 + u)) * kStep + 64 * s + 16 * h);
+                    else
+                        xv = x[u][s];
+                    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[u][s], xv, acc, 0, 0, 0);
+                }
             }
             load(i0 + u + U, u);
         }
     }
-
-    // the waves' sums, [wave][tile][lane]
-    float sx[MT];
-    __syncthreads();                               // every read of the codes is done
-#pragma unroll
-    for (int t = 0; t < MT; ++t) {
-        const int m = 16 * t + j;
-        sx[t] = a.part || m >= a.M ? 0.0f : FUSED ? sxs[m] : a.sx[m];
-    }
-    int4_t* red = reinterpret_cast<int4_t*>(smem);
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int b = 0; b < NBW; ++b) red[(wave * MT * NBW + t * NBW + b) * 64 + lane] = acc[t][b];
+    red[wave][lane] = acc;
     __syncthreads();
+    if (wave != 0) return;
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
+    for (int q = 1; q < kWaves; ++q) acc += red[q][lane];
+    const int n = n0 + 4 * h;
+    if (j < a.M && n < a.N)
+        store4<E>(a, j, n, acc, a.part ? 0.0f : FUSED ? sxs[j] : a.sx[j], load4(a.sw, n, a.N),
+                  a.bias ? load4(a.bias, n, a.N) : (float4_t){0.f, 0.f, 0.f, 0.f});
+}
+
+// ---------------------------------------------------------------------------
+// A decode batch (5 to 64 rows): HBM-bound on the weights, and the codes must
+// not be read from L2 as often as they are (a 16-column workgroup that loads
+// its own codes moves as many bytes from L2 as from HBM: 8192 x 28672 at M = 16
+// 65 us, 47 us without those loads).  A workgroup of WV waves owns 16 WV
+// columns, one block of 16 per wave over the whole K (or one split of it); the
+// codes go through LDS for all of them.  S steps of KT * 128 k are in flight:
+// codes direct to LDS, weights to registers.
+// ---------------------------------------------------------------------------
+template <int MT, int WV>
+struct BatchShape {
+    static constexpr int KT = AWQ_BATCH_KT;
+    static constexpr int XW = MT * 2 * KT / WV;    // 8-row loads of a wave per step
+    static constexpr int BUF = MT * 16 * KT * kStep;
+    static constexpr int LPS = XW + 2 * KT;
+    static constexpr int S = AWQ_BATCH_S;
+    static constexpr size_t LDS = (size_t)S * BUF;
+    static_assert(XW * WV == MT * 2 * KT, "every wave loads the same number of row groups");
+};
+
+template <class E, int MT, int WV>
+__global__ __launch_bounds__(64 * WV, AWQ_BATCH_OCC) void k_w8a8_batch(Args a) {
+    using T = BatchShape<MT, WV>;
+    constexpr int KT = T::KT, S = T::S;
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int j = lane & 15, h = lane >> 4;
+    const int n0 = ((int)blockIdx.x * WV + wave) * 16;
+    const int total = (a.K + kStep - 1) / kStep;
+    const int k0 = blockIdx.y * a.steps;           // a.steps: 128-k steps of a split, a multiple of KT
+    const int steps = (min(total - k0, a.steps) + KT - 1) / KT;
+    const size_t K = (size_t)a.K;
+    const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x, (size_t)a.M * K);
+    const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.w + (size_t)min(n0, a.N - 1) * K, (size_t)max(0, min(16, a.N - n0)) * K);
+
+    // a load fills 8 rows of 128 bytes, chunk l & 7 of row l >> 3 from the row's
+    // chunk (l & 7) ^ (row & 6); rows past M are past the buffer's end
+    const int lr = lane >> 3, kc = (lane & 7) ^ (lr & 6);
+    uint32_t xoff[T::XW];
 #pragma unroll
-        for (int b = 0; b < NBW; ++b) {
-            const int tile = t * NBW + b;
-            if (tile % kWaves != wave) continue;
-            int4_t sum = red[tile * 64 + lane];
+    for (int i = 0; i < T::XW; ++i)
+        xoff[i] = (uint32_t)((wave * T::XW + i) % (MT * 2) * 8 + lr) * (uint32_t)a.K + 16u * kc;
+    const uint32_t woff = (uint32_t)j * (uint32_t)a.K + 16u * h;
+    int4_t w[S][KT][2];
+    auto issue = [&](int step, int slot) {
 #pragma unroll
-            for (int q = 1; q < kWaves; ++q) sum += red[(q * MT * NBW + tile) * 64 + lane];
-            const int m = 16 * t + j, n = n0 + 16 * b + 4 * h;
-            if (m < a.M && n < a.N)
-                store4<E>(a, m, n, sum, sx[t], load4(a.sw, n, a.N),
-                          a.bias ? load4(a.bias, n, a.N) : (float4_t){0.f, 0.f, 0.f, 0.f});
+        for (int i = 0; i < T::XW; ++i) {
+            const int ii = wave * T::XW + i;
+            const uint32_t at = (uint32_t)__builtin_amdgcn_readfirstlane((k0 + step * KT + ii / (MT * 2)) * kStep);
+            // chunks past K, and all of the steps past the last one, load zeros
+            const bool ok = step < steps && (int)at + 16 * kc < a.K;
+            load16_lds(rx, smem + slot * T::BUF + ii * 1024, ok ? xoff[i] : kOutOfRange, at);
         }
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const uint32_t at = (uint32_t)(k0 + step * KT + t) * kStep + 64u * q;
+                const bool ok = step < steps && (int)at + 16 * h < a.K;
+                w[slot][t][q] = load16(rw, ok ? woff + at : kOutOfRange);
+            }
+    };
+    int4_t acc[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[m] = (int4_t){0, 0, 0, 0};
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s) {
+        __builtin_amdgcn_sched_barrier(0);
+        issue(s, s);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    int step0 = 0;
+    do {
+#pragma unroll
+        for (int st = 0; st < S; ++st) {
+            const int step = step0 + st;
+            // this wave's part of the step has landed; then everybody's, and
+            // everybody is done with the buffer that is loaded next (a bare
+            // barrier: a fence would also drain the later steps' loads)
+            __builtin_amdgcn_s_waitcnt(vmcnt_imm(T::LPS * (S - 2)));
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+            issue(step + S - 1, (st + S - 1) % S);
+            __builtin_amdgcn_sched_barrier(0);
+            if (step < steps) {
+#pragma unroll
+                for (int t = 0; t < KT; ++t)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) {
+                            const int4_t xv = *reinterpret_cast<const int4_t*>(
+                                smem + st * T::BUF + (t * MT + m) * 2048 + j * kStep + (((4 * q + h) ^ (j & 6)) << 4));
+                            acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[st][t][q], xv, acc[m], 0, 0, 0);
+                        }
+            }
+        }
+        step0 += S;
+    } while (step0 < steps);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+
+    const int n = n0 + 4 * h;
+    if (n >= a.N) return;
+    const float4_t sw = load4(a.sw, n, a.N);
+    const float4_t bias = a.bias ? load4(a.bias, n, a.N) : (float4_t){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        const int row = 16 * m + j;
+        if (row < a.M) store4<E>(a, row, n, acc[m], a.part ? 0.0f : a.sx[row], sw, bias);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -633,55 +713,52 @@ __global__ __launch_bounds__(256) void k_w8a8_join(Args a, int splits) {
 }
 
 // how a product is cut: the kernel, its tile and the K splits
+enum Kernel { FEW, BATCH, TILE, WIDE };
 struct Plan {
-    int few;                                       // k_w8a8_few
-    int mt, nbw;                                   // its row tiles and column blocks
-    int tm, tn;                                    // k_w8a8_tile
-    int blocks, splits, steps;                     // workgroups per split, splits, steps of each
+    Kernel kernel;
+    int blocks, splits, steps;                     // workgroups per split, splits, K steps of each
 };
+
+constexpr int kFewRows = 4, kBatchRows = 64, kBatchWaves = AWQ_BATCH_WV;
 
 Plan plan(int M, int N, int K) {
     Plan p{};
     const int cus = device_cu_count();
-    int total, least;
-    p.few = M <= 64;
-    if (p.few) {
-        p.mt = M <= 16 ? 1 : M <= 32 ? 2 : 4;
-        p.nbw = 1;
-        p.blocks = (N + 16 * p.nbw - 1) / (16 * p.nbw);
-        total = (K + kStep - 1) / kStep;
-        least = 16;
+    int step = kStep, unit = 1, want = cus;
+    if (M <= kFewRows) {
+        p.kernel = FEW;
+        p.blocks = (N + 15) / 16;
+    } else if (M <= kBatchRows) {
+        p.kernel = BATCH;
+        p.blocks = (N + 16 * kBatchWaves - 1) / (16 * kBatchWaves);
+        unit = AWQ_BATCH_KT;
+        want = AWQ_BATCH_FILL * cus;
+    } else if ((long long)((M + 255) / 256) * ((N + 255) / 256) >= cus) {
+        p.kernel = WIDE;
+        p.blocks = ((M + 255) / 256) * ((N + 255) / 256);
     } else {
-        p.tm = p.tn = 256;
-        if ((long long)((M + 255) / 256) * ((N + 255) / 256) < cus) p.tm = p.tn = 128;
-        p.blocks = ((M + p.tm - 1) / p.tm) * ((N + p.tn - 1) / p.tn);
-        total = (K + kTileStep - 1) / kTileStep;
-        least = 16;
+        p.kernel = TILE;
+        p.blocks = ((M + 127) / 128) * ((N + 127) / 128);
+        step = kTileStep;
     }
+    // fewer workgroups than compute units: cut K while a split keeps 16 steps
+    const int total = (K + step - 1) / step;
     p.splits = 1;
-    p.steps = total;
-    // fewer workgroups than compute units: cut K while a split keeps `least` steps
-    if (p.blocks < cus) {
-        const int s = min(cus / p.blocks, total / least);
+    p.steps = (total + unit - 1) / unit * unit;
+    if (p.blocks < want) {
+        const int s = min(want / p.blocks, total / 16);
         if (s > 1) {
-            p.steps = (total + s - 1) / s;
+            p.steps = ((total + s - 1) / s + unit - 1) / unit * unit;
             p.splits = (total + p.steps - 1) / p.steps;
         }
     }
     return p;
 }
 
-template <class E, int MT, int NBW, int U, bool FUSED>
+template <class E, int U, bool FUSED>
 int launch_few(const Args& a, const Plan& p, hipStream_t st) {
-    const size_t red = (size_t)kWaves * MT * NBW * 64 * 16;
-    const size_t codes = FUSED ? (size_t)a.M * ((size_t)(a.K + kStep - 1) / kStep * kStep + 16) : 0;
-    const size_t lds = max(red, codes);
-    auto kern = k_w8a8_few<E, MT, NBW, U, FUSED>;
-    if (lds > 64 * 1024)
-        if (int e = (int)hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds))
-            return e;
-    hipLaunchKernelGGL(kern, dim3(p.blocks, p.splits), dim3(64 * kWaves), lds, st, a);
+    const size_t lds = FUSED ? (size_t)a.M * ((size_t)(a.K + kStep - 1) / kStep * kStep + 16) : 0;
+    hipLaunchKernelGGL((k_w8a8_few<E, U, FUSED>), dim3(p.blocks, p.splits), dim3(64 * kWaves), lds, st, a);
     return (int)hipGetLastError();
 }
 
@@ -706,15 +783,27 @@ int launch_wide(const Args& a, const Plan& p, hipStream_t st) {
     return (int)hipGetLastError();
 }
 
+template <class E, int MT>
+int launch_batch(const Args& a, const Plan& p, hipStream_t st) {
+    using T = BatchShape<MT, kBatchWaves>;
+    auto kern = k_w8a8_batch<E, MT, kBatchWaves>;
+    if (T::LDS > 48 * 1024)
+        if (int e = (int)hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)T::LDS))
+            return e;
+    hipLaunchKernelGGL(kern, dim3(p.blocks, p.splits), dim3(64 * kBatchWaves), T::LDS, st, a);
+    return (int)hipGetLastError();
+}
+
 template <class E>
-int launch_t(Args a, const Plan& p, hipStream_t st) {
+int launch_t(const Args& a, const Plan& p, hipStream_t st) {
     int e;
-    if (a.rows) e = launch_few<E, 1, 1, 4, true>(a, p, st);
-    else if (p.few && p.mt == 1) e = launch_few<E, 1, 1, 4, false>(a, p, st);
-    else if (p.few && p.mt == 2) e = launch_few<E, 2, 1, 4, false>(a, p, st);
-    else if (p.few) e = launch_few<E, 4, 1, 2, false>(a, p, st);
-    else if (p.tm == 256) e = launch_wide<E>(a, p, st);
-    else e = launch_tile<E, 128, 128, 2, 2, 4>(a, p, st);
+    if (p.kernel == FEW) e = a.rows ? launch_few<E, 4, true>(a, p, st) : launch_few<E, 4, false>(a, p, st);
+    else if (p.kernel == WIDE) e = launch_wide<E>(a, p, st);
+    else if (p.kernel == TILE) e = launch_tile<E, 128, 128, 2, 2, 4>(a, p, st);
+    else if (a.M <= 16) e = launch_batch<E, 1>(a, p, st);
+    else if (a.M <= 32) e = launch_batch<E, 2>(a, p, st);
+    else e = launch_batch<E, 4>(a, p, st);
     if (e || !a.part) return e;
     const size_t total = (size_t)a.M * a.N;
     hipLaunchKernelGGL((k_w8a8_join<E>), dim3((unsigned)((total + 255) / 256)), dim3(256), 0, st, a, p.splits);
@@ -723,7 +812,7 @@ int launch_t(Args a, const Plan& p, hipStream_t st) {
 
 // the decode product quantizes its rows itself
 bool fused_rows(const Plan& p, int M, int K) {
-    return p.few && p.splits == 1 && M <= 4 && (M == 3 ? 4 : M) * (K / 8) <= kFusedChunks * 64 * kWaves;
+    return p.kernel == FEW && p.splits == 1 && (M == 3 ? 4 : M) * (K / 8) <= kFusedChunks * 64 * kWaves;
 }
 
 size_t align16(size_t v) { return (v + 15) & ~(size_t)15; }

@@ -11,6 +11,10 @@
 // n = 4 h + r, four consecutive outputs.
 #include "rows.h"
 
+#ifndef AWQ_T_WM
+#define AWQ_T_WM 2
+#define AWQ_T_WN 4
+#endif
 #ifndef AWQ_BATCH_S
 #define AWQ_BATCH_S 3
 #define AWQ_BATCH_KT 2
@@ -326,29 +330,27 @@ __global__ __launch_bounds__(64 * WV, AWQ_BATCH_OCC) void k_w8a8_batch(Args a) {
     }
 }
 
-// ---------------------------------------------------------------------------
-// Many rows: TM x TN output tiles, WM x WN waves.  Both operands go through LDS
-// in steps of 64 k (one MFMA deep), S steps in flight as direct-to-LDS loads;
-// a wave reads the fragments of step t + 1 while the MFMAs of step t run.
-// ---------------------------------------------------------------------------
-constexpr int kTileStep = 64;
+// XOR of the eight 16-byte chunks of row r in LDS (rows of 128 bytes).  A
+// ds_read_b128 serves lanes 0-3, 12-15, 20-23, 24-27 together (then 4-11, 16-19,
+// 28-31, and the same of the upper half); with this XOR each such group of a
+// fragment read (lane (j, h): row j, chunk c + h) takes 16 distinct bank
+// quadruples (no SQ_LDS_BANK_CONFLICT).
+__device__ __forceinline__ int chunk_swizzle(int r) { return r & 6; }
 
-// XOR of the four 16-byte chunks of row r (of 16) in LDS.  Four rows span the 64
-// banks, and a ds_read_b128 serves lanes 0-3, 12-15, 20-23, 24-27 together (then
-// 4-11, 16-19, 28-31, and the same of the upper half): with rows 0-3, 4-7, 8-11
-// and 12-15 XOR-ed by 0, 2, 3 and 1 each such group of a fragment read takes 16
-// distinct bank quadruples.  XOR by r >> 2 costs 4 conflict cycles per read
-// (SQ_LDS_BANK_CONFLICT).
-__device__ __forceinline__ int chunk_swizzle(int r) { return (((r >> 1) ^ (r >> 2)) & 2) | (r >> 3); }
-
+// ---------------------------------------------------------------------------
+// Many rows, fewer than 256 x 256 tiles for every compute unit: TM x TN output
+// tiles, WM x WN waves.  Both operands go through LDS in steps of 128 k, S steps
+// in flight as direct-to-LDS loads; a wave reads the fragments of step t + 1
+// while the MFMAs of step t run.
+// ---------------------------------------------------------------------------
 template <class E, int TM, int TN, int WM, int WN, int S>
 __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_w8a8_tile(Args a) {
     constexpr int WV = WM * WN;
     constexpr int FM = TM / WM / 16, FN = TN / WN / 16;      // 16-row fragments of a wave
-    constexpr int XI = TM / 16 / WV, WI = TN / 16 / WV;      // 16-row loads of a wave per step
-    constexpr int XB = TM * kTileStep, BUF = (TM + TN) * kTileStep;
+    constexpr int XI = TM / 8 / WV, WI = TN / 8 / WV;        // 8-row loads of a wave per step
+    constexpr int XB = TM * kStep, BUF = (TM + TN) * kStep;
     constexpr int LPS = XI + WI;
-    static_assert(XI * WV * 16 == TM && WI * WV * 16 == TN, "every wave loads the same number of row groups");
+    static_assert(XI * WV * 8 == TM && WI * WV * 8 == TN, "every wave loads the same number of row groups");
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     const int tid = threadIdx.x;
     const int lane = tid & 63;
@@ -358,7 +360,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_w8a8_tile(Args a)
     int tm, tn;
     tile_of(blockIdx.x, (a.M + TM - 1) / TM, (a.N + TN - 1) / TN, tm, tn);
     const int m0 = tm * TM, n0 = tn * TN;
-    const int total = (a.K + kTileStep - 1) / kTileStep;
+    const int total = (a.K + kStep - 1) / kStep;
     const int k0 = blockIdx.y * a.steps;
     const int steps = min(total - k0, a.steps);
     const size_t K = (size_t)a.K;
@@ -367,18 +369,17 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_w8a8_tile(Args a)
     const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x + (size_t)m0 * K, (size_t)mrows * K);
     const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.w + (size_t)n0 * K, (size_t)nrows * K);
 
-    // A load instruction fills 16 rows of 64 bytes: lane l writes chunk l & 3 of
-    // row l >> 2, which holds the row's global chunk (l & 3) ^ chunk_swizzle(row)
-    const int lr = lane >> 2, kc = (lane & 3) ^ chunk_swizzle(lr);
+    // A load instruction fills 8 rows: lane l writes chunk l & 7 of row l >> 3
+    const int lr = lane >> 3, kc = (lane & 7) ^ chunk_swizzle(lr);
     uint32_t xoff[XI], woff[WI];
 #pragma unroll
     for (int i = 0; i < XI; ++i)
-        xoff[i] = (uint32_t)min(16 * (wave * XI + i) + lr, mrows - 1) * (uint32_t)a.K + 16u * kc;
+        xoff[i] = (uint32_t)min(8 * (wave * XI + i) + lr, mrows - 1) * (uint32_t)a.K + 16u * kc;
 #pragma unroll
     for (int i = 0; i < WI; ++i)
-        woff[i] = (uint32_t)min(16 * (wave * WI + i) + lr, nrows - 1) * (uint32_t)a.K + 16u * kc;
+        woff[i] = (uint32_t)min(8 * (wave * WI + i) + lr, nrows - 1) * (uint32_t)a.K + 16u * kc;
     auto issue = [&](int step, int slot) {
-        const uint32_t at = (uint32_t)(k0 + step) * kTileStep;
+        const uint32_t at = (uint32_t)(k0 + step) * kStep;
         // chunks past K, and all of the steps past the last one, load zeros
         const bool ok = step < steps && (int)at + 16 * kc < a.K;
         unsigned char* xb = smem + slot * BUF;
@@ -389,21 +390,26 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_w8a8_tile(Args a)
         for (int i = 0; i < WI; ++i)
             load16_lds(rw, xb + XB + (wave * WI + i) * 1024, ok ? woff[i] : kOutOfRange, at);
     };
-    const int fat = j * kTileStep + ((h ^ chunk_swizzle(j)) << 4);   // this lane's chunk of a fragment
-    const unsigned char* xf = smem + wm * FM * 1024 + fat;
-    const unsigned char* wf = smem + XB + wn * FN * 1024 + fat;
+    int fat[2];                                    // this lane's chunks of a fragment: k 0..63 and 64..127
+#pragma unroll
+    for (int q = 0; q < 2; ++q) fat[q] = j * kStep + (((4 * q + h) ^ chunk_swizzle(j)) << 4);
+    const unsigned char* xf = smem + wm * FM * 2048;
+    const unsigned char* wf = smem + XB + wn * FN * 2048;
 
     int4_t acc[FM][FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int c = 0; c < FN; ++c) acc[i][c] = (int4_t){0, 0, 0, 0};
-    int4_t xv[2][FM], wv[2][FN];
+    int4_t xv[2][FM][2], wv[2][FN][2];
     auto fragments = [&](int slot, int f) {
 #pragma unroll
-        for (int c = 0; c < FN; ++c) wv[f][c] = *reinterpret_cast<const int4_t*>(wf + slot * BUF + c * 1024);
+        for (int q = 0; q < 2; ++q) {
 #pragma unroll
-        for (int i = 0; i < FM; ++i) xv[f][i] = *reinterpret_cast<const int4_t*>(xf + slot * BUF + i * 1024);
+            for (int c = 0; c < FN; ++c) wv[f][c][q] = *reinterpret_cast<const int4_t*>(wf + slot * BUF + c * 2048 + fat[q]);
+#pragma unroll
+            for (int i = 0; i < FM; ++i) xv[f][i][q] = *reinterpret_cast<const int4_t*>(xf + slot * BUF + i * 2048 + fat[q]);
+        }
     };
 
 #pragma unroll
@@ -427,10 +433,13 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_w8a8_tile(Args a)
             fragments((st + 1) % S, (st + 1) & 1);
             if (step < steps) {
 #pragma unroll
-                for (int i = 0; i < FM; ++i)
+                for (int q = 0; q < 2; ++q)
 #pragma unroll
-                    for (int c = 0; c < FN; ++c)
-                        acc[i][c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[st & 1][c], xv[st & 1][i], acc[i][c], 0, 0, 0);
+                    for (int i = 0; i < FM; ++i)
+#pragma unroll
+                        for (int c = 0; c < FN; ++c)
+                            acc[i][c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[st & 1][c][q], xv[st & 1][i][q],
+                                                                              acc[i][c], 0, 0, 0);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -440,19 +449,21 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_w8a8_tile(Args a)
 
     const int nb = n0 + wn * FN * 16 + 4 * h;
     float4_t sw[FN], bias[FN];
+    float sx[FM];
 #pragma unroll
     for (int c = 0; c < FN; ++c) {
         sw[c] = load4(a.sw, nb + 16 * c, a.N);
         bias[c] = a.bias ? load4(a.bias, nb + 16 * c, a.N) : (float4_t){0.f, 0.f, 0.f, 0.f};
     }
 #pragma unroll
+    for (int i = 0; i < FM; ++i) sx[i] = a.sx[min(m0 + (wm * FM + i) * 16 + j, a.M - 1)];
+#pragma unroll
     for (int i = 0; i < FM; ++i) {
         const int m = m0 + (wm * FM + i) * 16 + j;
         if (m >= a.M) continue;
-        const float sx = a.part ? 0.0f : a.sx[m];
 #pragma unroll
         for (int c = 0; c < FN; ++c)
-            if (nb + 16 * c < a.N) store4<E>(a, m, nb + 16 * c, acc[i][c], sx, sw[c], bias[c]);
+            if (nb + 16 * c < a.N) store4<E>(a, m, nb + 16 * c, acc[i][c], sx[i], sw[c], bias[c]);
     }
 }
 
@@ -502,13 +513,10 @@ __global__ __launch_bounds__(512, 2) void k_w8a8_wide(Args a, int tiles) {
     const int steps = (a.K + kStep - 1) / kStep;
     const size_t K = (size_t)a.K;
 
-    // A load fills 8 rows: lane l writes chunk l & 7 of row l >> 3, which holds
-    // the row's global chunk (l & 7) ^ (row & 6).  A ds_read_b128 serves lanes
-    // 0-3, 12-15, 20-23, 24-27 together (and so on): with that XOR each such
-    // group of a fragment read takes 16 distinct bank quadruples.
-    const int lr = lane >> 3, kc = (lane & 7) ^ (lr & 6);
-    const int at0 = ((h ^ (j & 6)) << 4) + j * kStep;        // this lane's chunk, k 0..63 of the step
-    const int at1 = (((4 + h) ^ (j & 6)) << 4) + j * kStep;  // k 64..127
+    // a load fills 8 rows: lane l writes chunk l & 7 of row l >> 3
+    const int lr = lane >> 3, kc = (lane & 7) ^ chunk_swizzle(lr);
+    const int at0 = ((h ^ chunk_swizzle(j)) << 4) + j * kStep;        // this lane's chunk, k 0..63 of the step
+    const int at1 = (((4 + h) ^ chunk_swizzle(j)) << 4) + j * kStep;  // k 64..127
 
     int4_t x[4][2], w0[2][2][2], w1[2][2], acc[2][2][4][2];
     auto read_x = [&](const unsigned char* half) {
@@ -724,7 +732,7 @@ constexpr int kFewRows = 4, kBatchRows = 64, kBatchWaves = AWQ_BATCH_WV;
 Plan plan(int M, int N, int K) {
     Plan p{};
     const int cus = device_cu_count();
-    int step = kStep, unit = 1, want = cus;
+    int unit = 1, want = cus;
     if (M <= kFewRows) {
         p.kernel = FEW;
         p.blocks = (N + 15) / 16;
@@ -739,10 +747,9 @@ Plan plan(int M, int N, int K) {
     } else {
         p.kernel = TILE;
         p.blocks = ((M + 127) / 128) * ((N + 127) / 128);
-        step = kTileStep;
     }
     // fewer workgroups than compute units: cut K while a split keeps 16 steps
-    const int total = (K + step - 1) / step;
+    const int total = (K + kStep - 1) / kStep;
     p.splits = 1;
     p.steps = (total + unit - 1) / unit * unit;
     if (p.blocks < want) {
@@ -764,7 +771,7 @@ int launch_few(const Args& a, const Plan& p, hipStream_t st) {
 
 template <class E, int TM, int TN, int WM, int WN, int S>
 int launch_tile(const Args& a, const Plan& p, hipStream_t st) {
-    constexpr size_t lds = S * (TM + TN) * kTileStep;
+    constexpr size_t lds = S * (TM + TN) * kStep;
     auto kern = k_w8a8_tile<E, TM, TN, WM, WN, S>;
     if (int e = (int)hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
                                          hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds))
@@ -800,7 +807,7 @@ int launch_t(const Args& a, const Plan& p, hipStream_t st) {
     int e;
     if (p.kernel == FEW) e = a.rows ? launch_few<E, 4, true>(a, p, st) : launch_few<E, 4, false>(a, p, st);
     else if (p.kernel == WIDE) e = launch_wide<E>(a, p, st);
-    else if (p.kernel == TILE) e = launch_tile<E, 128, 128, 2, 2, 4>(a, p, st);
+    else if (p.kernel == TILE) e = launch_tile<E, 128, 128, AWQ_T_WM, AWQ_T_WN, 4>(a, p, st);
     else if (a.M <= 16) e = launch_batch<E, 1>(a, p, st);
     else if (a.M <= 32) e = launch_batch<E, 2>(a, p, st);
     else e = launch_batch<E, 4>(a, p, st);

@@ -418,11 +418,12 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_w8a8_tile(Args a)
     asm volatile("s_barrier" ::: "memory");
     fragments(0, 0);
     static_assert(S % 2 == 0, "fragment sets alternate with the steps");
-    int step0 = 0;
-    do {
+    for (int step0 = 0;; step0 += S) {
+        bool more = true;
 #pragma unroll
         for (int st = 0; st < S; ++st) {
             const int step = step0 + st;
+            if (step >= steps) { more = false; break; }
             // this wave's part of step + 1 has landed and its fragments of step
             // have been read; then everybody's (a bare barrier: a fence would
             // drain the loads of the steps after)
@@ -431,21 +432,31 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_w8a8_tile(Args a)
             __builtin_amdgcn_sched_barrier(0);
             issue(step + S - 1, (st + S - 1) % S);
             fragments((st + 1) % S, (st + 1) & 1);
-            if (step < steps) {
 #pragma unroll
-                for (int q = 0; q < 2; ++q)
+            for (int q = 0; q < 2; ++q)
 #pragma unroll
-                    for (int i = 0; i < FM; ++i)
+                for (int i = 0; i < FM; ++i)
 #pragma unroll
-                        for (int c = 0; c < FN; ++c)
-                            acc[i][c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[st & 1][c][q], xv[st & 1][i][q],
-                                                                              acc[i][c], 0, 0, 0);
+                    for (int c = 0; c < FN; ++c)
+                        acc[i][c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[st & 1][c][q], xv[st & 1][i][q],
+                                                                          acc[i][c], 0, 0, 0);
+            // the MFMAs' operands are in registers: the next loads and fragment
+            // reads are issued between them
+#pragma unroll
+            for (int q = 0; q < LPS; ++q) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+            }
+#pragma unroll
+            for (int q = 0; q < 2 * FM * FN - LPS; ++q) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
-        step0 += S;
-    } while (step0 < steps);
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        if (!more) break;
+    }
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
 
     const int nb = n0 + wn * FN * 16 + 4 * h;
     float4_t sw[FN], bias[FN];

@@ -585,9 +585,11 @@ def norm_gate_residual(block, residual, pre_weight, post_weight=None, gate=None,
     scales = None
     if out is None:
         r = torch.empty_like(residual)
-        h = block.new_empty(shape, dtype=h_type)
         if quantize:
+            h = block.new_empty(shape, dtype=h_type)
             scales = block.new_empty(T, dtype=torch.float32)
+        else:
+            h = torch.empty_like(block)
     elif quantize:
         r, h, scales = out
     else:

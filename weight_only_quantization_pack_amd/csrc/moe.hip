@@ -30,14 +30,6 @@
 #include "packed.h"
 #include "rows.h"
 
-#ifndef AWQ_MOE_OCC
-#define AWQ_MOE_OCC 3
-#define AWQ_MOE_S2 4
-#define AWQ_MOE_S1 6
-#define AWQ_MOE_FILL 4
-#define AWQ_MOE_S64 4
-#define AWQ_MOE_OCC64 4
-#endif
 namespace awq {
 namespace {
 
@@ -313,11 +305,11 @@ __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f +
 // compute.
 // ---------------------------------------------------------------------------
 template <int BITS, int GS, int WK, bool GATEUP>
-__global__ __launch_bounds__(512, 4) void k_moe_token(ExpertArgs a) {
+__global__ __launch_bounds__(512, 6) void k_moe_token(ExpertArgs a) {
     constexpr int WQ = BITS == 4 ? 4 : 3;
     constexpr int NL = GATEUP ? 2 : 1;
     constexpr int SUB = 8 / WK;
-    constexpr int U = 4;
+    constexpr int U = GATEUP ? 2 : 4;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     __shared__ float4_t red[8][NL][64];
     const int tid = threadIdx.x, lane = tid & 63;
@@ -408,12 +400,14 @@ __global__ __launch_bounds__(512, 4) void k_moe_token(ExpertArgs a) {
         int before = 0;
         if (lane == 0) before = __hip_atomic_fetch_add(a.arrived + b, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         if (__builtin_amdgcn_readfirstlane(before) != a.top_k - 1) return;
-        if (lane < 16) {                           // every choice's sums are there
-            float sum = 0.0f;
-            for (int q = 0; q < a.top_k; ++q)
-                sum = __builtin_fmaf(a.weights[q], load_shared(a.part + (size_t)q * a.N + n), sum);
-            a.y[n] = (_Float16)sum;
-        }
+        // the last one: lane quarter hq sums choices hq, hq + 4, .., and the
+        // quarters are added in a fixed order
+        float sum = 0.0f;
+        for (int q = hq; q < a.top_k; q += 4)
+            sum = __builtin_fmaf(a.weights[q], load_shared(a.part + (size_t)q * a.N + n), sum);
+        sum += __shfl_down(sum, 32);
+        sum += __shfl_down(sum, 16);
+        if (lane < 16) a.y[n] = (_Float16)sum;
     }
 }
 
@@ -479,7 +473,7 @@ __device__ __forceinline__ int row_swizzle(int r) { return (r & 0xA) | ((r & 1) 
 
 // waves per SIMD that k_moe_tile's registers are held to
 constexpr int tile_waves(int GS, int MT, bool gate_up) {
-    return MT >= 4 ? (GS == 128 && !gate_up ? AWQ_MOE_OCC64 : 2) : MT == 2 && gate_up && GS == 64 ? 2 : AWQ_MOE_OCC;
+    return MT >= 4 ? (GS == 128 && !gate_up ? 4 : 2) : MT == 2 && gate_up && GS == 64 ? 2 : 3;
 }
 
 template <int BITS, int GS, int MT, int WV, bool GATEUP>
@@ -493,7 +487,7 @@ struct TileShape {
     static constexpr int TB = (XR + (GS == 64)) * 256;     // a tile's rows (and a row of zeros)
     static constexpr int BUF = TB * KT;
     static constexpr int LPS = XW + 3 * NL * KT;   // loads per step and wave
-    static constexpr int S = KT * NL >= 4 ? 3 : XR >= 64 ? AWQ_MOE_S64 : KT * NL == 2 ? AWQ_MOE_S2 : AWQ_MOE_S1;
+    static constexpr int S = KT * NL >= 4 ? 3 : XR >= 64 ? 4 : KT * NL == 2 ? 4 : 6;
     static constexpr size_t LDS = (size_t)S * BUF;
     static_assert(XW * WV == XR / 4 * KT, "every wave loads the same number of row groups");
     static_assert(LPS * (S - 2) <= 63, "vmcnt counts to 63");
@@ -728,12 +722,12 @@ int launch_experts_any(const ExpertArgs& a, int bits, int group_size, hipStream_
 }
 
 // K splits of the down projections of more than one token: as many as bring the
-// expert workgroups (of 4 row blocks) to two per compute unit while a split
+// expert workgroups (of 4 row blocks) to 6 per compute unit while a split
 // keeps 16 tiles
 int down_splits(int M, int K, int I, int E, int top_k) {
     if (M == 1) return 1;
     const int wgs = min(M * top_k, E) * ((K / 16 + 3) / 4);
-    return max(1, min((I / kGroup) / 16, AWQ_MOE_FILL * device_cu_count() / max(wgs, 1)));
+    return max(1, min((I / kGroup) / 16, 6 * device_cu_count() / max(wgs, 1)));
 }
 
 // the workspace's parts, each 256-byte aligned

@@ -87,6 +87,50 @@ __device__ __forceinline__ void store4(const Args& a, int m, int n, int4_t acc, 
     }
 }
 
+// Outputs leave through LDS: a wave turns ROWS rows of COLS columns there (row
+// r at stage + r * 2 COLS, its 16-byte chunks XOR-ed by row_xor(r)) and stores
+// them from row m0, column n0 on -- 16 bytes a lane where the rows of y are
+// 16-byte aligned (N a multiple of 8), else two bytes a lane along a row
+// (1123 x 768 x 20369: 74 us with four scattered two-byte stores a lane).
+template <int COLS>
+__device__ __forceinline__ int row_xor(int r) { return COLS == 64 ? r & 7 : (r >> 1) & 3; }
+
+template <class E, int COLS>
+__device__ __forceinline__ void stage4(unsigned char* stage, int r, int col, int4_t acc, float sx, float4_t sw,
+                                       float4_t bias) {
+    float v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = (float)acc[q] * (sx * sw[q]) + bias[q];
+    *reinterpret_cast<uint2*>(stage + r * (2 * COLS) + (((col >> 3) ^ row_xor<COLS>(r)) << 4) + (col & 4) * 2) =
+        make_uint2(pack2<E>(v[0], v[1]), pack2<E>(v[2], v[3]));
+}
+
+template <int ROWS, int COLS>
+__device__ __forceinline__ void store_rows(const Args& a, const unsigned char* stage, int m0, int n0) {
+    const int lane = threadIdx.x & 63;
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");       // the wave's own writes
+    if ((a.N & 7) == 0) {
+        constexpr int CH = COLS / 8, RI = 64 / CH;           // chunks of a row, rows of a store
+#pragma unroll
+        for (int g = 0; g < ROWS / RI; ++g) {
+            const int r = RI * g + lane / CH, c = lane % CH;
+            const uint4 o = *reinterpret_cast<const uint4*>(stage + r * (2 * COLS) + ((c ^ row_xor<COLS>(r)) << 4));
+            if (m0 + r < a.M && n0 + 8 * c < a.N)
+                *reinterpret_cast<uint4*>(a.y + (size_t)(m0 + r) * a.N + n0 + 8 * c) = o;
+        }
+    } else {
+        constexpr int RI = 64 / COLS;
+#pragma unroll 4
+        for (int g = 0; g < ROWS / RI; ++g) {
+            const int r = RI * g + lane / COLS, c = lane % COLS;
+            const uint16_t o = *reinterpret_cast<const uint16_t*>(
+                stage + r * (2 * COLS) + (((c >> 3) ^ row_xor<COLS>(r)) << 4) + (c & 7) * 2);
+            if (m0 + r < a.M && n0 + c < a.N) a.y[(size_t)(m0 + r) * a.N + n0 + c] = o;
+        }
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");       // read before the next rows are written
+}
+
 // Workgroup id -> output tile.  Ids go round-robin over the 8 XCDs: XCD x takes
 // a contiguous run of the tile sequence, which walks column by column through
 // bands of 8 tile rows, so that the tiles an XCD runs at once share operand
@@ -458,24 +502,33 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_w8a8_tile(Args a)
     }
     __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
 
-    const int nb = n0 + wn * FN * 16 + 4 * h;
+    const int mb = m0 + wm * FM * 16, nb = n0 + wn * FN * 16;
+    if (a.part) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int c = 0; c < FN; ++c) {
+                const int m = mb + 16 * i + j, n = nb + 16 * c + 4 * h;
+                if (m < a.M && n < a.N) store4<E>(a, m, n, acc[i][c], 0.0f, (float4_t){}, (float4_t){});
+            }
+        return;
+    }
     float4_t sw[FN], bias[FN];
     float sx[FM];
 #pragma unroll
     for (int c = 0; c < FN; ++c) {
-        sw[c] = load4(a.sw, nb + 16 * c, a.N);
-        bias[c] = a.bias ? load4(a.bias, nb + 16 * c, a.N) : (float4_t){0.f, 0.f, 0.f, 0.f};
+        sw[c] = load4(a.sw, nb + 16 * c + 4 * h, a.N);
+        bias[c] = a.bias ? load4(a.bias, nb + 16 * c + 4 * h, a.N) : (float4_t){0.f, 0.f, 0.f, 0.f};
     }
 #pragma unroll
-    for (int i = 0; i < FM; ++i) sx[i] = a.sx[min(m0 + (wm * FM + i) * 16 + j, a.M - 1)];
+    for (int i = 0; i < FM; ++i) sx[i] = a.sx[min(mb + 16 * i + j, a.M - 1)];
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");    // every fragment is read
+    unsigned char* stage = smem + wave * (FM * 16 * FN * 32);
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-        const int m = m0 + (wm * FM + i) * 16 + j;
-        if (m >= a.M) continue;
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
-        for (int c = 0; c < FN; ++c)
-            if (nb + 16 * c < a.N) store4<E>(a, m, nb + 16 * c, acc[i][c], sx[i], sw[c], bias[c]);
-    }
+        for (int c = 0; c < FN; ++c) stage4<E, FN * 16>(stage, 16 * i + j, 16 * c + 4 * h, acc[i][c], sx[i], sw[c], bias[c]);
+    store_rows<FM * 16, FN * 16>(a, stage, mb, nb);
 }
 
 // ---------------------------------------------------------------------------
@@ -672,50 +725,21 @@ __global__ __launch_bounds__(512, 2) void k_w8a8_wide(Args a, int tiles) {
             aim(id + gridDim.x);
             begin();
         }
-        if ((a.N & 7) == 0) {
-            unsigned char* stage = smem + 2 * BUF + wave * STAGE;
+        unsigned char* stage = smem + 2 * BUF + wave * STAGE;
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
+        for (int q = 0; q < 2; ++q)
 #pragma unroll
-                for (int i0 = 0; i0 < 4; i0 += 2) {
-                    // row 16 i + j of 128 bytes, its 16-byte chunks XOR-ed by j & 7
+            for (int i0 = 0; i0 < 4; i0 += 2) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                        for (int p = 0; p < 2; ++p)
+                    for (int p = 0; p < 2; ++p)
 #pragma unroll
-                            for (int c = 0; c < 2; ++c) {
-                                float v[4];
-#pragma unroll
-                                for (int r = 0; r < 4; ++r)
-                                    v[r] = (float)acc[q][p][i0 + i][c][r] * (sx[q][i0 + i] * sw[p][c][r]) + bias[p][c][r];
-                                const int chunk = 4 * p + 2 * c + (h >> 1);
-                                *reinterpret_cast<uint2*>(stage + (16 * i + j) * 128 + ((chunk ^ (j & 7)) << 4) +
-                                                          8 * (h & 1)) =
-                                    make_uint2(pack2<E>(v[0], v[1]), pack2<E>(v[2], v[3]));
-                            }
-                    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) {  // 8 rows a store, whole lines
-                        const int r = 8 * g + lr, n = nb + 8 * (lane & 7), m = mb + 128 * q + 16 * i0 + r;
-                        const uint4 o = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
-                        if (m < a.M && n < a.N) *reinterpret_cast<uint4*>(a.y + (size_t)m * a.N + n) = o;
-                    }
-                    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-                }
-        } else {
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-                for (int p = 0; p < 2; ++p)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const int m = mb + 128 * q + 16 * i + j, n = nb + 32 * p + 16 * c + 4 * h;
-                            if (m < a.M && n < a.N) store4<E>(a, m, n, acc[q][p][i][c], sx[q][i], sw[p][c], bias[p][c]);
-                        }
-        }
+                        for (int c = 0; c < 2; ++c)
+                            stage4<E, 64>(stage, 16 * i + j, 32 * p + 16 * c + 4 * h, acc[q][p][i0 + i][c], sx[q][i0 + i],
+                                          sw[p][c], bias[p][c]);
+                store_rows<32, 64>(a, stage, mb + 128 * q + 16 * i0, nb);
+            }
     }
 }
 

@@ -14,8 +14,6 @@
 // layer norm takes its mean first and sums squares of differences, so nothing
 // cancels), and r' is rounded once on its way out while h goes on from the
 // fp32 value.  Chunks past the row's end hold zeros and take no part.
-#include <type_traits>
-
 #include "rows.h"
 
 namespace awq {
@@ -192,27 +190,36 @@ __global__ __launch_bounds__(NT) void k_quantize_rows(QuantArgs a) {
 }
 
 // Threads and chunks per thread of a row of `chunks` 16-byte chunks: one wave
-// for the narrow rows, 1024 threads where there are fewer rows than compute
-// units (a row's latency is the cost) or where 256 would hold more than 8.
+// for the narrow rows; 1024 threads where there are fewer rows than compute
+// units (a row's latency is the cost); else few enough threads that several
+// rows share a compute unit.  2048 x 16384: 54.7 us with 512 threads of 4
+// chunks, 61.7 with 1024 of 2; 8193 x 8192: 97.5 with 512 of 2, 98.8 with 256
+// of 4, 102.5 with 1024 of 1; 2048 x 4096: 14.0 with 256 of 2, 16.7 with 512 of 1.
+template <int NT, int C>
+struct Shape {
+    static constexpr int threads = NT, chunks = C;
+};
+
 template <class F>
 void pick_row(int chunks, int rows, int cus, F&& f) {
-    if (chunks <= 64) return f(std::integral_constant<int, 64>(), std::integral_constant<int, 1>());
-    if (chunks <= 128) return f(std::integral_constant<int, 64>(), std::integral_constant<int, 2>());
-    if (chunks <= 256) return f(std::integral_constant<int, 256>(), std::integral_constant<int, 1>());
-    if (chunks > 1024 || rows < cus) {
-        if (chunks <= 1024) return f(std::integral_constant<int, 1024>(), std::integral_constant<int, 1>());
-        if (chunks <= 2048) return f(std::integral_constant<int, 1024>(), std::integral_constant<int, 2>());
-        return f(std::integral_constant<int, 1024>(), std::integral_constant<int, 4>());
+    if (chunks <= 64) return f(Shape<64, 1>());
+    if (chunks <= 128) return f(Shape<64, 2>());
+    if (chunks <= 256) return f(Shape<256, 1>());
+    if (rows < cus) {
+        if (chunks <= 1024) return f(Shape<1024, 1>());
+        if (chunks <= 2048) return f(Shape<1024, 2>());
     }
-    if (chunks <= 512) return f(std::integral_constant<int, 256>(), std::integral_constant<int, 2>());
-    return f(std::integral_constant<int, 256>(), std::integral_constant<int, 4>());
+    if (chunks <= 512) return f(Shape<256, 2>());
+    if (chunks <= 1024) return f(Shape<512, 2>());
+    if (chunks <= 2048) return f(Shape<512, 4>());
+    return f(Shape<1024, 4>());
 }
 
 template <class E>
 int launch_norm_t(const NormArgs& a, int T, hipStream_t st) {
-    pick_row(a.H / 8, T, device_cu_count(), [&](auto nt, auto c) {
-        hipLaunchKernelGGL((k_norm<E, decltype(nt)::value, decltype(c)::value>), dim3(T),
-                           dim3(decltype(nt)::value), 0, st, a);
+    pick_row(a.H / 8, T, device_cu_count(), [&](auto shape) {
+        using S = decltype(shape);
+        hipLaunchKernelGGL((k_norm<E, S::threads, S::chunks>), dim3(T), dim3(S::threads), 0, st, a);
     });
     return (int)hipGetLastError();
 }
@@ -222,9 +229,9 @@ int launch_quantize_rows_t(const QuantArgs& a, int M, hipStream_t st) {
     if (a.K / 8 > 4096) {
         hipLaunchKernelGGL((k_quantize_rows<E, 1024, 1, true>), dim3(M), dim3(1024), 0, st, a);
     } else {
-        pick_row(a.K / 8, M, device_cu_count(), [&](auto nt, auto c) {
-            hipLaunchKernelGGL((k_quantize_rows<E, decltype(nt)::value, decltype(c)::value, false>), dim3(M),
-                               dim3(decltype(nt)::value), 0, st, a);
+        pick_row(a.K / 8, M, device_cu_count(), [&](auto shape) {
+            using S = decltype(shape);
+            hipLaunchKernelGGL((k_quantize_rows<E, S::threads, S::chunks, false>), dim3(M), dim3(S::threads), 0, st, a);
         });
     }
     return (int)hipGetLastError();

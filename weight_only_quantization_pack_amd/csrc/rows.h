@@ -106,37 +106,31 @@ struct RowScale {
     __device__ __forceinline__ float scale() const { return top / 127.0f; }
 };
 
-template <int NV>
-__device__ __forceinline__ void row_codes(const float* v, const RowScale& s, int* q) {
-    float k[NV];
+// Adding 1.5 * 2^23 rounds t (|t| <= 127) to an integer, ties to even, and leaves
+// it in the sum's low byte.
+__device__ __forceinline__ uint2 pack_codes8(const float* v, const RowScale& s) {
+    constexpr float kRound = 0x1.8p23f;
+    uint32_t k[8];
     float far = 0.0f;                              // largest distance from an integer
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const float t = v[i] * s.inv;
-        k[i] = __builtin_rintf(t);
-        far = fmaxf(far, fabsf(t - k[i]));
+    for (int i = 0; i < 8; ++i) {
+        const float t = v[i] * s.inv, r = t + kRound;
+        k[i] = __builtin_bit_cast(uint32_t, r);
+        far = fmaxf(far, fabsf(t - (r - kRound)));
     }
     const bool slow = far > 0.5f - 0x1p-14f || s.tiny;
     if (__builtin_amdgcn_ballot_w64(slow)) {
         if (slow) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                k[i] = s.top == 0.0f ? 0.0f : __builtin_rintf(v[i] * 127.0f / s.top);
+            for (int i = 0; i < 8; ++i)
+                k[i] = s.top == 0.0f ? 0u : __builtin_bit_cast(uint32_t, v[i] * 127.0f / s.top + kRound);
         }
     }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) q[i] = (int)fminf(fmaxf(k[i], -127.0f), 127.0f);
-}
-
-__device__ __forceinline__ uint32_t pack_bytes(const int* q) {
-    return (uint32_t)(q[0] & 255) | (uint32_t)(q[1] & 255) << 8 | (uint32_t)(q[2] & 255) << 16 |
-           (uint32_t)(q[3] & 255) << 24;
-}
-
-__device__ __forceinline__ uint2 pack_codes8(const float* v, const RowScale& s) {
-    int q[8];
-    row_codes<8>(v, s, q);
-    return make_uint2(pack_bytes(q), pack_bytes(q + 4));
+    auto bytes = [](const uint32_t* q) {           // the low bytes of four words
+        return __builtin_amdgcn_perm(__builtin_amdgcn_perm(q[3], q[2], 0x0C0C0400u),
+                                     __builtin_amdgcn_perm(q[1], q[0], 0x0C0C0400u), 0x05040100u);
+    };
+    return make_uint2(bytes(k), bytes(k + 4));
 }
 
 }  // namespace awq

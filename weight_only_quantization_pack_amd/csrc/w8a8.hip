@@ -119,13 +119,24 @@ __device__ __forceinline__ void store_rows(const Args& a, const unsigned char* s
                 *reinterpret_cast<uint4*>(a.y + (size_t)(m0 + r) * a.N + n0 + 8 * c) = o;
         }
     } else {
-        constexpr int RI = 64 / COLS;
-#pragma unroll 4
-        for (int g = 0; g < ROWS / RI; ++g) {
-            const int r = RI * g + lane / COLS, c = lane % COLS;
-            const uint16_t o = *reinterpret_cast<const uint16_t*>(
-                stage + r * (2 * COLS) + (((c >> 3) ^ row_xor<COLS>(r)) << 4) + (c & 7) * 2);
-            if (m0 + r < a.M && n0 + c < a.N) a.y[(size_t)(m0 + r) * a.N + n0 + c] = o;
+        constexpr int RI = 64 / COLS, AT = 8;                // rows of a store, stores at a time
+        const int c = lane % COLS;
+        uint16_t* y = a.y + (size_t)(m0 + lane / COLS) * a.N + n0 + c;
+        const bool in = n0 + c < a.N;
+#pragma unroll
+        for (int g0 = 0; g0 < ROWS / RI; g0 += AT) {
+            uint16_t o[AT];
+#pragma unroll
+            for (int g = 0; g < AT; ++g) {
+                const int r = RI * (g0 + g) + lane / COLS;
+                o[g] = *reinterpret_cast<const uint16_t*>(stage + r * (2 * COLS) +
+                                                          (((c >> 3) ^ row_xor<COLS>(r)) << 4) + (c & 7) * 2);
+            }
+#pragma unroll
+            for (int g = 0; g < AT; ++g) {
+                if (in && m0 + RI * (g0 + g) + lane / COLS < a.M) *y = o[g];
+                y += (size_t)RI * a.N;
+            }
         }
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");       // read before the next rows are written
@@ -776,12 +787,22 @@ Plan plan(int M, int N, int K) {
         p.blocks = (N + 16 * kBatchWaves - 1) / (16 * kBatchWaves);
         unit = AWQ_BATCH_KT;
         want = AWQ_BATCH_FILL * cus;
-    } else if ((long long)((M + 255) / 256) * ((N + 255) / 256) >= cus) {
-        p.kernel = WIDE;
-        p.blocks = ((M + 255) / 256) * ((N + 255) / 256);
     } else {
-        p.kernel = TILE;
-        p.blocks = ((M + 127) / 128) * ((N + 127) / 128);
+        // The tile whose rounds over the compute units take less: a 128-k step of
+        // a 256 x 256 tile takes 1.5 us and a tile 4 us besides, 0.62 and 3 us at
+        // 128 x 128 (342 x 6528 x 23735: 76 against 100 us, 4684 x 4160 x 1292: 54
+        // against 46)
+        const long long wide = (long long)((M + 255) / 256) * ((N + 255) / 256);
+        const long long tiles = (long long)((M + 127) / 128) * ((N + 127) / 128);
+        const int steps = (K + kStep - 1) / kStep;
+        const bool w = (wide + cus - 1) / cus * (5 * steps + 13) <= (tiles + cus - 1) / cus * (2 * steps + 10);
+        p.kernel = w ? WIDE : TILE;
+        p.blocks = (int)(w ? wide : tiles);
+        if (w) {
+            p.splits = 1;
+            p.steps = steps;
+            return p;
+        }
     }
     // fewer workgroups than compute units: cut K while a split keeps 16 steps
     const int total = (K + kStep - 1) / kStep;

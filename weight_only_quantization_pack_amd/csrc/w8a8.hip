@@ -11,17 +11,6 @@
 // n = 4 h + r, four consecutive outputs.
 #include "rows.h"
 
-#ifndef AWQ_T_WM
-#define AWQ_T_WM 2
-#define AWQ_T_WN 4
-#endif
-#ifndef AWQ_BATCH_S
-#define AWQ_BATCH_S 3
-#define AWQ_BATCH_KT 2
-#define AWQ_BATCH_OCC 4
-#define AWQ_BATCH_WV 4
-#define AWQ_BATCH_FILL 1
-#endif
 namespace awq {
 namespace {
 
@@ -157,11 +146,11 @@ __device__ __forceinline__ void tile_of(int id, int nTm, int nTn, int& tm, int& 
 }
 
 // ---------------------------------------------------------------------------
-// Few rows (M <= 4): HBM-bound on the weights, each read once.  A workgroup of
+// Few rows (up to 16): HBM-bound on the weights, each read once.  A workgroup of
 // 4 waves owns 16 columns; its waves take the K steps in turn, each through a
 // ring of U steps in flight, and their exact int32 sums meet in LDS.
 //
-// FUSED (16-bit rows that fit in registers): the workgroup quantizes the rows
+// FUSED (up to 4 16-bit rows that fit in registers): the workgroup quantizes the rows
 // itself, behind its first weight loads, and keeps the codes in LDS.
 // ---------------------------------------------------------------------------
 constexpr int kWaves = 4;
@@ -272,27 +261,30 @@ __global__ __launch_bounds__(64 * kWaves, 4) void k_w8a8_few(Args a) {
 }
 
 // ---------------------------------------------------------------------------
-// A decode batch (5 to 64 rows): HBM-bound on the weights, and the codes must
+// A decode batch (up to 64 rows): HBM-bound on the weights, and the codes must
 // not be read from L2 as often as they are (a 16-column workgroup that loads
 // its own codes moves as many bytes from L2 as from HBM: 8192 x 28672 at M = 16
 // 65 us, 47 us without those loads).  A workgroup of WV waves owns 16 WV
 // columns, one block of 16 per wave over the whole K (or one split of it); the
 // codes go through LDS for all of them.  S steps of KT * 128 k are in flight:
-// codes direct to LDS, weights to registers.
+// codes direct to LDS, weights to registers.  8 waves of 512-byte runs where
+// their workgroups nearly fill the compute units (8192 x 28672 at M = 16 / 64:
+// 46 / 54 us, 50 / 63 with the others), else 4 waves of 256-byte runs (4096 x
+// 11008: 13 / 18 us, 16 / 22).
 // ---------------------------------------------------------------------------
 template <int MT, int WV>
 struct BatchShape {
-    static constexpr int KT = AWQ_BATCH_KT;
+    static constexpr int KT = WV / 2;
     static constexpr int XW = MT * 2 * KT / WV;    // 8-row loads of a wave per step
     static constexpr int BUF = MT * 16 * KT * kStep;
     static constexpr int LPS = XW + 2 * KT;
-    static constexpr int S = AWQ_BATCH_S;
+    static constexpr int S = WV == 8 ? 3 : 4;
     static constexpr size_t LDS = (size_t)S * BUF;
     static_assert(XW * WV == MT * 2 * KT, "every wave loads the same number of row groups");
 };
 
 template <class E, int MT, int WV>
-__global__ __launch_bounds__(64 * WV, AWQ_BATCH_OCC) void k_w8a8_batch(Args a) {
+__global__ __launch_bounds__(64 * WV, WV == 8 ? 2 : 4) void k_w8a8_batch(Args a) {
     using T = BatchShape<MT, WV>;
     constexpr int KT = T::KT, S = T::S;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
@@ -770,23 +762,26 @@ __global__ __launch_bounds__(256) void k_w8a8_join(Args a, int splits) {
 enum Kernel { FEW, BATCH, TILE, WIDE };
 struct Plan {
     Kernel kernel;
+    int waves;                                     // BATCH
     int blocks, splits, steps;                     // workgroups per split, splits, K steps of each
 };
-
-constexpr int kFewRows = 4, kBatchRows = 64, kBatchWaves = AWQ_BATCH_WV;
 
 Plan plan(int M, int N, int K) {
     Plan p{};
     const int cus = device_cu_count();
-    int unit = 1, want = cus;
-    if (M <= kFewRows) {
+    const int total = (K + kStep - 1) / kStep;
+    const int small = (N + 63) / 64;               // 4-wave workgroups of a decode batch
+    int unit = 1;
+    // up to 4 rows; up to 16 also where a decode batch would split a short K
+    // (4096 x 4096 at M = 16: 7.5 against 10.2 us)
+    if (M <= 4 || (M <= 16 && 2 * small <= cus && total <= 48)) {
         p.kernel = FEW;
         p.blocks = (N + 15) / 16;
-    } else if (M <= kBatchRows) {
+    } else if (M <= 64) {
         p.kernel = BATCH;
-        p.blocks = (N + 16 * kBatchWaves - 1) / (16 * kBatchWaves);
-        unit = AWQ_BATCH_KT;
-        want = AWQ_BATCH_FILL * cus;
+        p.waves = (N + 127) / 128 >= cus * 3 / 4 ? 8 : 4;
+        p.blocks = p.waves == 8 ? (N + 127) / 128 : small;
+        unit = p.waves / 2;
     } else {
         // The tile whose rounds over the compute units take less: a 128-k step of
         // a 256 x 256 tile takes 1.5 us and a tile 4 us besides, 0.62 and 3 us at
@@ -794,22 +789,15 @@ Plan plan(int M, int N, int K) {
         // against 46)
         const long long wide = (long long)((M + 255) / 256) * ((N + 255) / 256);
         const long long tiles = (long long)((M + 127) / 128) * ((N + 127) / 128);
-        const int steps = (K + kStep - 1) / kStep;
-        const bool w = (wide + cus - 1) / cus * (5 * steps + 13) <= (tiles + cus - 1) / cus * (2 * steps + 10);
+        const bool w = (wide + cus - 1) / cus * (5 * total + 13) <= (tiles + cus - 1) / cus * (2 * total + 10);
         p.kernel = w ? WIDE : TILE;
         p.blocks = (int)(w ? wide : tiles);
-        if (w) {
-            p.splits = 1;
-            p.steps = steps;
-            return p;
-        }
     }
-    // fewer workgroups than compute units: cut K while a split keeps 16 steps
-    const int total = (K + kStep - 1) / kStep;
     p.splits = 1;
     p.steps = (total + unit - 1) / unit * unit;
-    if (p.blocks < want) {
-        const int s = min(want / p.blocks, total / 16);
+    // fewer workgroups than compute units: cut K while a split keeps 16 steps
+    if (p.kernel != WIDE && p.blocks < cus) {
+        const int s = min(cus / p.blocks, total / 16);
         if (s > 1) {
             p.steps = ((total + s - 1) / s + unit - 1) / unit * unit;
             p.splits = (total + p.steps - 1) / p.steps;
@@ -846,16 +834,21 @@ int launch_wide(const Args& a, const Plan& p, hipStream_t st) {
     return (int)hipGetLastError();
 }
 
-template <class E, int MT>
-int launch_batch(const Args& a, const Plan& p, hipStream_t st) {
-    using T = BatchShape<MT, kBatchWaves>;
-    auto kern = k_w8a8_batch<E, MT, kBatchWaves>;
+template <class E, int MT, int WV>
+int launch_batch_t(const Args& a, const Plan& p, hipStream_t st) {
+    using T = BatchShape<MT, WV>;
+    auto kern = k_w8a8_batch<E, MT, WV>;
     if (T::LDS > 48 * 1024)
         if (int e = (int)hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)T::LDS))
             return e;
-    hipLaunchKernelGGL(kern, dim3(p.blocks, p.splits), dim3(64 * kBatchWaves), T::LDS, st, a);
+    hipLaunchKernelGGL(kern, dim3(p.blocks, p.splits), dim3(64 * WV), T::LDS, st, a);
     return (int)hipGetLastError();
+}
+
+template <class E, int MT>
+int launch_batch(const Args& a, const Plan& p, hipStream_t st) {
+    return p.waves == 8 ? launch_batch_t<E, MT, 8>(a, p, st) : launch_batch_t<E, MT, 4>(a, p, st);
 }
 
 template <class E>
@@ -863,7 +856,7 @@ int launch_t(const Args& a, const Plan& p, hipStream_t st) {
     int e;
     if (p.kernel == FEW) e = a.rows ? launch_few<E, 4, true>(a, p, st) : launch_few<E, 4, false>(a, p, st);
     else if (p.kernel == WIDE) e = launch_wide<E>(a, p, st);
-    else if (p.kernel == TILE) e = launch_tile<E, 128, 128, AWQ_T_WM, AWQ_T_WN, 4>(a, p, st);
+    else if (p.kernel == TILE) e = launch_tile<E, 128, 128, 2, 4, 4>(a, p, st);
     else if (a.M <= 16) e = launch_batch<E, 1>(a, p, st);
     else if (a.M <= 32) e = launch_batch<E, 2>(a, p, st);
     else e = launch_batch<E, 4>(a, p, st);
@@ -875,7 +868,7 @@ int launch_t(const Args& a, const Plan& p, hipStream_t st) {
 
 // the decode product quantizes its rows itself
 bool fused_rows(const Plan& p, int M, int K) {
-    return p.kernel == FEW && p.splits == 1 && (M == 3 ? 4 : M) * (K / 8) <= kFusedChunks * 64 * kWaves;
+    return p.kernel == FEW && p.splits == 1 && M <= 4 && (M == 3 ? 4 : M) * (K / 8) <= kFusedChunks * 64 * kWaves;
 }
 
 size_t align16(size_t v) { return (v + 15) & ~(size_t)15; }

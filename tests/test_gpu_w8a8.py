@@ -85,7 +85,34 @@ def test_linear_w8a8(gpu, M, N, K, dtype):
     check(y, R.gemm_w8a8(qr, sr, w.cpu().numpy(), R.to_f64(sw), R.to_f64(bias)), bias)
 
 
-@pytest.mark.parametrize("M,N", [(1, 64), (64, 64), (300, 512)])
+# (M, N, K) that take the 256 x 256 tiles: one, three and four K steps, ragged last steps and edges, more tiles than
+# compute units (workgroups that take a second one), widths of 8-, 4- and 1-element alignment
+WIDE = [(4352, 4352, 128), (4097, 4360, 384), (4400, 4701, 272), (300, 30004, 1040), (2049, 16392, 16),
+        (8192, 4096, 528)]
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("M,N,K", WIDE)
+def test_gemm_w8a8_wide(gpu, M, N, K, dtype):
+    import torch
+    announce("gemm_w8a8 wide", f"M={M} N={N} K={K} {dtype}")
+    x, w = codes(M, K, 1), codes(N, K, 2)
+    sx, sw, bias = scales(M, 3, 0.02), scales(N, 4, 0.01 / np.sqrt(K)), scales(N, 5, 1.0)
+    y, raw, n = guarded_empty((M, N), dtype_of(dtype))
+    awq.gemm_w8a8(x, sx, w, sw, bias=bias, out=y)
+    again = awq.gemm_w8a8(x, sx, w, sw, bias=bias, dtype=dtype_of(dtype))
+    torch.cuda.synchronize()
+    assert sentinel_intact(raw, n)
+    assert torch.equal(y.view(torch.int16), again.view(torch.int16))
+    # integers below 2^31 in 64 bits on the GPU: the reference of every output, without 4 GB of host arrays
+    acc = torch.round(x.double() @ w.double().t())
+    ref = acc * sx.double()[:, None] * sw.double()[None, :] + bias.double()[None, :]
+    bound = (R.unit(y.dtype) + 2.0 ** -22) * ref.abs() + 2.0 ** -23 * bias.double().abs()[None, :] + 2.0 ** -24
+    worst = ((y.double() - ref).abs() / bound).max().item()
+    assert worst <= 1.0, f"{worst:.3f} of the bound"
+
+
+@pytest.mark.parametrize("M,N", [(1, 64), (12, 64), (64, 64), (300, 512)])
 def test_largest_sums_are_exact(gpu, M, N):
     """Codes at the ends of their range over the longest K: the sum stays below 2^31."""
     import torch

@@ -146,20 +146,152 @@ __device__ __forceinline__ void tile_of(int id, int nTm, int nTn, int& tm, int& 
 }
 
 // ---------------------------------------------------------------------------
-// Few rows (up to 16): HBM-bound on the weights, each read once.  A workgroup of
-// 4 waves owns 16 columns; its waves take the K steps in turn, each through a
-// ring of U steps in flight, and their exact int32 sums meet in LDS.
+// Up to 4 rows: HBM-bound on the weights, each read once.  No matrix
+// instruction: a lane multiplies 16 codes of a weight row with four
+// v_dot4_i32_i8, so a wave reads 1 KB of one row at a time (the matrix operand
+// takes 64 bytes of 16 rows: 4096 x 11008 11.3 against 13.2 us).  A wave owns R
+// columns, whose steps of 1024 k share each read of x from LDS, U steps in
+// flight; the lanes' exact sums are added at the end.  R = 2 for one row (4096 x
+// 4096 6.0 us, 6.8 at R = 4), 4 for more (4 rows of 4096 x 11008: 13.8 us, 14.4
+// at R = 2).
 //
-// FUSED (up to 4 16-bit rows that fit in registers): the workgroup quantizes the rows
-// itself, behind its first weight loads, and keeps the codes in LDS.
+// FUSED (16-bit rows that fit in registers): the workgroup quantizes the rows
+// itself, behind its first weight loads.
 // ---------------------------------------------------------------------------
 constexpr int kWaves = 4;
+constexpr int kRowStep = 1024;                     // k of a wave's load
+constexpr int kRowLds = 64 * 1024;                 // codes of a split, at most
 constexpr int kFusedChunks = 8;                    // 16-byte chunks of x a thread quantizes at most
+constexpr int row_columns(int rows) { return rows == 1 ? 2 : 4; }
 
-template <class E, int U, bool FUSED>
-__global__ __launch_bounds__(64 * kWaves, 4) void k_w8a8_few(Args a) {
+__device__ __forceinline__ int sum_lanes(int v) {
+    struct Add {
+        __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const { return a + b; }
+    };
+    return (int)wave_reduce((uint32_t)v, Add());
+}
+
+template <class E, int MR, bool FUSED>
+__global__ __launch_bounds__(64 * kWaves, 4) void k_w8a8_row(Args a) {
+    constexpr int R = row_columns(MR), U = 8 / R;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     __shared__ uint32_t slots[kWaves];
+    const int tid = threadIdx.x;
+    const int lane = tid & 63, wave = tid >> 6;
+    const int n0 = __builtin_amdgcn_readfirstlane(((int)blockIdx.x * kWaves + wave) * R);
+    const int kb = blockIdx.y * a.steps * kStep, ke = min(a.K, kb + a.steps * kStep);      // of this split
+    const int steps = (ke - kb + kRowStep - 1) / kRowStep, stride = steps * kRowStep;
+    const size_t K = (size_t)a.K;
+    const __amdgpu_buffer_rsrc_t rw =
+        make_rsrc(a.w + (size_t)min(n0, a.N - 1) * K, (size_t)max(0, min(R, a.N - n0)) * K);
+    int4_t w[U][R];
+    auto load = [&](int step, int u) {
+        const int k = kb + step * kRowStep + 16 * lane;
+#pragma unroll
+        for (int r = 0; r < R; ++r) w[u][r] = load16(rw, k < ke ? (uint32_t)r * (uint32_t)a.K + (uint32_t)k : kOutOfRange);
+    };
+#pragma unroll
+    for (int u = 0; u < U; ++u) load(u, u);
+
+    // the codes [MR][stride]; what lies past the split's end meets zero weights
+    float sx[MR];
+    if constexpr (FUSED) {
+        constexpr int WPR = kWaves / MR, per = 64 * WPR;     // waves and threads of a row
+        const int row = wave / WPR, t = tid - row * per;
+        const int chunks = a.K / 8;
+        uint4 x[kFusedChunks];
+#pragma unroll
+        for (int c = 0; c < kFusedChunks; ++c) {
+            const int i = t + per * c;
+            x[c] = row < a.M && i < chunks ? a.rows[(size_t)row * chunks + i] : make_uint4(0, 0, 0, 0);
+        }
+        float v[8];
+        uint32_t top = 0;
+#pragma unroll
+        for (int c = 0; c < kFusedChunks; ++c) {
+            if (per * c >= chunks) continue;       // uniform
+            unpack8<E>(x[c], v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = max(top, abs_bits(v[e]));
+        }
+        top = wave_reduce(top, MaxU32());
+        if (lane == 0) slots[wave] = top;
+        __syncthreads();
+        uint32_t tops[MR];
+#pragma unroll
+        for (int m = 0; m < MR; ++m) {
+            tops[m] = slots[m * WPR];
+#pragma unroll
+            for (int q = 1; q < WPR; ++q) tops[m] = max(tops[m], slots[m * WPR + q]);
+            sx[m] = RowScale(tops[m]).scale();
+            if (m == row) top = tops[m];
+        }
+        const RowScale s(top);
+#pragma unroll
+        for (int c = 0; c < kFusedChunks; ++c) {
+            const int i = t + per * c;
+            if (per * c < chunks && i < chunks) {
+                unpack8<E>(x[c], v);
+                *reinterpret_cast<uint2*>(smem + row * stride + 8 * i) = pack_codes8(v, s);
+            }
+        }
+    } else {
+        const int chunks = (ke - kb) / 16;
+        for (int i = tid; i < MR * chunks; i += 64 * kWaves) {
+            const int m = i / chunks, c = i - m * chunks;
+            if (m < a.M)
+                *reinterpret_cast<int4_t*>(smem + m * stride + 16 * c) =
+                    *reinterpret_cast<const int4_t*>(a.x + (size_t)m * K + kb + 16 * c);
+        }
+#pragma unroll
+        for (int m = 0; m < MR; ++m) sx[m] = a.part ? 0.0f : a.sx[min(m, a.M - 1)];
+    }
+    __syncthreads();
+
+    int acc[MR][R] = {};
+    for (int i0 = 0; i0 < steps; i0 += U) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (i0 + u < steps) {                  // wave-uniform
+#pragma unroll
+                for (int m = 0; m < MR; ++m) {
+                    const int4_t x = *reinterpret_cast<const int4_t*>(smem + m * stride + (i0 + u) * kRowStep + 16 * lane);
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) acc[m][r] = __builtin_amdgcn_sdot4(w[u][r][q], x[q], acc[m][r], false);
+                }
+            }
+            load(i0 + u + U, u);
+        }
+    }
+    // lane 4 m + r keeps the sum of row m and column n0 + r
+    int sum = 0;
+    float scale = 0.0f;
+#pragma unroll
+    for (int m = 0; m < MR; ++m)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int v = sum_lanes(acc[m][r]);
+            if (lane == R * m + r) { sum = v; scale = sx[m]; }
+        }
+    const int m = lane / R, n = n0 + lane % R;
+    if (m >= a.M || lane >= MR * R || n >= a.N) return;
+    if (a.part) {
+        a.part[((size_t)blockIdx.y * a.M + m) * a.N + n] = sum;
+    } else {
+        const float v = (float)sum * (scale * a.sw[n]) + (a.bias ? a.bias[n] : 0.0f);
+        a.y[(size_t)m * a.N + n] = E::store(v);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Up to 16 rows of a short product: a workgroup of 4 waves owns 16 columns; its
+// waves take the K steps in turn, each through a ring of U steps in flight with
+// the codes straight from L2, and their exact int32 sums meet in LDS.
+// ---------------------------------------------------------------------------
+template <class E, int U>
+__global__ __launch_bounds__(64 * kWaves, 4) void k_w8a8_few(Args a) {
     __shared__ int4_t red[kWaves][64];
     const int tid = threadIdx.x;
     const int lane = tid & 63, wave = tid >> 6;
@@ -171,9 +303,9 @@ __global__ __launch_bounds__(64 * kWaves, 4) void k_w8a8_few(Args a) {
     const int nw = wave < mine ? (mine - wave + kWaves - 1) / kWaves : 0;
     const size_t K = (size_t)a.K;
     const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.w + (size_t)n0 * K, (size_t)min(16, a.N - n0) * K);
-    const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x, FUSED ? 0 : (size_t)a.M * K);
+    const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x, (size_t)a.M * K);
 
-    int4_t w[U][2], x[FUSED ? 1 : U][2];
+    int4_t w[U][2], x[U][2];
     auto load = [&](int i, int u) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
@@ -181,70 +313,18 @@ __global__ __launch_bounds__(64 * kWaves, 4) void k_w8a8_few(Args a) {
             // rows past N or M are past the buffers' ends
             const uint32_t off = i < nw && k < a.K ? (uint32_t)j * (uint32_t)a.K + (uint32_t)k : kOutOfRange;
             w[u][s] = load16(rw, off);
-            if constexpr (!FUSED) x[u][s] = load16(rx, off);
+            x[u][s] = load16(rx, off);
         }
     };
 #pragma unroll
     for (int u = 0; u < U; ++u) load(u, u);
-
-    // FUSED: 1, 2 or 4 rows (MP), kWaves / MP waves a row
-    float* sxs = reinterpret_cast<float*>(slots);
-    const int xstride = total * kStep + 16;
-    if constexpr (FUSED) {
-        const int MP = a.M > 2 ? 4 : a.M;
-        const int per = 64 * kWaves / MP;          // threads per row
-        const int row = tid / per, t = tid - row * per;
-        const int chunks = a.K / 8;
-        uint4 r[kFusedChunks];
-#pragma unroll
-        for (int c = 0; c < kFusedChunks; ++c) {
-            const int i = t + per * c;
-            r[c] = row < a.M && i < chunks ? a.rows[(size_t)row * chunks + i] : make_uint4(0, 0, 0, 0);
-        }
-        float v[8];
-        uint32_t top = 0;
-#pragma unroll
-        for (int c = 0; c < kFusedChunks; ++c) {
-            unpack8<E>(r[c], v);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) top = max(top, abs_bits(v[e]));
-        }
-        top = wave_reduce(top, MaxU32());
-        if (lane == 0) slots[wave] = top;
-        __syncthreads();
-        const int wpr = kWaves / MP;
-        top = 0;
-        for (int q = 0; q < wpr; ++q) top = max(top, slots[row * wpr + q]);
-        const RowScale s(top);
-        unsigned char* xr = smem + row * xstride;
-#pragma unroll
-        for (int c = 0; c < kFusedChunks; ++c) {
-            const int i = t + per * c;
-            // the last step ends past K: the chunks there are zero
-            if (row < a.M && i < total * (kStep / 8)) {
-                unpack8<E>(r[c], v);
-                *reinterpret_cast<uint2*>(xr + 8 * i) = pack_codes8(v, s);
-            }
-        }
-        __syncthreads();                           // codes complete, slots read
-        if (t == 0) sxs[row] = s.scale();
-    }
-
     int4_t acc = {0, 0, 0, 0};
     for (int i0 = 0; i0 < nw; i0 += U) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (i0 + u < nw) {                     // wave-uniform
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    int4_t xv;
-                    if constexpr (FUSED)
-                        xv = *reinterpret_cast<const int4_t*>(
-                            smem + (j < a.M ? j : 0) * xstride + (wave + kWaves * (i0 + u)) * kStep + 64 * s + 16 * h);
-                    else
-                        xv = x[u][s];
-                    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[u][s], xv, acc, 0, 0, 0);
-                }
+                for (int s = 0; s < 2; ++s) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[u][s], x[u][s], acc, 0, 0, 0);
             }
             load(i0 + u + U, u);
         }
@@ -256,7 +336,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void k_w8a8_few(Args a) {
     for (int q = 1; q < kWaves; ++q) acc += red[q][lane];
     const int n = n0 + 4 * h;
     if (j < a.M && n < a.N)
-        store4<E>(a, j, n, acc, a.part ? 0.0f : FUSED ? sxs[j] : a.sx[j], load4(a.sw, n, a.N),
+        store4<E>(a, j, n, acc, a.part ? 0.0f : a.sx[j], load4(a.sw, n, a.N),
                   a.bias ? load4(a.bias, n, a.N) : (float4_t){0.f, 0.f, 0.f, 0.f});
 }
 
@@ -759,21 +839,44 @@ __global__ __launch_bounds__(256) void k_w8a8_join(Args a, int splits) {
 }
 
 // how a product is cut: the kernel, its tile and the K splits
-enum Kernel { FEW, BATCH, TILE, WIDE };
+enum Kernel { ROW, FEW, BATCH, TILE, WIDE };
 struct Plan {
     Kernel kernel;
     int waves;                                     // BATCH
     int blocks, splits, steps;                     // workgroups per split, splits, K steps of each
 };
 
+// k_w8a8_row: its rows (1, 2 or 4) and the LDS of a split's codes
+int row_rows(int M) { return M > 2 ? 4 : M; }
+int row_lds(int M, int steps) { return row_rows(M) * ((steps * kStep + kRowStep - 1) / kRowStep * kRowStep); }
+
+// K cut into splits of at least 16 steps, in units of `unit` steps, where there
+// are fewer workgroups than compute units
+void split(Plan& p, int total, int unit, int cus) {
+    p.splits = 1;
+    p.steps = (total + unit - 1) / unit * unit;
+    if (p.blocks >= cus) return;
+    const int s = min(cus / p.blocks, total / 16);
+    if (s <= 1) return;
+    p.steps = ((total + s - 1) / s + unit - 1) / unit * unit;
+    p.splits = (total + p.steps - 1) / p.steps;
+}
+
 Plan plan(int M, int N, int K) {
     Plan p{};
-    const int cus = device_cu_count();
+    int cus = device_cu_count();
     const int total = (K + kStep - 1) / kStep;
     const int small = (N + 63) / 64;               // 4-wave workgroups of a decode batch
     int unit = 1;
-    // up to 4 rows; up to 16 also where a decode batch would split a short K
-    // (4096 x 4096 at M = 16: 7.5 against 10.2 us)
+    if (M <= 4) {
+        const int cols = kWaves * row_columns(row_rows(M));
+        p.kernel = ROW;
+        p.blocks = (N + cols - 1) / cols;
+        split(p, total, 1, cus);
+        if (row_lds(M, p.steps) <= kRowLds) return p;
+    }
+    // up to 16 rows where the codes of 4 do not fit in LDS, or a decode batch would
+    // split a short K (4096 x 4096 at M = 16: 7.5 against 10.2 us)
     if (M <= 4 || (M <= 16 && 2 * small <= cus && total <= 48)) {
         p.kernel = FEW;
         p.blocks = (N + 15) / 16;
@@ -792,24 +895,27 @@ Plan plan(int M, int N, int K) {
         const bool w = (wide + cus - 1) / cus * (5 * total + 13) <= (tiles + cus - 1) / cus * (2 * total + 10);
         p.kernel = w ? WIDE : TILE;
         p.blocks = (int)(w ? wide : tiles);
+        if (w) cus = 0;                            // no splits
     }
-    p.splits = 1;
-    p.steps = (total + unit - 1) / unit * unit;
-    // fewer workgroups than compute units: cut K while a split keeps 16 steps
-    if (p.kernel != WIDE && p.blocks < cus) {
-        const int s = min(cus / p.blocks, total / 16);
-        if (s > 1) {
-            p.steps = ((total + s - 1) / s + unit - 1) / unit * unit;
-            p.splits = (total + p.steps - 1) / p.steps;
-        }
-    }
+    split(p, total, unit, cus);
     return p;
 }
 
-template <class E, int U, bool FUSED>
+template <class E, int MR>
+int launch_row(const Args& a, const Plan& p, hipStream_t st) {
+    auto kern = a.rows ? k_w8a8_row<E, MR, true> : k_w8a8_row<E, MR, false>;
+    const int lds = row_lds(MR, p.steps);
+    if (lds > 48 * 1024)
+        if (int e = (int)hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, lds))
+            return e;
+    hipLaunchKernelGGL(kern, dim3(p.blocks, p.splits), dim3(64 * kWaves), lds, st, a);
+    return (int)hipGetLastError();
+}
+
+template <class E>
 int launch_few(const Args& a, const Plan& p, hipStream_t st) {
-    const size_t lds = FUSED ? (size_t)a.M * ((size_t)(a.K + kStep - 1) / kStep * kStep + 16) : 0;
-    hipLaunchKernelGGL((k_w8a8_few<E, U, FUSED>), dim3(p.blocks, p.splits), dim3(64 * kWaves), lds, st, a);
+    hipLaunchKernelGGL((k_w8a8_few<E, 4>), dim3(p.blocks, p.splits), dim3(64 * kWaves), 0, st, a);
     return (int)hipGetLastError();
 }
 
@@ -854,7 +960,9 @@ int launch_batch(const Args& a, const Plan& p, hipStream_t st) {
 template <class E>
 int launch_t(const Args& a, const Plan& p, hipStream_t st) {
     int e;
-    if (p.kernel == FEW) e = a.rows ? launch_few<E, 4, true>(a, p, st) : launch_few<E, 4, false>(a, p, st);
+    if (p.kernel == ROW) e = a.M == 1 ? launch_row<E, 1>(a, p, st) : a.M == 2 ? launch_row<E, 2>(a, p, st)
+                                                                              : launch_row<E, 4>(a, p, st);
+    else if (p.kernel == FEW) e = launch_few<E>(a, p, st);
     else if (p.kernel == WIDE) e = launch_wide<E>(a, p, st);
     else if (p.kernel == TILE) e = launch_tile<E, 128, 128, 2, 4, 4>(a, p, st);
     else if (a.M <= 16) e = launch_batch<E, 1>(a, p, st);
@@ -868,7 +976,7 @@ int launch_t(const Args& a, const Plan& p, hipStream_t st) {
 
 // the decode product quantizes its rows itself
 bool fused_rows(const Plan& p, int M, int K) {
-    return p.kernel == FEW && p.splits == 1 && M <= 4 && (M == 3 ? 4 : M) * (K / 8) <= kFusedChunks * 64 * kWaves;
+    return p.kernel == ROW && p.splits == 1 && row_rows(M) * (K / 8) <= kFusedChunks * 64 * kWaves;
 }
 
 size_t align16(size_t v) { return (v + 15) & ~(size_t)15; }

@@ -48,7 +48,10 @@ SHAPES = [(1, 1, 16), (1, 64, 128), (1, 4096, 4096), (1, 37, 28672), (2, 1000, 4
           (4, 300, 8192), (5, 96, 240), (13, 50, 2048), (16, 600, 1408), (17, 70, 11008), (31, 515, 4096),
           (33, 1030, 2160), (64, 256, 4096), (64, 48, 28672), (65, 300, 512), (127, 1000, 1024),
           (130, 257, 4096), (256, 256, 128), (257, 515, 1040), (509, 1024, 4096), (1000, 4100, 640),
-          (2048, 2048, 512), (4100, 300, 8192)]
+          (2048, 2048, 512), (4100, 300, 8192),
+          # workgroups of 8 waves for every compute unit at 5 to 64 rows, and codes that are split to fit in LDS
+          (5, 24577, 144), (16, 24600, 256), (33, 24577, 272), (64, 24640, 528), (3, 4200, 28672), (4, 4096, 20496),
+          (2, 2050, 65552), (1, 4099, 65568)]
 
 
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])

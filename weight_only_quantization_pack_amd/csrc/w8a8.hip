@@ -149,20 +149,27 @@ __device__ __forceinline__ void tile_of(int id, int nTm, int nTn, int& tm, int& 
 // Up to 4 rows: HBM-bound on the weights, each read once.  No matrix
 // instruction: a lane multiplies 16 codes of a weight row with four
 // v_dot4_i32_i8, so a wave reads 1 KB of one row at a time (the matrix operand
-// takes 64 bytes of 16 rows: 4096 x 11008 11.3 against 13.2 us).  A wave owns R
-// columns, whose steps of 1024 k share each read of x from LDS, U steps in
-// flight; the lanes' exact sums are added at the end.  R = 2 for one row (4096 x
-// 4096 6.0 us, 6.8 at R = 4), 4 for more (4 rows of 4096 x 11008: 13.8 us, 14.4
-// at R = 2).
+// takes 64 bytes of 16 rows: 4096 x 11008 at M = 1 / 4 14.5 / 14.8 us).  A wave
+// owns R columns, whose steps of 1024 k share each read of x from LDS, U steps
+// in flight; the lanes' exact sums are added at the end.
 //
-// FUSED (16-bit rows that fit in registers): the workgroup quantizes the rows
-// itself, behind its first weight loads.
+// What a workgroup does before its first product counts: the codes go direct to
+// LDS, asked for before the weights, since loads return in order (4096 x 11008
+// at M = 1 / 4: 12.3 us, 3.7 TB/s / 13.4 us, 13.2 / 17.9 with codes through
+// registers behind the weights).  R = 2 keeps two workgroups on a compute unit
+// there (R = 4: 14.5 at M = 4).  Codes of more than 64 KB are split along K
+// (28672 x 20480 at M = 4: 110 us, 119 on 16-row operands).
+//
+// FUSED (one or two 16-bit rows that fit in registers): the workgroup quantizes
+// the rows itself (4096 x 11008 at M = 1: 12.2 us, 15.7 with a launch of its own;
+// 4 rows of 4096 x 4096: 9.1 and 9.4, so only up to two).
 // ---------------------------------------------------------------------------
 constexpr int kWaves = 4;
 constexpr int kRowStep = 1024;                     // k of a wave's load
 constexpr int kRowLds = 64 * 1024;                 // codes of a split, at most
+constexpr int kFusedRows = 2;
 constexpr int kFusedChunks = 8;                    // 16-byte chunks of x a thread quantizes at most
-constexpr int row_columns(int rows) { return rows == 1 ? 2 : 4; }
+constexpr int kRowColumns = 2;                     // of a wave
 
 __device__ __forceinline__ int sum_lanes(int v) {
     struct Add {
@@ -173,38 +180,52 @@ __device__ __forceinline__ int sum_lanes(int v) {
 
 template <class E, int MR, bool FUSED>
 __global__ __launch_bounds__(64 * kWaves, 4) void k_w8a8_row(Args a) {
-    constexpr int R = row_columns(MR), U = 8 / R;
+    constexpr int R = kRowColumns, U = 4;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     __shared__ uint32_t slots[kWaves];
     const int tid = threadIdx.x;
-    const int lane = tid & 63, wave = tid >> 6;
-    const int n0 = __builtin_amdgcn_readfirstlane(((int)blockIdx.x * kWaves + wave) * R);
+    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int n0 = ((int)blockIdx.x * kWaves + wave) * R;
     const int kb = blockIdx.y * a.steps * kStep, ke = min(a.K, kb + a.steps * kStep);      // of this split
     const int steps = (ke - kb + kRowStep - 1) / kRowStep, stride = steps * kRowStep;
     const size_t K = (size_t)a.K;
-    const __amdgpu_buffer_rsrc_t rw =
-        make_rsrc(a.w + (size_t)min(n0, a.N - 1) * K, (size_t)max(0, min(R, a.N - n0)) * K);
+    // the size in a scalar register: a descriptor in vector registers costs every load a loop
+    const int columns = __builtin_amdgcn_readfirstlane(max(0, min(R, a.N - n0)));
+    const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.w + (size_t)min(n0, a.N - 1) * K, (size_t)columns * K);
     int4_t w[U][R];
     auto load = [&](int step, int u) {
         const int k = kb + step * kRowStep + 16 * lane;
 #pragma unroll
         for (int r = 0; r < R; ++r) w[u][r] = load16(rw, k < ke ? (uint32_t)r * (uint32_t)a.K + (uint32_t)k : kOutOfRange);
     };
-#pragma unroll
-    for (int u = 0; u < U; ++u) load(u, u);
-
-    // the codes [MR][stride]; what lies past the split's end meets zero weights
-    float sx[MR];
+    // The codes [MR][stride], first: loads return in order, and the weights take
+    // longer.  What lies past the split's end meets zero weights.
+    constexpr int WPR = kWaves / MR, per = 64 * WPR;         // waves and threads of a row
+    const int row = wave / WPR, t = tid - row * per;
+    const int chunks = a.K / 8;
+    uint4 x[kFusedChunks];
     if constexpr (FUSED) {
-        constexpr int WPR = kWaves / MR, per = 64 * WPR;     // waves and threads of a row
-        const int row = wave / WPR, t = tid - row * per;
-        const int chunks = a.K / 8;
-        uint4 x[kFusedChunks];
 #pragma unroll
         for (int c = 0; c < kFusedChunks; ++c) {
             const int i = t + per * c;
             x[c] = row < a.M && i < chunks ? a.rows[(size_t)row * chunks + i] : make_uint4(0, 0, 0, 0);
         }
+    } else {
+        const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x, (size_t)a.M * K);
+#pragma unroll
+        for (int m = 0; m < MR; ++m)
+            for (int i = wave; i < steps; i += kWaves) {
+                const int k = kb + i * kRowStep + 16 * lane;
+                load16_lds(rx, smem + m * stride + i * kRowStep,
+                           k < ke ? (uint32_t)m * (uint32_t)a.K + (uint32_t)k : kOutOfRange, 0);
+            }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) load(u, u);
+    __builtin_amdgcn_sched_barrier(0);
+    float sx[MR];
+    if constexpr (FUSED) {
         float v[8];
         uint32_t top = 0;
 #pragma unroll
@@ -235,18 +256,15 @@ __global__ __launch_bounds__(64 * kWaves, 4) void k_w8a8_row(Args a) {
                 *reinterpret_cast<uint2*>(smem + row * stride + 8 * i) = pack_codes8(v, s);
             }
         }
+        __syncthreads();
     } else {
-        const int chunks = (ke - kb) / 16;
-        for (int i = tid; i < MR * chunks; i += 64 * kWaves) {
-            const int m = i / chunks, c = i - m * chunks;
-            if (m < a.M)
-                *reinterpret_cast<int4_t*>(smem + m * stride + 16 * c) =
-                    *reinterpret_cast<const int4_t*>(a.x + (size_t)m * K + kb + 16 * c);
-        }
+        // the codes have landed, the weights need not have
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(U * R));
+        asm volatile("s_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int m = 0; m < MR; ++m) sx[m] = a.part ? 0.0f : a.sx[min(m, a.M - 1)];
     }
-    __syncthreads();
 
     int acc[MR][R] = {};
     for (int i0 = 0; i0 < steps; i0 += U) {
@@ -265,7 +283,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void k_w8a8_row(Args a) {
             load(i0 + u + U, u);
         }
     }
-    // lane 4 m + r keeps the sum of row m and column n0 + r
+    // lane R m + r keeps the sum of row m and column n0 + r
     int sum = 0;
     float scale = 0.0f;
 #pragma unroll
@@ -286,9 +304,10 @@ __global__ __launch_bounds__(64 * kWaves, 4) void k_w8a8_row(Args a) {
 }
 
 // ---------------------------------------------------------------------------
-// Up to 16 rows of a short product: a workgroup of 4 waves owns 16 columns; its
-// waves take the K steps in turn, each through a ring of U steps in flight with
-// the codes straight from L2, and their exact int32 sums meet in LDS.
+// 5 to 16 rows of a short product (4096 x 4096 at M = 16: 7.9 us, 2.1 TB/s): a
+// workgroup of 4 waves owns 16 columns; its waves take the K steps in turn, each
+// through a ring of U steps in flight with the codes straight from L2, and their
+// exact int32 sums meet in LDS.
 // ---------------------------------------------------------------------------
 template <class E, int U>
 __global__ __launch_bounds__(64 * kWaves, 4) void k_w8a8_few(Args a) {
@@ -378,7 +397,8 @@ __global__ __launch_bounds__(64 * WV, WV == 8 ? 2 : 4) void k_w8a8_batch(Args a)
     const int steps = (min(total - k0, a.steps) + KT - 1) / KT;
     const size_t K = (size_t)a.K;
     const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x, (size_t)a.M * K);
-    const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.w + (size_t)min(n0, a.N - 1) * K, (size_t)max(0, min(16, a.N - n0)) * K);
+    const int columns = __builtin_amdgcn_readfirstlane(max(0, min(16, a.N - n0)));      // in a scalar register
+    const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.w + (size_t)min(n0, a.N - 1) * K, (size_t)columns * K);
 
     // a load fills 8 rows of 128 bytes, chunk l & 7 of row l >> 3 from the row's
     // chunk (l & 7) ^ (row & 6); rows past M are past the buffer's end
@@ -465,10 +485,16 @@ __global__ __launch_bounds__(64 * WV, WV == 8 ? 2 : 4) void k_w8a8_batch(Args a)
 __device__ __forceinline__ int chunk_swizzle(int r) { return r & 6; }
 
 // ---------------------------------------------------------------------------
-// Many rows, fewer than 256 x 256 tiles for every compute unit: TM x TN output
+// Many rows, too few for 256 x 256 tiles on every compute unit: TM x TN output
 // tiles, WM x WN waves.  Both operands go through LDS in steps of 128 k, S steps
 // in flight as direct-to-LDS loads; a wave reads the fragments of step t + 1
 // while the MFMAs of step t run.
+//
+// 512 x 6144 x 4096: 19.3 us (1340 TOP/s) for 192 tiles on 256 compute units.  A
+// step takes 0.50 us against 0.21 of MFMA: a 128 x 128 tile reads twice the bytes
+// of a 256 x 256 tile for each product, and the barrier of a step is met by all 8
+// waves at once.  Two workgroups of 4 waves on a compute unit, and tiles of 64
+// rows, took longer.
 // ---------------------------------------------------------------------------
 template <class E, int TM, int TN, int WM, int WN, int S>
 __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_w8a8_tile(Args a) {
@@ -616,7 +642,8 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_w8a8_tile(Args a)
 
 // ---------------------------------------------------------------------------
 // 256 x 256 tiles of the largest products, 8 waves, one workgroup per compute
-// unit that takes tile after tile.
+// unit that takes tile after tile.  8192 x 4096 x 14336: 367 us (2620 TOP/s),
+// MFMAs running 66 % of the time; the clock is then below its limit (1.9 GHz).
 //
 // Steps of 128 k (whole 128-byte lines of every row), two of them in LDS, each
 // as four half tiles of 128 rows: X0, X1, W0, W1.  A wave computes 64 rows of
@@ -849,14 +876,14 @@ struct Plan {
 // k_w8a8_row: its rows (1, 2 or 4) and the LDS of a split's codes
 int row_rows(int M) { return M > 2 ? 4 : M; }
 int row_lds(int M, int steps) { return row_rows(M) * ((steps * kStep + kRowStep - 1) / kRowStep * kRowStep); }
+int row_steps(int M) { return kRowLds / row_rows(M) / kStep; }       // K steps whose codes fit
 
-// K cut into splits of at least 16 steps, in units of `unit` steps, where there
-// are fewer workgroups than compute units
-void split(Plan& p, int total, int unit, int cus) {
+// K cut into `splits` at least, or more of at least 16 steps where there are
+// fewer workgroups than compute units, in units of `unit` steps
+void split(Plan& p, int total, int splits, int unit, int cus) {
     p.splits = 1;
     p.steps = (total + unit - 1) / unit * unit;
-    if (p.blocks >= cus) return;
-    const int s = min(cus / p.blocks, total / 16);
+    const int s = max(splits, min(cus / p.blocks, total / 16));
     if (s <= 1) return;
     p.steps = ((total + s - 1) / s + unit - 1) / unit * unit;
     p.splits = (total + p.steps - 1) / p.steps;
@@ -869,15 +896,14 @@ Plan plan(int M, int N, int K) {
     const int small = (N + 63) / 64;               // 4-wave workgroups of a decode batch
     int unit = 1;
     if (M <= 4) {
-        const int cols = kWaves * row_columns(row_rows(M));
+        const int cols = kWaves * kRowColumns;
         p.kernel = ROW;
         p.blocks = (N + cols - 1) / cols;
-        split(p, total, 1, cus);
-        if (row_lds(M, p.steps) <= kRowLds) return p;
+        split(p, total, (total + row_steps(M) - 1) / row_steps(M), 1, cus);
+        return p;
     }
-    // up to 16 rows where the codes of 4 do not fit in LDS, or a decode batch would
-    // split a short K (4096 x 4096 at M = 16: 7.5 against 10.2 us)
-    if (M <= 4 || (M <= 16 && 2 * small <= cus && total <= 48)) {
+    // a short K that a decode batch would split (4096 x 4096 at M = 16: 7.9 against 10.2 us)
+    if (M <= 16 && 2 * small <= cus && total <= 48) {
         p.kernel = FEW;
         p.blocks = (N + 15) / 16;
     } else if (M <= 64) {
@@ -897,13 +923,15 @@ Plan plan(int M, int N, int K) {
         p.blocks = (int)(w ? wide : tiles);
         if (w) cus = 0;                            // no splits
     }
-    split(p, total, unit, cus);
+    split(p, total, 1, unit, cus);
     return p;
 }
 
 template <class E, int MR>
 int launch_row(const Args& a, const Plan& p, hipStream_t st) {
-    auto kern = a.rows ? k_w8a8_row<E, MR, true> : k_w8a8_row<E, MR, false>;
+    auto kern = k_w8a8_row<E, MR, false>;
+    if constexpr (MR <= kFusedRows)
+        if (a.rows) kern = k_w8a8_row<E, MR, true>;
     const int lds = row_lds(MR, p.steps);
     if (lds > 48 * 1024)
         if (int e = (int)hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
@@ -976,7 +1004,7 @@ int launch_t(const Args& a, const Plan& p, hipStream_t st) {
 
 // the decode product quantizes its rows itself
 bool fused_rows(const Plan& p, int M, int K) {
-    return p.kernel == ROW && p.splits == 1 && row_rows(M) * (K / 8) <= kFusedChunks * 64 * kWaves;
+        return p.kernel == ROW && p.splits == 1 && M <= kFusedRows && M * (K / 8) <= kFusedChunks * 64 * kWaves;
 }
 
 size_t align16(size_t v) { return (v + 15) & ~(size_t)15; }

@@ -304,7 +304,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void k_w8a8_row(Args a) {
 }
 
 // ---------------------------------------------------------------------------
-// 5 to 16 rows of a short product (4096 x 4096 at M = 16: 7.9 us, 2.1 TB/s): a
+// 5 to 16 rows of a short product (4096 x 4096 at M = 16: 7.5 us, 2.2 TB/s): a
 // workgroup of 4 waves owns 16 columns; its waves take the K steps in turn, each
 // through a ring of U steps in flight with the codes straight from L2, and their
 // exact int32 sums meet in LDS.
@@ -360,26 +360,31 @@ __global__ __launch_bounds__(64 * kWaves, 4) void k_w8a8_few(Args a) {
 }
 
 // ---------------------------------------------------------------------------
-// A decode batch (up to 64 rows): HBM-bound on the weights, and the codes must
-// not be read from L2 as often as they are (a 16-column workgroup that loads
-// its own codes moves as many bytes from L2 as from HBM: 8192 x 28672 at M = 16
-// 65 us, 47 us without those loads).  A workgroup of WV waves owns 16 WV
-// columns, one block of 16 per wave over the whole K (or one split of it); the
-// codes go through LDS for all of them.  S steps of KT * 128 k are in flight:
-// codes direct to LDS, weights to registers.  8 waves of 512-byte runs where
-// their workgroups nearly fill the compute units (8192 x 28672 at M = 16 / 64:
-// 46 / 54 us, 50 / 63 with the others), else 4 waves of 256-byte runs (4096 x
-// 11008: 13 / 18 us, 16 / 22).
+// A decode batch (up to 64 rows): HBM-bound on the weights.  A workgroup of WV
+// waves owns 16 WV columns, one block of 16 per wave over the whole K (or one
+// split of it).  Both operands go direct to LDS in whole 128-byte lines, S steps
+// of 256 k in flight; a wave waits for its own weights, and for everybody's part
+// of the codes, which all waves share (without sharing them a workgroup moves as
+// many bytes from L2 as from HBM: 8192 x 28672 at M = 16 65 us).  Weights loaded
+// straight into fragments, 64 bytes of 16 rows at a time, take longer: 8192 x
+// 28672 at M = 64 63.8 against 54.4 us, 4096 x 11008 19.1 and 17.0.
+//
+// 8 waves where their workgroups keep most compute units (20480 x 8192 at M = 64:
+// 41.7 us, 4.0 TB/s, 48.7 with 4 waves), else 4 (16384 x 4096: 17.3 us, 21.7 with
+// 8; 11008 x 4096 at M = 16: 11.3 and 14.9).
 // ---------------------------------------------------------------------------
+constexpr int kBatchSteps = 2;                     // 128-k steps at a time
+
 template <int MT, int WV>
 struct BatchShape {
-    static constexpr int KT = WV / 2;
-    static constexpr int XW = MT * 2 * KT / WV;    // 8-row loads of a wave per step
-    static constexpr int BUF = MT * 16 * KT * kStep;
+    static constexpr int KT = kBatchSteps;
+    static constexpr int XG = MT * 2 * KT;         // 8-row loads of the codes per step
+    static constexpr int XW = XG < WV ? 1 : XG / WV;         // of a wave
+    static constexpr int XB = XG * 1024, BUF = XB + WV * KT * 2048;
     static constexpr int LPS = XW + 2 * KT;
-    static constexpr int S = WV == 8 ? 3 : 4;
+    static constexpr int S = 160 * 1024 / BUF < 4 ? 160 * 1024 / BUF : 4;
     static constexpr size_t LDS = (size_t)S * BUF;
-    static_assert(XW * WV == MT * 2 * KT, "every wave loads the same number of row groups");
+    static_assert(XG % WV == 0 || WV % XG == 0, "every wave loads the same number of row groups");
 };
 
 template <class E, int MT, int WV>
@@ -406,13 +411,20 @@ __global__ __launch_bounds__(64 * WV, WV == 8 ? 2 : 4) void k_w8a8_batch(Args a)
     uint32_t xoff[T::XW];
 #pragma unroll
     for (int i = 0; i < T::XW; ++i)
-        xoff[i] = (uint32_t)((wave * T::XW + i) % (MT * 2) * 8 + lr) * (uint32_t)a.K + 16u * kc;
-    const uint32_t woff = (uint32_t)j * (uint32_t)a.K + 16u * h;
-    int4_t w[S][KT][2];
-    auto issue = [&](int step, int slot) {
+        xoff[i] = (uint32_t)((wave * T::XW + i) % T::XG % (MT * 2) * 8 + lr) * (uint32_t)a.K + 16u * kc;
+    uint32_t woff[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) woff[i] = (uint32_t)(8 * i + lr) * (uint32_t)a.K + 16u * kc;
+    // Rows lie K bytes apart: with K a power of two, workgroups at the same k
+    // would ask a few memory channels for all of their lines.  The sums are exact
+    // in any order, so each of an XCD's workgroups begins at a step of its own
+    // (28672 x 8192 at M = 16 / 64: 43.5 / 45 us, 52.6 / 56.4 from step 0).
+    const int first = (int)((blockIdx.x >> 3) % (unsigned)steps);
+    auto issue = [&](int i0, int slot) {
+        const int step = i0 >= steps ? steps : i0 + first < steps ? i0 + first : i0 + first - steps;
 #pragma unroll
         for (int i = 0; i < T::XW; ++i) {
-            const int ii = wave * T::XW + i;
+            const int ii = (wave * T::XW + i) % T::XG;
             const uint32_t at = (uint32_t)__builtin_amdgcn_readfirstlane((k0 + step * KT + ii / (MT * 2)) * kStep);
             // chunks past K, and all of the steps past the last one, load zeros
             const bool ok = step < steps && (int)at + 16 * kc < a.K;
@@ -421,10 +433,10 @@ __global__ __launch_bounds__(64 * WV, WV == 8 ? 2 : 4) void k_w8a8_batch(Args a)
 #pragma unroll
         for (int t = 0; t < KT; ++t)
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const uint32_t at = (uint32_t)(k0 + step * KT + t) * kStep + 64u * q;
-                const bool ok = step < steps && (int)at + 16 * h < a.K;
-                w[slot][t][q] = load16(rw, ok ? woff + at : kOutOfRange);
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t at = (uint32_t)(k0 + step * KT + t) * kStep;
+                const bool ok = step < steps && (int)at + 16 * kc < a.K;
+                load16_lds(rw, smem + slot * T::BUF + T::XB + (wave * KT + t) * 2048 + i * 1024, ok ? woff[i] : kOutOfRange, at);
             }
     };
     int4_t acc[MT];
@@ -453,13 +465,16 @@ __global__ __launch_bounds__(64 * WV, WV == 8 ? 2 : 4) void k_w8a8_batch(Args a)
 #pragma unroll
                 for (int t = 0; t < KT; ++t)
 #pragma unroll
-                    for (int q = 0; q < 2; ++q)
+                    for (int q = 0; q < 2; ++q) {
+                        const int4_t wv = *reinterpret_cast<const int4_t*>(
+                            smem + st * T::BUF + T::XB + (wave * KT + t) * 2048 + j * kStep + (((4 * q + h) ^ (j & 6)) << 4));
 #pragma unroll
                         for (int m = 0; m < MT; ++m) {
                             const int4_t xv = *reinterpret_cast<const int4_t*>(
                                 smem + st * T::BUF + (t * MT + m) * 2048 + j * kStep + (((4 * q + h) ^ (j & 6)) << 4));
-                            acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[st][t][q], xv, acc[m], 0, 0, 0);
+                            acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv, xv, acc[m], 0, 0, 0);
                         }
+                    }
             }
         }
         step0 += S;
@@ -902,15 +917,16 @@ Plan plan(int M, int N, int K) {
         split(p, total, (total + row_steps(M) - 1) / row_steps(M), 1, cus);
         return p;
     }
-    // a short K that a decode batch would split (4096 x 4096 at M = 16: 7.9 against 10.2 us)
-    if (M <= 16 && 2 * small <= cus && total <= 48) {
+    // a narrow product of a short K, which a decode batch would split (4096 x 4096 at
+    // M = 16: 7.5 against 9.1 us; 6144 x 4096: 11.7 and 10.3)
+    if (M <= 16 && 4 * small <= cus && total <= 48) {
         p.kernel = FEW;
         p.blocks = (N + 15) / 16;
     } else if (M <= 64) {
         p.kernel = BATCH;
-        p.waves = (N + 127) / 128 >= cus * 3 / 4 ? 8 : 4;
+        p.waves = (N + 127) / 128 >= cus * 5 / 8 ? 8 : 4;
         p.blocks = p.waves == 8 ? (N + 127) / 128 : small;
-        unit = p.waves / 2;
+        unit = kBatchSteps;
     } else {
         // The tile whose rounds over the compute units take less: a 128-k step of
         // a 256 x 256 tile takes 1.5 us and a tile 4 us besides, 0.62 and 3 us at

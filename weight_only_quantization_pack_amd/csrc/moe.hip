@@ -4,11 +4,13 @@
 //   y = sum_j p_j down_j(SiLU(gate_j x') * up_j x'),  x' = x * inv_s or x
 //
 // HBM-bound: every packed byte of an expert that some token takes is read
-// once, by whichever tokens take it.  Three launches:
+// once, by whichever tokens take it.  The launches:
 //   k_moe_route   one workgroup per token: its logits, choices and weights
 //   gate and up   h = SiLU(g) * u of every (token, choice)
-//   down          the projections of h; the workgroup that ends last on a
-//                 block of columns sums the choices there and writes y
+//   down          the projections of h
+//   k_moe_join    y = the weighted sum of a token's choices; with one token the
+//                 down product's workgroup that ends last on a block of columns
+//                 does it there, and this launch is saved
 // Both expert products run as k_moe_token (one token) or k_moe_tile (more).
 //
 // The weights are the B operand of v_mfma_f32_16x16x32_f16 (lane slot =
@@ -61,7 +63,8 @@ __device__ __forceinline__ float load_shared(const float* p) {
 }
 
 // ---------------------------------------------------------------------------
-// router and choices: one workgroup of 16 waves per token
+// router and choices: one workgroup of 16 waves per token, bound by what one
+// compute unit reads (64 experts x 2048: 9 us; 8 experts x 4096: 4.7 us)
 // ---------------------------------------------------------------------------
 struct RouteArgs {
     const _Float16 *x, *router;
@@ -302,7 +305,9 @@ __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f +
 // take its tiles in turn, each with U tiles in flight, and their sums meet in
 // LDS.  A workgroup is 8 / WK items and ends with them: with several
 // workgroups on a compute unit, one waits for its first tiles while others
-// compute.
+// compute.  2 of 8 experts of 14336 x 4096, int4 g128: gate and up 23.9 us (5.2
+// TB/s), down 16.2 us (3.9 TB/s; its operand, two planes of 28 KB, goes to LDS
+// first).  Held to 3 workgroups a compute unit by its registers.
 // ---------------------------------------------------------------------------
 template <int BITS, int GS, int WK, bool GATEUP>
 __global__ __launch_bounds__(512, 6) void k_moe_token(ExpertArgs a) {
@@ -415,7 +420,11 @@ __global__ __launch_bounds__(512, 6) void k_moe_token(ExpertArgs a) {
 // More tokens.  A workgroup of WV waves owns one expert and WV blocks of 16
 // output rows, one per wave over the whole K; the operand rows of the expert's
 // tokens go through LDS for all of them.  S steps of KT tiles are in flight:
-// operand rows direct to LDS, weights to registers.
+// operand rows direct to LDS, weights (whole 1 KB or 768-byte tiles) to registers.
+// 64 tokens, 2 of 8 experts of 14336 x 4096, int4 g128: gate and up 103 us (4.8
+// TB/s), down 92 us (2.7 TB/s: two operand rows a token, so twice the products
+// and fragment reads for a byte).  Int3 g64 unpacks three words into 32 values
+// for 12 bytes of a lane: there the vector instructions are what is waited for.
 // ---------------------------------------------------------------------------
 struct Lists {
     int ids[kMaxAssign];                           // every choice
@@ -641,7 +650,7 @@ __global__ __launch_bounds__(64 * WV, tile_waves(GS, MT, GATEUP)) void k_moe_til
 }
 
 // y[m] = the choices' rows (the sums of their splits), weighted, in their order;
-// 4 columns a thread
+// 4 columns a thread (64 x 4096, 2 choices: 5 us, of which the launch is half)
 __global__ __launch_bounds__(256) void k_moe_join(const float* part, const float* weights, _Float16* y, int top_k,
                                                   int K, int splits) {
     const int k = (blockIdx.x * 256 + threadIdx.x) * 4;

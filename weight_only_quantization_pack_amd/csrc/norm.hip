@@ -14,6 +14,11 @@
 // layer norm takes its mean first and sums squares of differences, so nothing
 // cancels), and r' is rounded once on its way out while h goes on from the
 // fp32 value.  Chunks past the row's end hold zeros and take no part.
+//
+// Both norms, cold rows: 8192 x 8192 98 us (5.5 TB/s), 95 us with h as codes;
+// 2048 x 4096 13.6 us (4.9 TB/s), 17.5 us with codes, whose exact quotients are
+// then what is waited for; 64 x 8192 4.2 us and 1 x 4096 2.9 us: a launch and
+// the latency of a load, two reductions and a store.
 #include "rows.h"
 
 namespace awq {
@@ -138,7 +143,7 @@ __global__ __launch_bounds__(NT) void k_norm(NormArgs a) {
 
 // Row quantizer: scale = max|x| / 127, q = rint(127 x / max|x|).  The row is
 // held in registers between the maximum and the codes, or (LONG: past the
-// widest instance) read a second time.
+// widest instance) read a second time.  509 x 4096: 3.0 us, mostly the launch.
 struct QuantArgs {
     const uint4* x;
     uint2* q;

@@ -9,6 +9,8 @@
 // row-major row, so neither operand needs repacking.  The weights are the A
 // operand: accumulator register r of lane (j, h) is then row m = j and column
 // n = 4 h + r, four consecutive outputs.
+//
+// Sizes below are M x N x K, or N x K of the weights.
 #include "rows.h"
 
 namespace awq {
@@ -508,8 +510,8 @@ __device__ __forceinline__ int chunk_swizzle(int r) { return r & 6; }
 // 512 x 6144 x 4096: 19.3 us (1340 TOP/s) for 192 tiles on 256 compute units.  A
 // step takes 0.50 us against 0.21 of MFMA: a 128 x 128 tile reads twice the bytes
 // of a 256 x 256 tile for each product, and the barrier of a step is met by all 8
-// waves at once.  Two workgroups of 4 waves on a compute unit, and tiles of 64
-// rows, took longer.
+// waves at once.  Two workgroups of 4 waves on a compute unit, and steps of 64 k,
+// took longer.
 // ---------------------------------------------------------------------------
 template <class E, int TM, int TN, int WM, int WN, int S>
 __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_w8a8_tile(Args a) {
@@ -657,8 +659,8 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_w8a8_tile(Args a)
 
 // ---------------------------------------------------------------------------
 // 256 x 256 tiles of the largest products, 8 waves, one workgroup per compute
-// unit that takes tile after tile.  8192 x 4096 x 14336: 367 us (2620 TOP/s),
-// MFMAs running 66 % of the time; the clock is then below its limit (1.9 GHz).
+// unit that takes tile after tile.  8192 x 14336 x 4096: 367 to 398 us (2420 to
+// 2620 TOP/s), MFMAs running 66 % of the time at a clock of 1.9 GHz.
 //
 // Steps of 128 k (whole 128-byte lines of every row), two of them in LDS, each
 // as four half tiles of 128 rows: X0, X1, W0, W1.  A wave computes 64 rows of

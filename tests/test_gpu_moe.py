@@ -115,6 +115,20 @@ def test_moe_long_rows(gpu, M, E, top_k, K, I):
     check(layer.run(x, router, top_k), layer.ref(x, router, top_k))
 
 
+@pytest.mark.parametrize("bits", [4, 3])
+@pytest.mark.parametrize("M,E,top_k,K,I", [(64, 8, 2, 2048, 2176), (31, 7, 4, 640, 3712)])
+def test_moe_batches(gpu, M, E, top_k, K, I, bits):
+    """Operands of 64 rows with a workgroup of 8 waves for half of the compute units or more, and with few
+    workgroups whose K is split."""
+    announce("moe batches", f"M={M} E={E} top_k={top_k} K={K} I={I} bits={bits}")
+    layer = Layer(E, K, I, bits, 128)
+    x = tokens(M, K, 5)
+    router = router_of(E, K, x, top_k, 6)
+    inv_s = dev(np.exp(0.3 * np.random.default_rng(7).standard_normal(K)).astype(np.float32))
+    for scale in (None, inv_s):
+        check(layer.run(x, router, top_k, inv_s=scale), layer.ref(x, router, top_k, True, scale))
+
+
 @pytest.mark.parametrize("group_size", [128, 64])
 def test_every_token_on_the_same_experts(gpu, group_size):
     """All tokens choose the same experts of many: the others get no token."""

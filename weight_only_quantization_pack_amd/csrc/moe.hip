@@ -481,8 +481,8 @@ __device__ __forceinline__ Share find_share(Lists& L, const int* ids, int assign
 __device__ __forceinline__ int row_swizzle(int r) { return (r & 0xA) | ((r & 1) << 2) | ((r >> 2) & 1); }
 
 // waves per SIMD that k_moe_tile's registers are held to
-constexpr int tile_waves(int GS, int MT, bool gate_up) {
-    return MT >= 4 ? (GS == 128 && !gate_up ? 4 : 2) : MT == 2 && gate_up && GS == 64 ? 2 : 3;
+constexpr int tile_waves(int GS, int MT, int WV, bool gate_up) {
+    return MT >= 4 ? (WV == 8 && !gate_up ? 4 : 2) : MT == 2 && gate_up && GS == 64 ? 2 : 3;
 }
 
 template <int BITS, int GS, int MT, int WV, bool GATEUP>
@@ -503,7 +503,7 @@ struct TileShape {
 };
 
 template <int BITS, int GS, int MT, int WV, bool GATEUP>
-__global__ __launch_bounds__(64 * WV, tile_waves(GS, MT, GATEUP)) void k_moe_tile(ExpertArgs a) {
+__global__ __launch_bounds__(64 * WV, tile_waves(GS, MT, WV, GATEUP)) void k_moe_tile(ExpertArgs a) {
     using T = TileShape<BITS, GS, MT, WV, GATEUP>;
     constexpr int WQ = BITS == 4 ? 4 : 3, NL = T::NL, S = T::S, KT = T::KT;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
@@ -695,9 +695,8 @@ int launch_token(const ExpertArgs& a, hipStream_t st) {
     return (int)hipGetLastError();
 }
 
-template <int BITS, int GS, bool GATEUP, int MT>
-int launch_tile(const ExpertArgs& a, hipStream_t st) {
-    constexpr int WV = MT * RowMap<GS>::HR >= 64 ? 8 : 4;
+template <int BITS, int GS, bool GATEUP, int MT, int WV>
+int launch_tile_waves(const ExpertArgs& a, hipStream_t st) {
     using T = TileShape<BITS, GS, MT, WV, GATEUP>;
     auto kern = k_moe_tile<BITS, GS, MT, WV, GATEUP>;
     if (T::LDS > 48 * 1024)
@@ -708,6 +707,17 @@ int launch_tile(const ExpertArgs& a, hipStream_t st) {
     const int experts = min(a.M * a.top_k, a.E);
     hipLaunchKernelGGL(kern, dim3(experts * NG, GATEUP ? 1 : a.splits), dim3(64 * WV), T::LDS, st, a);
     return (int)hipGetLastError();
+}
+
+// 8 waves share the operand rows of 64-row steps, unless that leaves more than
+// half of the compute units without a workgroup (23 tokens, 6 of 16 experts, 512 x
+// 2944: 50.6 us, 43.6 with 4 waves; 54 tokens, 3 of 11, 640 x 2048: 31.7 and 35.8)
+template <int BITS, int GS, bool GATEUP, int MT>
+int launch_tile(const ExpertArgs& a, hipStream_t st) {
+    if constexpr (MT * RowMap<GS>::HR >= 64)
+        if (min(a.M * a.top_k, a.E) * ((a.N + 127) / 128) * (GATEUP ? 1 : a.splits) >= device_cu_count() / 2)
+            return launch_tile_waves<BITS, GS, GATEUP, MT, 8>(a, st);
+    return launch_tile_waves<BITS, GS, GATEUP, MT, 4>(a, st);
 }
 
 template <int BITS, int GS, bool GATEUP>
@@ -734,11 +744,13 @@ int launch_experts_any(const ExpertArgs& a, int bits, int group_size, hipStream_
 
 // K splits of the down projections of more than one token: as many as bring the
 // expert workgroups (of 4 row blocks) to 6 per compute unit while a split
-// keeps 16 tiles
+// keeps 16 tiles, or to one while it keeps 8 (31 tokens, 4 of 7 experts, 3712 x
+// 640: 66 us without the second, 52 with it)
 int down_splits(int M, int K, int I, int E, int top_k) {
     if (M == 1) return 1;
     const int wgs = min(M * top_k, E) * ((K / 16 + 3) / 4);
-    return max(1, min((I / kGroup) / 16, 6 * device_cu_count() / max(wgs, 1)));
+    const int cus = device_cu_count();
+    return max(1, max(min((I / kGroup) / 16, 6 * cus / max(wgs, 1)), min((I / kGroup) / 8, cus / max(wgs, 1))));
 }
 
 // the workspace's parts, each 256-byte aligned

@@ -488,9 +488,7 @@ NORM_KINDS = {"rms": 0, "layer": 1}
 
 def _arg(t, dtype, shape, device, name):
     """The address of t, a contiguous tensor of this type and shape on GPU
-    `device` (its index); None passes through as NULL."""
-    if t is None:
-        return None
+    `device` (its index)."""
     try:
         if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
             return t.data_ptr()
@@ -500,9 +498,9 @@ def _arg(t, dtype, shape, device, name):
     raise ValueError(f"{name} must be on GPU {device}, got {t.device}")
 
 
-def _required(t, name):
-    if t is None:
-        raise TypeError(f"{name} must be a torch.Tensor")
+def _optional(t, dtype, shape, device, name):
+    """_arg, or NULL for None."""
+    return None if t is None else _arg(t, dtype, shape, device, name)
 
 
 def _dtype_code(dtype, name):
@@ -567,8 +565,7 @@ def norm_gate_residual(block, residual, pre_weight, post_weight=None, gate=None,
     dtype = block.dtype
     code = _dtype_code(dtype, "block")
     row = shape[1:]
-    _required(residual, "residual")
-    _required(pre_weight, "pre_weight")
+    residual_at = _arg(residual, dtype, shape, dev, "residual")
     if post_bias is not None and post_weight is None:
         raise ValueError("post_bias needs post_weight")
     if kind not in NORM_KINDS:
@@ -581,30 +578,30 @@ def norm_gate_residual(block, residual, pre_weight, post_weight=None, gate=None,
             gate_shape = (gate_rows, H)
             if gate_rows == 0 or T % gate_rows:
                 raise ValueError(f"gate rows ({gate_rows}) must divide the rows of block ({T})")
-    h_type = torch.int8 if quantize else dtype
-    scales = None
+    scales = scales_at = None
     if out is None:
         r = torch.empty_like(residual)
         if quantize:
-            h = block.new_empty(shape, dtype=h_type)
+            h = block.new_empty(shape, dtype=torch.int8)
             scales = block.new_empty(T, dtype=torch.float32)
+            scales_at = scales.data_ptr()
         else:
-            h = torch.empty_like(block)
-    elif quantize:
-        r, h, scales = out
+            h = torch.empty_like(residual)
+        r_at, h_at = r.data_ptr(), h.data_ptr()
     else:
-        r, h = out
-    _required(r, "out[0]")
-    _required(h, "out[1]")
-    if quantize:
-        _required(scales, "out[2]")
+        if quantize:
+            r, h, scales = out
+            scales_at = _arg(scales, torch.float32, shape[:1], dev, "out[2]")
+        else:
+            r, h = out
+        r_at = _arg(r, dtype, shape, dev, "out[0]")
+        h_at = _arg(h, torch.int8 if quantize else dtype, shape, dev, "out[1]")
     st = lib.awq_norm_gate_residual(
-        _arg(block, dtype, shape, dev, "block"), _arg(residual, dtype, shape, dev, "residual"),
-        _arg(post_weight, dtype, row, dev, "post_weight"), _arg(post_bias, dtype, row, dev, "post_bias"),
-        _arg(gate, dtype, gate_shape, dev, "gate"), gate_rows, residual_scale,
-        _arg(pre_weight, dtype, row, dev, "pre_weight"), _arg(pre_bias, dtype, row, dev, "pre_bias"),
-        NORM_KINDS[kind], eps, T, H, code, _arg(r, dtype, shape, dev, "out[0]"), _arg(h, h_type, shape, dev, "out[1]"),
-        _arg(scales, torch.float32, shape[:1], dev, "out[2]"), _raw_stream(dev))
+        _arg(block, dtype, shape, dev, "block"), residual_at,
+        _optional(post_weight, dtype, row, dev, "post_weight"), _optional(post_bias, dtype, row, dev, "post_bias"),
+        _optional(gate, dtype, gate_shape, dev, "gate"), gate_rows, residual_scale,
+        _arg(pre_weight, dtype, row, dev, "pre_weight"), _optional(pre_bias, dtype, row, dev, "pre_bias"),
+        NORM_KINDS[kind], eps, T, H, code, r_at, h_at, scales_at, _raw_stream(dev))
     _check(st, "awq_norm_gate_residual")
     return (r, h, scales) if quantize else (r, h)
 
@@ -623,8 +620,6 @@ def quantize_rows(x, out=None):
         scales = x.new_empty(shape[0], dtype=torch.float32)
     else:
         q, scales = out
-        _required(q, "out[0]")
-        _required(scales, "out[1]")
     st = lib.awq_quantize_rows(_arg(x, x.dtype, shape, dev, "x"), shape[0], shape[1], code,
                                _arg(q, torch.int8, shape, dev, "out[0]"),
                                _arg(scales, torch.float32, shape[:1], dev, "out[1]"), _raw_stream(dev))
@@ -651,18 +646,19 @@ def gemm_w8a8(q, q_scales, weight, weight_scales, bias=None, dtype=None, out=Non
     lib = load_library()
     (M, K), dev = _rows2d(q, "q")
     N = _rows2d(weight, "weight")[0][0]
-    _required(q_scales, "q_scales")
-    _required(weight_scales, "weight_scales")
     if dtype is None:
         dtype = torch.float16 if out is None else out.dtype
     code = _dtype_code(dtype, "dtype")
     if out is None:
         out = q.new_empty((M, N), dtype=dtype)
+        out_at = out.data_ptr()
+    else:
+        out_at = _arg(out, dtype, (M, N), dev, "out")
     keep, ws, ws_bytes = _workspace(workspace, lib.awq_gemm_w8a8_workspace_bytes(M, N, K), q)
     st = lib.awq_gemm_w8a8(_arg(q, torch.int8, (M, K), dev, "q"), _arg(q_scales, torch.float32, (M,), dev, "q_scales"),
                            _arg(weight, torch.int8, (N, K), dev, "weight"),
                            _arg(weight_scales, torch.float32, (N,), dev, "weight_scales"),
-                           _arg(bias, torch.float32, (N,), dev, "bias"), _arg(out, dtype, (M, N), dev, "out"),
+                           _optional(bias, torch.float32, (N,), dev, "bias"), out_at,
                            M, N, K, code, ws, ws_bytes, _raw_stream(dev))
     _check(st, "awq_gemm_w8a8")
     return out
@@ -678,13 +674,15 @@ def linear_w8a8(x, weight, weight_scales, bias=None, out=None, workspace=None):
     dtype = x.dtype
     code = _dtype_code(dtype, "x")
     N = _rows2d(weight, "weight")[0][0]
-    _required(weight_scales, "weight_scales")
     if out is None:
         out = x.new_empty((M, N))
+        out_at = out.data_ptr()
+    else:
+        out_at = _arg(out, dtype, (M, N), dev, "out")
     keep, ws, ws_bytes = _workspace(workspace, lib.awq_linear_w8a8_workspace_bytes(M, N, K), x)
     st = lib.awq_linear_w8a8(_arg(x, dtype, (M, K), dev, "x"), _arg(weight, torch.int8, (N, K), dev, "weight"),
                              _arg(weight_scales, torch.float32, (N,), dev, "weight_scales"),
-                             _arg(bias, torch.float32, (N,), dev, "bias"), _arg(out, dtype, (M, N), dev, "out"),
+                             _optional(bias, torch.float32, (N,), dev, "bias"), out_at,
                              M, N, K, code, ws, ws_bytes, _raw_stream(dev))
     _check(st, "awq_linear_w8a8")
     return out
@@ -716,21 +714,22 @@ def moe(x, router, gate, up, down, inter: int, top_k: int, bits: int = 4, group_
     half, I = torch.float16, inter
     if bits not in (3, 4) or group_size not in (64, 128):
         _check(3, "awq_moe")                                 # AWQ_ERR_UNSUPPORTED
+    x_at = _arg(x, half, shape, dev, "x")
     if out is None:
         out = torch.empty_like(x)
+        out_at = out.data_ptr()
+    else:
+        out_at = _arg(out, half, shape, dev, "out")
     keep, ws, ws_bytes = _workspace(workspace, lib.awq_moe_workspace_bytes(M, K, I, E, top_k), x)
-    args = [_arg(x, half, shape, dev, "x"), _arg(inv_s, torch.float32, shape[1:], dev, "inv_s"),
+    args = [x_at, _optional(inv_s, torch.float32, shape[1:], dev, "inv_s"),
             _arg(router, half, (E, K), dev, "router")]
     for layer, n, k, name in ((gate, I, K, "gate"), (up, I, K, "up"), (down, K, I, "down")):
         qweight, scales, zeros = layer
-        _required(qweight, name + " qweight")
-        _required(scales, name + " scales")
-        _required(zeros, name + " zeros")
         blocks = (n + 15) // 16
         params = (E, blocks, k // group_size, 16)
         args += [_arg(qweight, torch.int32, (E, blocks * 16 * (k // 32 * bits)), dev, name + " qweight"),
                  _arg(scales, half, params, dev, name + " scales"), _arg(zeros, half, params, dev, name + " zeros")]
-    st = lib.awq_moe(*args, _arg(out, half, shape, dev, "out"), M, K, I, E, top_k, bits, group_size,
+    st = lib.awq_moe(*args, out_at, M, K, I, E, top_k, bits, group_size,
                      int(renormalize), ws, ws_bytes, _raw_stream(dev))
     _check(st, "awq_moe")
     return out

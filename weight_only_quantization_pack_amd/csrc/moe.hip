@@ -305,10 +305,14 @@ __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f +
 // take its tiles in turn, each with U tiles in flight, and their sums meet in
 // LDS.  A workgroup is 8 / WK items and ends with them: with several
 // workgroups on a compute unit, one waits for its first tiles while others
-// compute.  2 of 8 experts of 14336 x 4096, int4 g128: gate and up 23.9 us (5.2
-// TB/s), down 16.2 us (3.9 TB/s; its operand, two planes of 28 KB, goes to LDS
-// first).  Held to 3 workgroups a compute unit by its registers.
+// compute.  2 of 8 experts of 14336 x 4096, int4 g128: gate and up 22.9 us (5.4
+// TB/s), down 14.0 us (4.4 TB/s; every workgroup reads its operand, two planes of
+// 28 KB).  With the operand through registers behind the weights 23.9 and 16.2 us.
+// Registers hold it to 3 workgroups a compute unit.
 // ---------------------------------------------------------------------------
+// LDS of an item's operand planes, in whole 1 KB loads
+__host__ __device__ __forceinline__ int token_lds(int split, int K) { return ((K * 2 << split) + 1023) / 1024 * 1024; }
+
 template <int BITS, int GS, int WK, bool GATEUP>
 __global__ __launch_bounds__(512, 6) void k_moe_token(ExpertArgs a) {
     constexpr int WQ = BITS == 4 ? 4 : 3;
@@ -326,32 +330,37 @@ __global__ __launch_bounds__(512, 6) void k_moe_token(ExpertArgs a) {
     const int item = (int)blockIdx.x * SUB + sub;
     const bool live = item < total;
     const int c = live ? item / NB : 0, b = live ? item % NB : 0;
-    const int e = __builtin_amdgcn_readfirstlane(a.ids[c]);
-    const Weights<BITS, GS, NL> rw(a, e);
     const int nw = live && wk < G ? (G - wk + WK - 1) / WK : 0;
 
+    // The operand planes of this item (gate/up: one token's for all items) go
+    // direct to LDS, asked for before the weights, since loads return in order
+    const int row_bytes = a.K * 2;
+    unsigned char* xs = smem + (GATEUP ? 0 : sub * token_lds(a.split, a.K));
+    {
+        const int n = row_bytes / 16 << a.split;             // 16-byte chunks
+        const __amdgpu_buffer_rsrc_t rx =
+            moe_rsrc(a.in, (size_t)__builtin_amdgcn_readfirstlane(a.rows * row_bytes << a.split));
+        for (int i0 = GATEUP ? wave : wk; i0 * 64 < n; i0 += GATEUP ? 8 : WK) {
+            const int i = i0 * 64 + lane, p = i >= row_bytes / 16;
+            const uint32_t at = (uint32_t)(p * a.rows + (GATEUP ? 0 : c) - p) * (uint32_t)row_bytes + 16u * (uint32_t)i;
+            load16_lds(rx, xs + i0 * 1024, i < n ? at : kOutOfRange, 0);
+        }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    const Weights<BITS, GS, NL> rw(a, __builtin_amdgcn_readfirstlane(a.ids[c]));
     TileRegs<WQ, NL> ring[U];
     auto load = [&](int i, int u) {
         load_tile<BITS, GS, NL>(rw, (uint32_t)b * (uint32_t)G + (uint32_t)(wk + WK * i), i < nw, lane, ring[u]);
     };
 #pragma unroll
-    for (int u = 0; u < U; ++u) load(u, u);
-
-    // the operand planes of this item in LDS (gate/up: one token's for all items)
-    const int planes = a.split ? 2 : 1;
-    const int row_bytes = a.K * 2;
-    unsigned char* xs = smem + (GATEUP ? 0 : sub * planes * row_bytes);
-    {
-        const int n = planes * (a.K / 8);
-        const size_t row = GATEUP ? 0 : c;
-        const int t0 = GATEUP ? tid : wk * 64 + lane, step = GATEUP ? 512 : 64 * WK;
-        for (int i = t0; i < n; i += step) {
-            const int p = i >= a.K / 8;
-            const size_t at = (((size_t)p * a.rows + row) * a.K) / 8 + (i - p * (a.K / 8));
-            reinterpret_cast<uint4*>(xs)[i] = reinterpret_cast<const uint4*>(a.in)[at];
-        }
+    for (int u = 0; u < U; ++u) {
+        __builtin_amdgcn_sched_barrier(0);
+        load(u, u);
     }
-    __syncthreads();
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(3 * NL * U));       // the weights need not have landed
+    asm volatile("s_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
     const RowMap<GS> map(a.split, j, hq);
     const unsigned char* xl = xs + (map.low ? row_bytes : 0) + 64 * hq;
     const uint32_t psh = 16u * (uint32_t)(j & 1);
@@ -689,7 +698,7 @@ int launch_token(const ExpertArgs& a, hipStream_t st) {
     ExpertFn kern = wk == 8 ? k_moe_token<BITS, GS, 8, GATEUP>
                             : wk == 4 ? k_moe_token<BITS, GS, 4, GATEUP> : k_moe_token<BITS, GS, 2, GATEUP>;
     const int sub = 8 / wk;
-    const size_t lds = (size_t)(GATEUP ? 1 : sub) * (a.split ? 2 : 1) * a.K * 2;
+    const size_t lds = (size_t)(GATEUP ? 1 : sub) * token_lds(a.split, a.K);
     if (int e = set_lds(kern, lds)) return e;
     hipLaunchKernelGGL(kern, dim3((a.top_k * NB + sub - 1) / sub), dim3(512), lds, st, a);
     return (int)hipGetLastError();

@@ -129,6 +129,22 @@ def test_moe_batches(gpu, M, E, top_k, K, I, bits):
         check(layer.run(x, router, top_k, inv_s=scale), layer.ref(x, router, top_k, True, scale))
 
 
+@pytest.mark.parametrize("bits", [4, 3])
+@pytest.mark.parametrize("group_size", [128, 64])
+@pytest.mark.parametrize("M,E,top_k,K,I", [(2, 9, 1, 1024, 128), (13, 6, 2, 1152, 384), (40, 5, 2, 1408, 256),
+                                           (64, 3, 3, 1664, 128)])
+def test_moe_few_row_blocks(gpu, M, E, top_k, K, I, group_size, bits):
+    """Gate and up projections whose row blocks are too few for the card: K in turns, with ragged last turns
+    and experts that take several passes."""
+    announce("moe few row blocks", f"M={M} E={E} top_k={top_k} K={K} I={I} bits={bits} gs={group_size}")
+    layer = Layer(E, K, I, bits, group_size)
+    x = tokens(M, K, 5)
+    router = router_of(E, K, x, top_k, 6)
+    inv_s = dev(np.exp(0.3 * np.random.default_rng(7).standard_normal(K)).astype(np.float32))
+    for scale in (None, inv_s):
+        check(layer.run(x, router, top_k, inv_s=scale), layer.ref(x, router, top_k, True, scale))
+
+
 @pytest.mark.parametrize("group_size", [128, 64])
 def test_every_token_on_the_same_experts(gpu, group_size):
     """All tokens choose the same experts of many: the others get no token."""

@@ -426,8 +426,8 @@ __global__ __launch_bounds__(512, 6) void k_moe_token(ExpertArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// More tokens.  A workgroup of WV waves owns one expert and WV blocks of 16
-// output rows, one per wave over the whole K; the operand rows of the expert's
+// More tokens.  A workgroup of WV waves owns one expert and WV / KW blocks of 16
+// output rows, each of KW waves over the whole K; the operand rows of the expert's
 // tokens go through LDS for all of them.  S steps of KT tiles are in flight:
 // operand rows direct to LDS, weights (whole 1 KB or 768-byte tiles) to registers.
 // 64 tokens, 2 of 8 experts of 14336 x 4096, int4 g128: gate and up 103 us (4.8
@@ -494,35 +494,38 @@ constexpr int tile_waves(int GS, int MT, int WV, bool gate_up) {
     return MT >= 4 ? (WV == 8 && !gate_up ? 4 : 2) : MT == 2 && gate_up && GS == 64 ? 2 : 3;
 }
 
-template <int BITS, int GS, int MT, int WV, bool GATEUP>
+template <int BITS, int GS, int MT, int WV, int KW, bool GATEUP>
 struct TileShape {
     static constexpr int NL = GATEUP ? 2 : 1;
     static constexpr int HR = RowMap<GS>::HR;
     static constexpr int XR = MT * HR;             // operand rows in LDS
-    // tiles per step: at least one 4-row load for every wave
-    static constexpr int KT = XR / 4 >= WV ? 1 : WV / (XR / 4);
+    // tiles per step: at least one 4-row load for every wave, and KW
+    static constexpr int KL = XR / 4 >= WV ? 1 : WV / (XR / 4), KT = KL > KW ? KL : KW;
+    static constexpr int KI = KT / KW;             // a wave's
     static constexpr int XW = XR / 4 * KT / WV;    // its loads per wave
     static constexpr int TB = (XR + (GS == 64)) * 256;     // a tile's rows (and a row of zeros)
     static constexpr int BUF = TB * KT;
-    static constexpr int LPS = XW + 3 * NL * KT;   // loads per step and wave
+    static constexpr int LPS = XW + 3 * NL * KI;   // loads per step and wave
     static constexpr int S = KT * NL >= 4 ? 3 : XR >= 64 ? 4 : KT * NL == 2 ? 4 : 6;
-    static constexpr size_t LDS = (size_t)S * BUF;
+    static constexpr int SUMS = KW > 1 ? WV * NL * MT * 1024 : 0;      // the waves' sums
+    static constexpr size_t LDS = (size_t)S * BUF + SUMS;
     static_assert(XW * WV == XR / 4 * KT, "every wave loads the same number of row groups");
     static_assert(LPS * (S - 2) <= 63, "vmcnt counts to 63");
 };
 
-template <int BITS, int GS, int MT, int WV, bool GATEUP>
+template <int BITS, int GS, int MT, int WV, int KW, bool GATEUP>
 __global__ __launch_bounds__(64 * WV, tile_waves(GS, MT, WV, GATEUP)) void k_moe_tile(ExpertArgs a) {
-    using T = TileShape<BITS, GS, MT, WV, GATEUP>;
-    constexpr int WQ = BITS == 4 ? 4 : 3, NL = T::NL, S = T::S, KT = T::KT;
+    using T = TileShape<BITS, GS, MT, WV, KW, GATEUP>;
+    constexpr int WQ = BITS == 4 ? 4 : 3, NL = T::NL, S = T::S, KT = T::KT, KI = T::KI;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     __shared__ Lists L;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int j = lane & 15, hq = lane >> 4;
-    const int G = a.K / kGroup, NB = (a.N + 15) / 16, NG = (NB + WV - 1) / WV;
+    const int G = a.K / kGroup, NB = (a.N + 15) / 16, NG = (NB + WV / KW - 1) / (WV / KW);
     const int assigned = a.M * a.top_k;
-    const int b = (int)blockIdx.x % NG * WV + wave;            // this wave's row block
+    const int b = (int)blockIdx.x % NG * (WV / KW) + wave / KW;         // this wave's row block,
+    const int kw = wave % KW;                      // and which of each step's KW tiles
     const Share share = find_share<64 * WV>(L, a.ids, assigned, (int)blockIdx.x / NG);
     if (share.expert < 0) return;
     const int cnt = share.count;
@@ -559,7 +562,7 @@ __global__ __launch_bounds__(64 * WV, tile_waves(GS, MT, WV, GATEUP)) void k_moe
                                     16u * (uint32_t)((lane & 15) ^ row_swizzle(jr))
                               : kOutOfRange;
         }
-        TileRegs<WQ, NL> ring[S][KT];
+        TileRegs<WQ, NL> ring[S][KI];
         auto issue = [&](int step, int slot) {
 #pragma unroll
             for (int i = 0; i < T::XW; ++i) {
@@ -570,8 +573,8 @@ __global__ __launch_bounds__(64 * WV, tile_waves(GS, MT, WV, GATEUP)) void k_moe
                            g < g1 ? xoff[i] : kOutOfRange, (uint32_t)g * 256u);
             }
 #pragma unroll
-            for (int t = 0; t < KT; ++t) {
-                const int g = g0 + step * KT + t;
+            for (int t = 0; t < KI; ++t) {
+                const int g = g0 + step * KT + kw + KW * t;
                 load_tile<BITS, GS, NL>(rw, tile0 + (uint32_t)g, g < g1, lane, ring[slot][t]);
             }
         };
@@ -590,15 +593,15 @@ __global__ __launch_bounds__(64 * WV, tile_waves(GS, MT, WV, GATEUP)) void k_moe
         const int mstep = map.mine ? T::HR * 256 : 0;
         auto compute = [&](int slot, const TileRegs<WQ, NL>* regs, auto tiles) {
             constexpr int LM = decltype(tiles)::value;
-            const unsigned char* xb = smem + slot * T::BUF;
+            const unsigned char* xb = smem + slot * T::BUF + kw * T::TB;
 #pragma unroll
-            for (int t = 0; t < KT; ++t) {
+            for (int t = 0; t < KI; ++t) {
                 half8_t x[4][LM];
 #pragma unroll
                 for (int m = 0; m < LM; ++m)
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
-                        x[q][m] = *reinterpret_cast<const half8_t*>(xb + t * T::TB + m * mstep + xat[q]);
+                        x[q][m] = *reinterpret_cast<const half8_t*>(xb + KW * t * T::TB + m * mstep + xat[q]);
 #pragma unroll
                 for (int l = 0; l < NL; ++l)
                     tile_product<BITS, WQ, LM>(regs[t].w[l], regs[t].d[l], regs[t].z[l], psh, x, acc[l]);
@@ -634,10 +637,30 @@ __global__ __launch_bounds__(64 * WV, tile_waves(GS, MT, WV, GATEUP)) void k_moe
             step0 += S;
         } while (step0 < steps);
 
+        if constexpr (KW > 1) {                    // the first wave of a row block adds the others' sums
+            float4_t* sums = reinterpret_cast<float4_t*>(smem + S * T::BUF) + wave * (NL * MT * 64) + lane;
+#pragma unroll
+            for (int l = 0; l < NL; ++l)
+#pragma unroll
+                for (int m = 0; m < MT; ++m) sums[(l * MT + m) * 64] = acc[l][m];
+            __syncthreads();
+            if (kw == 0) {
+#pragma unroll
+                for (int l = 0; l < NL; ++l)
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int q = 1; q < KW; ++q) {
+                            const float4_t o = sums[((q * NL + l) * MT + m) * 64];
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) acc[l][m][r] += o[r];
+                        }
+            }
+        }
         const int n = 16 * b + j;
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            if (m >= live) continue;
+            if (m >= live || kw != 0) continue;
             float4_t v[NL];
 #pragma unroll
             for (int l = 0; l < NL; ++l) v[l] = map.join(acc[l][m]);
@@ -704,15 +727,15 @@ int launch_token(const ExpertArgs& a, hipStream_t st) {
     return (int)hipGetLastError();
 }
 
-template <int BITS, int GS, bool GATEUP, int MT, int WV>
+template <int BITS, int GS, bool GATEUP, int MT, int WV, int KW>
 int launch_tile_waves(const ExpertArgs& a, hipStream_t st) {
-    using T = TileShape<BITS, GS, MT, WV, GATEUP>;
-    auto kern = k_moe_tile<BITS, GS, MT, WV, GATEUP>;
+    using T = TileShape<BITS, GS, MT, WV, KW, GATEUP>;
+    auto kern = k_moe_tile<BITS, GS, MT, WV, KW, GATEUP>;
     if (T::LDS > 48 * 1024)
         if (int e = (int)hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)T::LDS))
             return e;
-    const int NG = ((a.N + 15) / 16 + WV - 1) / WV;
+    const int NG = ((a.N + 15) / 16 + WV / KW - 1) / (WV / KW);
     const int experts = min(a.M * a.top_k, a.E);
     hipLaunchKernelGGL(kern, dim3(experts * NG, GATEUP ? 1 : a.splits), dim3(64 * WV), T::LDS, st, a);
     return (int)hipGetLastError();
@@ -720,13 +743,21 @@ int launch_tile_waves(const ExpertArgs& a, hipStream_t st) {
 
 // 8 waves share the operand rows of 64-row steps, unless that leaves more than
 // half of the compute units without a workgroup (23 tokens, 6 of 16 experts, 512 x
-// 2944: 50.6 us, 43.6 with 4 waves; 54 tokens, 3 of 11, 640 x 2048: 31.7 and 35.8)
+// 2944: 50.6 us, 43.6 with 4 waves; 54 tokens, 3 of 11, 640 x 2048: 31.7 and 35.8).
+// Gate and up of few row blocks: KW waves take each step's KW tiles in turn, one
+// block of rows for all of them, and the first adds their sums (36 tokens, 4 of 6
+// experts, 256 x 1920: 39.3 us, 35.3 so; 64 tokens, 2 of 8, 1024 x 4096: 52.4 and
+// 44.0).  KW = 4 where the steps' operand rows then leave LDS for two workgroups.
 template <int BITS, int GS, bool GATEUP, int MT>
 int launch_tile(const ExpertArgs& a, hipStream_t st) {
+    const int cus = device_cu_count(), experts = min(a.M * a.top_k, a.E);
     if constexpr (MT * RowMap<GS>::HR >= 64)
-        if (min(a.M * a.top_k, a.E) * ((a.N + 127) / 128) * (GATEUP ? 1 : a.splits) >= device_cu_count() / 2)
-            return launch_tile_waves<BITS, GS, GATEUP, MT, 8>(a, st);
-    return launch_tile_waves<BITS, GS, GATEUP, MT, 4>(a, st);
+        if (experts * ((a.N + 127) / 128) * (GATEUP ? 1 : a.splits) >= cus / 2)
+            return launch_tile_waves<BITS, GS, GATEUP, MT, 8, 1>(a, st);
+    if constexpr (GATEUP)
+        if (experts * ((a.N + 63) / 64) < cus && a.K / kGroup >= 8)
+            return launch_tile_waves<BITS, GS, GATEUP, MT, 4, (MT * RowMap<GS>::HR >= 32 ? 2 : 4)>(a, st);
+    return launch_tile_waves<BITS, GS, GATEUP, MT, 4, 1>(a, st);
 }
 
 template <int BITS, int GS, bool GATEUP>

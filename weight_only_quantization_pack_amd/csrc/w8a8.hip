@@ -507,11 +507,12 @@ __device__ __forceinline__ int chunk_swizzle(int r) { return r & 6; }
 // in flight as direct-to-LDS loads; a wave reads the fragments of step t + 1
 // while the MFMAs of step t run.
 //
-// 512 x 6144 x 4096: 19.3 us (1340 TOP/s) for 192 tiles on 256 compute units.  A
-// step takes 0.50 us against 0.21 of MFMA: a 128 x 128 tile reads twice the bytes
-// of a 256 x 256 tile for each product, and the barrier of a step is met by all 8
-// waves at once.  Two workgroups of 4 waves on a compute unit, and steps of 64 k,
-// took longer.
+// 512 x 6144 x 4096: 19 to 23 us (1100 to 1340 TOP/s) for 192 tiles on 256 compute
+// units.  A step takes 0.58 us against 0.22 of MFMA: the loads are what is waited
+// for (0.49 us when all of them hit L2, 0.41 without the weights'; without the
+// fragment reads still 0.57), since a 128 x 128 tile reads twice the bytes of a
+// 256 x 256 tile for each product.  Two workgroups of 4 waves on a compute unit,
+// 4 waves in place of 8, 64 columns, and steps of 64 k were no faster.
 // ---------------------------------------------------------------------------
 template <class E, int TM, int TN, int WM, int WN, int S>
 __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_w8a8_tile(Args a) {

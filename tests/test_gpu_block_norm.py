@@ -195,6 +195,67 @@ def test_quantize_rows_extremes(gpu):
     assert (q[5] == -127).all()
 
 
+# Rows of 64 around a maximum of 2^e (nearly 2^(e + 1) in "full"): half of it (a quotient of 63.5), quarters, tenths
+# and halves of every size down to 2^-32 of it, and the smallest numbers
+LARGE = [118, 119, 120, 121, 122, 125, 126, 127]
+
+
+def large_rows():
+    import torch
+    g = np.random.default_rng(0)
+    out = []
+    for e in LARGE:
+        for top in (1.0, 2.0 - 2.0 ** -7):
+            row = np.concatenate([[1, .5, .25, -.75, .1, -1, 0, .3], 2.0 ** -np.arange(1, 33), [1e-30, -1e-30],
+                                  (np.arange(14) - 7 + 0.5) / 127, g.uniform(-1, 1, 8)])
+            out.append(row * top * 2.0 ** e)
+    x = torch.tensor(np.stack(out), dtype=torch.float64).to(torch.bfloat16)
+    x[:, 62] = 2.0 ** -130
+    x[:, 63] = -2.0 ** -133
+    return x.cuda()
+
+
+def test_codes_of_large_rows(gpu):
+    """bfloat16 rows up to the largest finite numbers: 127 v is past fp32 there, the quotient is not."""
+    x = large_rows()
+    qr, sr = R.quantize_rows(f64(x))
+    q, s = awq.quantize_rows(x)
+    assert np.array_equal(R.to_f64(q), qr)
+    assert np.array_equal(s.cpu().numpy(), np.abs(f64(x)).max(-1).astype(np.float32) / np.float32(127))
+
+
+@pytest.mark.parametrize("M", [1, 2])
+def test_large_rows_quantized_inside_the_product(gpu, M):
+    """The same codes where the product's own launch quantizes one or two rows: an identity for weights, whose
+    channel scales bring the outputs to the codes times fp32 factors (three roundings of 2^-24 and bfloat16's)."""
+    import torch
+    x = large_rows()
+    w, sw = torch.eye(64, dtype=torch.int8, device="cuda"), torch.full((64,), 2.0 ** -100, device="cuda")
+    assert awq.linear_w8a8_workspace_bytes(M, 64, 64) == 0
+    qr, sr = R.quantize_rows(f64(x))
+    for m in range(0, len(x), M):
+        y = awq.linear_w8a8(x[m:m + M], w, sw)
+        ref = qr[m:m + M] * sr[m:m + M, None] * 2.0 ** -100
+        assert np.all(np.abs(R.to_f64(y) - ref) <= (2.0 ** -8 + 2.0 ** -22) * np.abs(ref))
+
+
+def test_norm_codes_of_large_rows(gpu):
+    """The same behind a norm whose weights are as large: a row of ones of either sign, so h is +-weight within
+    2^-16 and a code may differ by one where the quotient is that near half way."""
+    import torch
+    w = large_rows()
+    signs = torch.where(torch.arange(64, device="cuda") % 3 == 0, -1.0, 1.0).to(torch.bfloat16)[None]
+    for k in range(len(w)):
+        r, q, s = awq.norm_gate_residual(torch.zeros_like(signs), signs, w[k], eps=0.0, quantize=True)
+        href = R.norm_gate_residual(np.zeros((1, 64)), f64(signs), f64(w[k]), eps=0.0)[1]
+        qr, sr = R.quantize_rows(href)
+        t = href * 127.0 / np.abs(href).max()
+        near = np.abs(np.abs(t - np.floor(t)) - 0.5) <= 127 * FP32
+        off = R.to_f64(q) - qr
+        assert np.all((off == 0) | (near & (np.abs(off) == 1)))
+        assert np.all(np.abs(R.to_f64(s) - sr) <= FP32 * sr)
+
+
 def test_refusals(gpu):
     import torch
     b, w = rows(4, 512, 1, "fp16"), vector(512, 2, "fp16")

@@ -94,13 +94,17 @@ __device__ __forceinline__ uint32_t abs_bits(float f) { return __builtin_bit_cas
 // to even: with v = a 2^i and top = b 2^(i + d), a and b in [2^10, 2^11) and
 // d >= -1, the quotient is a half-integer or misses it by at least
 // 2^-(12 + max(d, 0)), and its rounding (127 v is exact) moves it by at most
-// 2^-(16 + d).
+// 2^-(16 + d).  127 v would overflow in rows whose top is near the largest
+// fp32: from 2^120 on both are brought down by 2^64 first, exactly but for
+// values below 2^-62, whose code is 0 either way.
 struct RowScale {
     float top, inv;          // max |v|; 127 / top
+    float down;              // what v and top are multiplied by for the division
     bool tiny;               // 127 / top would overflow: always divide
     __device__ __forceinline__ explicit RowScale(uint32_t top_bits) {
         top = __builtin_bit_cast(float, top_bits);
         inv = 127.0f / top;
+        down = top >= 0x1p120f ? 0x1p-64f : 1.0f;
         tiny = top < 0x1p-100f;
     }
     __device__ __forceinline__ float scale() const { return top / 127.0f; }
@@ -123,7 +127,7 @@ __device__ __forceinline__ uint2 pack_codes8(const float* v, const RowScale& s) 
         if (slow) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                k[i] = s.top == 0.0f ? 0u : __builtin_bit_cast(uint32_t, v[i] * 127.0f / s.top + kRound);
+                k[i] = s.top == 0.0f ? 0u : __builtin_bit_cast(uint32_t, v[i] * s.down * 127.0f / (s.top * s.down) + kRound);
         }
     }
     auto bytes = [](const uint32_t* q) {           // the low bytes of four words

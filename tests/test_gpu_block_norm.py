@@ -256,6 +256,33 @@ def test_norm_codes_of_large_rows(gpu):
         assert np.all(np.abs(R.to_f64(s) - sr) <= FP32 * sr)
 
 
+def test_more_rows_than_a_launch_holds(gpu):
+    """2^26 rows and a few: 2^32 threads of the narrowest workgroups.  Every row has codes of its own."""
+    import torch
+    M = (1 << 26) + 3
+    announce("quantize_rows", f"M={M} K=16")
+    x = torch.zeros(M, 16, dtype=torch.float16, device="cuda")
+    t = torch.arange(M, device="cuda")
+    x[:, 5] = (t % 251 - 125).half()
+    x[:, 15] = 127.0
+    q, s = awq.quantize_rows(x)
+    assert bool((s == 1.0).all()) and bool((q[:, 15] == 127).all()) and bool((q[:, 5] == (t % 251 - 125)).all())
+    assert not q[:, :5].any() and not q[:, 6:15].any()
+    del x, q, s
+    announce("norm_gate_residual", f"T={M} H=8")
+    residual = torch.zeros(M, 8, dtype=torch.float16, device="cuda")
+    residual[:, 0] = (t % 2048 + 1).half()
+    gate = torch.tensor([[1.0], [2.0], [3.0]], device="cuda").repeat_interleave(8, dim=1).half().contiguous()
+    n = M // 3 * 3                                           # three gate rows
+    r, h = awq.norm_gate_residual(torch.ones_like(residual)[:n], residual[:n], torch.ones(8, device="cuda").half(),
+                                  gate=gate, eps=0.0)
+    g = torch.arange(n, device="cuda") // (n // 3) + 1
+    assert bool((r[:, 1] == g.half()).all()) and bool((r[:, 0] == (t[:n] % 2048 + 1 + g).half()).all())
+    # h = r' / sqrt((r0^2 + 7 g^2) / 8), one rounding of fp16 (2^-11) past fp32's
+    ref = g.float() * torch.rsqrt(((t[:n] % 2048 + 1 + g).float() ** 2 + 7 * g.float() ** 2) / 8)
+    assert bool(((h[:, 7].float() - ref).abs() <= ref * 2.0 ** -10 + 2.0 ** -24).all())
+
+
 def test_refusals(gpu):
     import torch
     b, w = rows(4, 512, 1, "fp16"), vector(512, 2, "fp16")

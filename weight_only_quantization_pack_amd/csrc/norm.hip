@@ -33,6 +33,7 @@ struct NormArgs {
     int H, rows_per_gate;
     float alpha, eps;
     int layer;
+    int row0;                                      // of this launch
 };
 
 template <class E, int NT, int C>
@@ -41,7 +42,7 @@ __global__ __launch_bounds__(NT) void k_norm(NormArgs a) {
     __shared__ uint32_t slots[5][W];               // one row of slots per reduction
     const int tid = threadIdx.x;
     const int chunks = a.H / 8;
-    const size_t row = blockIdx.x;
+    const size_t row = (size_t)a.row0 + blockIdx.x;
     const size_t at = row * (size_t)chunks;
     const size_t gat = a.gate ? row / (size_t)a.rows_per_gate * (size_t)chunks : 0;
     const float inv_h = 1.0f / (float)a.H;
@@ -149,6 +150,7 @@ struct QuantArgs {
     uint2* q;
     float* scales;
     int K;
+    int row0;                                      // of this launch
 };
 
 template <class E, int NT, int C, bool LONG>
@@ -157,7 +159,7 @@ __global__ __launch_bounds__(NT) void k_quantize_rows(QuantArgs a) {
     __shared__ uint32_t slots[W];
     const int tid = threadIdx.x;
     const int chunks = a.K / 8;
-    const size_t row = blockIdx.x;
+    const size_t row = (size_t)a.row0 + blockIdx.x;
     const size_t at = row * (size_t)chunks;
     uint32_t top = 0;
     float v[C][8];
@@ -220,26 +222,37 @@ void pick_row(int chunks, int rows, int cus, F&& f) {
     return f(Shape<1024, 4>());
 }
 
+// A launch counts its threads in 32 bits: 2^21 rows of up to 1024 threads at a time
+constexpr int kLaunchRows = 1 << 21;
+
 template <class E>
-int launch_norm_t(const NormArgs& a, int T, hipStream_t st) {
-    pick_row(a.H / 8, T, device_cu_count(), [&](auto shape) {
-        using S = decltype(shape);
-        hipLaunchKernelGGL((k_norm<E, S::threads, S::chunks>), dim3(T), dim3(S::threads), 0, st, a);
-    });
-    return (int)hipGetLastError();
+int launch_norm_t(NormArgs a, int T, hipStream_t st) {
+    for (a.row0 = 0;; a.row0 += kLaunchRows) {
+        const int rows = min(T - a.row0, kLaunchRows);
+        pick_row(a.H / 8, T, device_cu_count(), [&](auto shape) {
+            using S = decltype(shape);
+            hipLaunchKernelGGL((k_norm<E, S::threads, S::chunks>), dim3(rows), dim3(S::threads), 0, st, a);
+        });
+        if (int e = (int)hipGetLastError()) return e;
+        if (T - a.row0 <= kLaunchRows) return 0;
+    }
 }
 
 template <class E>
-int launch_quantize_rows_t(const QuantArgs& a, int M, hipStream_t st) {
-    if (a.K / 8 > 4096) {
-        hipLaunchKernelGGL((k_quantize_rows<E, 1024, 1, true>), dim3(M), dim3(1024), 0, st, a);
-    } else {
-        pick_row(a.K / 8, M, device_cu_count(), [&](auto shape) {
-            using S = decltype(shape);
-            hipLaunchKernelGGL((k_quantize_rows<E, S::threads, S::chunks, false>), dim3(M), dim3(S::threads), 0, st, a);
-        });
+int launch_quantize_rows_t(QuantArgs a, int M, hipStream_t st) {
+    for (a.row0 = 0;; a.row0 += kLaunchRows) {
+        const int rows = min(M - a.row0, kLaunchRows);
+        if (a.K / 8 > 4096) {
+            hipLaunchKernelGGL((k_quantize_rows<E, 1024, 1, true>), dim3(rows), dim3(1024), 0, st, a);
+        } else {
+            pick_row(a.K / 8, M, device_cu_count(), [&](auto shape) {
+                using S = decltype(shape);
+                hipLaunchKernelGGL((k_quantize_rows<E, S::threads, S::chunks, false>), dim3(rows), dim3(S::threads), 0, st, a);
+            });
+        }
+        if (int e = (int)hipGetLastError()) return e;
+        if (M - a.row0 <= kLaunchRows) return 0;
     }
-    return (int)hipGetLastError();
 }
 
 }  // namespace
@@ -265,7 +278,7 @@ int launch_norm(const NormProblem& p, hipStream_t st) {
 }
 
 int launch_quantize_rows(const void* x, int M, int K, int dtype, void* q, float* scales, hipStream_t st) {
-    const QuantArgs a{(const uint4*)x, (uint2*)q, scales, K};
+    const QuantArgs a{(const uint4*)x, (uint2*)q, scales, K, 0};
     return dtype == AWQ_BF16 ? launch_quantize_rows_t<BF16>(a, M, st) : launch_quantize_rows_t<F16>(a, M, st);
 }
 

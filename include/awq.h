@@ -458,7 +458,7 @@ awq_status awq_quantize_rows(const void* x, int M, int K, int dtype, void* q, fl
  *   x  int8 [M][K], x_scales fp32 [M], weight int8 [N][K], weight_scales fp32
  *   [N]: as awq_quantize_rows writes them;  bias  fp32 [N] or NULL;
  *   y  dtype [M][N] out.  The sum is exact in int32: K a multiple of 16 and
- *   < 2^17 (else AWQ_ERR_SHAPE); M * N < 2^40.
+ *   < 2^17; M < 2^29, N < 2^26 and M * N < 2^40 (else AWQ_ERR_SHAPE).
  *   workspace / workspace_bytes: device scratch of at least
  *   awq_gemm_w8a8_workspace_bytes(M, N, K) bytes (may be NULL when that is 0;
  *   else too small is AWQ_ERR_WORKSPACE): int32 partial sums of the K splits

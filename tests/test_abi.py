@@ -408,6 +408,18 @@ def test_w8a8_validation(lib):
         assert call(**shape, ws=P, ws_bytes=need - 1) == WS
 
 
+def test_w8a8_sizes_past_a_launch(lib):
+    """Products whose launch would count 2^32 threads or more are refused; the rows of the quantizer are not."""
+    for M, N in ((1 << 29, 1), (1 << 30, 64), (1, 1 << 26), (4, (1 << 31) - 1), ((1 << 31) - 1, 1), (64, 1 << 27)):
+        assert lib.awq_gemm_w8a8(P, P2, P3, P4, NUL, P5, M, N, 16, 0, NUL, 0, NUL) == SHAPE, (M, N)
+        assert lib.awq_linear_w8a8(P, P3, P4, NUL, P5, M, N, 16, 0, P2, 1 << 62, NUL) == SHAPE, (M, N)
+        assert lib.awq_gemm_w8a8_workspace_bytes(M, N, 16) == lib.awq_linear_w8a8_workspace_bytes(M, N, 16) == 0
+    # inside the limits: the null pointer is what is refused
+    for M, N in (((1 << 29) - 1, 1), (1, (1 << 26) - 1), (4096, (1 << 26) - 1)):
+        assert lib.awq_gemm_w8a8(NUL, P2, P3, P4, NUL, P5, M, N, 16, 0, NUL, 0, NUL) == NULL, (M, N)
+    assert lib.awq_quantize_rows(NUL, (1 << 31) - 1, 16, 0, P2, P3, NUL) == NULL
+
+
 def test_moe_validation(lib):
     def call(ptrs=None, inv_s=NUL, M=4, K=256, I=128, E=8, top_k=2, bits=4, gs=128, renorm=1, ws=P5, ws_bytes=1 << 30):
         p = dict(x=P, router=P2, gq=P3, gs_=P3, gz=P3, uq=P4, us=P4, uz=P4, dq=P5, ds=P5, dz=P5, y=P)

@@ -399,9 +399,17 @@ int check_optional(std::initializer_list<const void*> ps) {
     return AWQ_OK;
 }
 
-int check_w8a8(int M, int N, int K, int dtype) {
+int check_rows(int M, int K, int dtype) {
     if (int st = check_dtype(dtype)) return st;
-    if (M < 0 || N < 0 || K <= 0 || K % 16 != 0 || K >= kMaxW8a8K) return AWQ_ERR_SHAPE;
+    return M < 0 || K <= 0 || K % 16 != 0 || K >= kMaxW8a8K ? AWQ_ERR_SHAPE : AWQ_OK;
+}
+
+// A launch counts its threads in 32 bits.  The most: 32 a column with up to 4
+// rows, 4 a row for narrow products on 128 x 128 tiles (wider ones of that many
+// tiles go to the 256 x 256 kernel, which launches one workgroup a compute unit).
+int check_w8a8(int M, int N, int K, int dtype) {
+    if (int st = check_rows(M, K, dtype)) return st;
+    if (N < 0 || M >= 1 << 29 || N >= 1 << 26) return AWQ_ERR_SHAPE;
     if ((long long)M * N >= (1LL << 40)) return AWQ_ERR_SHAPE;
     return AWQ_OK;
 }
@@ -438,7 +446,7 @@ awq_status awq_norm_gate_residual(const void* block, const void* residual, const
 
 awq_status awq_quantize_rows(const void* x, int M, int K, int dtype, void* q, float* scales,
                              hipStream_t stream) {
-    int st = check_w8a8(M, 0, K, dtype);
+    int st = check_rows(M, K, dtype);
     if (st) return as_status(st);
     if (M == 0) return AWQ_OK;
     if ((st = check_ptrs({x, q, scales}))) return as_status(st);

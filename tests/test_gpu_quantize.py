@@ -218,3 +218,15 @@ def test_fake_quantize_full_layer_chain(gpu):
     q, d, z = O.quantize(W, None, 4)
     want = O.fake_quantize(O.pack(q, 4), d, z, 4, 4096)
     assert np.array_equal(host(got).view(np.uint16), want.view(np.uint16))
+
+
+def test_scale_activations_past_a_launch(gpu):
+    """More than 2^35 elements, 2^32 chunks of a thread: in place, every row divided once."""
+    import torch
+    M, K = (1 << 28) + 3, 128
+    announce("scale_activations", f"M={M} K={K} in place")
+    x = torch.full((M, K), 3.0, dtype=torch.float16, device="cuda")
+    s = torch.full((K,), 2.0, device="cuda")
+    awq.scale_activations(x, s, out=x)
+    for m in range(0, M, 1 << 25):
+        assert bool((x[m:m + (1 << 25)] == 1.5).all()), m

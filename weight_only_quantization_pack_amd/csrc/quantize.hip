@@ -190,12 +190,17 @@ int launch_quantize_pack(const void* W, const float* s, int N, int K, int bits, 
 
 int launch_scale_activations(const void* x, const float* s, void* x_out, int M, int K,
                              hipStream_t st) {
-    const long long n_chunks = (long long)M * K / 8;
-    const int block = 256;
-    const long long grid = (n_chunks + block - 1) / block;
-    hipLaunchKernelGGL(k_scale_activations, dim3((unsigned)grid), dim3(block), 0, st,
-                       (const uint4*)x, s, (uint4*)x_out, K, n_chunks);
-    return (int)hipGetLastError();
+    // a launch counts its threads in 32 bits: rows of up to 2^30 chunks at a time
+    const int block = 256, step = (1 << 30) / (K / 8);
+    for (int m = 0; m < M; m += min(step, M - m)) {
+        const long long n_chunks = (long long)min(step, M - m) * (K / 8);
+        const long long grid = (n_chunks + block - 1) / block;
+        const size_t at = (size_t)m * (K / 8);
+        hipLaunchKernelGGL(k_scale_activations, dim3((unsigned)grid), dim3(block), 0, st,
+                           (const uint4*)x + at, s, (uint4*)x_out + at, K, n_chunks);
+        if (int e = (int)hipGetLastError()) return e;
+    }
+    return 0;
 }
 
 int launch_dequantize(const void* qweight, const void* scales, const void* zeros, void* W_hat, int N,

@@ -256,6 +256,45 @@ def test_norm_codes_of_large_rows(gpu):
         assert np.all(np.abs(R.to_f64(s) - sr) <= FP32 * sr)
 
 
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("T,H", [(300, 16384), (257, 24576), (40, 512), (300, 1536)])
+def test_widths_in_more_rows_than_compute_units(gpu, T, H, dtype):
+    """The widest rows where there are many of them, in 16 bits and as codes, and the narrow ones."""
+    block, residual, pre = rows(T, H, 1, dtype), rows(T, H, 2, dtype, 4.0), vector(H, 3, dtype)
+    r, h = awq.norm_gate_residual(block, residual, pre, kind="layer")
+    rr, hr = R.norm_gate_residual(f64(block), f64(residual), f64(pre), kind="layer")
+    check(r, rr, dtype, "r'")
+    check(h, hr, dtype, "h")
+    q, s = awq.quantize_rows(block)
+    qr, sr = R.quantize_rows(f64(block))
+    assert np.array_equal(R.to_f64(q), qr)
+    assert np.array_equal(s.cpu().numpy(), np.abs(f64(block)).max(-1).astype(np.float32) / np.float32(127))
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("T,H", [(1, 520), (6, 4096), (300, 2048), (260, 8192)])
+def test_every_norm_with_codes(gpu, T, H, kind, dtype):
+    """Codes behind norms with a norm after the block, gates and biases.  h and the row's maximum are both off by at
+    most 2^-16 of that maximum: a quotient by 2 * 127 * 2^-16."""
+    import torch
+    block, residual = rows(T, H, 1, dtype), rows(T, H, 2, dtype, 4.0)
+    pre, post = vector(H, 3, dtype), vector(H, 4, dtype, 0.5, 0.1)
+    opt = dict(post_weight=post, gate=vector(H, 7, dtype, 0.0, 0.7), pre_bias=vector(H, 5, dtype, 0.0, 0.1),
+               post_bias=vector(H, 6, dtype, 0.0, 0.1))
+    r, q, s = awq.norm_gate_residual(block, residual, pre, kind=kind, residual_scale=0.7, quantize=True, **opt)
+    r0, _ = awq.norm_gate_residual(block, residual, pre, kind=kind, residual_scale=0.7, **opt)
+    assert torch.equal(r.view(torch.int16), r0.view(torch.int16))
+    href = R.norm_gate_residual(f64(block), f64(residual), f64(pre), kind=kind, residual_scale=np.float32(0.7),
+                                **{k: f64(v) for k, v in opt.items()})[1]
+    qr, sr = R.quantize_rows(href)
+    assert np.all(np.abs(R.to_f64(s) - sr) <= FP32 * sr + 2.0 ** -23 * sr)
+    off = R.to_f64(q) - qr
+    t = href * 127.0 / np.abs(href).max(-1, keepdims=True)
+    near = np.abs(np.abs(t - np.floor(t)) - 0.5) <= 2 * 127 * FP32
+    assert np.all((off == 0) | (near & (np.abs(off) == 1)))
+
+
 def test_more_rows_than_a_launch_holds(gpu):
     """2^26 rows and a few: 2^32 threads of the narrowest workgroups.  Every row has codes of its own."""
     import torch

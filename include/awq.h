@@ -427,10 +427,14 @@ typedef enum {
  *   kind     awq_norm_kind of both norms;  eps >= 0, added to the mean square
  *   residual_out  dtype [T][H] out: r', rounded once (may be `residual`)
  *   h        out: dtype [T][H] rounded once; or, with h_scales, int8 [T][H]
- *   h_scales NULL, or fp32 [T] out: h is then written as the codes of
- *            awq_quantize_rows of the fp32 h, ready for awq_gemm_w8a8
+ *   h_scales NULL, or fp32 [T] out: h is then written as the codes of the fp32
+ *            h as awq_quantize_rows forms them, ready for awq_gemm_w8a8 (the
+ *            quotient is rounded to fp32 here, so one that is half an integer
+ *            to 2^-16 may go to either side)
  *   H a multiple of 8, at most 32768 (else AWQ_ERR_SHAPE).  All arithmetic is
- *   fp32.  T == 0 is a valid empty call.
+ *   fp32: a row whose mean square is past the fp32 maximum (bf16 values from
+ *   about 1.8e19) is divided by infinity, so its norm is 0 (+ bias).  T == 0 is
+ *   a valid empty call.
  */
 awq_status awq_norm_gate_residual(const void* block, const void* residual,
                                   const void* post_weight, const void* post_bias,
@@ -454,7 +458,7 @@ awq_status awq_quantize_rows(const void* x, int M, int K, int dtype, void* q, fl
 /*
  * awq_gemm_w8a8 -- product in 8-bit integers with a scale for each token and
  * each channel, for any M >= 1:
- *   y[m][n] = x_scales[m] * weight_scales[n] * sum_k x[m][k] weight[n][k] + bias[n]
+ *   y[m][n] = (x_scales[m] * weight_scales[n]) * sum_k x[m][k] weight[n][k] + bias[n]
  *   x  int8 [M][K], x_scales fp32 [M], weight int8 [N][K], weight_scales fp32
  *   [N]: as awq_quantize_rows writes them;  bias  fp32 [N] or NULL;
  *   y  dtype [M][N] out.  The sum is exact in int32: K a multiple of 16 and
@@ -496,8 +500,11 @@ awq_status awq_linear_w8a8(const void* x, const void* weight, const float* weigh
  *   other, each as awq_quantize_pack writes it (same bits and group_size):
  *   qweight [E][awq_packed_words], scales and zeros fp16 [E][ceil(N/16)][G][16]
  *   y  fp16 [M][K] out, rounded once: products take the exact (q - z), sums
- *   and group scales are fp32, and SiLU(gate) * up goes on as two fp16 numbers
- *   (22 bits).  It must stay below the fp16 maximum, as in awq_gemv_gate_up.
+ *   and group scales are fp32, and x * inv_s and SiLU(gate) * up go on as two
+ *   fp16 numbers each (22 bits of magnitudes from 2^-14 up; below, steps of
+ *   2^-35).  Both must stay below the fp16 maximum, 65504, as in
+ *   awq_gemv_scaled and awq_gemv_gate_up: a token with a larger one has a row
+ *   of NaN, and no other token changes.
  *   0 <= M <= 64, 1 <= top_k <= min(E, 16), E <= 512 (else
  *   AWQ_ERR_UNSUPPORTED); K and I multiples of 128, at most 32768 (else
  *   AWQ_ERR_SHAPE).

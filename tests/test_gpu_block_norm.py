@@ -356,3 +356,15 @@ def test_refusals(gpu):
     assert r.shape == h.shape == (0, 512)
     q, s = awq.quantize_rows(e)
     assert q.shape == (0, 512) and s.shape == (0,)
+
+
+def test_mean_squares_past_fp32(gpu):
+    """bfloat16 rows whose squares overflow are divided by infinity: the bias is what is left, and no other row
+    changes."""
+    import torch
+    block, residual, pre = rows(3, 512, 1, "bf16"), rows(3, 512, 2, "bf16"), vector(512, 3, "bf16")
+    bias = vector(512, 4, "bf16", 0.0, 0.5)
+    _, h0 = awq.norm_gate_residual(block, residual, pre, pre_bias=bias)
+    residual[1] = 1e20
+    _, h = awq.norm_gate_residual(block, residual, pre, pre_bias=bias)
+    assert torch.equal(h[1], bias) and torch.equal(h[[0, 2]], h0[[0, 2]])

@@ -136,3 +136,37 @@ def test_router_weights_below_the_normal_fp16_range(gpu):
     for rows in (slice(0, 1), slice(0, 4)):
         # x / 300: the same choices from logits 300 times smaller, fp32 sums of gaps above 3e-6
         check(layer.run(x[rows] / 300, router, 2), layer.ref(x[rows] / 300, router, 2))
+
+
+@pytest.mark.parametrize("M", [1, 3])
+def test_scaled_tokens_up_to_the_fp16_maximum(gpu, M):
+    """x * inv_s of 60000 is exact to 22 bits like any other; past the fp16 maximum its token's row is NaN and no
+    other token changes."""
+    import torch
+    layer = SharedLayer(5, 256, 128, 4, 128, size=5e-4)
+    x = tokens(M, 256, 5)
+    inv_s = torch.ones(256, device="cuda")
+    inv_s[7] = 100.0
+    x[0, 7] = 600.0
+    router = router_of(5, 256, x, 2, 6)
+    router[:, 7] = 0
+    logits = np.sort(R.to_f64(x) @ R.to_f64(router).T, axis=1)
+    assert np.min(logits[:, -2] - logits[:, -3]) > 1e-3
+    y0 = layer.run(x, router, 2, inv_s=inv_s)
+    check(y0, layer.ref(x, router, 2, True, inv_s))
+    x[0, 7] = 700.0
+    y = layer.run(x, router, 2, inv_s=inv_s)
+    assert torch.isnan(y[0]).all() and torch.equal(y[1:].view(torch.int16), y0[1:].view(torch.int16))
+
+
+@pytest.mark.parametrize("M", [1, 3])
+def test_gated_values_past_the_fp16_maximum(gpu, M):
+    """SiLU(gate) * up past the fp16 maximum: a row of NaN, and no other token changes."""
+    import torch
+    layer = SharedLayer(5, 256, 128, 4, 64)
+    x = tokens(M, 256, 5)
+    router = router_of(5, 256, x, 2, 6)
+    y0 = layer.run(x, router, 2)
+    x[0] *= 2000
+    y = layer.run(x, router, 2)
+    assert torch.isnan(y[0]).all() and torch.equal(y[1:].view(torch.int16), y0[1:].view(torch.int16))

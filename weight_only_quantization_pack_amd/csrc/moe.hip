@@ -3,8 +3,11 @@
 //   p = softmax(l) over the chosen ones, or over all experts
 //   y = sum_j p_j down_j(SiLU(gate_j x') * up_j x'),  x' = x * inv_s or x
 //
-// HBM-bound: every packed byte of an expert that some token takes is read
-// once, by whichever tokens take it.  The launches:
+// HBM-bound: the packed bytes of an expert are read once for up to 16, 32 or 64
+// rows of its tokens' operands (launch_experts; 64-wide groups and an operand in
+// two planes take 2 rows a token each, so 64 rows are 16 to 64 tokens), and once
+// more for every further pass; an expert that no token takes is not read.  The
+// launches:
 //   k_moe_route   one workgroup per token: its logits, choices and weights
 //   gate and up   h = SiLU(g) * u of every (token, choice)
 //   down          the projections of h
@@ -20,8 +23,9 @@
 // where that keeps the products exact:
 //   - an operand that is not an fp16 number (h, and x' = x * inv_s) is split
 //     into hi = fp16(v) and lo = fp16((v - hi) * 2^11), two rows whose sums
-//     are added as hi + lo / 2^11: 22 bits of v, for matrix time that is free
-//     while the weights are what is waited for;
+//     are added as hi + lo / 2^11: 22 bits of v (from 2^-14 up; steps of 2^-35
+//     below; past 65504 hi is infinite and the sums NaN), for matrix time that
+//     is free while the weights are what is waited for;
 //   - with 64-wide groups a k32 product mixes both groups of a tile (lane
 //     quarters 0, 1 and 2, 3), so rows 0..7 hold the tokens with quarters 2, 3
 //     zeroed and rows 8..15 the same tokens with quarters 0, 1 zeroed: the
@@ -64,7 +68,7 @@ __device__ __forceinline__ float load_shared(const float* p) {
 
 // ---------------------------------------------------------------------------
 // router and choices: one workgroup of 16 waves per token, bound by what one
-// compute unit reads (64 experts x 2048: 9 us; 8 experts x 4096: 4.7 us)
+// compute unit reads (64 experts x 2048: 8 us; 8 experts x 4096: 4 to 5 us)
 // ---------------------------------------------------------------------------
 struct RouteArgs {
     const _Float16 *x, *router;
@@ -136,7 +140,11 @@ __device__ void route_token(const float* partial, int slabs, int E, int top_k, b
 
 // The logits are units of RB experts by kSlab k, taken by the 16 waves in turn:
 // a lane holds 8 k of every 512 of x and of RB router rows, all of them loaded
-// at once.  RB = 4 where that still gives every wave a unit, else 1.
+// at once.  RB = 4 where that still gives every wave a unit, else 1.  The layer with
+// RB = 4 / 1, one token, 4 experts of 256 channels, router of 128 x 2048 18.5 / 21.4 us, 64 x
+// 2048 15.4 / 16.9, 32 x 4096 15.7 / 17.2 (64 units each or more); below, where the
+// rule takes 1, 32 x 2048 14.2 / 14.8, 16 x 4096 14.6 / 15.2, 8 x 4096 14.0 / 14.3:
+// 4 is no slower there either.
 constexpr int kSlab = 2048;
 
 template <int RB>
@@ -308,7 +316,8 @@ __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f +
 // compute.  2 of 8 experts of 14336 x 4096, int4 g128: gate and up 22.9 us (5.4
 // TB/s), down 14.0 us (4.4 TB/s; every workgroup reads its operand, two planes of
 // 28 KB).  With the operand through registers behind the weights 23.9 and 16.2 us.
-// Registers hold it to 3 workgroups a compute unit.
+// Registers hold it to 3 workgroups a compute unit, LDS to 2 in that down product
+// (its operand planes of 56 KB and the waves' sums of 8 KB).
 // ---------------------------------------------------------------------------
 // LDS of an item's operand planes, in whole 1 KB loads
 __host__ __device__ __forceinline__ int token_lds(int split, int K) { return ((K * 2 << split) + 1023) / 1024 * 1024; }
@@ -432,8 +441,11 @@ __global__ __launch_bounds__(512, 6) void k_moe_token(ExpertArgs a) {
 // operand rows direct to LDS, weights (whole 1 KB or 768-byte tiles) to registers.
 // 64 tokens, 2 of 8 experts of 14336 x 4096, int4 g128: gate and up 103 us (4.8
 // TB/s), down 92 us (2.7 TB/s: two operand rows a token, so twice the products
-// and fragment reads for a byte).  Int3 g64 unpacks three words into 32 values
-// for 12 bytes of a lane: there the vector instructions are what is waited for.
+// and fragment reads for a byte); an expert of more than 32 of the tokens takes a
+// second pass (the layer 239 to 252 us, 202 to 214 without one).  13 tokens, 6 of
+// 64 experts of 1408 x 2048, int3 g64, x' = x * inv_s: the layer 56.5 us, 51.4 in
+// a build that multiplies the words without unpacking them, and 58.0 with int4:
+// the unpacking is a tenth of it, not what bounds it.
 // ---------------------------------------------------------------------------
 struct Lists {
     int ids[kMaxAssign];                           // every choice
@@ -713,7 +725,13 @@ int set_lds(ExpertFn kern, size_t lds) {
                                     hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
 }
 
-// one token: waves of an item -- 8 where each still has 4 tiles, else fewer
+// one token: waves of an item by the K tiles, so that a workgroup is one item of
+// long rows or several of short ones.  The layer at 2 / 4 / 8 waves, int4 g128:
+// 8 of 64 experts, 512 x 512 15.6 / 15.0 / 14.8 us, 896 x 896 18.2 / 17.0 / 17.2,
+// 1024 x 1024 18.7 / 17.6 / 17.9; 4 of 32, 2048 x 2048 20.2 / 18.3 / 18.2, 3968 x
+// 3968 31.6 / 31.5 / 32.5, 4096 x 4096 30.5 / 30.4 / 32.4; 1 of 4, 8192 x 4096 - /
+// 21.5 / 20.1.  So 2 waves are a few per cent behind 4 in short rows, and 8 ahead
+// of 4 only where items are fewer than the card holds.
 template <int BITS, int GS, bool GATEUP>
 int launch_token(const ExpertArgs& a, hipStream_t st) {
     const int G = a.K / kGroup, NB = (a.N + 15) / 16;
@@ -748,6 +766,8 @@ int launch_tile_waves(const ExpertArgs& a, hipStream_t st) {
 // block of rows for all of them, and the first adds their sums (36 tokens, 4 of 6
 // experts, 256 x 1920: 39.3 us, 35.3 so; 64 tokens, 2 of 8, 1024 x 4096: 52.4 and
 // 44.0).  KW = 4 where the steps' operand rows then leave LDS for two workgroups.
+// From 8 K tiles on (36 tokens, 2 of 8, 512 x 1024: 19.9 us, 21.0 without; 8 tokens
+// 15.8 and 17.4; of 6 tiles 19.5 and 20.5, of 4 18.1 and 18.2).
 template <int BITS, int GS, bool GATEUP, int MT>
 int launch_tile(const ExpertArgs& a, hipStream_t st) {
     const int cus = device_cu_count(), experts = min(a.M * a.top_k, a.E);
@@ -785,7 +805,10 @@ int launch_experts_any(const ExpertArgs& a, int bits, int group_size, hipStream_
 // K splits of the down projections of more than one token: as many as bring the
 // expert workgroups (of 4 row blocks) to 6 per compute unit while a split
 // keeps 16 tiles, or to one while it keeps 8 (31 tokens, 4 of 7 experts, 3712 x
-// 640: 66 us without the second, 52 with it)
+// 640: 66 us without the second, 52 with it).  The layer with 2 of 8 experts of
+// 14336 x 4096 and 64 tokens: 217 us at 6 a compute unit, 252 at 3, 215 at 12; of
+// 4096 x 4096 93, 98, 93, with 8 tiles a split 91, with 32 98; but 16 tokens of
+// 8192 x 4096 91 us at 6, 87 at 3, 94 at 12.
 int down_splits(int M, int K, int I, int E, int top_k) {
     if (M == 1) return 1;
     const int wgs = min(M * top_k, E) * ((K / 16 + 3) / 4);

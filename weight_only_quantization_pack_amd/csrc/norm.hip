@@ -15,10 +15,11 @@
 // cancels), and r' is rounded once on its way out while h goes on from the
 // fp32 value.  Chunks past the row's end hold zeros and take no part.
 //
-// Both norms, cold rows: 8192 x 8192 98 us (5.5 TB/s), 95 us with h as codes;
-// 2048 x 4096 13.6 us (4.9 TB/s), 17.5 us with codes, whose exact quotients are
-// then what is waited for; 64 x 8192 4.2 us and 1 x 4096 2.9 us: a launch and
-// the latency of a load, two reductions and a store.
+// Both norms, cold rows: 8192 x 8192 94 us (5.7 TB/s), 86 us with h as codes (5.5
+// TB/s); 2048 x 4096 14.4 us (4.7 TB/s), 17.2 us with codes (3.4 TB/s).  One norm,
+// 2048 x 4096: 14.4 and 15.9 us; 14.9 in a build whose codes never divide, and 16.0
+// where the third reduction is left out as well.  64 x 8192 3.8 us and 1 x 4096 3.1
+// us: a launch and the latency of a load, two reductions and a store.
 #include "rows.h"
 
 namespace awq {
@@ -144,7 +145,9 @@ __global__ __launch_bounds__(NT) void k_norm(NormArgs a) {
 
 // Row quantizer: scale = max|x| / 127, q = rint(127 x / max|x|).  The row is
 // held in registers between the maximum and the codes, or (LONG: past the
-// widest instance) read a second time.  509 x 4096: 3.0 us, mostly the launch.
+// widest instance) read a second time.  509 x 4096: 3.8 us, mostly the launch; 2048
+// x 4096 7.7 us (3.3 TB/s), 11008 x 4096 26.7 us (5.1 TB/s), 28672 x 8192 118 us (6.0
+// TB/s).
 struct QuantArgs {
     const uint4* x;
     uint2* q;
@@ -197,7 +200,10 @@ __global__ __launch_bounds__(NT) void k_quantize_rows(QuantArgs a) {
 }
 
 // Threads and chunks per thread of a row of `chunks` 16-byte chunks: one wave
-// for the narrow rows; 1024 threads where there are fewer rows than compute
+// for the narrow rows, which needs no barrier (the norm of 8192 rows of 512: 7.3 us,
+// 9.1 with 256 threads; of 1024 12.7 with one wave of 2, 14.8 with 256 threads or 128,
+// one row 2.5 against 2.1; of 2048 26.0 with 256 of 1, 27.7 with 64 of 4, 25.2 with 128
+// of 2, one row 2.2, 3.7 and 2.4); 1024 threads where there are fewer rows than compute
 // units (a row's latency is the cost); else few enough threads that several
 // rows share a compute unit.  2048 x 16384: 54.7 us with 512 threads of 4
 // chunks, 61.7 with 1024 of 2; 8193 x 8192: 97.5 with 512 of 2, 98.8 with 256

@@ -661,7 +661,9 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void k_w8a8_tile(Args a)
 // ---------------------------------------------------------------------------
 // 256 x 256 tiles of the largest products, 8 waves, one workgroup per compute
 // unit that takes tile after tile.  8192 x 14336 x 4096: 367 to 398 us (2420 to
-// 2620 TOP/s), MFMAs running 66 % of the time at a clock of 1.9 GHz.
+// 2620 TOP/s), MFMAs running 68 % of the time at a clock of 1.9 GHz; up to 484 us in
+// a first burst of launches, while the clock is lower still (24 launches, in order:
+// 373 three times, 386 rising to 484 in the ninth, 441 to 446, 407 in the last).
 //
 // Steps of 128 k (whole 128-byte lines of every row), two of them in LDS, each
 // as four half tiles of 128 rows: X0, X1, W0, W1.  A wave computes 64 rows of
@@ -897,7 +899,11 @@ int row_lds(int M, int steps) { return row_rows(M) * ((steps * kStep + kRowStep 
 int row_steps(int M) { return kRowLds / row_rows(M) / kStep; }       // K steps whose codes fit
 
 // K cut into `splits` at least, or more of at least 16 steps where there are
-// fewer workgroups than compute units, in units of `unit` steps
+// fewer workgroups than compute units, in units of `unit` steps.  At 8 / 16 / 32
+// steps at least (M x N x K): 16 x 1024 x 8192 8.6 / 8.0 / 9.1 us, 64 x 4096 x 11008
+// 17.1 / 17.1 / 21.6, 128 x 4096 x 4096 15.0 / 15.3 / 16.0, 512 x 1024 x 8192 17.5 /
+// 15.8 / 20.2; 8 gains for 128 x 2048 x 8192 (12.3 / 13.7 / 19.0) and 65 x 4096 x 4096
+// (12.2 / 13.5 / 15.5), and one row of 1024 x 4096 is better whole (5.0 / 5.0 / 3.0).
 void split(Plan& p, int total, int splits, int unit, int cus) {
     p.splits = 1;
     p.steps = (total + unit - 1) / unit * unit;

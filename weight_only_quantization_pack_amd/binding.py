@@ -704,7 +704,8 @@ def moe(x, router, gate, up, down, inter: int, top_k: int, bits: int = 4, group_
     [E][ceil(inter / 16)][K / group_size][16]) -- the E layers of quantize_pack,
     stacked; down the same of K x inter layers.  p = softmax over the chosen
     experts (renormalize) or over all.  inv_s (fp32 [K], the reciprocal of the
-    AWQ scale of gate and up): x' = x * inv_s; the router reads x.
+    AWQ scale of gate and up): x' = x * inv_s; the router reads x.  A token whose
+    x' or SiLU(gate) * up passes the fp16 maximum (65504) has a row of NaN.
     """
     torch = _torch()
     lib = load_library()

@@ -520,6 +520,191 @@ awq_status awq_moe(const void* x, const float* inv_s, const void* router,
                    void* y, int M, int K, int I, int E, int top_k, int bits, int group_size,
                    int renormalize, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Rotary positions, and a key and value cache held in 8 bits.
+ *
+ * The cache of a layer is paged: a page holds page_size (16, 32, 64 or 128)
+ * consecutive tokens of one sequence for every kv head as int8 codes
+ * [pages][kv_heads][page_size][head_dim], keys (k_codes) and values (v_codes)
+ * apart, with one fp32 scale for each page and head (k_scales, v_scales
+ * [pages][kv_heads]): value = code * scale, -127 <= code <= 127.  head_dim is
+ * 64, 96, 128, 192 or 256 (else AWQ_ERR_UNSUPPORTED).
+ *
+ * The sequences of a call, all int32 on the device:
+ *   tables [B][W]  the pages of sequence b in order: token t is in slot
+ *                  t % page_size of page tables[b][t / page_size].  An entry
+ *                  outside 0..pages-1 is a page that holds nothing: it is not
+ *                  written, not attended to and reads as zeros.  So are the
+ *                  tokens past W pages.
+ *   lens   [B]     tokens of each sequence, those of this call included
+ *   starts [B + 1] rows starts[b] .. starts[b + 1] - 1 of the call are the last
+ *                  tokens of sequence b, in order; it ascends from 0.  NULL: one
+ *                  row for each sequence (T == B).  Rows from starts[B] on belong
+ *                  to no sequence: what a call would write for them stays as it
+ *                  was.  Rows before a sequence's first token (more rows than
+ *                  lens[b]) are not cached, attend to nothing and read as zeros.
+ * A page may be in the rows of several sequences as long as no call writes to
+ * it.  int32 and fp32 arrays need 4-byte alignment only.  T, B <= 2^20, and
+ * what a launch cannot count (2^24 workgroups) is AWQ_ERR_SHAPE.
+ * ------------------------------------------------------------------------ */
+
+typedef enum {
+    AWQ_ROPE_HALF = 0,        /* pairs of channels (i, i + rotary_dim / 2) */
+    AWQ_ROPE_INTERLEAVED = 1  /* pairs (2i, 2i + 1)                        */
+} awq_rope_layout;
+
+typedef enum {
+    AWQ_ROPE_PLAIN = 0,       /* f[i] = base^(-2i / rotary_dim)                       */
+    AWQ_ROPE_LINEAR = 1,      /* f[i] / factor                                        */
+    AWQ_ROPE_BASE = 2,        /* base * factor^(rotary_dim / (rotary_dim - 2))        */
+    AWQ_ROPE_YARN = 3,        /* f[i] kept for channels that turn `high` times or more
+                               * in original_length, divided by factor for those that
+                               * turn `low` times or fewer, a ramp over i between; the
+                               * magnitude is 0.1 ln(factor) + 1                      */
+    AWQ_ROPE_BANDS = 4        /* the same ends, a ramp over the number of turns
+                               * (original_length * f / 2 pi); magnitude 1            */
+} awq_rope_scaling;
+
+/*
+ * awq_rope_frequencies -- the rotary_dim / 2 inverse frequencies of a rotary
+ * embedding and the magnitude of its rotations, on the HOST (both outputs are
+ * HOST arrays).  rotary_dim even, at most 512; base > 1; factor >= 1 unless
+ * AWQ_ROPE_PLAIN; original_length > 0 and high > low > 0 for AWQ_ROPE_YARN and
+ * AWQ_ROPE_BANDS (ignored otherwise), else AWQ_ERR_UNSUPPORTED.
+ */
+awq_status awq_rope_frequencies(int rotary_dim, double base, int scaling, double factor,
+                                double original_length, double low, double high,
+                                float* inv_freq, float* magnitude);
+
+/*
+ * awq_rope -- rows turned by their positions: with t = positions[row] *
+ * inv_freq[i] and m = magnitude, each pair (a, b) of a head's first rotary_dim
+ * channels becomes
+ *   a' = m (a cos t - b sin t),   b' = m (b cos t + a sin t)
+ * (inverse = 1: by -t, the transposed map, which is also its gradient's); the
+ * other channels are copied.
+ *   x, out  dtype [T][heads][head_dim], heads and channels dense, rows x_stride
+ *   and out_stride elements apart (multiples of 8, at least heads * head_dim);
+ *   out may be x; otherwise they do not overlap.  positions int32 [T],
+ *   inv_freq fp32 [rotary_dim / 2].  head_dim a multiple of 16, at most 512,
+ *   rotary_dim a multiple of 16, at most head_dim (else AWQ_ERR_SHAPE).
+ *   Angles are taken in 64 bits, rotations in 32, one rounding to dtype.
+ */
+awq_status awq_rope(const void* x, long long x_stride, const int* positions, const float* inv_freq,
+                    float magnitude, void* out, long long out_stride, int T, int heads, int head_dim,
+                    int rotary_dim, int layout, int inverse, int dtype, hipStream_t stream);
+
+/*
+ * awq_cache_append -- new tokens into the cache, their queries and keys turned
+ * by their positions (awq_rope, with position = place in the sequence; inv_freq
+ * NULL: not turned).  For each page and kv head that new tokens x (keys in
+ * fp32 after the turn, values) fall into:
+ *   s' = max(s, max|x| / 127),  s the scale the block had, 0 if no token before
+ *        the new ones is in it
+ *   codes it held become rint(code * (s / s')), new ones are rint(x / s')
+ *   q  dtype [T][heads][head_dim] or NULL, k, v dtype [T][kv_heads][head_dim]:
+ *   rows q_stride, k_stride, v_stride elements apart as in awq_rope (parts of one
+ *   fused projection's rows);  q_out dtype [T][heads][head_dim] dense, may be q
+ *   where that is dense.
+ *   Every page that is written is in one sequence's row only.
+ */
+awq_status awq_cache_append(const void* q, long long q_stride, const void* k, long long k_stride,
+                            const void* v, long long v_stride, void* q_out, const float* inv_freq,
+                            float magnitude, int rotary_dim, int layout, void* k_codes,
+                            float* k_scales, void* v_codes, float* v_scales, const int* tables,
+                            const int* lens, const int* starts, int T, int B, int W, int heads,
+                            int kv_heads, int head_dim, int pages, int page_size, int dtype,
+                            hipStream_t stream);
+
+/*
+ * awq_cache_read -- the sequences' last rows as the values that the cache holds
+ * for them, code * scale rounded to dtype: k_out, v_out [T][kv_heads][head_dim].
+ */
+awq_status awq_cache_read(const void* k_codes, const float* k_scales, const void* v_codes,
+                          const float* v_scales, const int* tables, const int* lens,
+                          const int* starts, int T, int B, int W, int kv_heads, int head_dim,
+                          int pages, int page_size, int dtype, void* k_out, void* v_out,
+                          hipStream_t stream);
+
+/*
+ * awq_cache_attention -- attention of each sequence's last tokens over its cache:
+ *   s_j = scale * q.k_j, or softcap * tanh(scale * q.k_j / softcap) with softcap > 0
+ *   out = sum_j p_j v_j,  p = softmax over the keys j <= the query's place (and
+ *         j > place - window with window > 0)
+ *   lse = ln sum_j exp(s_j)
+ *   Query head h reads kv head h / (heads / kv_heads).  A query with no key has
+ *   out 0 and lse -infinity.
+ *   q dtype [T][heads][head_dim], rows q_stride elements apart as in awq_rope; out
+ *   dtype [T][heads][head_dim] dense; lse fp32 [T][heads] or NULL.
+ *   Scores, softmax and sums are fp32 over the exact codes; softmax weights
+ *   (times the block's value scale, relative to the largest) are rounded to fp16
+ *   for the product with the values.
+ *   max_new, max_len: bounds of a sequence's rows and tokens that the host knows;
+ *   they choose among kernels, and larger sequences are still right.
+ *   workspace / workspace_bytes: device scratch of at least
+ *   awq_cache_attention_workspace_bytes(T, B, heads, kv_heads, head_dim, max_new,
+ *   max_len) bytes on the current device, 16-byte aligned (may be NULL when that is 0).
+ *   The same inputs give the same bits on the same kind of device.
+ */
+size_t awq_cache_attention_workspace_bytes(int T, int B, int heads, int kv_heads, int head_dim,
+                                           int max_new, int max_len);
+awq_status awq_cache_attention(const void* q, long long q_stride, const void* k_codes,
+                               const float* k_scales, const void* v_codes, const float* v_scales,
+                               const int* tables, const int* lens, const int* starts, void* out,
+                               float* lse, float scale, int window, float softcap, int T, int B,
+                               int W, int heads, int kv_heads, int head_dim, int pages,
+                               int page_size, int max_new, int max_len, int dtype, void* workspace,
+                               size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * The book of a cache whose pages sequences share: tables and lens as above
+ * (ceil(lens[b] / page_size) entries of row b count, B <= 65535) and refs int32
+ * [pages], the number of rows that hold each page (0: free; a caller that keeps
+ * a page for other ends adds one).  pages <= 2^30.
+ *
+ * awq_cache_fork -- rows from their parents: out row b is a copy of row
+ * parents[b] (-1 or any other index outside 0..B-1: an empty row), all at once:
+ * beams forked, reordered and dropped.  Every old row gives its references back
+ * and every new one takes its own.  Entries behind a row's pages are -1.
+ *   tables [B][W], lens [B]; parents [B_out]; out_tables [B_out][W], out_lens
+ *   [B_out] (not `tables`, `lens`).
+ *
+ * awq_cache_reserve -- room for counts[b] more tokens in each row: lens[b] grows
+ * by it, new pages are the lowest free ones in the order of the rows.  A partly
+ * filled last page that other rows hold too (refs > 1) is not written: the row
+ * gets a fresh page in its place (before its other new pages), and pairs[b] =
+ * (old page, fresh page) asks for the copy (awq_cache_copy_pages); other pairs
+ * are (-1, -1).  Where only rows of this call hold the page and all of them
+ * grow, the first of them keeps it.
+ *   status[0] = pages that were missing, status[1] = rows that would pass W pages
+ *   (or 2^31 tokens).  If either is not 0, no row, length or count has changed.
+ *   counts [B] >= 0 (negative: 0), pairs [B][2], status [2]; B <= 4096 (else
+ *   AWQ_ERR_UNSUPPORTED).
+ *
+ * awq_cache_compact -- used pages (refs > 0) to the front: of U used pages, the
+ * k-th with an index >= U moves to the k-th free one below U.  tables and refs
+ * follow; moves [pages][2] lists (old, new) in order and (-1, -1) behind, count
+ * [1] their number, for awq_cache_copy_pages.
+ *
+ * awq_cache_copy_pages -- page src to page dst in every tensor and layer for
+ * each pair (src, dst) of pairs [max_pairs][2]; pairs with an index outside
+ * 0..pages-1 are passed over.  count: device int32, how many pairs there are, or
+ * NULL: max_pairs.  No dst may be another pair's src or dst.
+ *   tensors  HOST array of n_tensors (1..8) device pointers, each [layers][pages]
+ *   pages of page_bytes[t] (HOST array; multiples of 4, at most 2^30) bytes.
+ */
+awq_status awq_cache_fork(const int* tables, const int* lens, int* refs, const int* parents,
+                          int* out_tables, int* out_lens, int B, int B_out, int W, int pages,
+                          int page_size, hipStream_t stream);
+awq_status awq_cache_reserve(int* tables, int* lens, int* refs, const int* counts, int* pairs,
+                             int* status, int B, int W, int pages, int page_size,
+                             hipStream_t stream);
+awq_status awq_cache_compact(int* tables, const int* lens, int* refs, int* moves, int* count, int B,
+                             int W, int pages, int page_size, hipStream_t stream);
+awq_status awq_cache_copy_pages(void* const* tensors, const size_t* page_bytes, int n_tensors,
+                                int layers, const int* pairs, const int* count, int max_pairs,
+                                int pages, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -13,6 +13,9 @@ from .binding import (AwqError, quantize_pack, search_scale, search_scale_shared
                       fake_quantize,
                       norm_gate_residual, quantize_rows, gemm_w8a8, linear_w8a8,
                       gemm_w8a8_workspace_bytes, linear_w8a8_workspace_bytes, moe, moe_workspace_bytes,
+                      rope_frequencies, rope, empty_cache, cache_append, cache_read, cache_attention,
+                      cache_attention_workspace_bytes, cache_fork, cache_reserve, cache_compact,
+                      cache_copy_pages,
                       library_path,
                       load_library,
                       pack_format_version, packed_words_per_row, packed_words)
@@ -23,4 +26,6 @@ __all__ = ["AwqError", "quantize_pack", "search_scale", "search_scale_shared", "
            "gemm_splitk_noalloc", "gemm_splitk_noalloc_max_bytes", "scale_activations", "fake_quantize", "library_path", "load_library",
            "norm_gate_residual", "quantize_rows", "gemm_w8a8", "linear_w8a8",
            "gemm_w8a8_workspace_bytes", "linear_w8a8_workspace_bytes", "moe", "moe_workspace_bytes",
+           "rope_frequencies", "rope", "empty_cache", "cache_append", "cache_read", "cache_attention",
+           "cache_attention_workspace_bytes", "cache_fork", "cache_reserve", "cache_compact", "cache_copy_pages",
            "pack_format_version", "packed_words_per_row", "packed_words"]

@@ -8,6 +8,7 @@ device pointers and the current HIP stream.  A missing library raises
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -18,6 +19,8 @@ _c_void_p = ctypes.c_void_p
 _c_int = ctypes.c_int
 _c_size_t = ctypes.c_size_t
 _c_float = ctypes.c_float
+_c_double = ctypes.c_double
+_c_int64 = ctypes.c_int64
 
 # (name, restype, argtypes) for every exported symbol of include/awq.h
 SIGNATURES = [
@@ -72,6 +75,21 @@ SIGNATURES = [
                                  _c_int, _c_int, _c_void_p, _c_size_t, _c_void_p]),
     ("awq_moe_workspace_bytes", _c_size_t, [_c_int] * 5),
     ("awq_moe", _c_int, [_c_void_p] * 13 + [_c_int] * 8 + [_c_void_p, _c_size_t, _c_void_p]),
+    ("awq_rope_frequencies", _c_int, [_c_int, _c_double, _c_int, _c_double, _c_double, _c_double, _c_double,
+                                      _c_void_p, _c_void_p]),
+    ("awq_rope", _c_int, [_c_void_p, _c_int64, _c_void_p, _c_void_p, _c_float, _c_void_p, _c_int64] + [_c_int] * 7
+     + [_c_void_p]),
+    ("awq_cache_append", _c_int, [_c_void_p, _c_int64] * 3 + [_c_void_p, _c_void_p, _c_float, _c_int, _c_int]
+     + [_c_void_p] * 7 + [_c_int] * 9 + [_c_void_p]),
+    ("awq_cache_read", _c_int, [_c_void_p] * 7 + [_c_int] * 8 + [_c_void_p] * 3),
+    ("awq_cache_attention_workspace_bytes", _c_size_t, [_c_int] * 7),
+    ("awq_cache_attention", _c_int, [_c_void_p, _c_int64] + [_c_void_p] * 9 + [_c_float, _c_int, _c_float]
+     + [_c_int] * 11 + [_c_void_p, _c_size_t, _c_void_p]),
+    ("awq_cache_fork", _c_int, [_c_void_p] * 6 + [_c_int] * 5 + [_c_void_p]),
+    ("awq_cache_reserve", _c_int, [_c_void_p] * 6 + [_c_int] * 4 + [_c_void_p]),
+    ("awq_cache_compact", _c_int, [_c_void_p] * 5 + [_c_int] * 4 + [_c_void_p]),
+    ("awq_cache_copy_pages", _c_int, [_c_void_p, _c_void_p, _c_int, _c_int, _c_void_p, _c_void_p, _c_int, _c_int,
+                                      _c_void_p]),
 ]
 
 STATUS = {0: "AWQ_OK", 1: "AWQ_ERR_NULL", 2: "AWQ_ERR_SHAPE", 3: "AWQ_ERR_UNSUPPORTED",
@@ -734,3 +752,323 @@ def moe(x, router, gate, up, down, inter: int, top_k: int, bits: int = 4, group_
                      int(renormalize), ws, ws_bytes, _raw_stream(dev))
     _check(st, "awq_moe")
     return out
+
+
+# ---------------------------------------------------------------------------
+# rotary positions and the paged 8-bit cache
+#
+# A layer's cache is (k_codes int8 [pages][kv][page][dim], k_scales fp32
+# [pages][kv], v_codes, v_scales); a call's sequences are tables int32 [B][W],
+# lens int32 [B] and starts int32 [B + 1] (or None: one row each), as in awq.h.
+# ---------------------------------------------------------------------------
+_NO_GUARD = contextlib.nullcontext()
+
+
+def _call(name, device, *args):
+    """The library's call with GPU `device` the current one; its status raises."""
+    torch = _torch()
+    fn = getattr(load_library(), name)
+    if torch._C._cuda_getDevice() == device:
+        st = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args)
+    _check(st, name)
+
+
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {None: 0, "linear": 1, "base": 2, "yarn": 3, "bands": 4}
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling=None, factor: float = 1.0,
+                     original_length: float = 0.0, low: float = 1.0, high: float = 32.0, device="cuda"):
+    """(inv_freq fp32 [rotary_dim / 2] on `device`, magnitude) of a rotary
+    embedding (awq_rope_frequencies): scaling None, "linear", "base" (a larger
+    base), "yarn" or "bands" (frequencies that turn `high` times or more in
+    original_length are kept, those that turn `low` times or fewer are divided by
+    factor; a ramp over the channels, or over the number of turns)."""
+    torch = _torch()
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {list(ROPE_SCALINGS)}, got {scaling!r}")
+    inv_freq, magnitude = (_c_float * max(rotary_dim // 2, 1))(), _c_float()
+    st = load_library().awq_rope_frequencies(rotary_dim, base, ROPE_SCALINGS[scaling], factor, original_length, low,
+                                             high, inv_freq, ctypes.byref(magnitude))
+    _check(st, "awq_rope_frequencies")
+    return torch.tensor(list(inv_freq), dtype=torch.float32).to(device), float(magnitude.value)
+
+
+def _heads3d(t, dtype, device, name):
+    """(address, row stride) of a GPU tensor [T][heads][dim] of dense rows."""
+    try:
+        if t.dtype is dtype and t.dim() == 3 and t.get_device() == device >= 0:
+            T, h, d = t.shape
+            row, head, channel = t.stride()
+            if (channel == 1 or d == 1) and (head == d or h == 1):
+                return t.data_ptr(), row if T > 1 else -(-h * d // 8) * 8
+    except AttributeError:
+        pass
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have 3 dimensions [rows][heads][channels], got shape {tuple(t.shape)}")
+    if t.get_device() != device or device < 0:
+        raise ValueError(f"{name} must be on the GPU" + (f" {device}, got {t.device}" if device >= 0 else ""))
+    raise ValueError(f"{name}'s rows must be dense (heads x channels), got strides {t.stride()}")
+
+
+def _gpu_of(t, name):
+    """The index of the GPU that t is on."""
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    device = t.get_device()
+    if device < 0:
+        raise ValueError(f"{name} must be on the GPU")
+    return device
+
+
+def _layout(layout):
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}, got {layout!r}")
+    return ROPE_LAYOUTS[layout]
+
+
+def rope(x, positions, inv_freq, layout: str = "half", magnitude: float = 1.0, inverse: bool = False, out=None):
+    """Rows turned by their positions (awq_rope): x fp16 or bf16 [T][heads][dim]
+    (dense rows, which may be apart: a part of a fused projection), positions
+    int32 [T], inv_freq fp32 [rotary / 2] as rope_frequencies gives it; the first
+    rotary channels of each head are turned.  inverse turns back, which is also
+    the gradient.  out may be x."""
+    torch = _torch()
+    dev = _gpu_of(x, "x")
+    dtype = x.dtype
+    code = _dtype_code(dtype, "x")
+    x_at, x_stride = _heads3d(x, dtype, dev, "x")
+    T, heads, dim = x.shape
+    if out is None:
+        out = x.new_empty((T, heads, dim))
+    elif out.shape != x.shape:
+        raise ValueError(f"out must have shape {tuple(x.shape)}, got {tuple(out.shape)}")
+    out_at, out_stride = _heads3d(out, dtype, dev, "out")
+    n = inv_freq.numel()
+    _call("awq_rope", dev, x_at, x_stride, _arg(positions, torch.int32, (T,), dev, "positions"),
+          _arg(inv_freq, torch.float32, (n,), dev, "inv_freq"), magnitude, out_at, out_stride, T, heads, dim, 2 * n,
+          _layout(layout), int(inverse), code, _raw_stream(dev))
+    return out
+
+
+def empty_cache(pages: int, kv_heads: int, page_size: int, head_dim: int, layers=None, device="cuda"):
+    """(k_codes, k_scales, v_codes, v_scales) of zeros, with a leading dimension of
+    `layers` if given (a layer's cache is then each tensor's slice of it)."""
+    torch = _torch()
+    lead = (pages,) if layers is None else (layers, pages)
+    return tuple(t for _ in range(2) for t in (
+        torch.zeros((*lead, kv_heads, page_size, head_dim), dtype=torch.int8, device=device),
+        torch.zeros((*lead, kv_heads), dtype=torch.float32, device=device)))
+
+
+def _cache_args(cache, device):
+    """(addresses, (pages, kv heads, page size, head dim)) of a layer's cache on GPU `device`."""
+    torch = _torch()
+    k, ks, v, vs = cache
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("cache must be (k_codes [pages][kv][page][dim], k_scales [pages][kv], v_codes, v_scales)")
+    shape = k.shape
+    few = shape[:2]
+    return (_arg(k, torch.int8, shape, device, "k_codes"), _arg(ks, torch.float32, few, device, "k_scales"),
+            _arg(v, torch.int8, shape, device, "v_codes"), _arg(vs, torch.float32, few, device, "v_scales")), shape
+
+
+def _sequence_args(tables, lens, starts, device):
+    """(addresses, B, W) of a call's sequences."""
+    torch = _torch()
+    if not isinstance(tables, torch.Tensor) or tables.dim() != 2:
+        raise ValueError("tables must be an int32 tensor [sequences][pages]")
+    B, W = tables.shape
+    return (_arg(tables, torch.int32, (B, W), device, "tables"), _arg(lens, torch.int32, (B,), device, "lens"),
+            _optional(starts, torch.int32, (B + 1,), device, "starts")), B, W
+
+
+def cache_append(q, k, v, cache, tables, lens, starts=None, inv_freq=None, layout: str = "half",
+                 magnitude: float = 1.0, out=None):
+    """New tokens into the cache (awq_cache_append): k, v fp16 or bf16
+    [T][kv][dim] become codes with one scale for each page and head, k turned by
+    its place in the sequence if inv_freq is given, as is q [T][heads][dim] (or
+    None).  lens counts the new tokens.  Returns the turned q (`out` if given)."""
+    torch = _torch()
+    dev = _gpu_of(k, "k")
+    dtype = k.dtype
+    code = _dtype_code(dtype, "k")
+    k_at, k_stride = _heads3d(k, dtype, dev, "k")
+    T, kv, dim = k.shape
+    v_at, v_stride = _heads3d(v, dtype, dev, "v")
+    if v.shape != k.shape:
+        raise ValueError(f"v must have shape {tuple(k.shape)}, got {tuple(v.shape)}")
+    codes, (pages, c_kv, page, c_dim) = _cache_args(cache, dev)
+    if (c_kv, c_dim) != (kv, dim):
+        raise ValueError(f"k has {kv} heads of {dim}, the cache {c_kv} of {c_dim}")
+    seqs, B, W = _sequence_args(tables, lens, starts, dev)
+    q_at = out_at = None
+    q_stride = heads = 0
+    if q is not None:
+        q_at, q_stride = _heads3d(q, dtype, dev, "q")
+        heads = q.shape[1]
+        if q.shape[0] != T or q.shape[2] != dim:
+            raise ValueError(f"q must have shape ({T}, heads, {dim}), got {tuple(q.shape)}")
+        if out is None:
+            out = q.new_empty((T, heads, dim))
+        out_at = _arg(out, dtype, (T, heads, dim), dev, "out")
+    freq_at, rotary = None, 0
+    if inv_freq is not None:
+        rotary = 2 * inv_freq.numel()
+        freq_at = _arg(inv_freq, torch.float32, (rotary // 2,), dev, "inv_freq")
+    _call("awq_cache_append", dev, q_at, q_stride, k_at, k_stride, v_at, v_stride, out_at, freq_at, magnitude, rotary,
+          _layout(layout), *codes, *seqs, T, B, W, heads, kv, dim, pages, page, code, _raw_stream(dev))
+    return out if q is not None else None
+
+
+def cache_read(cache, tables, lens, starts=None, tokens=None, dtype=None, out=None):
+    """The last starts[b + 1] - starts[b] tokens of each sequence as the values the
+    cache holds (awq_cache_read): (k, v) of `dtype` (default torch.float16)
+    [tokens][kv][dim].  tokens: the rows of the call (default: one a sequence)."""
+    torch = _torch()
+    dev = _gpu_of(tables, "tables")
+    codes, (pages, kv, page, dim) = _cache_args(cache, dev)
+    seqs, B, W = _sequence_args(tables, lens, starts, dev)
+    if tokens is None:
+        if starts is not None:
+            raise ValueError("starts needs tokens, the number of rows")
+        tokens = B
+    if out is None:
+        dtype = dtype or torch.float16
+        code = _dtype_code(dtype, "dtype")
+        k, v = (cache[0].new_empty((tokens, kv, dim), dtype=dtype) for _ in range(2))
+    else:
+        k, v = out
+        dtype = k.dtype
+        code = _dtype_code(dtype, "out[0]")
+    _call("awq_cache_read", dev, *codes, *seqs, tokens, B, W, kv, dim, pages, page, code,
+          _arg(k, dtype, (tokens, kv, dim), dev, "out[0]"), _arg(v, dtype, (tokens, kv, dim), dev, "out[1]"),
+          _raw_stream(dev))
+    return k, v
+
+
+def cache_attention_workspace_bytes(tokens: int, sequences: int, heads: int, kv_heads: int, head_dim: int,
+                                    max_new: int, max_len: int) -> int:
+    """Workspace bytes of cache_attention (0: none) on the current device."""
+    return int(load_library().awq_cache_attention_workspace_bytes(tokens, sequences, heads, kv_heads, head_dim,
+                                                                  max_new, max_len))
+
+
+def cache_attention(q, cache, tables, lens, starts=None, scale=None, window: int = 0, softcap: float = 0.0,
+                    max_new=None, max_len=None, lse=None, out=None, workspace=None):
+    """Attention of each sequence's last tokens over its cached keys and values
+    (awq_cache_attention): q fp16 or bf16 [T][heads][dim], causal, within `window`
+    keys (0: all), scores scale * q.k (default dim^-1/2) capped by softcap (0:
+    not).  max_new, max_len: the most rows and tokens of a sequence, if known (they
+    choose the kernel; default T, or 1 without starts, and the table's).  lse: fp32
+    [T][heads] to write, or None.  Returns out, [T][heads][dim] like q."""
+    torch = _torch()
+    dev = _gpu_of(q, "q")
+    dtype = q.dtype
+    code = _dtype_code(dtype, "q")
+    q_at, q_stride = _heads3d(q, dtype, dev, "q")
+    T, heads, dim = q.shape
+    codes, (pages, kv, page, c_dim) = _cache_args(cache, dev)
+    if c_dim != dim:
+        raise ValueError(f"q has heads of {dim} channels, the cache of {c_dim}")
+    seqs, B, W = _sequence_args(tables, lens, starts, dev)
+    if max_new is None:
+        max_new = max(T, 1) if starts is not None else 1
+    if max_len is None:
+        max_len = W * page
+    if out is None:
+        out = q.new_empty((T, heads, dim))
+        out_at = out.data_ptr()
+    else:
+        out_at = _arg(out, dtype, (T, heads, dim), dev, "out")
+    lse_at = _optional(lse, torch.float32, (T, heads), dev, "lse")
+    with torch.cuda.device(dev) if torch._C._cuda_getDevice() != dev else _NO_GUARD:
+        need = load_library().awq_cache_attention_workspace_bytes(T, B, heads, kv, dim, max_new, max_len)
+    keep, ws, ws_bytes = _workspace(workspace, need, q)
+    _call("awq_cache_attention", dev, q_at, q_stride, *codes, *seqs, out_at, lse_at,
+          dim ** -0.5 if scale is None else scale, window, softcap, T, B, W, heads, kv, dim, pages, page, max_new,
+          max_len, code, ws, ws_bytes, _raw_stream(dev))
+    return out
+
+
+def _book_args(tables, lens, refs):
+    """(addresses, device, B, W, pages) of a cache's book."""
+    torch = _torch()
+    dev = _gpu_of(tables, "tables")
+    (t_at, l_at, _), B, W = _sequence_args(tables, lens, None, dev)
+    return (t_at, l_at, _arg(refs, torch.int32, (refs.numel(),), dev, "refs")), dev, B, W, refs.numel()
+
+
+def cache_fork(tables, lens, refs, parents, page_size: int, out=None):
+    """Table rows from their parents, all at once (awq_cache_fork): row b of the
+    result is row parents[b] (-1: an empty row).  refs, int32 [pages], follows in
+    place.  Returns (tables, lens) of parents' length (`out` if given)."""
+    torch = _torch()
+    book, dev, B, W, pages = _book_args(tables, lens, refs)
+    n = parents.numel()
+    if out is None:
+        new_tables, new_lens = tables.new_empty((n, W)), lens.new_empty(n)
+    else:
+        new_tables, new_lens = out
+    _call("awq_cache_fork", dev, *book, _arg(parents, torch.int32, (n,), dev, "parents"),
+          _arg(new_tables, torch.int32, (n, W), dev, "out[0]"), _arg(new_lens, torch.int32, (n,), dev, "out[1]"), B, n,
+          W, pages, page_size, _raw_stream(dev))
+    return new_tables, new_lens
+
+
+def cache_reserve(tables, lens, refs, counts, page_size: int, out=None):
+    """Room for counts[b] more tokens in every row, in place (awq_cache_reserve).
+    Returns (pairs int32 [B][2]: the pages to copy before they are written, for
+    cache_copy_pages; status int32 [2]: pages missing, rows past the table -- if
+    either is not 0 nothing has changed)."""
+    torch = _torch()
+    book, dev, B, W, pages = _book_args(tables, lens, refs)
+    pairs, status = (tables.new_empty((B, 2)), lens.new_empty(2)) if out is None else out
+    _call("awq_cache_reserve", dev, *book, _arg(counts, torch.int32, (B,), dev, "counts"),
+          _arg(pairs, torch.int32, (B, 2), dev, "out[0]"), _arg(status, torch.int32, (2,), dev, "out[1]"), B, W, pages,
+          page_size, _raw_stream(dev))
+    return pairs, status
+
+
+def cache_compact(tables, lens, refs, page_size: int, out=None):
+    """Used pages moved to the front of the cache (awq_cache_compact); tables and
+    refs follow in place.  Returns (moves int32 [pages][2], count int32 [1]) for
+    cache_copy_pages."""
+    torch = _torch()
+    book, dev, B, W, pages = _book_args(tables, lens, refs)
+    moves, count = (refs.new_empty((pages, 2)), refs.new_empty(1)) if out is None else out
+    _call("awq_cache_compact", dev, *book, _arg(moves, torch.int32, (pages, 2), dev, "out[0]"),
+          _arg(count, torch.int32, (1,), dev, "out[1]"), B, W, pages, page_size, _raw_stream(dev))
+    return moves, count
+
+
+def cache_copy_pages(tensors, pairs, count=None, layers=None):
+    """Page pairs[i][0] to page pairs[i][1] in every tensor, in place
+    (awq_cache_copy_pages).  tensors: up to 8, each [pages][...], or
+    [layers][pages][...] with layers given; pairs int32 [n][2], entries outside
+    the cache are passed over; count int32 [1] on the GPU: how many pairs there
+    are (None: all)."""
+    torch = _torch()
+    tensors = list(tensors)
+    shape, dev = _rows2d(pairs, "pairs")
+    lead = 0 if layers is None else 1
+    if not tensors or tensors[0].dim() <= lead or 0 in tensors[0].shape:
+        raise ValueError("tensors must hold at least one tensor of at least one page")
+    n = len(tensors)
+    at, size = (_c_void_p * n)(), (_c_size_t * n)()
+    pages = tensors[0].shape[lead]
+    for i, t in enumerate(tensors):
+        if t.dim() <= lead or t.shape[lead] != pages or (lead and t.shape[0] != layers):
+            raise ValueError(f"tensors[{i}] must be [{'layers][' if lead else ''}pages][...], got {tuple(t.shape)}")
+        at[i] = _arg(t, t.dtype, t.shape, dev, f"tensors[{i}]")
+        size[i] = t.numel() // (pages * (layers if lead else 1)) * t.element_size()
+    _call("awq_cache_copy_pages", dev, at, size, n, layers if lead else 1,
+          _arg(pairs, torch.int32, (shape[0], 2), dev, "pairs"), _optional(count, torch.int32, (1,), dev, "count"),
+          shape[0], pages, _raw_stream(dev))

@@ -1,8 +1,9 @@
 // C ABI of libawq: argument validation on the host, then dispatch to the
 // kernel launchers.  Nothing here touches the GPU before every argument has
 // been checked, so invalid calls never launch and never write an output.
-#include "awq_internal.h"
+#include "cache.h"
 
+#include <math.h>
 #include <mutex>
 
 namespace {
@@ -528,6 +529,272 @@ awq_status awq_moe(const void* x, const float* inv_s, const void* router, const 
                       {gate_scales, up_scales, down_scales}, {gate_zeros, up_zeros, down_zeros}, y, M, K, I, E,
                       top_k, bits, group_size, renormalize};
     return hip_status(awq::launch_moe(p, workspace, stream));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// rotary positions and the paged 8-bit cache
+// ---------------------------------------------------------------------------
+namespace {
+constexpr int kMaxRopeDim = 512;
+constexpr long long kMaxGroups = 1LL << 24;      // workgroups of 256 threads: a launch counts threads in 32 bits
+constexpr int kMaxCacheRows = 1 << 20;           // rows (tokens) and sequences of a call
+constexpr int kMaxBookRows = 65535;              // table rows are a launch's second dimension
+constexpr int kMaxPages = 1 << 30;
+
+// index arrays are int32 and need no more than their own alignment
+int check_index(std::initializer_list<const void*> ps) {
+    for (const void* p : ps) if (p == nullptr) return AWQ_ERR_NULL;
+    for (const void* p : ps) if (reinterpret_cast<uintptr_t>(p) & 3u) return AWQ_ERR_ALIGN;
+    return AWQ_OK;
+}
+
+// rows of `heads` heads, `stride` elements apart
+int check_stride(long long stride, int heads, int dim) {
+    return stride < (long long)heads * dim || stride % 8 != 0 ? AWQ_ERR_SHAPE : AWQ_OK;
+}
+
+int check_rotation(const float* inv_freq, int rotary_dim, int dim, int layout, float magnitude) {
+    if (inv_freq == nullptr) return AWQ_OK;
+    if (layout != AWQ_ROPE_HALF && layout != AWQ_ROPE_INTERLEAVED) return AWQ_ERR_UNSUPPORTED;
+    if (!isfinite(magnitude)) return AWQ_ERR_UNSUPPORTED;
+    if (rotary_dim <= 0 || rotary_dim % 16 != 0 || rotary_dim > dim) return AWQ_ERR_SHAPE;
+    return reinterpret_cast<uintptr_t>(inv_freq) & 3u ? AWQ_ERR_ALIGN : AWQ_OK;
+}
+
+awq::Rotation rotation(const float* inv_freq, int rotary_dim, int layout, float magnitude, int inverse) {
+    return {inv_freq, magnitude, inv_freq ? rotary_dim / 2 : 0, layout == AWQ_ROPE_INTERLEAVED, inverse};
+}
+
+int check_page(int page_size) {
+    return page_size == 16 || page_size == 32 || page_size == 64 || page_size == 128 ? AWQ_OK : AWQ_ERR_UNSUPPORTED;
+}
+
+int check_cache(int kv_heads, int dim, int pages, int page_size) {
+    if (int st = check_page(page_size)) return st;
+    if (dim != 64 && dim != 96 && dim != 128 && dim != 192 && dim != 256) return AWQ_ERR_UNSUPPORTED;
+    return kv_heads <= 0 || pages <= 0 || pages > kMaxPages ? AWQ_ERR_SHAPE : AWQ_OK;
+}
+
+// T rows of B sequences with tables of W pages; without starts every sequence has one row
+int check_sequences(const int* starts, int T, int B, int W) {
+    if (T < 0 || B < 0 || W <= 0 || T > kMaxCacheRows || B > kMaxCacheRows) return AWQ_ERR_SHAPE;
+    return starts == nullptr && T != B ? AWQ_ERR_SHAPE : AWQ_OK;
+}
+
+int log2_of(int page_size) { return __builtin_ctz((unsigned)page_size); }
+
+awq::Cache cache_of(const void* k, const float* ks, const void* v, const float* vs, int pages, int kv, int page_size,
+                    int dim) {
+    return {{(int8_t*)k, (int8_t*)v}, {(float*)ks, (float*)vs}, pages, kv, log2_of(page_size), dim};
+}
+
+int check_attention(int T, int B, int W, int heads, int kv_heads, int dim, int pages, int page_size, int max_new,
+                    int max_len) {
+    if (int st = check_cache(kv_heads, dim, pages, page_size)) return st;
+    if (T < 0 || B < 0 || W <= 0 || T > kMaxCacheRows || B > kMaxCacheRows) return AWQ_ERR_SHAPE;
+    if (heads <= 0 || heads % kv_heads != 0 || max_new <= 0 || max_len <= 0) return AWQ_ERR_SHAPE;
+    // one workgroup for each row and head joins, one for each tile of rows computes
+    return (long long)T * heads >= kMaxGroups || ((long long)T * (heads / kv_heads) / 16 + B) * kv_heads >= kMaxGroups
+               ? AWQ_ERR_SHAPE : AWQ_OK;
+}
+
+int check_book(int B, int W, int pages, int page_size) {
+    if (int st = check_page(page_size)) return st;
+    return B < 0 || B > kMaxBookRows || W <= 0 || pages <= 0 || pages > kMaxPages ? AWQ_ERR_SHAPE : AWQ_OK;
+}
+}  // namespace
+
+extern "C" {
+
+awq_status awq_rope_frequencies(int rotary_dim, double base, int scaling, double factor, double original_length,
+                                double low, double high, float* inv_freq, float* magnitude) {
+    if (inv_freq == nullptr || magnitude == nullptr) return AWQ_ERR_NULL;
+    if (rotary_dim <= 0 || rotary_dim % 2 != 0 || rotary_dim > kMaxRopeDim) return AWQ_ERR_SHAPE;
+    if (!(base > 1.0) || !isfinite(base)) return AWQ_ERR_UNSUPPORTED;
+    if (scaling < AWQ_ROPE_PLAIN || scaling > AWQ_ROPE_BANDS) return AWQ_ERR_UNSUPPORTED;
+    if (scaling != AWQ_ROPE_PLAIN && (!(factor >= 1.0) || !isfinite(factor))) return AWQ_ERR_UNSUPPORTED;
+    if (scaling == AWQ_ROPE_BASE && rotary_dim <= 2) return AWQ_ERR_SHAPE;
+    const bool parts = scaling == AWQ_ROPE_YARN || scaling == AWQ_ROPE_BANDS;
+    if (parts && (!(original_length > 0.0) || !(low > 0.0) || !(high > low))) return AWQ_ERR_UNSUPPORTED;
+    const int n = rotary_dim / 2;
+    const double two_pi = 6.283185307179586476925;
+    if (scaling == AWQ_ROPE_BASE) base *= pow(factor, (double)rotary_dim / (rotary_dim - 2));
+    *magnitude = scaling == AWQ_ROPE_YARN ? (float)(0.1 * log(factor) + 1.0) : 1.0f;
+    for (int i = 0; i < n; ++i) {
+        const double f = pow(base, -(double)i / n);
+        double keep = 1.0;                       // the share of the unscaled frequency
+        if (scaling == AWQ_ROPE_LINEAR) keep = 0.0;
+        if (scaling == AWQ_ROPE_BANDS) keep = (original_length * f / two_pi - low) / (high - low);
+        if (scaling == AWQ_ROPE_YARN) {          // a ramp over the channels between those that turn high and low times
+            const double from = n * log(original_length / (high * two_pi)) / log(base);
+            const double to = n * log(original_length / (low * two_pi)) / log(base);
+            keep = 1.0 - (i - from) / (to - from);
+        }
+        keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
+        inv_freq[i] = (float)(f * keep + (keep < 1.0 ? f / factor * (1.0 - keep) : 0.0));
+    }
+    return AWQ_OK;
+}
+
+awq_status awq_rope(const void* x, long long x_stride, const int* positions, const float* inv_freq, float magnitude,
+                    void* out, long long out_stride, int T, int heads, int head_dim, int rotary_dim, int layout,
+                    int inverse, int dtype, hipStream_t stream) {
+    int st = check_dtype(dtype);
+    if (st) return as_status(st);
+    if (T < 0 || heads <= 0 || head_dim <= 0 || head_dim % 16 != 0 || head_dim > kMaxRopeDim) return AWQ_ERR_SHAPE;
+    if (T / 4 + 1 >= kMaxGroups) return AWQ_ERR_SHAPE;
+    if (inverse != 0 && inverse != 1) return AWQ_ERR_UNSUPPORTED;
+    if (inv_freq == nullptr && T > 0) return AWQ_ERR_NULL;
+    if ((st = check_rotation(inv_freq, rotary_dim, head_dim, layout, magnitude))) return as_status(st);
+    if ((st = check_stride(x_stride, heads, head_dim)) || (st = check_stride(out_stride, heads, head_dim)))
+        return as_status(st);
+    if (T == 0) return AWQ_OK;
+    if ((st = check_ptrs({x, out})) || (st = check_index({positions}))) return as_status(st);
+    const awq::RopeProblem p{x, x_stride, positions, out, out_stride,
+                             rotation(inv_freq, rotary_dim, layout, magnitude, inverse), T, heads, head_dim, dtype};
+    return hip_status(awq::launch_rope(p, stream));
+}
+
+awq_status awq_cache_append(const void* q, long long q_stride, const void* k, long long k_stride, const void* v,
+                            long long v_stride, void* q_out, const float* inv_freq, float magnitude, int rotary_dim,
+                            int layout, void* k_codes, float* k_scales, void* v_codes, float* v_scales,
+                            const int* tables, const int* lens, const int* starts, int T, int B, int W, int heads,
+                            int kv_heads, int head_dim, int pages, int page_size, int dtype, hipStream_t stream) {
+    int st = check_dtype(dtype);
+    if (st) return as_status(st);
+    if ((st = check_cache(kv_heads, head_dim, pages, page_size)) || (st = check_sequences(starts, T, B, W)))
+        return as_status(st);
+    if (q != nullptr && heads <= 0) return AWQ_ERR_SHAPE;
+    if ((st = check_rotation(inv_freq, rotary_dim, head_dim, layout, magnitude))) return as_status(st);
+    if (q != nullptr && (st = check_stride(q_stride, heads, head_dim))) return as_status(st);
+    if ((st = check_stride(k_stride, kv_heads, head_dim)) || (st = check_stride(v_stride, kv_heads, head_dim)))
+        return as_status(st);
+    // workgroups: rows by four for q, and two a kv head for every page that is reached
+    const long long items = starts ? (long long)T / page_size + 2LL * B : B;
+    if (T / 4 + 1 + 2 * (items < T ? items : T) * kv_heads >= kMaxGroups) return AWQ_ERR_SHAPE;
+    if (T == 0 || B == 0) return AWQ_OK;
+    if ((st = check_ptrs({k, v, k_codes, v_codes})) || (st = check_index({k_scales, v_scales, tables, lens})))
+        return as_status(st);
+    if (q != nullptr && (st = check_ptrs({q, q_out}))) return as_status(st);
+    if (starts != nullptr && (st = check_index({starts}))) return as_status(st);
+    const awq::AppendProblem p{q, k, v, q_stride, k_stride, v_stride, q_out,
+                               rotation(inv_freq, rotary_dim, layout, magnitude, 0),
+                               cache_of(k_codes, k_scales, v_codes, v_scales, pages, kv_heads, page_size, head_dim),
+                               awq::Sequences{tables, lens, starts, T, B, W}, heads, dtype};
+    return hip_status(awq::launch_cache_append(p, stream));
+}
+
+awq_status awq_cache_read(const void* k_codes, const float* k_scales, const void* v_codes, const float* v_scales,
+                          const int* tables, const int* lens, const int* starts, int T, int B, int W, int kv_heads,
+                          int head_dim, int pages, int page_size, int dtype, void* k_out, void* v_out,
+                          hipStream_t stream) {
+    int st = check_dtype(dtype);
+    if (st) return as_status(st);
+    if ((st = check_cache(kv_heads, head_dim, pages, page_size)) || (st = check_sequences(starts, T, B, W)))
+        return as_status(st);
+    if (T == 0 || B == 0) return AWQ_OK;
+    if ((st = check_ptrs({k_codes, v_codes, k_out, v_out})) || (st = check_index({k_scales, v_scales, tables, lens})))
+        return as_status(st);
+    if (starts != nullptr && (st = check_index({starts}))) return as_status(st);
+    const awq::ReadProblem p{cache_of(k_codes, k_scales, v_codes, v_scales, pages, kv_heads, page_size, head_dim),
+                             awq::Sequences{tables, lens, starts, T, B, W}, k_out, v_out, dtype};
+    return hip_status(awq::launch_cache_read(p, stream));
+}
+
+size_t awq_cache_attention_workspace_bytes(int T, int B, int heads, int kv_heads, int head_dim, int max_new,
+                                           int max_len) {
+    if (T <= 0 || B <= 0 || check_attention(T, B, 1, heads, kv_heads, head_dim, 1, 16, max_new, max_len) != AWQ_OK)
+        return 0;
+    return awq::attend_workspace_bytes(T, B, heads, kv_heads, head_dim, max_new, max_len);
+}
+
+awq_status awq_cache_attention(const void* q, long long q_stride, const void* k_codes, const float* k_scales,
+                               const void* v_codes, const float* v_scales, const int* tables, const int* lens,
+                               const int* starts, void* out, float* lse, float scale, int window, float softcap, int T,
+                               int B, int W, int heads, int kv_heads, int head_dim, int pages, int page_size,
+                               int max_new, int max_len, int dtype, void* workspace, size_t workspace_bytes,
+                               hipStream_t stream) {
+    int st = check_dtype(dtype);
+    if (st) return as_status(st);
+    if ((st = check_attention(T, B, W, heads, kv_heads, head_dim, pages, page_size, max_new, max_len)) ||
+        (st = check_sequences(starts, T, B, W)) || (st = check_stride(q_stride, heads, head_dim)))
+        return as_status(st);
+    if (!isfinite(scale) || window < 0 || !(softcap >= 0.0f) || !isfinite(softcap)) return AWQ_ERR_UNSUPPORTED;
+    if (T == 0 || B == 0) return AWQ_OK;
+    if ((st = check_ptrs({q, k_codes, v_codes, out})) || (st = check_index({k_scales, v_scales, tables, lens})))
+        return as_status(st);
+    if (starts != nullptr && (st = check_index({starts}))) return as_status(st);
+    if (lse != nullptr && (st = check_index({lse}))) return as_status(st);
+    if ((st = check_workspace(workspace, workspace_bytes,
+                              awq::attend_workspace_bytes(T, B, heads, kv_heads, head_dim, max_new, max_len))))
+        return as_status(st);
+    const awq::AttendProblem p{q, q_stride, out, lse,
+                               cache_of(k_codes, k_scales, v_codes, v_scales, pages, kv_heads, page_size, head_dim),
+                               awq::Sequences{tables, lens, starts, T, B, W}, scale, softcap, heads, window, max_new,
+                               max_len, dtype};
+    return hip_status(awq::launch_cache_attention(p, workspace, stream));
+}
+
+awq_status awq_cache_fork(const int* tables, const int* lens, int* refs, const int* parents, int* out_tables,
+                          int* out_lens, int B, int B_out, int W, int pages, int page_size, hipStream_t stream) {
+    int st = check_book(B, W, pages, page_size);
+    if (st) return as_status(st);
+    if (B_out < 0 || B_out > kMaxBookRows) return AWQ_ERR_SHAPE;
+    if (B == 0 && B_out == 0) return AWQ_OK;
+    if ((st = check_index({refs}))) return as_status(st);
+    if (B > 0 && (st = check_index({tables, lens}))) return as_status(st);
+    if (B_out > 0 && (st = check_index({parents, out_tables, out_lens}))) return as_status(st);
+    if (out_tables != nullptr && out_tables == tables) return AWQ_ERR_UNSUPPORTED;
+    return hip_status(awq::launch_cache_fork(tables, lens, refs, parents, out_tables, out_lens, B, B_out, W, pages,
+                                             log2_of(page_size), stream));
+}
+
+awq_status awq_cache_reserve(int* tables, int* lens, int* refs, const int* counts, int* pairs, int* status, int B,
+                             int W, int pages, int page_size, hipStream_t stream) {
+    int st = check_book(B, W, pages, page_size);
+    if (st) return as_status(st);
+    if (B > awq::kMaxReserveRows) return AWQ_ERR_UNSUPPORTED;
+    if ((st = check_index({status}))) return as_status(st);
+    if (B > 0 && (st = check_index({tables, lens, refs, counts, pairs}))) return as_status(st);
+    return hip_status(awq::launch_cache_reserve(tables, lens, refs, counts, pairs, status, B, W, pages,
+                                                log2_of(page_size), stream));
+}
+
+awq_status awq_cache_compact(int* tables, const int* lens, int* refs, int* moves, int* count, int B, int W, int pages,
+                             int page_size, hipStream_t stream) {
+    int st = check_book(B, W, pages, page_size);
+    if (st) return as_status(st);
+    if ((st = check_index({refs, moves, count}))) return as_status(st);
+    if (B > 0 && (st = check_index({tables, lens}))) return as_status(st);
+    return hip_status(awq::launch_cache_compact(tables, lens, refs, moves, count, B, W, pages, log2_of(page_size), stream));
+}
+
+awq_status awq_cache_copy_pages(void* const* tensors, const size_t* page_bytes, int n_tensors, int layers,
+                                const int* pairs, const int* count, int max_pairs, int pages, hipStream_t stream) {
+    if (n_tensors < 1 || n_tensors > awq::kMaxCopyTensors) return AWQ_ERR_UNSUPPORTED;
+    if (layers <= 0 || max_pairs < 0 || pages <= 0 || pages > kMaxPages) return AWQ_ERR_SHAPE;
+    if (tensors == nullptr || page_bytes == nullptr) return AWQ_ERR_NULL;
+    awq::CopyProblem p{};
+    for (int t = 0; t < n_tensors; ++t) {
+        if (page_bytes[t] == 0 || page_bytes[t] % 4 != 0 || page_bytes[t] > (size_t)1 << 30) return AWQ_ERR_SHAPE;
+        p.tensors[t] = (char*)tensors[t];
+        p.page_bytes[t] = page_bytes[t];
+    }
+    if (max_pairs == 0) return AWQ_OK;
+    int st = AWQ_OK;
+    for (int t = 0; t < n_tensors; ++t) if (tensors[t] == nullptr) return AWQ_ERR_NULL;
+    for (int t = 0; t < n_tensors; ++t) if ((st = check_ptr(tensors[t]))) return as_status(st);
+    if ((st = check_index({pairs}))) return as_status(st);
+    if (count != nullptr && (st = check_index({count}))) return as_status(st);
+    p.n = n_tensors;
+    p.layers = layers;
+    p.max_pairs = max_pairs;
+    p.pages = pages;
+    p.pairs = pairs;
+    p.count = count;
+    return hip_status(awq::launch_cache_copy_pages(p, stream));
 }
 
 }  // extern "C"

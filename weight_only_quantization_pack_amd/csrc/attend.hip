@@ -1,0 +1,657 @@
+// Attention of a sequence's last tokens over its cached keys and values.
+//
+//   s_j = scale * q.k_j            (or cap * tanh(that / cap))
+//   p = softmax(s) over the keys j at or before the query's position (and within
+//   the window);  o = sum_j p_j v_j
+//
+// Keys and values are int8 codes with one scale for each page and kv head, so a
+// step of 32 keys has one key scale ks and one value scale vs (two with 16-token
+// pages).  The running maximum M is taken over t = log2(e) s + log2(vs): the weight
+// w = exp2(t - M) is then what multiplies a value's code, and the softmax's sum is
+// the sum of w / vs.  One fused multiply-add a score brings ks, scale and vs in.
+//
+// Queries are the columns and keys the rows of a 16 x 16 x 32 product, so that a
+// lane ends with 8 consecutive keys of one query: exactly the operand that the
+// product with the values wants, with no exchange between lanes.  Codes become
+// fp16 operands by one byte permutation for two of them: code + 128 is put into
+// the low bits of an fp16 number, where it stands for (code + 128) 2^-24, exactly.
+// The bias leaves the scores through the product's initial value (-128 2^-24 times
+// the sum of q) and the output through one more product, of a constant with the
+// weights.  The keys' and values' bytes are read once, straight into registers.
+//
+// Work is cut evenly: all (sequence, head, tile of rows) with their steps of 32
+// keys form one line, and every workgroup takes an equal stretch of it.  Stretches
+// that end inside a tile leave (M, sum, o) in the workspace and a second launch
+// joins them in order.
+#include "cache.h"
+
+namespace awq {
+namespace {
+
+constexpr int kStep = 32;                // keys of a step
+constexpr int kW = 4;                    // waves of a workgroup
+constexpr float kLow = -1e30f;           // below every score: the maximum before the first key
+constexpr float kSlack = 8.0f;           // the maximum may lag by 2^8: weights stay far below fp16's maximum
+
+struct AttendArgs {
+    const uint16_t* q;
+    long long q_stride;
+    uint16_t* out;
+    float* lse;
+    Cache cache;
+    Sequences seqs;
+    float scale, softcap;                // |scale| 2^24, for the operands' unit; its sign goes into q
+    float sign;
+    int heads, group, window, bf16;
+    int split;                           // stretches may end inside a tile
+    int groups;                          // workgroups of the first launch
+    float* parts;                        // [groups][2][rows * (dim + 2)]
+};
+
+// the steps of a sequence: the same for all its tiles of rows (their own first and
+// last keys lie inside)
+struct Line {
+    int rows, tiles, step0, steps;
+    int len, n;
+    __device__ __forceinline__ Line(const AttendArgs& a, int b, int tile_rows) {
+        const Sequences& s = a.seqs;
+        n = s.rows(b);
+        len = s.len(b);
+        rows = n * a.group;
+        tiles = (rows + tile_rows - 1) / tile_rows;
+        const int span = s.span(b, a.cache.page_log2);
+        int first = 0;
+        if (a.window > 0) first = max((int)max((long long)len - n + 1 - a.window, 0LL), 0);
+        step0 = first / kStep;
+        steps = max((span + kStep - 1) / kStep - step0, 1);
+    }
+    __device__ __forceinline__ long long units(int kv) const { return (long long)tiles * kv * steps; }
+};
+
+// units a workgroup takes: an even share, but at least two steps for every wave
+__device__ __forceinline__ long long stretch(long long total, int groups) {
+    return max((total + groups - 1) / groups, (long long)(2 * kW));
+}
+
+// all units, and those before sequence b_stop; by one wave
+__device__ __forceinline__ void count_units(const AttendArgs& a, int tile_rows, int b_stop, long long& total,
+                                            long long& before) {
+    const int lane = threadIdx.x & 63;
+    total = before = 0;
+    for (int b0 = 0; b0 < a.seqs.B; b0 += 64) {
+        const int b = b0 + lane;
+        long long u = b < a.seqs.B ? Line(a, b, tile_rows).units(a.cache.kv) : 0;
+        long long v = b < b_stop ? u : 0;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            u += __shfl_xor(u, d);
+            v += __shfl_xor(v, d);
+        }
+        total += u;
+        before += v;
+    }
+}
+
+// the sequence that holds the unit at `at` (or, unsplit, the tile at `at`) and the
+// units (tiles) before it; -1 past the last.  By one wave.
+__device__ __forceinline__ int find_line(const AttendArgs& a, int tile_rows, bool tiles, long long at, long long& before) {
+    const int lane = threadIdx.x & 63;
+    before = 0;
+    for (int b0 = 0; b0 < a.seqs.B; b0 += 64) {
+        const int b = b0 + lane;
+        long long u = 0;
+        if (b < a.seqs.B) {
+            const Line l(a, b, tile_rows);
+            u = tiles ? (long long)l.tiles * a.cache.kv : l.units(a.cache.kv);
+        }
+        long long sum = u;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const long long o = __shfl_up(sum, d);
+            if (lane >= d) sum += o;
+        }
+        const long long all = __shfl(sum, 63);
+        if (at < before + all) {
+            const uint64_t hit = __builtin_amdgcn_ballot_w64(at < before + sum);
+            const int f = __builtin_ctzll(hit);
+            before += __shfl(sum - u, f);
+            return b0 + f;
+        }
+        before += all;
+    }
+    return -1;
+}
+
+// one step's codes of a wave: keys as 16 x 32 operands, values as 8 rows of D / 16
+template <int D>
+struct Codes {
+    static constexpr int VD = D == 96 ? 128 : D;   // 96 channels: 12 of 16 lanes hold 8 values each
+    static constexpr int NK = D / 32, VB = VD / 16, VW = VB / 4;
+    uint32_t k[2][NK][2];                          // [key tile][chunk]: 8 codes
+    uint32_t v[8][VW];                             // [key]: VB codes
+    float c[2], lv[2], iv[2];                      // per half of the step: ks scale 2^24 (< 0: no page), log2(vs), 1 / vs
+};
+
+__device__ __forceinline__ float lane_value(float v, int lane) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+
+// bytes i, i + 1 of w (biased codes) as two fp16 numbers of 2^-24 steps
+__device__ __forceinline__ uint32_t key_pair(uint32_t w, int i) {
+    return __builtin_amdgcn_perm(0u, w, i ? 0x0C030C02u : 0x0C010C00u);
+}
+// byte j of two rows' words
+__device__ __forceinline__ uint32_t value_pair(uint32_t lo, uint32_t hi, int j) {
+    return __builtin_amdgcn_perm(hi, lo, 0x0C000C00u | (uint32_t)(4 + j) << 16 | (uint32_t)j);
+}
+
+union Half8 {
+    uint32_t w[4];
+    half8_t h;
+};
+
+template <int D, int C, bool SMALL>
+__global__ __launch_bounds__(64 * kW) void k_attend(AttendArgs a) {
+    using K = Codes<D>;
+    constexpr int R = 16 * C, NK = K::NK, VB = K::VB, VW = K::VW;
+    constexpr int JB = VB > 8 ? VB / 2 : VB;       // channels of a lane that one pass of the join takes
+    __shared__ float join[kW][4][64][JB + 1];      // [wave][i][lane][j]; padded against bank conflicts
+    __shared__ float stat[kW][2][R];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 15, g = lane >> 4;
+    const Sequences& s = a.seqs;
+    const int kv = a.cache.kv, page_log2 = a.cache.page_log2;
+
+    // this workgroup's stretch [u, u_end)
+    long long u, u_end, before;
+    int b;
+    if (a.split) {
+        long long total, unused;
+        count_units(a, R, 0, total, unused);
+        const long long share = stretch(total, a.groups);
+        u = blockIdx.x * share;
+        u_end = min(u + share, total);
+        if (u >= u_end) return;
+        b = find_line(a, R, false, u, before);
+        u -= before;                               // from here on relative to sequence b
+        u_end -= before;
+    } else {
+        b = find_line(a, R, true, blockIdx.x, before);
+        if (b < 0) return;
+        const Line l(a, b, R);
+        u = (blockIdx.x - before) * l.steps;
+        u_end = u + l.steps;
+    }
+    b = __builtin_amdgcn_readfirstlane(b);
+    bool first_segment = true;
+
+    while (true) {
+        const Line l(a, b, R);
+        const long long units = l.units(kv);
+        if (u >= units) {                          // on to the next sequence
+            u -= units;
+            u_end -= units;
+            if (++b >= s.B || u >= u_end) return;
+            continue;
+        }
+        const int tile_at = __builtin_amdgcn_readfirstlane((int)(u / l.steps));
+        const int head = tile_at / l.tiles, tile = tile_at - head * l.tiles;
+        const int s0 = __builtin_amdgcn_readfirstlane((int)(u - (long long)tile_at * l.steps));
+        const int s1 = (int)min((long long)l.steps, s0 + (u_end - u));
+        const bool whole = s0 == 0 && s1 == l.steps;
+        u += s1 - s0;
+
+        // rows of the tile: column r of column tile ct is row 16 ct + r
+        int pos[C];
+        half8_t q[C][NK];
+        float qf[C];                               // what brings a column's products back to q.k
+        float4_t bias[C];
+#pragma unroll
+        for (int ct = 0; ct < C; ++ct) {
+            const int row = min(tile * R + 16 * ct + r, l.rows - 1);
+            const int j = row / a.group, h = head * a.group + (row - j * a.group);
+            pos[ct] = l.len - l.n + j;
+            const uint16_t* from = a.q + (size_t)(s.start(b) + j) * a.q_stride + (size_t)h * D;
+            uint4 raw[NK];
+#pragma unroll
+            for (int c = 0; c < NK; ++c)
+                raw[c] = *(const uint4*)(from + (NK % 2 == 1 && c == NK - 1 ? 32 * c + 8 * g : 64 * (c / 2) + 16 * g + 8 * (c & 1)));
+            // q times a power of two that brings its largest channel to 2^13: fp16 then
+            // holds all of its bits (bf16 has 8) down to 2^-27 of the largest
+            float f[NK][8], top = 0.0f;
+#pragma unroll
+            for (int c = 0; c < NK; ++c) {
+                if (a.bf16) unpack8<BF16>(raw[c], f[c]); else unpack8<F16>(raw[c], f[c]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[c][e]));
+            }
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            int e2 = 0;
+            if (top > 0.0f) e2 = 13 - ((int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127);
+            e2 = min(max(e2, -120), 120);
+            const float up = __builtin_bit_cast(float, (uint32_t)(127 + e2) << 23);
+            qf[ct] = __builtin_bit_cast(float, (uint32_t)(127 - e2) << 23);
+            float sum = 0.0f;
+#pragma unroll
+            for (int c = 0; c < NK; ++c)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    q[ct][c][e] = (_Float16)(f[c][e] * (up * a.sign));
+                    sum += (float)q[ct][c][e];
+                }
+            sum += __shfl_xor(sum, 16);
+            sum += __shfl_xor(sum, 32);
+            bias[ct] = float4_t{1, 1, 1, 1} * (sum * -0x1p-17f);
+        }
+        // positions of the tile's first and last row: what no key of a step needs a mask for
+        const int pos_lo = l.len - l.n + min(tile * R, l.rows - 1) / a.group;
+        const int pos_hi = l.len - l.n + min(tile * R + R - 1, l.rows - 1) / a.group;
+
+        float M[C], sum[C];
+        float4_t o[C][VB], obias[C];
+#pragma unroll
+        for (int ct = 0; ct < C; ++ct) {
+            M[ct] = kLow;
+            sum[ct] = 0.0f;
+            obias[ct] = float4_t{0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < VB; ++j) o[ct][j] = float4_t{0, 0, 0, 0};
+        }
+
+        // pages and scales of the wave's next 64 steps, one a lane
+        int page_l[2];
+        float c_l[2], lv_l[2], iv_l[2];
+        auto fetch_pages = [&](int i0) {           // the wave's steps i0 ..
+            const int step = s0 + wave + kW * (i0 + lane);
+#pragma unroll
+            for (int x = 0; x < (SMALL ? 2 : 1); ++x) {
+                const long long key = (long long)(l.step0 + step) * kStep + 16 * x;
+                const int p = step < s1 ? s.page(b, (int)(key >> page_log2), a.cache.pages) : -1;
+                page_l[x] = p;
+                const size_t at = (size_t)max(p, 0) * kv + head;
+                c_l[x] = p >= 0 ? a.cache.scales[0][at] * a.scale : -1.0f;
+                const float vs = p >= 0 ? fmaxf(a.cache.scales[1][at], 0x1p-100f) : 1.0f;
+                lv_l[x] = __builtin_amdgcn_logf(vs);
+                iv_l[x] = 1.0f / vs;
+            }
+        };
+        auto load = [&](K& d, int i) {             // the wave's step i
+            if ((i & 63) == 0) fetch_pages(i);
+            const int at = i & 63;
+            const int step = s0 + wave + kW * i;
+            const int slot = ((l.step0 + step) * kStep) & ((1 << page_log2) - 1);
+            const int8_t *kb[2], *vb[2];
+#pragma unroll
+            for (int x = 0; x < (SMALL ? 2 : 1); ++x) {
+                const int p = __builtin_amdgcn_readlane(page_l[x], at);
+                const size_t off = a.cache.block(max(p, 0), head) + (SMALL ? (size_t)0 : (size_t)slot * D);
+                kb[x] = a.cache.codes[0] + off;
+                vb[x] = a.cache.codes[1] + off;
+                d.c[x] = lane_value(c_l[x], at);
+                d.lv[x] = lane_value(lv_l[x], at);
+                d.iv[x] = lane_value(iv_l[x], at);
+            }
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int key = 8 * (r >> 2) + 4 * t + (r & 3);
+                const int8_t* row = SMALL ? (r < 8 ? kb[0] : kb[1]) + (uint32_t)((key & 15) * D) : kb[0] + (uint32_t)(key * D);
+#pragma unroll
+                for (int c = 0; c + 1 < NK; c += 2) {
+                    const uint4 w = *(const uint4*)(row + 32 * c + 16 * g);
+                    d.k[t][c][0] = w.x;
+                    d.k[t][c][1] = w.y;
+                    d.k[t][c + 1][0] = w.z;
+                    d.k[t][c + 1][1] = w.w;
+                }
+                if constexpr (NK % 2 == 1) {
+                    const uint2 w = *(const uint2*)(row + 32 * (NK - 1) + 8 * g);
+                    d.k[t][NK - 1][0] = w.x;
+                    d.k[t][NK - 1][1] = w.y;
+                }
+            }
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+                const int key = 8 * g + y;
+                const int8_t* row = SMALL ? (g < 2 ? vb[0] : vb[1]) + (uint32_t)((key & 15) * D) : vb[0] + (uint32_t)(key * D);
+                const int lr = D == 96 ? min(r, 11) : r;      // lanes 12.. repeat the last channels
+                const uint32_t* from = (const uint32_t*)(row + VB * lr);
+#pragma unroll
+                for (int x = 0; x < VW; ++x) d.v[y][x] = from[x];
+            }
+        };
+        auto compute = [&](K& d, int i) {
+            const int key0 = (l.step0 + s0 + wave + kW * i) * kStep;
+            // scores
+            float4_t sc[C][2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+#pragma unroll
+                for (int ct = 0; ct < C; ++ct) sc[ct][t] = bias[ct];
+#pragma unroll
+                for (int c = 0; c < NK; ++c) {
+                    Half8 x;
+                    const uint32_t w0 = d.k[t][c][0] ^ 0x80808080u, w1 = d.k[t][c][1] ^ 0x80808080u;
+                    x.w[0] = key_pair(w0, 0);
+                    x.w[1] = key_pair(w0, 1);
+                    x.w[2] = key_pair(w1, 0);
+                    x.w[3] = key_pair(w1, 1);
+#pragma unroll
+                    for (int ct = 0; ct < C; ++ct)
+                        sc[ct][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x.h, q[ct][c], sc[ct][t], 0, 0, 0);
+                }
+            }
+            const float kLog2e = 1.44269504088896340736f;
+            const int half = SMALL ? g >> 1 : 0;   // keys 8 g .. lie in one half
+            const float ks = SMALL && half ? d.c[1] : d.c[0];
+            const float lv = SMALL && half ? d.lv[1] : d.lv[0];
+            const float iv = SMALL && half ? d.iv[1] : d.iv[0];
+            const bool pages = SMALL ? d.c[0] >= 0.0f && d.c[1] >= 0.0f : d.c[0] >= 0.0f;
+            const bool open = pages && key0 + kStep - 1 <= pos_lo && (a.window <= 0 || key0 > pos_hi - a.window);
+            half8_t w[C];
+#pragma unroll
+            for (int ct = 0; ct < C; ++ct) {
+                float t[8];
+                const float f = ks * qf[ct];
+                if (a.softcap > 0.0f) {
+                    // cap tanh(x / cap) = cap - 2 cap / (exp(2 x / cap) + 1)
+                    const float e = 2.0f * kLog2e / a.softcap * f;
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) {
+                        const float z = __builtin_amdgcn_exp2f(sc[ct][y >> 2][y & 3] * e);
+                        t[y] = __builtin_fmaf(kLog2e * a.softcap, 1.0f - 2.0f * __builtin_amdgcn_rcpf(z + 1.0f), lv);
+                    }
+                } else {
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) t[y] = __builtin_fmaf(sc[ct][y >> 2][y & 3], f * kLog2e, lv);
+                }
+                if (!open) {
+                    const int key = key0 + 8 * g;
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) {
+                        const bool seen = ks >= 0.0f && key + y <= pos[ct] && (a.window <= 0 || key + y > pos[ct] - a.window);
+                        t[y] = seen ? t[y] : -INFINITY;
+                    }
+                }
+                float top = t[0];
+#pragma unroll
+                for (int y = 1; y < 8; ++y) top = fmaxf(top, t[y]);
+                if (__builtin_amdgcn_ballot_w64(top > M[ct] + kSlack)) {
+                    top = fmaxf(top, __shfl_xor(top, 16));
+                    top = fmaxf(top, __shfl_xor(top, 32));
+                    const float m = fmaxf(M[ct], top);
+                    const float down = __builtin_amdgcn_exp2f(M[ct] - m);
+                    M[ct] = m;
+                    sum[ct] *= down;
+                    obias[ct] *= down;
+#pragma unroll
+                    for (int j = 0; j < VB; ++j) o[ct][j] *= down;
+                }
+                float part = 0.0f;
+#pragma unroll
+                for (int y = 0; y < 8; ++y) {
+                    const float p = __builtin_amdgcn_exp2f(t[y] - M[ct]);
+                    part += p;
+                    w[ct][y] = (_Float16)p;
+                }
+                sum[ct] = __builtin_fmaf(part, iv, sum[ct]);
+            }
+            // values
+            const Half8 one{{0x00800080u, 0x00800080u, 0x00800080u, 0x00800080u}};      // 128 2^-24
+#pragma unroll
+            for (int ct = 0; ct < C; ++ct) obias[ct] = __builtin_amdgcn_mfma_f32_16x16x32_f16(one.h, w[ct], obias[ct], 0, 0, 0);
+#pragma unroll
+            for (int x = 0; x < VW; ++x) {
+                uint32_t v[8];
+#pragma unroll
+                for (int y = 0; y < 8; ++y) v[y] = d.v[y][x] ^ 0x80808080u;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    Half8 e;
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) e.w[y] = value_pair(v[2 * y], v[2 * y + 1], j);
+#pragma unroll
+                    for (int ct = 0; ct < C; ++ct)
+                        o[ct][4 * x + j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(e.h, w[ct], o[ct][4 * x + j], 0, 0, 0);
+                }
+            }
+        };
+
+        {
+            const int mine = s1 - s0 > wave ? (s1 - s0 - wave + kW - 1) / kW : 0;      // steps of this wave
+            K da, db;
+            if (mine > 0) load(da, 0);
+            for (int i = 0; i < mine; i += 2) {
+                if (i + 1 < mine) load(db, i + 1);
+                compute(da, i);
+                if (i + 1 < mine) {
+                    if (i + 2 < mine) load(da, i + 2);
+                    compute(db, i + 1);
+                }
+            }
+        }
+
+        // the four waves' results: one maximum, sums and outputs added in order
+#pragma unroll
+        for (int ct = 0; ct < C; ++ct) {
+            sum[ct] += __shfl_xor(sum[ct], 16);
+            sum[ct] += __shfl_xor(sum[ct], 32);
+            if (g == 0) {
+                stat[wave][0][16 * ct + r] = M[ct];
+                stat[wave][1][16 * ct + r] = sum[ct];
+            }
+        }
+        __syncthreads();
+        float* part = nullptr;
+        if (!whole) part = a.parts + ((size_t)blockIdx.x * 2 + (first_segment ? 0 : 1)) * (size_t)(R * (D + 2));
+        first_segment = false;
+#pragma unroll
+        for (int ct = 0; ct < C; ++ct) {
+            float m = stat[0][0][16 * ct + r];
+#pragma unroll
+            for (int x = 1; x < kW; ++x) m = fmaxf(m, stat[x][0][16 * ct + r]);
+            float all = 0.0f;
+#pragma unroll
+            for (int x = 0; x < kW; ++x)
+                all += stat[x][1][16 * ct + r] * __builtin_amdgcn_exp2f(stat[x][0][16 * ct + r] - m);
+            const float down = __builtin_amdgcn_exp2f(M[ct] - m) * 0x1p24f;
+            const int row = tile * R + 16 * ct + r;
+            const bool live = row < l.rows;
+            const int j = row / a.group, h = head * a.group + (row - j * a.group);
+            const float inv = all > 0.0f ? 1.0f / all : 0.0f;
+            const size_t at = (size_t)(s.start(b) + j) * a.heads + h;
+            for (int jb = 0; jb < VB; jb += JB) {
+#pragma unroll
+                for (int x = 0; x < VB; ++x)
+                    if (x >= jb && x < jb + JB)
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            join[wave][y][lane][x - jb] = (o[ct][x][y] - obias[ct][y]) * down;
+                __syncthreads();
+                float v[JB];
+#pragma unroll
+                for (int x = 0; x < JB; ++x) {
+                    v[x] = join[0][wave][lane][x];
+#pragma unroll
+                    for (int z = 1; z < kW; ++z) v[x] += join[z][wave][lane][x];
+                }
+                // channels VB (4 g + wave) + jb ..
+                const int d0 = VB * (4 * g + wave) + jb;
+                if (d0 < D) {
+                    if (whole) {
+                        if (live) {
+                            uint32_t* to = (uint32_t*)(a.out + at * D + d0);
+#pragma unroll
+                            for (int x = 0; x < JB; x += 2)
+                                to[x / 2] = a.bf16 ? pack2<BF16>(v[x] * inv, v[x + 1] * inv) : pack2<F16>(v[x] * inv, v[x + 1] * inv);
+                        }
+                    } else {
+                        float* to = part + 2 * R + (16 * ct + r) * D + d0;
+#pragma unroll
+                        for (int x = 0; x < JB; ++x) to[x] = v[x];
+                    }
+                }
+                __syncthreads();
+            }
+            if (wave == 0 && g == 0) {
+                if (!whole) {
+                    part[16 * ct + r] = m;
+                    part[R + 16 * ct + r] = all;
+                } else if (live && a.lse) {
+                    a.lse[at] = all > 0.0f ? (m + __builtin_amdgcn_logf(all)) * 0.69314718055994530942f : -INFINITY;
+                }
+            }
+        }
+        if (u >= u_end) return;
+    }
+}
+
+// Joins the parts of a row: one workgroup for each row of the call and head, 8
+// groups of 32 threads over the parts.
+struct JoinArgs {
+    AttendArgs a;
+    int rows, dim;                       // of a tile
+};
+
+__global__ __launch_bounds__(256) void k_attend_join(JoinArgs ja) {
+    const AttendArgs& a = ja.a;
+    const int R = ja.rows, D = ja.dim;
+    const int t = blockIdx.x / a.heads, h = blockIdx.x % a.heads;
+    const Sequences& s = a.seqs;
+    const int b = s.of_row(t);
+    if (b < 0) return;
+    const Line l(a, b, R);
+    const int head = h / a.group;
+    const int row = (t - s.start(b)) * a.group + (h - head * a.group);
+    const int tile = row / R;
+    long long total, before;
+    count_units(a, R, b, total, before);
+    const long long share = stretch(total, a.groups);
+    const long long u0 = before + ((long long)head * l.tiles + tile) * l.steps, u1 = u0 + l.steps;
+    const int w0 = (int)(u0 / share), w1 = (int)((u1 - 1) / share);
+    if (w0 == w1) return;                          // written by its workgroup
+    const int in = row - tile * R;
+    const size_t size = (size_t)(R * (D + 2));
+    auto part = [&](int w) {                       // a workgroup's first segment is in its first place
+        return a.parts + ((size_t)w * 2 + (w == w0 && u0 != w0 * share ? 1 : 0)) * size;
+    };
+    __shared__ float slots[8];
+    __shared__ float acc[8][256 + 1];
+    __shared__ float sums[8];
+    const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
+    float m = kLow;
+    for (int w = w0 + threadIdx.x; w <= w1; w += 256) m = fmaxf(m, part(w)[in]);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+    if (lane == 0) slots[grp] = m;
+    __syncthreads();
+    m = slots[0];
+#pragma unroll
+    for (int x = 1; x < 8; ++x) m = fmaxf(m, slots[x]);
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, all = 0.0f;
+    for (int w = w0 + grp; w <= w1; w += 8) {
+        const float* p = part(w);
+        const float f = __builtin_amdgcn_exp2f(p[in] - m);
+        all += p[R + in] * f;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            const int d = lane + 32 * x;
+            if (d < D) v[x] = __builtin_fmaf(p[2 * R + (size_t)in * D + d], f, v[x]);
+        }
+    }
+#pragma unroll
+    for (int x = 0; x < 8; ++x) acc[grp][lane + 32 * x] = v[x];
+    if (lane == 0) sums[grp] = all;
+    __syncthreads();
+    all = 0.0f;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) all += sums[x];
+    const float inv = all > 0.0f ? 1.0f / all : 0.0f;
+    const size_t at = (size_t)t * a.heads + h;
+    if ((int)threadIdx.x < D / 2) {
+        float y[2] = {0, 0};
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            y[0] += acc[x][2 * threadIdx.x];
+            y[1] += acc[x][2 * threadIdx.x + 1];
+        }
+        ((uint32_t*)(a.out + at * D))[threadIdx.x] =
+            a.bf16 ? pack2<BF16>(y[0] * inv, y[1] * inv) : pack2<F16>(y[0] * inv, y[1] * inv);
+    }
+    if (threadIdx.x == 0 && a.lse)
+        a.lse[at] = all > 0.0f ? (m + __builtin_amdgcn_logf(all)) * 0.69314718055994530942f : -INFINITY;
+}
+
+// columns of 16 rows, the workgroups and whether tiles are split over them
+struct Plan {
+    int columns, split, groups;
+};
+
+Plan plan(int T, int B, int heads, int kv, int dim, int max_new, int max_len) {
+    Plan p;
+    const long long rows = (long long)max_new * (heads / kv);
+    const int most = dim <= 128 ? 4 : 2;
+    p.columns = rows <= 16 ? 1 : rows <= 32 || most == 2 ? 2 : 4;
+    const int R = 16 * p.columns;
+    p.split = max_len > 2 * kW * kStep;
+    const long long tiles = ((long long)T * (heads / kv) / R + B) * kv;
+    p.groups = p.split ? device_cu_count() * 2 : (int)tiles;
+    return p;
+}
+
+template <int D, int C>
+void launch_c(const AttendArgs& a, hipStream_t st) {
+    if (a.cache.page_log2 == 4)
+        hipLaunchKernelGGL((k_attend<D, C, true>), dim3(a.groups), dim3(64 * kW), 0, st, a);
+    else
+        hipLaunchKernelGGL((k_attend<D, C, false>), dim3(a.groups), dim3(64 * kW), 0, st, a);
+}
+
+template <int D>
+void launch_d(const AttendArgs& a, int columns, hipStream_t st) {
+    if (columns == 1) return launch_c<D, 1>(a, st);
+    if (columns == 2) return launch_c<D, 2>(a, st);
+    if constexpr (D <= 128) launch_c<D, 4>(a, st);
+}
+
+}  // namespace
+
+size_t attend_workspace_bytes(int T, int B, int heads, int kv, int dim, int max_new, int max_len) {
+    const Plan p = plan(T, B, heads, kv, dim, max_new, max_len);
+    return p.split ? (size_t)p.groups * 2 * (16 * p.columns) * (dim + 2) * sizeof(float) : 0;
+}
+
+int launch_cache_attention(const AttendProblem& p, void* workspace, hipStream_t st) {
+    const Plan pl = plan(p.seqs.T, p.seqs.B, p.heads, p.cache.kv, p.cache.dim, p.max_new, p.max_len);
+    AttendArgs a{};
+    a.q = (const uint16_t*)p.q;
+    a.q_stride = p.q_stride;
+    a.out = (uint16_t*)p.out;
+    a.lse = p.lse;
+    a.cache = p.cache;
+    a.seqs = p.seqs;
+    a.scale = fabsf(p.scale) * 0x1p24f;
+    a.sign = p.scale < 0.0f ? -1.0f : 1.0f;
+    a.softcap = p.softcap;
+    a.heads = p.heads;
+    a.group = p.heads / p.cache.kv;
+    a.window = p.window;
+    a.bf16 = p.dtype == AWQ_BF16;
+    a.split = pl.split;
+    a.groups = pl.groups;
+    a.parts = (float*)workspace;
+    switch (p.cache.dim) {
+        case 64: launch_d<64>(a, pl.columns, st); break;
+        case 96: launch_d<96>(a, pl.columns, st); break;
+        case 128: launch_d<128>(a, pl.columns, st); break;
+        case 192: launch_d<192>(a, pl.columns, st); break;
+        default: launch_d<256>(a, pl.columns, st); break;
+    }
+    if (int e = (int)hipGetLastError()) return e;
+    if (!pl.split) return 0;
+    const JoinArgs ja{a, 16 * pl.columns, p.cache.dim};
+    hipLaunchKernelGGL(k_attend_join, dim3((unsigned)p.seqs.T * p.heads), dim3(256), 0, st, ja);
+    return (int)hipGetLastError();
+}
+
+}  // namespace awq

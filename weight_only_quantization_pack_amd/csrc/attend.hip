@@ -23,103 +23,16 @@
 // keys form one line, and every workgroup takes an equal stretch of it.  Stretches
 // that end inside a tile leave (M, sum, o) in the workspace and a second launch
 // joins them in order.
-#include "cache.h"
+#include "attend.h"
 
 namespace awq {
 namespace {
 
-constexpr int kStep = 32;                // keys of a step
 constexpr int kW = 4;                    // waves of a workgroup
-constexpr float kLow = -1e30f;           // below every score: the maximum before the first key
-constexpr float kSlack = 8.0f;           // the maximum may lag by 2^8: weights stay far below fp16's maximum
-
-struct AttendArgs {
-    const uint16_t* q;
-    long long q_stride;
-    uint16_t* out;
-    float* lse;
-    Cache cache;
-    Sequences seqs;
-    float scale, softcap;                // |scale| 2^24, for the operands' unit; its sign goes into q
-    float sign;
-    int heads, group, window, bf16;
-    int split;                           // stretches may end inside a tile
-    int groups;                          // workgroups of the first launch
-    float* parts;                        // [groups][2][rows * (dim + 2)]
-};
-
-// the steps of a sequence: the same for all its tiles of rows (their own first and
-// last keys lie inside)
-struct Line {
-    int rows, tiles, step0, steps;
-    int len, n;
-    __device__ __forceinline__ Line(const AttendArgs& a, int b, int tile_rows) {
-        const Sequences& s = a.seqs;
-        n = s.rows(b);
-        len = s.len(b);
-        rows = n * a.group;
-        tiles = (rows + tile_rows - 1) / tile_rows;
-        const int span = s.span(b, a.cache.page_log2);
-        int first = 0;
-        if (a.window > 0) first = max((int)max((long long)len - n + 1 - a.window, 0LL), 0);
-        step0 = first / kStep;
-        steps = max((span + kStep - 1) / kStep - step0, 1);
-    }
-    __device__ __forceinline__ long long units(int kv) const { return (long long)tiles * kv * steps; }
-};
 
 // units a workgroup takes: an even share, but at least two steps for every wave
 __device__ __forceinline__ long long stretch(long long total, int groups) {
     return max((total + groups - 1) / groups, (long long)(2 * kW));
-}
-
-// all units, and those before sequence b_stop; by one wave
-__device__ __forceinline__ void count_units(const AttendArgs& a, int tile_rows, int b_stop, long long& total,
-                                            long long& before) {
-    const int lane = threadIdx.x & 63;
-    total = before = 0;
-    for (int b0 = 0; b0 < a.seqs.B; b0 += 64) {
-        const int b = b0 + lane;
-        long long u = b < a.seqs.B ? Line(a, b, tile_rows).units(a.cache.kv) : 0;
-        long long v = b < b_stop ? u : 0;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            u += __shfl_xor(u, d);
-            v += __shfl_xor(v, d);
-        }
-        total += u;
-        before += v;
-    }
-}
-
-// the sequence that holds the unit at `at` (or, unsplit, the tile at `at`) and the
-// units (tiles) before it; -1 past the last.  By one wave.
-__device__ __forceinline__ int find_line(const AttendArgs& a, int tile_rows, bool tiles, long long at, long long& before) {
-    const int lane = threadIdx.x & 63;
-    before = 0;
-    for (int b0 = 0; b0 < a.seqs.B; b0 += 64) {
-        const int b = b0 + lane;
-        long long u = 0;
-        if (b < a.seqs.B) {
-            const Line l(a, b, tile_rows);
-            u = tiles ? (long long)l.tiles * a.cache.kv : l.units(a.cache.kv);
-        }
-        long long sum = u;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const long long o = __shfl_up(sum, d);
-            if (lane >= d) sum += o;
-        }
-        const long long all = __shfl(sum, 63);
-        if (at < before + all) {
-            const uint64_t hit = __builtin_amdgcn_ballot_w64(at < before + sum);
-            const int f = __builtin_ctzll(hit);
-            before += __shfl(sum - u, f);
-            return b0 + f;
-        }
-        before += all;
-    }
-    return -1;
 }
 
 // one step's codes of a wave: keys as 16 x 32 operands, values as 8 rows of D / 16
@@ -132,23 +45,10 @@ struct Codes {
     float c[2], lv[2], iv[2];                      // per half of the step: ks scale 2^24 (< 0: no page), log2(vs), 1 / vs
 };
 
-__device__ __forceinline__ float lane_value(float v, int lane) {
-    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
-}
-
-// bytes i, i + 1 of w (biased codes) as two fp16 numbers of 2^-24 steps
-__device__ __forceinline__ uint32_t key_pair(uint32_t w, int i) {
-    return __builtin_amdgcn_perm(0u, w, i ? 0x0C030C02u : 0x0C010C00u);
-}
 // byte j of two rows' words
 __device__ __forceinline__ uint32_t value_pair(uint32_t lo, uint32_t hi, int j) {
     return __builtin_amdgcn_perm(hi, lo, 0x0C000C00u | (uint32_t)(4 + j) << 16 | (uint32_t)j);
 }
-
-union Half8 {
-    uint32_t w[4];
-    half8_t h;
-};
 
 template <int D, int C, bool SMALL>
 __global__ __launch_bounds__(64 * kW) void k_attend(AttendArgs a) {
@@ -167,7 +67,7 @@ __global__ __launch_bounds__(64 * kW) void k_attend(AttendArgs a) {
     int b;
     if (a.split) {
         long long total, unused;
-        count_units(a, R, 0, total, unused);
+        count_units(a, R, false, 0, total, unused);
         const long long share = stretch(total, a.groups);
         u = blockIdx.x * share;
         u_end = min(u + share, total);
@@ -216,8 +116,6 @@ __global__ __launch_bounds__(64 * kW) void k_attend(AttendArgs a) {
 #pragma unroll
             for (int c = 0; c < NK; ++c)
                 raw[c] = *(const uint4*)(from + (NK % 2 == 1 && c == NK - 1 ? 32 * c + 8 * g : 64 * (c / 2) + 16 * g + 8 * (c & 1)));
-            // q times a power of two that brings its largest channel to 2^13: fp16 then
-            // holds all of its bits (bf16 has 8) down to 2^-27 of the largest
             float f[NK][8], top = 0.0f;
 #pragma unroll
             for (int c = 0; c < NK; ++c) {
@@ -227,17 +125,15 @@ __global__ __launch_bounds__(64 * kW) void k_attend(AttendArgs a) {
             }
             top = fmaxf(top, __shfl_xor(top, 16));
             top = fmaxf(top, __shfl_xor(top, 32));
-            int e2 = 0;
-            if (top > 0.0f) e2 = 13 - ((int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127);
-            e2 = min(max(e2, -120), 120);
-            const float up = __builtin_bit_cast(float, (uint32_t)(127 + e2) << 23);
-            qf[ct] = __builtin_bit_cast(float, (uint32_t)(127 - e2) << 23);
+            const int e2 = query_exponent(top);
+            const float up = power_of_two(e2) * a.sign;
+            qf[ct] = power_of_two(-e2);
             float sum = 0.0f;
 #pragma unroll
             for (int c = 0; c < NK; ++c)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    q[ct][c][e] = (_Float16)(f[c][e] * (up * a.sign));
+                    q[ct][c][e] = (_Float16)(f[c][e] * up);
                     sum += (float)q[ct][c][e];
                 }
             sum += __shfl_xor(sum, 16);
@@ -341,7 +237,6 @@ __global__ __launch_bounds__(64 * kW) void k_attend(AttendArgs a) {
                         sc[ct][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x.h, q[ct][c], sc[ct][t], 0, 0, 0);
                 }
             }
-            const float kLog2e = 1.44269504088896340736f;
             const int half = SMALL ? g >> 1 : 0;   // keys 8 g .. lie in one half
             const float ks = SMALL && half ? d.c[1] : d.c[0];
             const float lv = SMALL && half ? d.lv[1] : d.lv[0];
@@ -498,7 +393,7 @@ __global__ __launch_bounds__(64 * kW) void k_attend(AttendArgs a) {
                     part[16 * ct + r] = m;
                     part[R + 16 * ct + r] = all;
                 } else if (live && a.lse) {
-                    a.lse[at] = all > 0.0f ? (m + __builtin_amdgcn_logf(all)) * 0.69314718055994530942f : -INFINITY;
+                    a.lse[at] = all > 0.0f ? (m + __builtin_amdgcn_logf(all)) * kLn2 : -INFINITY;
                 }
             }
         }
@@ -511,6 +406,7 @@ __global__ __launch_bounds__(64 * kW) void k_attend(AttendArgs a) {
 struct JoinArgs {
     AttendArgs a;
     int rows, dim;                       // of a tile
+    int tile_parts;                      // 0: stretches; else the parts of a tile (attend_tile.hip)
 };
 
 __global__ __launch_bounds__(256) void k_attend_join(JoinArgs ja) {
@@ -524,17 +420,30 @@ __global__ __launch_bounds__(256) void k_attend_join(JoinArgs ja) {
     const int head = h / a.group;
     const int row = (t - s.start(b)) * a.group + (h - head * a.group);
     const int tile = row / R;
-    long long total, before;
-    count_units(a, R, b, total, before);
-    const long long share = stretch(total, a.groups);
-    const long long u0 = before + ((long long)head * l.tiles + tile) * l.steps, u1 = u0 + l.steps;
-    const int w0 = (int)(u0 / share), w1 = (int)((u1 - 1) / share);
-    if (w0 == w1) return;                          // written by its workgroup
     const int in = row - tile * R;
     const size_t size = (size_t)(R * (D + 2));
-    auto part = [&](int w) {                       // a workgroup's first segment is in its first place
-        return a.parts + ((size_t)w * 2 + (w == w0 && u0 != w0 * share ? 1 : 0)) * size;
-    };
+    const float* base;
+    int w0 = 0, w1;
+    size_t second = 0, step;                       // what part w0's place is past base, and the others' distance
+    long long total, before;
+    if (ja.tile_parts) {
+        count_units(a, R, true, b, total, before);
+        w1 = ja.tile_parts - 1;
+        step = (size_t)a.cache.kv * size;
+        base = a.parts + (((size_t)before + (size_t)(l.tiles - 1 - tile) * a.cache.kv) * ja.tile_parts + head) * size;
+    } else {
+        count_units(a, R, false, b, total, before);
+        const long long share = stretch(total, a.groups);
+        const long long u0 = before + ((long long)head * l.tiles + tile) * l.steps, u1 = u0 + l.steps;
+        w0 = (int)(u0 / share);
+        w1 = (int)((u1 - 1) / share);
+        if (w0 == w1) return;                      // written by its workgroup
+        // a workgroup's first segment is in its first place, the last one in its second
+        base = a.parts;
+        step = 2 * size;
+        second = u0 != w0 * share ? size : 0;
+    }
+    auto part = [&](int w) { return base + (size_t)w * step + (w == w0 ? second : 0); };
     __shared__ float slots[8];
     __shared__ float acc[8][256 + 1];
     __shared__ float sums[8];
@@ -579,19 +488,30 @@ __global__ __launch_bounds__(256) void k_attend_join(JoinArgs ja) {
             a.bf16 ? pack2<BF16>(y[0] * inv, y[1] * inv) : pack2<F16>(y[0] * inv, y[1] * inv);
     }
     if (threadIdx.x == 0 && a.lse)
-        a.lse[at] = all > 0.0f ? (m + __builtin_amdgcn_logf(all)) * 0.69314718055994530942f : -INFINITY;
+        a.lse[at] = all > 0.0f ? (m + __builtin_amdgcn_logf(all)) * kLn2 : -INFINITY;
 }
 
-// columns of 16 rows, the workgroups and whether tiles are split over them
+// columns of 16 rows (0: attend_tile.hip's tiles), the workgroups and whether tiles
+// are split over them
 struct Plan {
     int columns, split, groups;
+    TilePlan tile;
+    int rows() const { return columns ? 16 * columns : tile.rows; }
+    int places() const { return columns ? 2 : 1; }           // parts that a workgroup may leave
 };
 
 Plan plan(int T, int B, int heads, int kv, int dim, int max_new, int max_len) {
     Plan p;
     const long long rows = (long long)max_new * (heads / kv);
-    const int most = dim <= 128 ? 4 : 2;
-    p.columns = rows <= 16 ? 1 : rows <= 32 || most == 2 ? 2 : 4;
+    p.tile = TilePlan{0, 1};
+    if (rows > 32) {
+        p.columns = 0;
+        p.tile = tile_plan(T, B, heads / kv, kv, dim, max_new, max_len, device_cu_count());
+        p.split = p.tile.parts > 1;
+        p.groups = (int)(((long long)T * (heads / kv) / p.tile.rows + B) * kv * p.tile.parts);
+        return p;
+    }
+    p.columns = rows <= 16 ? 1 : 2;
     const int R = 16 * p.columns;
     p.split = max_len > 2 * kW * kStep;
     const long long tiles = ((long long)T * (heads / kv) / R + B) * kv;
@@ -610,15 +530,14 @@ void launch_c(const AttendArgs& a, hipStream_t st) {
 template <int D>
 void launch_d(const AttendArgs& a, int columns, hipStream_t st) {
     if (columns == 1) return launch_c<D, 1>(a, st);
-    if (columns == 2) return launch_c<D, 2>(a, st);
-    if constexpr (D <= 128) launch_c<D, 4>(a, st);
+    return launch_c<D, 2>(a, st);
 }
 
 }  // namespace
 
 size_t attend_workspace_bytes(int T, int B, int heads, int kv, int dim, int max_new, int max_len) {
     const Plan p = plan(T, B, heads, kv, dim, max_new, max_len);
-    return p.split ? (size_t)p.groups * 2 * (16 * p.columns) * (dim + 2) * sizeof(float) : 0;
+    return p.split ? (size_t)p.groups * p.places() * p.rows() * (dim + 2) * sizeof(float) : 0;
 }
 
 int launch_cache_attention(const AttendProblem& p, void* workspace, hipStream_t st) {
@@ -640,16 +559,18 @@ int launch_cache_attention(const AttendProblem& p, void* workspace, hipStream_t 
     a.split = pl.split;
     a.groups = pl.groups;
     a.parts = (float*)workspace;
-    switch (p.cache.dim) {
+    int e = 0;
+    if (!pl.columns) e = launch_attend_tile(a, pl.tile, st);
+    else switch (p.cache.dim) {
         case 64: launch_d<64>(a, pl.columns, st); break;
         case 96: launch_d<96>(a, pl.columns, st); break;
         case 128: launch_d<128>(a, pl.columns, st); break;
         case 192: launch_d<192>(a, pl.columns, st); break;
         default: launch_d<256>(a, pl.columns, st); break;
     }
-    if (int e = (int)hipGetLastError()) return e;
+    if (e || (e = (int)hipGetLastError())) return e;
     if (!pl.split) return 0;
-    const JoinArgs ja{a, 16 * pl.columns, p.cache.dim};
+    const JoinArgs ja{a, pl.rows(), p.cache.dim, pl.columns ? 0 : pl.tile.parts};
     hipLaunchKernelGGL(k_attend_join, dim3((unsigned)p.seqs.T * p.heads), dim3(256), 0, st, ja);
     return (int)hipGetLastError();
 }

@@ -32,7 +32,7 @@ constexpr int kW = 4;                    // waves of a workgroup
 
 // units a workgroup takes: an even share, but at least two steps for every wave
 __device__ __forceinline__ long long stretch(long long total, int groups) {
-    return max((total + groups - 1) / groups, (long long)(2 * kW));
+    return max(quotient(total + groups - 1, groups), (long long)(2 * kW));
 }
 
 // one step's codes of a wave: keys as 16 x 32 operands, values as 8 rows of D / 16
@@ -51,7 +51,7 @@ __device__ __forceinline__ uint32_t value_pair(uint32_t lo, uint32_t hi, int j) 
 }
 
 template <int D, int C, bool SMALL>
-__global__ __launch_bounds__(64 * kW) void k_attend(AttendArgs a) {
+__global__ __launch_bounds__(64 * kW, 2) void k_attend(AttendArgs a) {
     using K = Codes<D>;
     constexpr int R = 16 * C, NK = K::NK, VB = K::VB, VW = K::VW;
     constexpr int JB = VB > 8 ? VB / 2 : VB;       // channels of a lane that one pass of the join takes
@@ -62,64 +62,145 @@ __global__ __launch_bounds__(64 * kW) void k_attend(AttendArgs a) {
     const Sequences& s = a.seqs;
     const int kv = a.cache.kv, page_log2 = a.cache.page_log2;
 
-    // this workgroup's stretch [u, u_end)
-    long long u, u_end, before;
-    int b;
+    // this workgroup's stretch [u, u_end), relative to sequence b
+    const LineWalk walk(a, R, !a.split);
+    long long u = blockIdx.x, u_end = 0;
     if (a.split) {
-        long long total, unused;
-        count_units(a, R, false, 0, total, unused);
+        const bool note = blockIdx.x == 0;         // the join wants to know the line
+        const long long total = walk([&](int b, long long, long long before) {
+            if (note && b < s.B) a.line[b] = before;
+            return false;
+        }).before;
         const long long share = stretch(total, a.groups);
-        u = blockIdx.x * share;
+        if (note && threadIdx.x == 0) a.line[s.B] = share;
+        u *= share;
         u_end = min(u + share, total);
         if (u >= u_end) return;
-        b = find_line(a, R, false, u, before);
-        u -= before;                               // from here on relative to sequence b
-        u_end -= before;
-    } else {
-        b = find_line(a, R, true, blockIdx.x, before);
-        if (b < 0) return;
-        const Line l(a, b, R);
-        u = (blockIdx.x - before) * l.steps;
-        u_end = u + l.steps;
     }
-    b = __builtin_amdgcn_readfirstlane(b);
-    bool first_segment = true;
+    const auto p = walk([&](int, long long n, long long before) { return u < before + n; });
+    if (p.b < 0) return;
+    int b = p.b;
+    Line l = p.line;
+    u -= p.before;
+    u_end -= p.before;
+    if (!a.split) {
+        u *= l.tile_units();
+        u_end = u + l.tile_units();
+    }
 
     while (true) {
-        const Line l(a, b, R);
         const long long units = l.units(kv);
         if (u >= units) {                          // on to the next sequence
             u -= units;
             u_end -= units;
             if (++b >= s.B || u >= u_end) return;
+            l = walk.line(b);
             continue;
         }
-        const int tile_at = __builtin_amdgcn_readfirstlane((int)(u / l.steps));
+        // of the tile's units the stretch has [from, to); its steps are those behind kFixed
+        const int tile_at = __builtin_amdgcn_readfirstlane((int)quotient(u, l.tile_units()));
         const int head = tile_at / l.tiles, tile = tile_at - head * l.tiles;
-        const int s0 = __builtin_amdgcn_readfirstlane((int)(u - (long long)tile_at * l.steps));
-        const int s1 = (int)min((long long)l.steps, s0 + (u_end - u));
+        const int from = __builtin_amdgcn_readfirstlane((int)(u - (long long)tile_at * l.tile_units()));
+        const int to = (int)min((long long)l.tile_units(), from + (u_end - u));
+        u += to - from;
+        const int s0 = max(from - kFixed, 0), s1 = to - kFixed;
+        if (s0 >= s1) {
+            if (u >= u_end) return;
+            continue;
+        }
         const bool whole = s0 == 0 && s1 == l.steps;
-        u += s1 - s0;
 
-        // rows of the tile: column r of column tile ct is row 16 ct + r
+        // rows of the tile: column r of column tile ct is row 16 ct + r.  Their loads are on
+        // their way while the first step's pages and codes are asked for
         int pos[C];
-        half8_t q[C][NK];
-        float qf[C];                               // what brings a column's products back to q.k
-        float4_t bias[C];
+        uint4 raw[C][NK];
 #pragma unroll
         for (int ct = 0; ct < C; ++ct) {
             const int row = min(tile * R + 16 * ct + r, l.rows - 1);
             const int j = row / a.group, h = head * a.group + (row - j * a.group);
             pos[ct] = l.len - l.n + j;
-            const uint16_t* from = a.q + (size_t)(s.start(b) + j) * a.q_stride + (size_t)h * D;
-            uint4 raw[NK];
+            const uint16_t* row_q = a.q + (size_t)(l.start + j) * a.q_stride + (size_t)h * D;
 #pragma unroll
             for (int c = 0; c < NK; ++c)
-                raw[c] = *(const uint4*)(from + (NK % 2 == 1 && c == NK - 1 ? 32 * c + 8 * g : 64 * (c / 2) + 16 * g + 8 * (c & 1)));
+                raw[ct][c] = *(const uint4*)(row_q + (NK % 2 == 1 && c == NK - 1 ? 32 * c + 8 * g : 64 * (c / 2) + 16 * g + 8 * (c & 1)));
+        }
+        // pages and scales of the wave's next 64 steps, one a lane
+        int page_l[2];
+        float c_l[2], lv_l[2], iv_l[2];
+        auto fetch_pages = [&](int i0) {           // the wave's steps i0 ..
+            const int step = s0 + wave + kW * (i0 + lane);
+#pragma unroll
+            for (int x = 0; x < (SMALL ? 2 : 1); ++x) {
+                const long long key = (long long)(l.step0 + step) * kStep + 16 * x;
+                const int p = step < s1 ? s.page(b, (int)(key >> page_log2), a.cache.pages) : -1;
+                page_l[x] = p;
+                const size_t at = (size_t)max(p, 0) * kv + head;
+                c_l[x] = p >= 0 ? a.cache.scales[0][at] * a.scale : -1.0f;
+                const float vs = p >= 0 ? fmaxf(a.cache.scales[1][at], 0x1p-100f) : 1.0f;
+                lv_l[x] = __builtin_amdgcn_logf(vs);
+                iv_l[x] = 1.0f / vs;
+            }
+        };
+        auto load = [&](K& d, int i) {             // the wave's step i
+            if ((i & 63) == 0) fetch_pages(i);
+            const int at = i & 63;
+            const int step = s0 + wave + kW * i;
+            const int slot = ((l.step0 + step) * kStep) & ((1 << page_log2) - 1);
+            const int8_t *kb[2], *vb[2];
+#pragma unroll
+            for (int x = 0; x < (SMALL ? 2 : 1); ++x) {
+                const int p = __builtin_amdgcn_readlane(page_l[x], at);
+                const size_t off = a.cache.block(max(p, 0), head) + (SMALL ? (size_t)0 : (size_t)slot * D);
+                kb[x] = a.cache.codes[0] + off;
+                vb[x] = a.cache.codes[1] + off;
+            }
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int key = 8 * (r >> 2) + 4 * t + (r & 3);
+                const int8_t* row = SMALL ? (r < 8 ? kb[0] : kb[1]) + (uint32_t)((key & 15) * D) : kb[0] + (uint32_t)(key * D);
+#pragma unroll
+                for (int c = 0; c + 1 < NK; c += 2) {
+                    const uint4 w = *(const uint4*)(row + 32 * c + 16 * g);
+                    d.k[t][c][0] = w.x;
+                    d.k[t][c][1] = w.y;
+                    d.k[t][c + 1][0] = w.z;
+                    d.k[t][c + 1][1] = w.w;
+                }
+                if constexpr (NK % 2 == 1) {
+                    const uint2 w = *(const uint2*)(row + 32 * (NK - 1) + 8 * g);
+                    d.k[t][NK - 1][0] = w.x;
+                    d.k[t][NK - 1][1] = w.y;
+                }
+            }
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+                const int key = 8 * g + y;
+                const int8_t* row = SMALL ? (g < 2 ? vb[0] : vb[1]) + (uint32_t)((key & 15) * D) : vb[0] + (uint32_t)(key * D);
+                const int lr = D == 96 ? min(r, 11) : r;      // lanes 12.. repeat the last channels
+                const uint32_t* from = (const uint32_t*)(row + VB * lr);
+#pragma unroll
+                for (int x = 0; x < VW; ++x) d.v[y][x] = from[x];
+            }
+#pragma unroll
+            for (int x = 0; x < (SMALL ? 2 : 1); ++x) {
+                d.c[x] = lane_value(c_l[x], at);
+                d.lv[x] = lane_value(lv_l[x], at);
+                d.iv[x] = lane_value(iv_l[x], at);
+            }
+        };
+        const int mine = s1 - s0 > wave ? (s1 - s0 - wave + kW - 1) / kW : 0;      // steps of this wave
+        K da;
+        if (mine > 0) load(da, 0);
+
+        half8_t q[C][NK];
+        float qf[C];                               // what brings a column's products back to q.k
+        float4_t bias[C];
+#pragma unroll
+        for (int ct = 0; ct < C; ++ct) {
             float f[NK][8], top = 0.0f;
 #pragma unroll
             for (int c = 0; c < NK; ++c) {
-                if (a.bf16) unpack8<BF16>(raw[c], f[c]); else unpack8<F16>(raw[c], f[c]);
+                if (a.bf16) unpack8<BF16>(raw[ct][c], f[c]); else unpack8<F16>(raw[ct][c], f[c]);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[c][e]));
             }
@@ -155,67 +236,6 @@ __global__ __launch_bounds__(64 * kW) void k_attend(AttendArgs a) {
             for (int j = 0; j < VB; ++j) o[ct][j] = float4_t{0, 0, 0, 0};
         }
 
-        // pages and scales of the wave's next 64 steps, one a lane
-        int page_l[2];
-        float c_l[2], lv_l[2], iv_l[2];
-        auto fetch_pages = [&](int i0) {           // the wave's steps i0 ..
-            const int step = s0 + wave + kW * (i0 + lane);
-#pragma unroll
-            for (int x = 0; x < (SMALL ? 2 : 1); ++x) {
-                const long long key = (long long)(l.step0 + step) * kStep + 16 * x;
-                const int p = step < s1 ? s.page(b, (int)(key >> page_log2), a.cache.pages) : -1;
-                page_l[x] = p;
-                const size_t at = (size_t)max(p, 0) * kv + head;
-                c_l[x] = p >= 0 ? a.cache.scales[0][at] * a.scale : -1.0f;
-                const float vs = p >= 0 ? fmaxf(a.cache.scales[1][at], 0x1p-100f) : 1.0f;
-                lv_l[x] = __builtin_amdgcn_logf(vs);
-                iv_l[x] = 1.0f / vs;
-            }
-        };
-        auto load = [&](K& d, int i) {             // the wave's step i
-            if ((i & 63) == 0) fetch_pages(i);
-            const int at = i & 63;
-            const int step = s0 + wave + kW * i;
-            const int slot = ((l.step0 + step) * kStep) & ((1 << page_log2) - 1);
-            const int8_t *kb[2], *vb[2];
-#pragma unroll
-            for (int x = 0; x < (SMALL ? 2 : 1); ++x) {
-                const int p = __builtin_amdgcn_readlane(page_l[x], at);
-                const size_t off = a.cache.block(max(p, 0), head) + (SMALL ? (size_t)0 : (size_t)slot * D);
-                kb[x] = a.cache.codes[0] + off;
-                vb[x] = a.cache.codes[1] + off;
-                d.c[x] = lane_value(c_l[x], at);
-                d.lv[x] = lane_value(lv_l[x], at);
-                d.iv[x] = lane_value(iv_l[x], at);
-            }
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const int key = 8 * (r >> 2) + 4 * t + (r & 3);
-                const int8_t* row = SMALL ? (r < 8 ? kb[0] : kb[1]) + (uint32_t)((key & 15) * D) : kb[0] + (uint32_t)(key * D);
-#pragma unroll
-                for (int c = 0; c + 1 < NK; c += 2) {
-                    const uint4 w = *(const uint4*)(row + 32 * c + 16 * g);
-                    d.k[t][c][0] = w.x;
-                    d.k[t][c][1] = w.y;
-                    d.k[t][c + 1][0] = w.z;
-                    d.k[t][c + 1][1] = w.w;
-                }
-                if constexpr (NK % 2 == 1) {
-                    const uint2 w = *(const uint2*)(row + 32 * (NK - 1) + 8 * g);
-                    d.k[t][NK - 1][0] = w.x;
-                    d.k[t][NK - 1][1] = w.y;
-                }
-            }
-#pragma unroll
-            for (int y = 0; y < 8; ++y) {
-                const int key = 8 * g + y;
-                const int8_t* row = SMALL ? (g < 2 ? vb[0] : vb[1]) + (uint32_t)((key & 15) * D) : vb[0] + (uint32_t)(key * D);
-                const int lr = D == 96 ? min(r, 11) : r;      // lanes 12.. repeat the last channels
-                const uint32_t* from = (const uint32_t*)(row + VB * lr);
-#pragma unroll
-                for (int x = 0; x < VW; ++x) d.v[y][x] = from[x];
-            }
-        };
         auto compute = [&](K& d, int i) {
             const int key0 = (l.step0 + s0 + wave + kW * i) * kStep;
             // scores
@@ -312,18 +332,14 @@ __global__ __launch_bounds__(64 * kW) void k_attend(AttendArgs a) {
             }
         };
 
-        {
-            const int mine = s1 - s0 > wave ? (s1 - s0 - wave + kW - 1) / kW : 0;      // steps of this wave
-            K da, db;
-            if (mine > 0) load(da, 0);
-            for (int i = 0; i < mine; i += 2) {
-                if (i + 1 < mine) load(db, i + 1);
-                compute(da, i);
-                if (i + 1 < mine) {
-                    if (i + 2 < mine) load(da, i + 2);
-                    compute(db, i + 1);
-                }
-            }
+        // loads under no condition, so that a wait counts only those before it: behind the
+        // last step they repeat it
+        K db;
+        for (int i = 0; i < mine; i += 2) {
+            load(db, min(i + 1, mine - 1));
+            compute(da, i);
+            load(da, min(i + 2, mine - 1));
+            if (i + 1 < mine) compute(db, i + 1);
         }
 
         // the four waves' results: one maximum, sums and outputs added in order
@@ -338,8 +354,8 @@ __global__ __launch_bounds__(64 * kW) void k_attend(AttendArgs a) {
         }
         __syncthreads();
         float* part = nullptr;
-        if (!whole) part = a.parts + ((size_t)blockIdx.x * 2 + (first_segment ? 0 : 1)) * (size_t)(R * (D + 2));
-        first_segment = false;
+        // a tile that began before the stretch leaves its part in the first place, one that goes on in the second
+        if (!whole) part = a.parts + ((size_t)blockIdx.x * 2 + (from > 0 ? 0 : 1)) * (size_t)(R * (D + 2));
 #pragma unroll
         for (int ct = 0; ct < C; ++ct) {
             float m = stat[0][0][16 * ct + r];
@@ -354,7 +370,7 @@ __global__ __launch_bounds__(64 * kW) void k_attend(AttendArgs a) {
             const bool live = row < l.rows;
             const int j = row / a.group, h = head * a.group + (row - j * a.group);
             const float inv = all > 0.0f ? 1.0f / all : 0.0f;
-            const size_t at = (size_t)(s.start(b) + j) * a.heads + h;
+            const size_t at = (size_t)(l.start + j) * a.heads + h;
             for (int jb = 0; jb < VB; jb += JB) {
 #pragma unroll
                 for (int x = 0; x < VB; ++x)
@@ -380,7 +396,7 @@ __global__ __launch_bounds__(64 * kW) void k_attend(AttendArgs a) {
                             for (int x = 0; x < JB; x += 2)
                                 to[x / 2] = a.bf16 ? pack2<BF16>(v[x] * inv, v[x + 1] * inv) : pack2<F16>(v[x] * inv, v[x + 1] * inv);
                         }
-                    } else {
+                    } else if (live) {
                         float* to = part + 2 * R + (16 * ct + r) * D + d0;
 #pragma unroll
                         for (int x = 0; x < JB; ++x) to[x] = v[x];
@@ -401,94 +417,109 @@ __global__ __launch_bounds__(64 * kW) void k_attend(AttendArgs a) {
     }
 }
 
-// Joins the parts of a row: one workgroup for each row of the call and head, 8
-// groups of 32 threads over the parts.
+// Joins the parts of a row (one of the call's, one head).  WAVES waves share a row:
+// its parts in turns, four at a time in flight; one wave each where there are rows
+// enough.
 struct JoinArgs {
     AttendArgs a;
     int rows, dim;                       // of a tile
     int tile_parts;                      // 0: stretches; else the parts of a tile (attend_tile.hip)
 };
 
-__global__ __launch_bounds__(256) void k_attend_join(JoinArgs ja) {
+template <int WAVES>
+__global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void k_attend_join(JoinArgs ja) {
     const AttendArgs& a = ja.a;
     const int R = ja.rows, D = ja.dim;
-    const int t = blockIdx.x / a.heads, h = blockIdx.x % a.heads;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int id = __builtin_amdgcn_readfirstlane(WAVES == 1 ? blockIdx.x * 4 + wave : blockIdx.x);
     const Sequences& s = a.seqs;
-    const int b = s.of_row(t);
+    const int t = id / a.heads, h = id - t * a.heads;
+    if (t >= s.T) return;
+    const int b = s.of_row_by_wave(t);
     if (b < 0) return;
+    const long long before = a.line[b], share = ja.tile_parts ? 1 : a.line[s.B];
     const Line l(a, b, R);
     const int head = h / a.group;
-    const int row = (t - s.start(b)) * a.group + (h - head * a.group);
-    const int tile = row / R;
-    const int in = row - tile * R;
+    const int row = (t - l.start) * a.group + (h - head * a.group);
+    const int tile = row / R, in = row - tile * R;
     const size_t size = (size_t)(R * (D + 2));
     const float* base;
     int w0 = 0, w1;
     size_t second = 0, step;                       // what part w0's place is past base, and the others' distance
-    long long total, before;
     if (ja.tile_parts) {
-        count_units(a, R, true, b, total, before);
         w1 = ja.tile_parts - 1;
         step = (size_t)a.cache.kv * size;
         base = a.parts + (((size_t)before + (size_t)(l.tiles - 1 - tile) * a.cache.kv) * ja.tile_parts + head) * size;
     } else {
-        count_units(a, R, false, b, total, before);
-        const long long share = stretch(total, a.groups);
-        const long long u0 = before + ((long long)head * l.tiles + tile) * l.steps, u1 = u0 + l.steps;
-        w0 = (int)(u0 / share);
-        w1 = (int)((u1 - 1) / share);
+        const long long u0 = before + ((long long)head * l.tiles + tile) * l.tile_units();
+        w0 = (int)quotient(u0 + kFixed, share);
+        w1 = (int)quotient(u0 + l.tile_units() - 1, share);
         if (w0 == w1) return;                      // written by its workgroup
-        // a workgroup's first segment is in its first place, the last one in its second
+        // stretches that begin inside the tile leave their parts in the first place
         base = a.parts;
         step = 2 * size;
-        second = u0 != w0 * share ? size : 0;
+        second = u0 < w0 * share ? 0 : size;
     }
     auto part = [&](int w) { return base + (size_t)w * step + (w == w0 ? second : 0); };
-    __shared__ float slots[8];
-    __shared__ float acc[8][256 + 1];
-    __shared__ float sums[8];
-    const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
-    float m = kLow;
-    for (int w = w0 + threadIdx.x; w <= w1; w += 256) m = fmaxf(m, part(w)[in]);
+    constexpr int kMost = 4, kDeep = 4;            // 64 channels at a time; parts in flight
+    float m = kLow, all = 0.0f, v[kMost] = {0, 0, 0, 0};
+    for (int w = w0 + (WAVES == 1 ? 0 : wave); w <= w1; w += WAVES * kDeep) {
+        float pm[kDeep], ps[kDeep], pv[kDeep][kMost];
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
-    if (lane == 0) slots[grp] = m;
-    __syncthreads();
-    m = slots[0];
+        for (int i = 0; i < kDeep; ++i) {
+            const float* p = part(min(w + WAVES * i, w1));
+            pm[i] = p[in];
+            ps[i] = p[R + in];
 #pragma unroll
-    for (int x = 1; x < 8; ++x) m = fmaxf(m, slots[x]);
-    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, all = 0.0f;
-    for (int w = w0 + grp; w <= w1; w += 8) {
-        const float* p = part(w);
-        const float f = __builtin_amdgcn_exp2f(p[in] - m);
-        all += p[R + in] * f;
+            for (int x = 0; x < kMost; ++x) pv[i][x] = lane + 64 * x < D ? p[2 * R + (size_t)in * D + lane + 64 * x] : 0.0f;
+        }
+        float top = m;
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-            const int d = lane + 32 * x;
-            if (d < D) v[x] = __builtin_fmaf(p[2 * R + (size_t)in * D + d], f, v[x]);
+        for (int i = 0; i < kDeep; ++i) {
+            if (w + WAVES * i > w1) pm[i] = -INFINITY;       // a part twice
+            top = fmaxf(top, pm[i]);
+        }
+        const float down = __builtin_amdgcn_exp2f(m - top);
+        m = top;
+        all *= down;
+#pragma unroll
+        for (int x = 0; x < kMost; ++x) v[x] *= down;
+#pragma unroll
+        for (int i = 0; i < kDeep; ++i) {
+            const float f = __builtin_amdgcn_exp2f(pm[i] - m);
+            all = __builtin_fmaf(ps[i], f, all);
+#pragma unroll
+            for (int x = 0; x < kMost; ++x) v[x] = __builtin_fmaf(pv[i][x], f, v[x]);
         }
     }
+    if constexpr (WAVES > 1) {
+        __shared__ float acc[WAVES][kMost][64], stat[WAVES][2];
 #pragma unroll
-    for (int x = 0; x < 8; ++x) acc[grp][lane + 32 * x] = v[x];
-    if (lane == 0) sums[grp] = all;
-    __syncthreads();
-    all = 0.0f;
+        for (int x = 0; x < kMost; ++x) acc[wave][x][lane] = v[x];
+        if (lane == 0) stat[wave][0] = m, stat[wave][1] = all;
+        __syncthreads();
+        if (wave > 0) return;
+        float top = stat[0][0];
 #pragma unroll
-    for (int x = 0; x < 8; ++x) all += sums[x];
+        for (int z = 1; z < WAVES; ++z) top = fmaxf(top, stat[z][0]);
+        m = top;
+        all = 0.0f;
+#pragma unroll
+        for (int x = 0; x < kMost; ++x) v[x] = 0.0f;
+#pragma unroll
+        for (int z = 0; z < WAVES; ++z) {
+            const float f = __builtin_amdgcn_exp2f(stat[z][0] - m);
+            all = __builtin_fmaf(stat[z][1], f, all);
+#pragma unroll
+            for (int x = 0; x < kMost; ++x) v[x] = __builtin_fmaf(acc[z][x][lane], f, v[x]);
+        }
+    }
     const float inv = all > 0.0f ? 1.0f / all : 0.0f;
     const size_t at = (size_t)t * a.heads + h;
-    if ((int)threadIdx.x < D / 2) {
-        float y[2] = {0, 0};
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-            y[0] += acc[x][2 * threadIdx.x];
-            y[1] += acc[x][2 * threadIdx.x + 1];
-        }
-        ((uint32_t*)(a.out + at * D))[threadIdx.x] =
-            a.bf16 ? pack2<BF16>(y[0] * inv, y[1] * inv) : pack2<F16>(y[0] * inv, y[1] * inv);
-    }
-    if (threadIdx.x == 0 && a.lse)
-        a.lse[at] = all > 0.0f ? (m + __builtin_amdgcn_logf(all)) * kLn2 : -INFINITY;
+    for (int x = 0; x < kMost; ++x)
+        if (lane + 64 * x < D) a.out[at * D + lane + 64 * x] = a.bf16 ? BF16::store(v[x] * inv) : F16::store(v[x] * inv);
+    if (lane == 0 && a.lse) a.lse[at] = all > 0.0f ? (m + __builtin_amdgcn_logf(all)) * kLn2 : -INFINITY;
 }
 
 // columns of 16 rows (0: attend_tile.hip's tiles), the workgroups and whether tiles
@@ -499,6 +530,8 @@ struct Plan {
     int rows() const { return columns ? 16 * columns : tile.rows; }
     int places() const { return columns ? 2 : 1; }           // parts that a workgroup may leave
 };
+
+size_t line_bytes(int B) { return ((size_t)B + 1) * sizeof(long long) / 16 * 16 + 16; }
 
 Plan plan(int T, int B, int heads, int kv, int dim, int max_new, int max_len) {
     Plan p;
@@ -537,7 +570,8 @@ void launch_d(const AttendArgs& a, int columns, hipStream_t st) {
 
 size_t attend_workspace_bytes(int T, int B, int heads, int kv, int dim, int max_new, int max_len) {
     const Plan p = plan(T, B, heads, kv, dim, max_new, max_len);
-    return p.split ? (size_t)p.groups * p.places() * p.rows() * (dim + 2) * sizeof(float) : 0;
+    if (!p.split) return 0;
+    return line_bytes(B) + (size_t)p.groups * p.places() * p.rows() * (dim + 2) * sizeof(float);
 }
 
 int launch_cache_attention(const AttendProblem& p, void* workspace, hipStream_t st) {
@@ -558,7 +592,8 @@ int launch_cache_attention(const AttendProblem& p, void* workspace, hipStream_t 
     a.bf16 = p.dtype == AWQ_BF16;
     a.split = pl.split;
     a.groups = pl.groups;
-    a.parts = (float*)workspace;
+    a.line = (long long*)workspace;
+    a.parts = (float*)((char*)workspace + (pl.split ? line_bytes(p.seqs.B) : 0));
     int e = 0;
     if (!pl.columns) e = launch_attend_tile(a, pl.tile, st);
     else switch (p.cache.dim) {
@@ -571,7 +606,11 @@ int launch_cache_attention(const AttendProblem& p, void* workspace, hipStream_t 
     if (e || (e = (int)hipGetLastError())) return e;
     if (!pl.split) return 0;
     const JoinArgs ja{a, pl.rows(), p.cache.dim, pl.columns ? 0 : pl.tile.parts};
-    hipLaunchKernelGGL(k_attend_join, dim3((unsigned)p.seqs.T * p.heads), dim3(256), 0, st, ja);
+    const unsigned rows = (unsigned)p.seqs.T * p.heads;
+    if (rows < (unsigned)device_cu_count() * 4)
+        hipLaunchKernelGGL((k_attend_join<16>), dim3(rows), dim3(1024), 0, st, ja);
+    else
+        hipLaunchKernelGGL((k_attend_join<1>), dim3((rows + 3) / 4), dim3(256), 0, st, ja);
     return (int)hipGetLastError();
 }
 

@@ -50,12 +50,18 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attend_tile(Atten
 
     // the tile: heads first (neighbouring workgroups, on different XCDs, read different
     // heads), long rows of keys before short ones
-    long long before;
-    int b = find_line(a, R, true, blockIdx.x / parts, before);
+    const LineWalk walk(a, R, true);
+    if (parts > 1 && blockIdx.x == 0)              // the join wants to know the line
+        walk([&](int b, long long, long long before) {
+            if (b < s.B) a.line[b] = before;
+            return false;
+        });
+    const long long unit = blockIdx.x / parts;
+    const auto mine = walk([&](int, long long u, long long before) { return unit < before + u; });
+    const int b = mine.b;
     if (b < 0) return;
-    b = __builtin_amdgcn_readfirstlane(b);
-    const Line l(a, b, R);
-    const int at = __builtin_amdgcn_readfirstlane((int)(blockIdx.x - before * parts));
+    const Line& l = mine.line;
+    const int at = (int)(blockIdx.x - mine.before * parts);
     const int head = at % kv;
     const int part = at / kv % parts;
     const int tile = l.tiles - 1 - at / kv / parts;
@@ -63,7 +69,7 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attend_tile(Atten
     const int pos_lo = pos0 + tile * R / a.group;
     const int pos_hi = pos0 + min(tile * R + R - 1, l.rows - 1) / a.group;
     // tiles of keys [t0, t1) that some row sees, and this part's share
-    const int span = s.span(b, page_log2);
+    const int span = s.span(l.len, page_log2);
     const int first = a.window > 0 ? max((int)max((long long)pos_lo + 1 - a.window, 0LL), 0) : 0;
     const int last = min(pos_hi, span - 1);                          // -1: nothing
     int t0 = first / kKeys, t1 = last >= first ? last / kKeys + 1 : t0;
@@ -83,7 +89,7 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attend_tile(Atten
         const int row = min(row0 + 32 * ct + col, l.rows - 1);
         const int j = row / a.group, h = head * a.group + (row - j * a.group);
         pos[ct] = pos0 + j;
-        const uint16_t* from = a.q + (size_t)(s.start(b) + j) * a.q_stride + (size_t)h * D + 8 * hf;
+        const uint16_t* from = a.q + (size_t)(l.start + j) * a.q_stride + (size_t)h * D + 8 * hf;
         uint4 raw[NC];
 #pragma unroll
         for (int c = 0; c < NC; ++c) raw[c] = *(const uint4*)(from + 16 * c);
@@ -341,7 +347,7 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attend_tile(Atten
             continue;
         }
         const int j = row / a.group, h = head * a.group + (row - j * a.group);
-        const size_t out = (size_t)(s.start(b) + j) * a.heads + h;
+        const size_t out = (size_t)(l.start + j) * a.heads + h;
         const float inv = all > 0.0f ? 1.0f / all : 0.0f;
 #pragma unroll
         for (int d = 0; d < ND; ++d) {

@@ -30,9 +30,9 @@ struct Sequences {
     __device__ __forceinline__ int start(int b) const { return starts ? min(max(starts[b], 0), T) : b; }
     __device__ __forceinline__ int rows(int b) const { return starts ? max(start(b + 1) - start(b), 0) : 1; }
     __device__ __forceinline__ int len(int b) const { return max(lens[b], 0); }
-    // its tokens that a table row has room for
-    __device__ __forceinline__ int span(int b, int page_log2) const {
-        return (int)min((long long)len(b), (long long)W << page_log2);
+    // of `len` tokens those that a table row has room for
+    __device__ __forceinline__ int span(int len, int page_log2) const {
+        return (int)min((long long)len, (long long)W << page_log2);
     }
     __device__ __forceinline__ int page(int b, int w, int pages) const {
         const int p = (unsigned)w < (unsigned)W ? tables[(size_t)b * W + w] : -1;
@@ -47,6 +47,29 @@ struct Sequences {
             if (starts[mid] <= t) lo = mid; else hi = mid;
         }
         return B > 0 && starts[lo] <= t && t < starts[lo + 1] ? lo : -1;
+    }
+    // the same for a whole wave, t the same in all lanes: 256 sequences a load
+    __device__ __forceinline__ int of_row_by_wave(int t) const {
+        if (!starts) return t < B ? t : -1;
+        const int lane = threadIdx.x & 63;
+        for (int b0 = 0; b0 < B; b0 += 256) {
+            int from[4], to[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int b = min(b0 + 64 * k + lane, B - 1);
+                from[k] = starts[b];
+                to[k] = starts[b + 1];
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint64_t hit = __builtin_amdgcn_ballot_w64(to[k] > t);
+                if (hit) {
+                    const int i = __builtin_ctzll(hit), b = b0 + 64 * k + i;
+                    return b < B && __builtin_amdgcn_readlane(from[k], i) <= t ? b : -1;
+                }
+            }
+        }
+        return -1;
     }
 };
 

@@ -545,6 +545,7 @@ awq_status awq_moe(const void* x, const float* inv_s, const void* router,
  *                  lens[b]) are not cached, attend to nothing and read as zeros.
  * A page may be in the rows of several sequences as long as no call writes to
  * it.  int32 and fp32 arrays need 4-byte alignment only.  T, B <= 2^20, and
+ * kv_heads <= 65535, and
  * what a launch cannot count (2^24 workgroups) is AWQ_ERR_SHAPE.
  * ------------------------------------------------------------------------ */
 
@@ -630,7 +631,7 @@ awq_status awq_cache_read(const void* k_codes, const float* k_scales, const void
  * awq_cache_attention -- attention of each sequence's last tokens over its cache:
  *   s_j = scale * q.k_j, or softcap * tanh(scale * q.k_j / softcap) with softcap > 0
  *   out = sum_j p_j v_j,  p = softmax over the keys j <= the query's place (and
- *         j > place - window with window > 0)
+ *         j > place - window with window > 0; from 2^30 on it counts as 2^30)
  *   lse = ln sum_j exp(s_j)
  *   Query head h reads kv head h / (heads / kv_heads).  A query with no key has
  *   out 0 and lse -infinity.

@@ -87,8 +87,8 @@ def attention(q, cache, tables, lens, starts, scale, window=0, softcap=0.0):
 
     Scores: fp32 sums of D products of q with codes of up to 255 (biased), in any order, (D + 2) 2^-24 of the
     sum of magnitudes; one multiply-add, the exponential and the scales' logarithm 2^-20 with room.  Weights
-    times the value scale are rounded to fp16: half a step, 2^-11 relative, or 2^-25 of the largest one's unit (the
-    largest is at least 1 in it); then D-wide sums in fp32."""
+    times the value scale are rounded to fp16: half a step, 2^-11 relative, or 2^-25 of a unit in which the
+    largest one is at least 2^-2 (the running maximum is set at most 2^2 above it), 2^-23 of that one; then D-wide sums in fp32."""
     kc, ks, vc, vs = cache
     T, H, D = q.shape
     pages, kv, page = kc.shape[:3]
@@ -117,7 +117,7 @@ def attention(q, cache, tables, lens, starts, scale, window=0, softcap=0.0):
                 score = (D + 2) * 2.0 ** -24 * abs(scale) * np.abs(q[row, h]).sum() * 255.0 * sk.max()
                 score += 2.0 ** -20 * (1.0 + (softcap or 0.0) / 8.0)
                 weight = 2.0 ** -11 + 2.0 * math.expm1(score) + 2.0 ** -20 * (2.0 + abs(np.log2(np.maximum(sv, 2.0 ** -100))).max())
-                bound[row, h] = weight * (p @ np.abs(v)) + 2.0 ** -25 * (p * sv).max() * np.abs(codes).sum(0)
+                bound[row, h] = weight * (p @ np.abs(v)) + 2.0 ** -23 * (p * sv).max() * np.abs(codes).sum(0)
                 bound[row, h] += 2.0 ** -20 * 128.0 * (p @ sv)      # the bias of 128 leaves fp32 sums
     return out, lse, bound
 

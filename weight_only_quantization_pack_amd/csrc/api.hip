@@ -542,6 +542,8 @@ constexpr long long kMaxGroups = 1LL << 24;      // workgroups of 256 threads: a
 constexpr int kMaxCacheRows = 1 << 20;           // rows (tokens) and sequences of a call
 constexpr int kMaxBookRows = 65535;              // table rows are a launch's second dimension
 constexpr int kMaxPages = 1 << 30;
+constexpr int kMaxKvHeads = 65535;
+constexpr int kMaxWindow = 1 << 30;              // positions less a window stay in 31 bits
 
 // index arrays are int32 and need no more than their own alignment
 int check_index(std::initializer_list<const void*> ps) {
@@ -574,7 +576,8 @@ int check_page(int page_size) {
 int check_cache(int kv_heads, int dim, int pages, int page_size) {
     if (int st = check_page(page_size)) return st;
     if (dim != 64 && dim != 96 && dim != 128 && dim != 192 && dim != 256) return AWQ_ERR_UNSUPPORTED;
-    return kv_heads <= 0 || pages <= 0 || pages > kMaxPages ? AWQ_ERR_SHAPE : AWQ_OK;
+    // a page of all heads stays below 2^31 codes
+    return kv_heads <= 0 || kv_heads > kMaxKvHeads || pages <= 0 || pages > kMaxPages ? AWQ_ERR_SHAPE : AWQ_OK;
 }
 
 // T rows of B sequences with tables of W pages; without starts every sequence has one row
@@ -732,7 +735,8 @@ awq_status awq_cache_attention(const void* q, long long q_stride, const void* k_
         return as_status(st);
     const awq::AttendProblem p{q, q_stride, out, lse,
                                cache_of(k_codes, k_scales, v_codes, v_scales, pages, kv_heads, page_size, head_dim),
-                               awq::Sequences{tables, lens, starts, T, B, W}, scale, softcap, heads, window, max_new,
+                               awq::Sequences{tables, lens, starts, T, B, W}, scale, softcap, heads,
+                               window < kMaxWindow ? window : kMaxWindow, max_new,
                                max_len, dtype};
     return hip_status(awq::launch_cache_attention(p, workspace, stream));
 }

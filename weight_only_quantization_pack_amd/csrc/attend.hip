@@ -270,11 +270,11 @@ __global__ __launch_bounds__(64 * kW, 2) void k_attend(AttendArgs a) {
                 const float f = ks * qf[ct];
                 if (a.softcap > 0.0f) {
                     // cap tanh(x / cap) = cap - 2 cap / (exp(2 x / cap) + 1)
-                    const float e = 2.0f * kLog2e / a.softcap * f;
+                    const float e = 2.0f * kLog2e / a.softcap * f, cap = kLog2e * a.softcap;
 #pragma unroll
                     for (int y = 0; y < 8; ++y) {
                         const float z = __builtin_amdgcn_exp2f(sc[ct][y >> 2][y & 3] * e);
-                        t[y] = __builtin_fmaf(kLog2e * a.softcap, 1.0f - 2.0f * __builtin_amdgcn_rcpf(z + 1.0f), lv);
+                        t[y] = __builtin_fmaf(2.0f * cap, __builtin_amdgcn_rcpf(-1.0f - z), lv + cap);
                     }
                 } else {
 #pragma unroll

@@ -26,25 +26,34 @@ template <int D>
 struct Image {
     static constexpr int KS = D == 96 ? 128 : D;            // halves of a key row (swizzled in blocks of 64)
     static constexpr int keys = kKeys * KS * 2, values = D * kKeys * 2;
-    static constexpr int bytes = keys + values;
 };
 
-// rows of A (32 of them, r) to keys and channels, so that a lane's 16 results are
-// 2 x 8 consecutive keys, or 16 consecutive channels
-__device__ __forceinline__ int key_of(int r) { return 16 * (r >> 4) + 8 * (r >> 2 & 1) + 4 * (r >> 3 & 1) + (r & 3); }
-__device__ __forceinline__ int channel_of(int r) { return 16 * (r >> 2 & 1) + 4 * (r >> 3) + (r & 3); }
-__device__ __forceinline__ int key_swizzle(int key) { return (key & 3) | (key >> 3 & 1) << 2; }
-__device__ __forceinline__ int channel_swizzle(int d) { return ((d ^ d >> 2) & 3) | (d >> 4 & 1) << 2; }
 
-template <int D, int CT, int NW>
+// Row r of the A operand with the keys of score tile t (of two that make 32 keys), and
+// with the channels of output tile t (of two that make 32): a lane's results are then 8
+// consecutive keys of each 32, which is what it holds as B of the next product, and 8
+// consecutive channels.
+__device__ __forceinline__ int row_of(int t, int r) { return 8 * (r >> 2) + 4 * t + (r & 3); }
+
+// Position of 16-byte chunk c of a row of an image, for rows of ROW bytes: the 16 lanes
+// that read a chunk of 16 rows together (they differ in bits 0, 1, 3 and 4 of the row)
+// meet 16 different quarters of the 64 banks; the other bits spread the writes.
+template <int ROW>
+__device__ __forceinline__ int swizzle(int row) {
+    if constexpr (ROW % 256 == 0) return ((row & 3) | (row >> 3 & 3) << 2) ^ (row >> 2 & 1);
+    return ((row >> 1 & 1) | (row >> 3 & 3) << 1) ^ (row >> 2 & 1);
+}
+
+template <int D, int NW>
 __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attend_tile(AttendArgs a, int parts) {
-    constexpr int NT = 64 * NW, R = 32 * CT * NW, NC = D / 16, ND = D / 32;
+    constexpr int NT = 64 * NW, CT = 2, R = 16 * CT * NW, NC = D / 32, ND = D / 16;
     constexpr int KP = kKeys * D / 16, VP = kKeys / 4 * D / 4;       // pieces of a tile: 16 codes; 4 x 4 codes
     constexpr int KN = (KP + NT - 1) / NT, VN = (VP + NT - 1) / NT;
     using I = Image<D>;
+    constexpr int kRow = 2 * I::KS, vRow = 2 * kKeys;                // bytes of the images' rows
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int col = lane & 31, hf = lane >> 5;
+    const int col = lane & 15, g = lane >> 4;
     const Sequences& s = a.seqs;
     const int kv = a.cache.kv, page_log2 = a.cache.page_log2;
 
@@ -79,20 +88,21 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attend_tile(Atten
         t0 = t0 + (int)((long long)n * part / parts);
     }
 
-    // rows of the wave: column col of column tile ct is row 32 (CT wave + ct) + col
+    // rows of the wave: column col of column tile ct is row 16 (2 wave + ct) + col
     int pos[CT];
     half8_t q[CT][NC];
-    float qf[CT], bias[CT];
-    const int row0 = tile * R + 32 * CT * wave;
+    float qf[CT];
+    float4_t bias[CT];
+    const int row0 = tile * R + 16 * CT * wave;
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
-        const int row = min(row0 + 32 * ct + col, l.rows - 1);
+        const int row = min(row0 + 16 * ct + col, l.rows - 1);
         const int j = row / a.group, h = head * a.group + (row - j * a.group);
         pos[ct] = pos0 + j;
-        const uint16_t* from = a.q + (size_t)(l.start + j) * a.q_stride + (size_t)h * D + 8 * hf;
+        const uint16_t* from = a.q + (size_t)(l.start + j) * a.q_stride + (size_t)h * D + 8 * g;
         uint4 raw[NC];
 #pragma unroll
-        for (int c = 0; c < NC; ++c) raw[c] = *(const uint4*)(from + 16 * c);
+        for (int c = 0; c < NC; ++c) raw[c] = *(const uint4*)(from + 32 * c);
         float top = 0.0f;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
@@ -101,10 +111,11 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attend_tile(Atten
 #pragma unroll
             for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
         }
+        top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
         const int e2 = query_exponent(top);
         const float up = power_of_two(e2) * a.sign;
-        qf[ct] = power_of_two(-e2);
+        qf[ct] = power_of_two(-e2) * kLog2e;
         float sum = 0.0f;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
@@ -116,81 +127,76 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attend_tile(Atten
                 sum += (float)q[ct][c][e];
             }
         }
+        sum += __shfl_xor(sum, 16);
         sum += __shfl_xor(sum, 32);
-        bias[ct] = sum * -0x1p-17f;
+        bias[ct] = float4_t{1, 1, 1, 1} * (sum * -0x1p-17f);
     }
-    // positions of the wave's rows; a wave without rows only helps to stage
-    const bool idle = row0 >= l.rows;
+    // positions of the wave's rows; a wave without rows goes along with the last one
     const int wave_lo = pos0 + min(row0, l.rows - 1) / a.group;
-    const int wave_hi = idle ? -1 : pos0 + min(row0 + 32 * CT - 1, l.rows - 1) / a.group;
+    const int wave_hi = pos0 + min(row0 + 16 * CT - 1, l.rows - 1) / a.group;
 
     float M[CT], sum[CT];
-    float16_t o[CT][ND];
+    float4_t o[CT][ND];
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
         M[ct] = kLow;
         sum[ct] = 0.0f;
 #pragma unroll
-        for (int d = 0; d < ND; ++d)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[ct][d][i] = 0.0f;
+        for (int d = 0; d < ND; ++d) o[ct][d] = float4_t{0, 0, 0, 0};
     }
 
-    // pages and scales of the next 64 chunks of 16 keys (16 tiles), one a lane
-    int page_l = -1;
-    float c_l = -1.0f, lv_l = 0.0f, iv_l = 1.0f;
-    auto fetch_pages = [&](int t) {
+    // Pages of 64 chunks of 16 keys (16 tiles), one a lane, asked for a block of chunks
+    // ahead; their scales are asked for with the block's first codes and taken over when
+    // its first scores need them.
+    auto page_ids = [&](int t) {
         const long long key = (long long)t * kKeys + 16 * lane;
-        const int p = key < span ? s.page(b, (int)(key >> page_log2), a.cache.pages) : -1;
-        const size_t i = (size_t)max(p, 0) * kv + head;
-        page_l = p;
-        c_l = p >= 0 ? a.cache.scales[0][i] * a.scale : -1.0f;
-        const float vs = p >= 0 ? fmaxf(a.cache.scales[1][i], 0x1p-100f) : 1.0f;
-        lv_l = __builtin_amdgcn_logf(vs);
-        iv_l = 1.0f / vs;
+        return key < span ? s.page(b, (int)(key >> page_log2), a.cache.pages) : -1;
     };
-    // a tile's codes on their way, and its chunks' scales
+    int page_l = -1, page_next = page_ids(t0);
+    float ks_next = 0.0f, vs_next = 0.0f;
+    float c_l = -1.0f, lv_l = 0.0f, iv_l = 1.0f;
+    // a tile's codes on their way
+    const int mask = (1 << page_log2) - 1;
+    const uint32_t page_bytes = (uint32_t)kv * (uint32_t)D << page_log2, head_bytes = (uint32_t)head * (uint32_t)D << page_log2;
     uint4 kr[KN];
     uint32_t vr[VN][4];
-    float cs[4], lvs[4], ivs[4];
     auto load = [&](int t) {
         const int i = (t - t0) & 15;
-        if (i == 0) fetch_pages(t);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            cs[c] = lane_value(c_l, 4 * i + c);
-            lvs[c] = lane_value(lv_l, 4 * i + c);
-            ivs[c] = lane_value(iv_l, 4 * i + c);
+        if (i == 0) {
+            page_l = page_next;
+            page_next = page_ids(t + 16);
+            const size_t at = (size_t)max(page_l, 0) * kv + head;
+            ks_next = page_l >= 0 ? a.cache.scales[0][at] * a.scale : -1.0f;
+            vs_next = page_l >= 0 ? a.cache.scales[1][at] : 1.0f;
         }
-        const int mask = (1 << page_log2) - 1;
+        // tiles start at a page or in the middle of one: a key's slot is the tile's plus its own
+        const uint32_t slot = (uint32_t)((t * kKeys) & mask) * D + head_bytes;
 #pragma unroll
         for (int x = 0; x < KN; ++x) {
-            const int p = tid + NT * x, key = p / NC, c = p - key * NC;
-            const int page = max(__shfl(page_l, 4 * i + (key >> 4 & 3)), 0);
+            const int p = tid + NT * x, key = p / (D / 16), c = p - key * (D / 16);
+            const uint32_t page = (uint32_t)max(__shfl(page_l, 4 * i + (key >> 4 & 3)), 0);
             if (KP % NT == 0 || p < KP)
-                kr[x] = *(const uint4*)(a.cache.codes[0] + a.cache.block(page, head) +
-                                        (uint32_t)(((t * kKeys + key) & mask) * D + 16 * c));
+                kr[x] = *(const uint4*)(a.cache.codes[0] + ((uint64_t)page * page_bytes + slot) + (uint32_t)((key & mask) * D + 16 * c));
         }
 #pragma unroll
         for (int x = 0; x < VN; ++x) {
             const int p = tid + NT * x, kg = p / (D / 4), dg = p - kg * (D / 4);
-            const int page = max(__shfl(page_l, 4 * i + (kg >> 2 & 3)), 0);
+            const uint32_t page = (uint32_t)max(__shfl(page_l, 4 * i + (kg >> 2 & 3)), 0);
             if (VP % NT == 0 || p < VP) {
-                const int8_t* from = a.cache.codes[1] + a.cache.block(page, head) +
-                                     (uint32_t)(((t * kKeys + 4 * kg) & mask) * D + 4 * dg);
+                const int8_t* from = a.cache.codes[1] + ((uint64_t)page * page_bytes + slot) + (uint32_t)((4 * kg & mask) * D + 4 * dg);
 #pragma unroll
                 for (int y = 0; y < 4; ++y) vr[x][y] = *(const uint32_t*)(from + y * D);
             }
         }
     };
-    auto store = [&](unsigned char* image) {
+    auto store = [&](unsigned char* keys, unsigned char* values) {
 #pragma unroll
         for (int x = 0; x < KN; ++x) {
-            const int p = tid + NT * x, key = p / NC, c = p - key * NC;
+            const int p = tid + NT * x, key = p / (D / 16), c = p - key * (D / 16);
             if (KP % NT == 0 || p < KP) {
                 const uint32_t w[4] = {kr[x].x ^ 0x80808080u, kr[x].y ^ 0x80808080u, kr[x].z ^ 0x80808080u, kr[x].w ^ 0x80808080u};
-                unsigned char* row = image + key * (2 * I::KS);
-                const int sw = key_swizzle(key);
+                unsigned char* row = keys + key * kRow;
+                const int sw = swizzle<kRow>(key);
                 *(uint4*)(row + ((2 * c ^ sw) << 4)) = make_uint4(key_pair(w[0], 0), key_pair(w[0], 1), key_pair(w[1], 0), key_pair(w[1], 1));
                 *(uint4*)(row + (((2 * c + 1) ^ sw) << 4)) = make_uint4(key_pair(w[2], 0), key_pair(w[2], 1), key_pair(w[3], 0), key_pair(w[3], 1));
             }
@@ -210,76 +216,110 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attend_tile(Atten
                     const half2_t lo = __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(w[1], w[0], sel) | 0x64006400u) + m;
                     const half2_t hi = __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(w[3], w[2], sel) | 0x64006400u) + m;
                     const int d = 4 * dg + j;
-                    *(uint2*)(image + I::keys + d * (2 * kKeys) + (((kg >> 1) ^ channel_swizzle(d)) << 4) + (kg & 1) * 8) =
+                    *(uint2*)(values + d * vRow + (((kg >> 1) ^ swizzle<vRow>(d)) << 4) + (kg & 1) * 8) =
                         make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
                 }
             }
         }
     };
 
-    const int key_row = key_of(col) * (2 * I::KS), key_x = hf ^ key_swizzle(key_of(col));
-    const int channel_row = I::keys + channel_of(col) * (2 * kKeys), channel_x = hf ^ channel_swizzle(channel_of(col));
+    // A operands: row_of(0 or 1, col) + 32 n, chunk 4 c + g; rows 32 apart swizzle alike, and
+    // the two tiles of 32 rows differ in bit 2 of the row, which flips bit 0
+    const int key_row = row_of(0, col) * kRow, key_x = g ^ swizzle<kRow>(row_of(0, col));
+    const int channel_row = row_of(0, col) * vRow, channel_x = g ^ swizzle<vRow>(row_of(0, col));
+    auto key_operand = [&](const unsigned char* keys, int kt, int c) {
+        return *(const half8_t*)(keys + (32 * (kt >> 1) + 4 * (kt & 1)) * kRow + key_row + ((4 * c ^ key_x ^ (kt & 1)) << 4));
+    };
+    auto value_operand = [&](const unsigned char* values, int d, int kc) {
+        return *(const half8_t*)(values + (32 * (d >> 1) + 4 * (d & 1)) * vRow + channel_row + ((4 * kc ^ channel_x ^ (d & 1)) << 4));
+    };
 
-    auto compute = [&](const unsigned char* image, int t, const float* c4, const float* lv4, const float* iv4) {
-        const int key0 = t * kKeys;
-        if (key0 > wave_hi) return;
-        float16_t sc[CT][2];
+    float4_t sc[CT][4];
+    half8_t w[CT][2];
+    auto scores = [&](const unsigned char* keys) {
 #pragma unroll
-        for (int st = 0; st < 2; ++st) {
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) sc[ct][st][i] = bias[ct];
+        for (int kt = 0; kt < 4; ++kt)
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
-                const half8_t k = *(const half8_t*)(image + st * (32 * 2 * I::KS) + key_row + ((2 * c ^ key_x) << 4));
+                const half8_t k = key_operand(keys, kt, c);
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct)
-                    sc[ct][st] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[ct][c], sc[ct][st], 0, 0, 0);
+                    sc[ct][kt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[ct][c], c == 0 ? bias[ct] : sc[ct][kt], 0, 0, 0);
             }
+        // eight operands under way before the first product needs one
+        constexpr int kAhead = 8;
+        __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+        for (int i = 0; i < 4 * NC - kAhead; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, CT, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
         }
-        const bool pages = c4[0] >= 0.0f && c4[1] >= 0.0f && c4[2] >= 0.0f && c4[3] >= 0.0f;
-        const bool open = pages && key0 + kKeys - 1 <= wave_lo && (a.window <= 0 || key0 > wave_hi - a.window);
-        half8_t w[CT][4];
+        __builtin_amdgcn_sched_group_barrier(0x008, CT * kAhead, 0);
+    };
+    auto weights = [&](int t) {
+        const int i = (t - t0) & 15, key0 = t * kKeys;
+        if (i == 0) {
+            c_l = ks_next;
+            const float vs = fmaxf(vs_next, 0x1p-100f);
+            lv_l = __builtin_amdgcn_logf(vs);
+            iv_l = 1.0f / vs;
+        }
+        // scales of this lane's halves of the two 32 keys
+        float ks[2], lv[2], iv[2];
+#pragma unroll
+        for (int kc = 0; kc < 2; ++kc) {
+            const int from = 4 * i + 2 * kc + (g >> 1);
+            ks[kc] = __shfl(c_l, from);
+            lv[kc] = __shfl(lv_l, from);
+            iv[kc] = __shfl(iv_l, from);
+        }
+        const bool closed = __builtin_amdgcn_ballot_w64(fminf(ks[0], ks[1]) < 0.0f) || key0 + kKeys - 1 > wave_lo ||
+                            (a.window > 0 && key0 <= wave_hi - a.window);
+        float f[CT][2];                            // log2 weights are f * product + lv
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
-            // a chunk's scores are f * product; the product of no product is left at 0
-            float f[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) f[c] = fmaxf(c4[c] * qf[ct] * kLog2e, 0x1p-126f);
+            for (int kc = 0; kc < 2; ++kc) f[ct][kc] = fmaxf(ks[kc] * qf[ct], 0x1p-126f);
             if (a.softcap > 0.0f) {
-                // cap tanh(x / cap) = cap (1 - 2 / (exp(2 x / cap) + 1))
+                // cap tanh(x / cap) = cap - 2 cap / (exp(2 x / cap) + 1): the product becomes
+                // -1 / (exp(2 x / cap) + 1), its factor 2 cap, and cap is added with lv
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const float e = 2.0f / a.softcap * f[c];
-#pragma unroll
-                    for (int y = 0; y < 8; ++y) {
-                        const float x = sc[ct][c >> 1][8 * (c & 1) + y] * e;
-                        sc[ct][c >> 1][8 * (c & 1) + y] = 1.0f - 2.0f * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(x) + 1.0f);
-                    }
-                    f[c] = kLog2e * a.softcap;
-                }
-            }
-            if (!open) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int key = key0 + 16 * c + 8 * hf;
+                for (int kc = 0; kc < 2; ++kc) {
+                    const float e = 2.0f / a.softcap * f[ct][kc];
 #pragma unroll
                     for (int y = 0; y < 8; ++y) {
-                        const bool seen = c4[c] >= 0.0f && key + y <= pos[ct] && (a.window <= 0 || key + y > pos[ct] - a.window);
-                        if (!seen) sc[ct][c >> 1][8 * (c & 1) + y] = -INFINITY;
+                        const float x = sc[ct][2 * kc + (y >> 2)][y & 3] * e;
+                        sc[ct][2 * kc + (y >> 2)][y & 3] = __builtin_amdgcn_rcpf(-1.0f - __builtin_amdgcn_exp2f(x));
                     }
+                    f[ct][kc] = 2.0f * kLog2e * a.softcap;
+                    if (ct == 0) lv[kc] = __builtin_fmaf(kLog2e, a.softcap, lv[kc]);
                 }
             }
+            if (closed) {
+                // the product of a key that the row does not see is -infinity (f > 0)
+#pragma unroll
+                for (int kc = 0; kc < 2; ++kc) {
+                    const int key = key0 + 32 * kc + 8 * g;
+                    const int hi = ks[kc] >= 0.0f ? pos[ct] - key : -1;                  // keys y <= hi, > lo are seen
+                    const int lo = a.window > 0 ? pos[ct] - a.window - key : -1;
+#pragma unroll
+                    for (int y = 0; y < 8; ++y)
+                        sc[ct][2 * kc + (y >> 2)][y & 3] = y <= hi && y > lo ? sc[ct][2 * kc + (y >> 2)][y & 3] : -INFINITY;
+                }
+            }
+        }
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
             float top = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                float m = sc[ct][c >> 1][8 * (c & 1)];
+            for (int kc = 0; kc < 2; ++kc) {
+                float m = sc[ct][2 * kc][0];
 #pragma unroll
-                for (int y = 1; y < 8; ++y) m = fmaxf(m, sc[ct][c >> 1][8 * (c & 1) + y]);
-                top = fmaxf(top, __builtin_fmaf(m, f[c], lv4[c]));
+                for (int y = 1; y < 8; ++y) m = fmaxf(m, sc[ct][2 * kc + (y >> 2)][y & 3]);
+                top = fmaxf(top, __builtin_fmaf(m, f[ct][kc], lv[kc]));
             }
             if (__builtin_amdgcn_ballot_w64(top > M[ct] + kSlack)) {
+                top = fmaxf(top, __shfl_xor(top, 16));
                 top = fmaxf(top, __shfl_xor(top, 32));
                 const float m = fmaxf(M[ct], top);
                 const float down = __builtin_amdgcn_exp2f(M[ct] - m);
@@ -288,61 +328,68 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attend_tile(Atten
 #pragma unroll
                 for (int d = 0; d < ND; ++d) o[ct][d] *= down;
             }
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const float less = lv4[c] - M[ct];
-                float p8 = 0.0f;
-#pragma unroll
-                for (int y = 0; y < 8; ++y) {
-                    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[ct][c >> 1][8 * (c & 1) + y], f[c], less));
-                    p8 += p;
-                    w[ct][c][y] = (_Float16)p;
-                }
-                sum[ct] = __builtin_fmaf(p8, iv4[c], sum[ct]);
-            }
         }
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int kc = 0; kc < 2; ++kc)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                // summed in fp32: a block whose values are small (or zeros) has weights that fp16
+                // loses, but not its share of the softmax
+                const float less = lv[kc] - M[ct];
+                float all = 0.0f;
+#pragma unroll
+                for (int y = 0; y < 8; ++y) {
+                    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[ct][2 * kc + (y >> 2)][y & 3], f[ct][kc], less));
+                    all += p;
+                    w[ct][kc][y] = (_Float16)p;
+                }
+                sum[ct] = __builtin_fmaf(all, iv[kc], sum[ct]);
+            }
+    };
+    auto values = [&](const unsigned char* values) {
+#pragma unroll
+        for (int kc = 0; kc < 2; ++kc)
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
-                const half8_t v = *(const half8_t*)(image + channel_row + d * (32 * 2 * kKeys) + ((2 * c ^ channel_x) << 4));
+                const half8_t v = value_operand(values, d, kc);
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct)
-                    o[ct][d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w[ct][c], o[ct][d], 0, 0, 0);
+                    o[ct][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, w[ct][kc], o[ct][d], 0, 0, 0);
             }
     };
 
+    unsigned char* const value_images = smem + 2 * I::keys;
     if (t0 < t1) {
         load(t0);
         for (int t = t0; t < t1; ++t) {
-            unsigned char* image = smem + ((t - t0) & 1) * I::bytes;
-            float c4[4], lv4[4], iv4[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) c4[c] = cs[c], lv4[c] = lvs[c], iv4[c] = ivs[c];
-            store(image);                // the other image is still being read by slower waves
+            const int at = (t - t0) & 1;
+            store(smem + at * I::keys, value_images + at * I::values);      // slower waves still read the other place
             if (t + 1 < t1) load(t + 1);
             __syncthreads();
-            compute(image, t, c4, lv4, iv4);
+            scores(smem + at * I::keys);
+            weights(t);
+            values(value_images + at * I::values);
         }
     }
 
     float* slot = parts > 1 ? a.parts + (size_t)blockIdx.x * (size_t)(R * (D + 2)) : nullptr;
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
-        const float all = sum[ct] + __shfl_xor(sum[ct], 32);
-        const int in = 32 * (CT * wave + ct) + col, row = tile * R + in;
+        float all = sum[ct];
+        all += __shfl_xor(all, 16);
+        all += __shfl_xor(all, 32);
+        const int in = 16 * (CT * wave + ct) + col, row = tile * R + in;
         if (row >= l.rows) continue;
         if (parts > 1) {
-            if (hf == 0) {
+            if (g == 0) {
                 slot[in] = M[ct];
                 slot[R + in] = all;
             }
 #pragma unroll
-            for (int d = 0; d < ND; ++d) {
-                float4* to = (float4*)(slot + 2 * R + in * D + 32 * d + 16 * hf);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    to[i] = make_float4(o[ct][d][4 * i], o[ct][d][4 * i + 1], o[ct][d][4 * i + 2], o[ct][d][4 * i + 3]);
+            for (int d = 0; d < ND; d += 2) {
+                float4* to = (float4*)(slot + 2 * R + in * D + 16 * d + 8 * g);
+                to[0] = make_float4(o[ct][d][0], o[ct][d][1], o[ct][d][2], o[ct][d][3]);
+                to[1] = make_float4(o[ct][d + 1][0], o[ct][d + 1][1], o[ct][d + 1][2], o[ct][d + 1][3]);
             }
             continue;
         }
@@ -350,22 +397,20 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attend_tile(Atten
         const size_t out = (size_t)(l.start + j) * a.heads + h;
         const float inv = all > 0.0f ? 1.0f / all : 0.0f;
 #pragma unroll
-        for (int d = 0; d < ND; ++d) {
-            float f[16];
+        for (int d = 0; d < ND; d += 2) {
+            float f[8];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) f[i] = o[ct][d][i] * inv;
-            uint4* to = (uint4*)(a.out + out * D + 32 * d + 16 * hf);
-            to[0] = a.bf16 ? pack8<BF16>(f) : pack8<F16>(f);
-            to[1] = a.bf16 ? pack8<BF16>(f + 8) : pack8<F16>(f + 8);
+            for (int i = 0; i < 8; ++i) f[i] = o[ct][d + (i >> 2)][i & 3] * inv;
+            *(uint4*)(a.out + out * D + 16 * d + 8 * g) = a.bf16 ? pack8<BF16>(f) : pack8<F16>(f);
         }
-        if (hf == 0 && a.lse) a.lse[out] = all > 0.0f ? (M[ct] + __builtin_amdgcn_logf(all)) * kLn2 : -INFINITY;
+        if (g == 0 && a.lse) a.lse[out] = all > 0.0f ? (M[ct] + __builtin_amdgcn_logf(all)) * kLn2 : -INFINITY;
     }
 }
 
-template <int D, int CT, int NW>
+template <int D, int NW>
 int launch_t(const AttendArgs& a, int parts, hipStream_t st) {
-    constexpr int bytes = 2 * Image<D>::bytes;
-    auto kern = k_attend_tile<D, CT, NW>;
+    constexpr int bytes = 2 * (Image<D>::keys + Image<D>::values);
+    auto kern = k_attend_tile<D, NW>;
     if (bytes > 65536)
         if (int e = (int)hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, bytes))
             return e;
@@ -376,8 +421,8 @@ int launch_t(const AttendArgs& a, int parts, hipStream_t st) {
 template <int D>
 int launch_d(const AttendArgs& a, const TilePlan& p, hipStream_t st) {
     if constexpr (D <= 128)
-        if (p.rows == 256) return launch_t<D, 1, 8>(a, p.parts, st);
-    return launch_t<D, 1, 4>(a, p.parts, st);
+        if (p.rows == 256) return launch_t<D, 8>(a, p.parts, st);
+    return launch_t<D, 4>(a, p.parts, st);
 }
 
 }  // namespace

@@ -546,7 +546,7 @@ awq_status awq_moe(const void* x, const float* inv_s, const void* router,
  * A page may be in the rows of several sequences as long as no call writes to
  * it.  int32 and fp32 arrays need 4-byte alignment only.  T, B <= 2^20, and
  * kv_heads <= 65535, and
- * what a launch cannot count (2^24 workgroups) is AWQ_ERR_SHAPE.
+ * what a launch cannot count (2^32 threads) is AWQ_ERR_SHAPE.
  * ------------------------------------------------------------------------ */
 
 typedef enum {

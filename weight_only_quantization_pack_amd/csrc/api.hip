@@ -598,8 +598,8 @@ int check_attention(int T, int B, int W, int heads, int kv_heads, int dim, int p
     if (int st = check_cache(kv_heads, dim, pages, page_size)) return st;
     if (T < 0 || B < 0 || W <= 0 || T > kMaxCacheRows || B > kMaxCacheRows) return AWQ_ERR_SHAPE;
     if (heads <= 0 || heads % kv_heads != 0 || max_new <= 0 || max_len <= 0) return AWQ_ERR_SHAPE;
-    // one workgroup for each row and head joins, one for each tile of rows computes
-    return (long long)T * heads >= kMaxGroups || ((long long)T * (heads / kv_heads) / 16 + B) * kv_heads >= kMaxGroups
+    // a wave for each row and head joins, a workgroup of up to 512 threads for each tile of rows computes
+    return (long long)T * heads >= kMaxGroups || ((long long)T * (heads / kv_heads) / 16 + B) * kv_heads >= kMaxGroups / 2
                ? AWQ_ERR_SHAPE : AWQ_OK;
 }
 

@@ -51,7 +51,7 @@ __device__ __forceinline__ uint32_t value_pair(uint32_t lo, uint32_t hi, int j) 
 }
 
 template <int D, int C, bool SMALL>
-__global__ __launch_bounds__(64 * kW, 2) void k_attend(AttendArgs a) {
+__global__ __launch_bounds__(64 * kW, D * C > 256 ? 1 : 2) void k_attend(AttendArgs a) {
     using K = Codes<D>;
     constexpr int R = 16 * C, NK = K::NK, VB = K::VB, VW = K::VW;
     constexpr int JB = VB > 8 ? VB / 2 : VB;       // channels of a lane that one pass of the join takes
@@ -533,22 +533,28 @@ struct Plan {
 
 size_t line_bytes(int B) { return ((size_t)B + 1) * sizeof(long long) / 16 * 16 + 16; }
 
+// Up to 32 rows a kv head (a query's rows of all its heads): this file's kernel.  Up to 64
+// as well while tiles of 128 rows would not fill the card: its stretches are even
+// whatever the lengths, tiles are converted once for all their rows.  48 rows, 36
+// sequences of 400 to 7800 tokens, 3 kv heads: 55 us here, 89 in tiles; 64 rows, 64
+// sequences of 250 to 1000, 8 kv heads: 70 here, 49 in tiles; 128 rows, 16 of 500 to 2000:
+// 53 here, 44 in tiles.
 Plan plan(int T, int B, int heads, int kv, int dim, int max_new, int max_len) {
     Plan p;
-    const long long rows = (long long)max_new * (heads / kv);
+    const int group = heads / kv, cus = device_cu_count();
+    const long long rows = (long long)max_new * group;
     p.tile = TilePlan{0, 1};
-    if (rows > 32) {
+    if (rows > 64 || (rows > 32 && (long long)B * kv >= 2 * cus)) {
         p.columns = 0;
-        p.tile = tile_plan(T, B, heads / kv, kv, dim, max_new, max_len, device_cu_count());
+        p.tile = tile_plan(T, B, group, kv, dim, max_new, max_len, cus);
         p.split = p.tile.parts > 1;
-        p.groups = (int)(((long long)T * (heads / kv) / p.tile.rows + B) * kv * p.tile.parts);
+        p.groups = (int)(((long long)T * group / p.tile.rows + B) * kv * p.tile.parts);
         return p;
     }
     p.columns = rows <= 16 ? 1 : 2;
-    const int R = 16 * p.columns;
+    // two steps a wave at least: shorter sequences go unsplit, a workgroup for each tile
     p.split = max_len > 2 * kW * kStep;
-    const long long tiles = ((long long)T * (heads / kv) / R + B) * kv;
-    p.groups = p.split ? device_cu_count() * 2 : (int)tiles;
+    p.groups = p.split ? cus * 2 : (int)(((long long)T * group / (16 * p.columns) + B) * kv);
     return p;
 }
 

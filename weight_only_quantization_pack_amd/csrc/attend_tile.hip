@@ -429,13 +429,19 @@ int launch_d(const AttendArgs& a, const TilePlan& p, hipStream_t st) {
 
 TilePlan tile_plan(int T, int B, int group, int kv, int dim, int max_new, int max_len, int cus) {
     TilePlan p;
-    const long long rows = (long long)T * group;
-    p.rows = dim <= 128 && (rows / 256 + B) * kv >= cus && (long long)max_new * group > 128 ? 256 : 128;
-    const long long tiles = (rows / p.rows + B) * kv;
-    const long long most = max_len / (8 * kKeys);
-    long long parts = cus / tiles;
-    if (parts > most) parts = most;
-    p.parts = parts > 8 ? 8 : parts < 1 ? 1 : (int)parts;
+    const long long rows = (long long)max_new * group;
+    p.rows = dim <= 128 && rows > 128 ? 256 : 128;
+    // tiles there will be, if the bounds hold
+    const long long most_tiles = ((long long)T * group / p.rows + B) * kv;
+    const long long tiles = min(most_tiles, B * ((rows + p.rows - 1) / p.rows) * kv);
+    // Parts that fill the workgroups that run at a time, of four tiles of keys at least.  512
+    // rows of 4 heads each over 30000 tokens, 8 kv heads: 301 us in 3 parts, 315 in 7 and 917 in
+    // one; 3 ragged chunks 192 us in one part and 223 in two (the parts' outputs are written
+    // and read again); 32 rows of 8 heads over 30000 tokens, one kv head: 36 us in 64 parts, 77 in 16.
+    const long long slots = (p.rows == 128 && dim <= 128 ? 2 : 1) * cus;
+    long long parts = min(slots / tiles, (long long)(max_len / (4 * kKeys)));
+    parts = min(parts, 2 * slots / most_tiles);    // the workspace holds for every T rows, whatever max_new says
+    p.parts = (int)max(1LL, min(parts, 64LL));
     return p;
 }
 

@@ -661,7 +661,7 @@ awq_status awq_cache_attention(const void* q, long long q_stride, const void* k_
  * The book of a cache whose pages sequences share: tables and lens as above
  * (ceil(lens[b] / page_size) entries of row b count, B <= 65535) and refs int32
  * [pages], the number of rows that hold each page (0: free; a caller that keeps
- * a page for other ends adds one).  pages <= 2^30.
+ * a page for other ends adds one).  pages <= 2^30, B * W < 2^31.
  *
  * awq_cache_fork -- rows from their parents: out row b is a copy of row
  * parents[b] (-1 or any other index outside 0..B-1: an empty row), all at once:

@@ -139,7 +139,8 @@ def test_book_validation(lib):
         for name in names:
             assert call(**{name: NUL}) == NULL, name
             assert call(**{name: ODD}) == ALIGN, name
-        for bad in (dict(B=-1), dict(B=65536), dict(W=0), dict(pages=0), dict(pages=(1 << 30) + 1)):
+        for bad in (dict(B=-1), dict(B=65536), dict(W=0), dict(pages=0), dict(pages=(1 << 30) + 1),
+                    dict(B=4096, W=1 << 19)):
             assert call(**bad) == SHAPE, bad
         assert call(page=24) == UNSUP
     assert fork(n=-1) == SHAPE and fork(ot=P) == UNSUP and fork(B=0, n=0, r=NUL) == OK

@@ -8,7 +8,6 @@ device pointers and the current HIP stream.  A missing library raises
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -761,21 +760,6 @@ def moe(x, router, gate, up, down, inter: int, top_k: int, bits: int = 4, group_
 # [pages][kv], v_codes, v_scales); a call's sequences are tables int32 [B][W],
 # lens int32 [B] and starts int32 [B + 1] (or None: one row each), as in awq.h.
 # ---------------------------------------------------------------------------
-_NO_GUARD = contextlib.nullcontext()
-
-
-def _call(name, device, *args):
-    """The library's call with GPU `device` the current one; its status raises."""
-    torch = _torch()
-    fn = getattr(load_library(), name)
-    if torch._C._cuda_getDevice() == device:
-        st = fn(*args)
-    else:
-        with torch.cuda.device(device):
-            st = fn(*args)
-    _check(st, name)
-
-
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 ROPE_SCALINGS = {None: 0, "linear": 1, "base": 2, "yarn": 3, "bands": 4}
 
@@ -842,19 +826,27 @@ def rope(x, positions, inv_freq, layout: str = "half", magnitude: float = 1.0, i
     the gradient.  out may be x."""
     torch = _torch()
     dev = _gpu_of(x, "x")
+    if torch._C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            return rope(x, positions, inv_freq, layout, magnitude, inverse, out)
+    lib = load_library()
     dtype = x.dtype
     code = _dtype_code(dtype, "x")
     x_at, x_stride = _heads3d(x, dtype, dev, "x")
     T, heads, dim = x.shape
     if out is None:
         out = x.new_empty((T, heads, dim))
-    elif out.shape != x.shape:
-        raise ValueError(f"out must have shape {tuple(x.shape)}, got {tuple(out.shape)}")
-    out_at, out_stride = _heads3d(out, dtype, dev, "out")
+        out_at, out_stride = out.data_ptr(), heads * dim
+    else:
+        if out.shape != x.shape:
+            raise ValueError(f"out must have shape {tuple(x.shape)}, got {tuple(out.shape)}")
+        out_at, out_stride = _heads3d(out, dtype, dev, "out")
     n = inv_freq.numel()
-    _call("awq_rope", dev, x_at, x_stride, _arg(positions, torch.int32, (T,), dev, "positions"),
-          _arg(inv_freq, torch.float32, (n,), dev, "inv_freq"), magnitude, out_at, out_stride, T, heads, dim, 2 * n,
-          _layout(layout), int(inverse), code, _raw_stream(dev))
+    st = lib.awq_rope(x_at, x_stride, _arg(positions, torch.int32, (T,), dev, "positions"),
+                      _arg(inv_freq, torch.float32, (n,), dev, "inv_freq"), magnitude, out_at, out_stride, T, heads,
+                      dim, 2 * n, _layout(layout), int(inverse), code, _raw_stream(dev))
+    if st:
+        _check(st, "awq_rope")
     return out
 
 
@@ -871,23 +863,43 @@ def empty_cache(pages: int, kv_heads: int, page_size: int, head_dim: int, layers
 def _cache_args(cache, device):
     """(addresses, (pages, kv heads, page size, head dim)) of a layer's cache on GPU `device`."""
     torch = _torch()
+    i8, f32 = torch.int8, torch.float32
     k, ks, v, vs = cache
+    try:
+        shape, few = k.shape, ks.shape
+        pages, kv, page, dim = shape
+        if (few == (pages, kv) and v.shape == shape and vs.shape == few and k.dtype is i8 and v.dtype is i8
+                and ks.dtype is f32 and vs.dtype is f32 and k.get_device() == device and ks.get_device() == device
+                and v.get_device() == device and vs.get_device() == device and k.is_contiguous()
+                and ks.is_contiguous() and v.is_contiguous() and vs.is_contiguous()):
+            return (k.data_ptr(), ks.data_ptr(), v.data_ptr(), vs.data_ptr()), shape
+    except (AttributeError, ValueError):
+        pass
     if not isinstance(k, torch.Tensor) or k.dim() != 4:
         raise ValueError("cache must be (k_codes [pages][kv][page][dim], k_scales [pages][kv], v_codes, v_scales)")
     shape = k.shape
     few = shape[:2]
-    return (_arg(k, torch.int8, shape, device, "k_codes"), _arg(ks, torch.float32, few, device, "k_scales"),
-            _arg(v, torch.int8, shape, device, "v_codes"), _arg(vs, torch.float32, few, device, "v_scales")), shape
+    return (_arg(k, i8, shape, device, "k_codes"), _arg(ks, f32, few, device, "k_scales"),
+            _arg(v, i8, shape, device, "v_codes"), _arg(vs, f32, few, device, "v_scales")), shape
 
 
 def _sequence_args(tables, lens, starts, device):
     """(addresses, B, W) of a call's sequences."""
     torch = _torch()
+    i32 = torch.int32
+    try:
+        B, W = tables.shape
+        if (tables.dtype is i32 and lens.dtype is i32 and lens.shape == (B,) and tables.get_device() == device
+                and lens.get_device() == device and tables.is_contiguous() and lens.is_contiguous()):
+            return (tables.data_ptr(), lens.data_ptr(), None if starts is None else
+                    _arg(starts, i32, (B + 1,), device, "starts")), B, W
+    except (AttributeError, ValueError):
+        pass                                     # said below, argument by argument
     if not isinstance(tables, torch.Tensor) or tables.dim() != 2:
         raise ValueError("tables must be an int32 tensor [sequences][pages]")
     B, W = tables.shape
-    return (_arg(tables, torch.int32, (B, W), device, "tables"), _arg(lens, torch.int32, (B,), device, "lens"),
-            _optional(starts, torch.int32, (B + 1,), device, "starts")), B, W
+    return (_arg(tables, i32, (B, W), device, "tables"), _arg(lens, i32, (B,), device, "lens"),
+            _optional(starts, i32, (B + 1,), device, "starts")), B, W
 
 
 def cache_append(q, k, v, cache, tables, lens, starts=None, inv_freq=None, layout: str = "half",
@@ -898,6 +910,10 @@ def cache_append(q, k, v, cache, tables, lens, starts=None, inv_freq=None, layou
     None).  lens counts the new tokens.  Returns the turned q (`out` if given)."""
     torch = _torch()
     dev = _gpu_of(k, "k")
+    if torch._C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            return cache_append(q, k, v, cache, tables, lens, starts, inv_freq, layout, magnitude, out)
+    lib = load_library()
     dtype = k.dtype
     code = _dtype_code(dtype, "k")
     k_at, k_stride = _heads3d(k, dtype, dev, "k")
@@ -918,13 +934,18 @@ def cache_append(q, k, v, cache, tables, lens, starts=None, inv_freq=None, layou
             raise ValueError(f"q must have shape ({T}, heads, {dim}), got {tuple(q.shape)}")
         if out is None:
             out = q.new_empty((T, heads, dim))
-        out_at = _arg(out, dtype, (T, heads, dim), dev, "out")
+            out_at = out.data_ptr()
+        else:
+            out_at = _arg(out, dtype, (T, heads, dim), dev, "out")
     freq_at, rotary = None, 0
     if inv_freq is not None:
         rotary = 2 * inv_freq.numel()
         freq_at = _arg(inv_freq, torch.float32, (rotary // 2,), dev, "inv_freq")
-    _call("awq_cache_append", dev, q_at, q_stride, k_at, k_stride, v_at, v_stride, out_at, freq_at, magnitude, rotary,
-          _layout(layout), *codes, *seqs, T, B, W, heads, kv, dim, pages, page, code, _raw_stream(dev))
+    st = lib.awq_cache_append(q_at, q_stride, k_at, k_stride, v_at, v_stride, out_at, freq_at, magnitude, rotary,
+                              _layout(layout), *codes, *seqs, T, B, W, heads, kv, dim, pages, page, code,
+                              _raw_stream(dev))
+    if st:
+        _check(st, "awq_cache_append")
     return out if q is not None else None
 
 
@@ -934,6 +955,10 @@ def cache_read(cache, tables, lens, starts=None, tokens=None, dtype=None, out=No
     [tokens][kv][dim].  tokens: the rows of the call (default: one a sequence)."""
     torch = _torch()
     dev = _gpu_of(tables, "tables")
+    if torch._C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            return cache_read(cache, tables, lens, starts, tokens, dtype, out)
+    lib = load_library()
     codes, (pages, kv, page, dim) = _cache_args(cache, dev)
     seqs, B, W = _sequence_args(tables, lens, starts, dev)
     if tokens is None:
@@ -943,14 +968,18 @@ def cache_read(cache, tables, lens, starts=None, tokens=None, dtype=None, out=No
     if out is None:
         dtype = dtype or torch.float16
         code = _dtype_code(dtype, "dtype")
-        k, v = (cache[0].new_empty((tokens, kv, dim), dtype=dtype) for _ in range(2))
+        shape = (tokens, kv, dim)
+        k, v = cache[0].new_empty(shape, dtype=dtype), cache[0].new_empty(shape, dtype=dtype)
+        k_at, v_at = k.data_ptr(), v.data_ptr()
     else:
         k, v = out
         dtype = k.dtype
         code = _dtype_code(dtype, "out[0]")
-    _call("awq_cache_read", dev, *codes, *seqs, tokens, B, W, kv, dim, pages, page, code,
-          _arg(k, dtype, (tokens, kv, dim), dev, "out[0]"), _arg(v, dtype, (tokens, kv, dim), dev, "out[1]"),
-          _raw_stream(dev))
+        k_at = _arg(k, dtype, (tokens, kv, dim), dev, "out[0]")
+        v_at = _arg(v, dtype, (tokens, kv, dim), dev, "out[1]")
+    st = lib.awq_cache_read(*codes, *seqs, tokens, B, W, kv, dim, pages, page, code, k_at, v_at, _raw_stream(dev))
+    if st:
+        _check(st, "awq_cache_read")
     return k, v
 
 
@@ -971,6 +1000,11 @@ def cache_attention(q, cache, tables, lens, starts=None, scale=None, window: int
     [T][heads] to write, or None.  Returns out, [T][heads][dim] like q."""
     torch = _torch()
     dev = _gpu_of(q, "q")
+    if torch._C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            return cache_attention(q, cache, tables, lens, starts, scale, window, softcap, max_new, max_len, lse, out,
+                                   workspace)
+    lib = load_library()
     dtype = q.dtype
     code = _dtype_code(dtype, "q")
     q_at, q_stride = _heads3d(q, dtype, dev, "q")
@@ -989,12 +1023,13 @@ def cache_attention(q, cache, tables, lens, starts=None, scale=None, window: int
     else:
         out_at = _arg(out, dtype, (T, heads, dim), dev, "out")
     lse_at = _optional(lse, torch.float32, (T, heads), dev, "lse")
-    with torch.cuda.device(dev) if torch._C._cuda_getDevice() != dev else _NO_GUARD:
-        need = load_library().awq_cache_attention_workspace_bytes(T, B, heads, kv, dim, max_new, max_len)
+    need = lib.awq_cache_attention_workspace_bytes(T, B, heads, kv, dim, max_new, max_len)
     keep, ws, ws_bytes = _workspace(workspace, need, q)
-    _call("awq_cache_attention", dev, q_at, q_stride, *codes, *seqs, out_at, lse_at,
-          dim ** -0.5 if scale is None else scale, window, softcap, T, B, W, heads, kv, dim, pages, page, max_new,
-          max_len, code, ws, ws_bytes, _raw_stream(dev))
+    st = lib.awq_cache_attention(q_at, q_stride, *codes, *seqs, out_at, lse_at,
+                                 dim ** -0.5 if scale is None else scale, window, softcap, T, B, W, heads, kv, dim,
+                                 pages, page, max_new, max_len, code, ws, ws_bytes, _raw_stream(dev))
+    if st:
+        _check(st, "awq_cache_attention")
     return out
 
 
@@ -1012,14 +1047,21 @@ def cache_fork(tables, lens, refs, parents, page_size: int, out=None):
     place.  Returns (tables, lens) of parents' length (`out` if given)."""
     torch = _torch()
     book, dev, B, W, pages = _book_args(tables, lens, refs)
+    if torch._C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            return cache_fork(tables, lens, refs, parents, page_size, out)
+    lib = load_library()
     n = parents.numel()
     if out is None:
         new_tables, new_lens = tables.new_empty((n, W)), lens.new_empty(n)
+        out_at = new_tables.data_ptr(), new_lens.data_ptr()
     else:
         new_tables, new_lens = out
-    _call("awq_cache_fork", dev, *book, _arg(parents, torch.int32, (n,), dev, "parents"),
-          _arg(new_tables, torch.int32, (n, W), dev, "out[0]"), _arg(new_lens, torch.int32, (n,), dev, "out[1]"), B, n,
-          W, pages, page_size, _raw_stream(dev))
+        out_at = (_arg(new_tables, torch.int32, (n, W), dev, "out[0]"), _arg(new_lens, torch.int32, (n,), dev, "out[1]"))
+    st = lib.awq_cache_fork(*book, _arg(parents, torch.int32, (n,), dev, "parents"), *out_at, B, n, W, pages, page_size,
+                            _raw_stream(dev))
+    if st:
+        _check(st, "awq_cache_fork")
     return new_tables, new_lens
 
 
@@ -1030,10 +1072,20 @@ def cache_reserve(tables, lens, refs, counts, page_size: int, out=None):
     either is not 0 nothing has changed)."""
     torch = _torch()
     book, dev, B, W, pages = _book_args(tables, lens, refs)
-    pairs, status = (tables.new_empty((B, 2)), lens.new_empty(2)) if out is None else out
-    _call("awq_cache_reserve", dev, *book, _arg(counts, torch.int32, (B,), dev, "counts"),
-          _arg(pairs, torch.int32, (B, 2), dev, "out[0]"), _arg(status, torch.int32, (2,), dev, "out[1]"), B, W, pages,
-          page_size, _raw_stream(dev))
+    if torch._C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            return cache_reserve(tables, lens, refs, counts, page_size, out)
+    lib = load_library()
+    if out is None:
+        pairs, status = tables.new_empty((B, 2)), lens.new_empty(2)
+        out_at = pairs.data_ptr(), status.data_ptr()
+    else:
+        pairs, status = out
+        out_at = _arg(pairs, torch.int32, (B, 2), dev, "out[0]"), _arg(status, torch.int32, (2,), dev, "out[1]")
+    st = lib.awq_cache_reserve(*book, _arg(counts, torch.int32, (B,), dev, "counts"), *out_at, B, W, pages, page_size,
+                               _raw_stream(dev))
+    if st:
+        _check(st, "awq_cache_reserve")
     return pairs, status
 
 
@@ -1043,9 +1095,15 @@ def cache_compact(tables, lens, refs, page_size: int, out=None):
     cache_copy_pages."""
     torch = _torch()
     book, dev, B, W, pages = _book_args(tables, lens, refs)
+    if torch._C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            return cache_compact(tables, lens, refs, page_size, out)
+    lib = load_library()
     moves, count = (refs.new_empty((pages, 2)), refs.new_empty(1)) if out is None else out
-    _call("awq_cache_compact", dev, *book, _arg(moves, torch.int32, (pages, 2), dev, "out[0]"),
-          _arg(count, torch.int32, (1,), dev, "out[1]"), B, W, pages, page_size, _raw_stream(dev))
+    st = lib.awq_cache_compact(*book, _arg(moves, torch.int32, (pages, 2), dev, "out[0]"),
+                               _arg(count, torch.int32, (1,), dev, "out[1]"), B, W, pages, page_size, _raw_stream(dev))
+    if st:
+        _check(st, "awq_cache_compact")
     return moves, count
 
 
@@ -1058,6 +1116,10 @@ def cache_copy_pages(tensors, pairs, count=None, layers=None):
     torch = _torch()
     tensors = list(tensors)
     shape, dev = _rows2d(pairs, "pairs")
+    if torch._C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            return cache_copy_pages(tensors, pairs, count, layers)
+    lib = load_library()
     lead = 0 if layers is None else 1
     if not tensors or tensors[0].dim() <= lead or 0 in tensors[0].shape:
         raise ValueError("tensors must hold at least one tensor of at least one page")
@@ -1069,6 +1131,8 @@ def cache_copy_pages(tensors, pairs, count=None, layers=None):
             raise ValueError(f"tensors[{i}] must be [{'layers][' if lead else ''}pages][...], got {tuple(t.shape)}")
         at[i] = _arg(t, t.dtype, t.shape, dev, f"tensors[{i}]")
         size[i] = t.numel() // (pages * (layers if lead else 1)) * t.element_size()
-    _call("awq_cache_copy_pages", dev, at, size, n, layers if lead else 1,
-          _arg(pairs, torch.int32, (shape[0], 2), dev, "pairs"), _optional(count, torch.int32, (1,), dev, "count"),
-          shape[0], pages, _raw_stream(dev))
+    st = lib.awq_cache_copy_pages(at, size, n, layers if lead else 1,
+                                  _arg(pairs, torch.int32, (shape[0], 2), dev, "pairs"),
+                                  _optional(count, torch.int32, (1,), dev, "count"), shape[0], pages, _raw_stream(dev))
+    if st:
+        _check(st, "awq_cache_copy_pages")

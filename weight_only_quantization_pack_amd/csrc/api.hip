@@ -605,7 +605,8 @@ int check_attention(int T, int B, int W, int heads, int kv_heads, int dim, int p
 
 int check_book(int B, int W, int pages, int page_size) {
     if (int st = check_page(page_size)) return st;
-    return B < 0 || B > kMaxBookRows || W <= 0 || pages <= 0 || pages > kMaxPages ? AWQ_ERR_SHAPE : AWQ_OK;
+    if (B < 0 || B > kMaxBookRows || W <= 0 || pages <= 0 || pages > kMaxPages) return AWQ_ERR_SHAPE;
+    return (long long)B * W >= 1LL << 31 ? AWQ_ERR_SHAPE : AWQ_OK;       // pages of all rows are summed in 31 bits
 }
 }  // namespace
 
@@ -745,7 +746,7 @@ awq_status awq_cache_fork(const int* tables, const int* lens, int* refs, const i
                           int* out_lens, int B, int B_out, int W, int pages, int page_size, hipStream_t stream) {
     int st = check_book(B, W, pages, page_size);
     if (st) return as_status(st);
-    if (B_out < 0 || B_out > kMaxBookRows) return AWQ_ERR_SHAPE;
+    if ((st = check_book(B_out, W, pages, page_size))) return as_status(st);
     if (B == 0 && B_out == 0) return AWQ_OK;
     if ((st = check_index({refs}))) return as_status(st);
     if (B > 0 && (st = check_index({tables, lens}))) return as_status(st);

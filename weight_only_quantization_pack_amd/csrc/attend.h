@@ -52,17 +52,8 @@ struct Line {
     __device__ __forceinline__ long long units(int kv) const { return (long long)tiles * kv * tile_units(); }
 };
 
-// Inclusive prefix of v >= 0 over the lanes, in two parts of 26 and 32 bits:
-// 32-bit adds between lanes (DPP) instead of 64-bit ones through LDS.
-__device__ __forceinline__ uint32_t lane_prefix(uint32_t v) {
-    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, true);   // row_shr:1
-    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, true);   // row_shr:2
-    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, true);   // row_shr:4
-    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, true);   // row_shr:8
-    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false);  // row_bcast:15
-    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false);  // row_bcast:31
-    return v;
-}
+// Inclusive prefix of v >= 0 over the lanes, in two parts of 26 and 32 bits: 32-bit adds
+// between lanes instead of 64-bit ones through LDS.
 __device__ __forceinline__ long long lane_prefix(long long v) {
     constexpr int kBits = 26;            // 64 values of 26 bits stay in 32
     const uint32_t lo = lane_prefix((uint32_t)v & ((1u << kBits) - 1)), hi = lane_prefix((uint32_t)(v >> kBits));

@@ -38,17 +38,8 @@ struct Sequences {
         const int p = (unsigned)w < (unsigned)W ? tables[(size_t)b * W + w] : -1;
         return (unsigned)p < (unsigned)pages ? p : -1;
     }
-    // the sequence of row t, or -1 behind the last one
-    __device__ __forceinline__ int of_row(int t) const {
-        if (!starts) return t < B ? t : -1;
-        int lo = 0, hi = B;              // the last b with starts[b] <= t
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (starts[mid] <= t) lo = mid; else hi = mid;
-        }
-        return B > 0 && starts[lo] <= t && t < starts[lo + 1] ? lo : -1;
-    }
-    // the same for a whole wave, t the same in all lanes: 256 sequences a load
+    // the sequence of row t, or -1 behind the last one; by a whole wave, t the same in all
+    // lanes: 256 sequences a load
     __device__ __forceinline__ int of_row_by_wave(int t) const {
         if (!starts) return t < B ? t : -1;
         const int lane = threadIdx.x & 63;
@@ -72,6 +63,17 @@ struct Sequences {
         return -1;
     }
 };
+
+// inclusive prefix of v over the lanes (DPP: no LDS round trip)
+__device__ __forceinline__ uint32_t lane_prefix(uint32_t v) {
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, true);   // row_shr:1
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, true);   // row_shr:2
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, true);   // row_shr:4
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, true);   // row_shr:8
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false);  // row_bcast:15
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false);  // row_bcast:31
+    return v;
+}
 
 struct Rotation {
     const float* inv_freq;               // [pairs], or null: no rotation

@@ -45,16 +45,11 @@ __global__ __launch_bounds__(256) void k_fork(const int* tables, const int* lens
 
 constexpr int kT = 1024, kWaves = kT / 64;     // one workgroup that sees the whole book
 
-// Exclusive prefix of v over the workgroup's threads, and the total.  `slots` holds
-// kWaves + 1 words; two barriers.
+// Exclusive prefix of v >= 0 over the workgroup's threads, and the total.  `slots` holds
+// kWaves words; two barriers.
 __device__ __forceinline__ int group_scan(int v, int* slots, int& total) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int s = v;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_up(s, d);
-        if (lane >= d) s += o;
-    }
+    const int s = (int)lane_prefix((uint32_t)v);
     if (lane == 63) slots[wave] = s;
     __syncthreads();
     int before = 0;
@@ -69,31 +64,35 @@ __device__ __forceinline__ int group_scan(int v, int* slots, int& total) {
     return before + s - v;
 }
 
-// Goes over refs[0 .. pages) in chunks of kWaves * 1024 (each wave 16 lines of 64
-// in order, so that ranks follow page numbers), calling f(page, rank) for the pages
-// with pick(page, ref) until `most` have been met.  Returns how many were met (all
-// of them if fewer than `most`; at least `most` otherwise).
-template <class Pick, class F>
-__device__ __forceinline__ int ranked(const int* refs, int pages, int most, int* slots, Pick pick, F f) {
-    constexpr int R = 16;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int met = 0;
-    for (int base = 0; base < pages && met < most; base += kT * R) {
-        const int first = base + wave * (64 * R) + lane;
-        int r[R];
+// A look over refs[0 .. pages) in chunks of kWaves * 1024 pages (each wave 16 lines of 64
+// in order, so that ranks follow page numbers) for the pages with pick(page, ref).
+constexpr int kLines = 16, kChunk = kT * kLines;
+template <class Pick>
+struct Ranked {
+    const int* refs;
+    int pages;
+    int* slots;
+    Pick pick;
+    uint64_t hit[kLines];                // of the chunk looked at last
+    int before;                          // its pages that were picked in waves before this one
+    // looks at a chunk, says how many it holds; two barriers
+    __device__ __forceinline__ int chunk(int base) {
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+        const int first = base + wave * (64 * kLines) + lane;
+        int r[kLines];
 #pragma unroll
-        for (int i = 0; i < R; ++i) r[i] = first + 64 * i < pages ? refs[first + 64 * i] : 0;
-        uint64_t hit[R];
+        for (int i = 0; i < kLines; ++i) r[i] = first + 64 * i < pages ? refs[first + 64 * i] : 0;
         int mine = 0;
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
+        for (int i = 0; i < kLines; ++i) {
             const int p = first + 64 * i;
             hit[i] = __builtin_amdgcn_ballot_w64(p < pages && pick(p, r[i]));
             mine += __builtin_popcountll(hit[i]);
         }
-        int total = 0, before = 0;
         if (lane == 0) slots[wave] = mine;
         __syncthreads();
+        int total = 0;
+        before = 0;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
             const int c = slots[w];
@@ -101,16 +100,46 @@ __device__ __forceinline__ int ranked(const int* refs, int pages, int most, int*
             total += c;
         }
         __syncthreads();
+        return total;
+    }
+    // f(page, rank) for the chunk's picked pages, `met` of which came in chunks before
+    template <class F>
+    __device__ __forceinline__ void each(int base, int met, F f) const {
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
         int rank = met + before;
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            if (hit[i] >> lane & 1) f(first + 64 * i, rank + __builtin_popcountll(hit[i] & ((1ull << lane) - 1)));
+        for (int i = 0; i < kLines; ++i) {
+            if (hit[i] >> lane & 1)
+                f(base + wave * (64 * kLines) + 64 * i + lane, rank + __builtin_popcountll(hit[i] & ((1ull << lane) - 1)));
             rank += __builtin_popcountll(hit[i]);
         }
-        met += total;
-        if (base > pages - kT * R) break;                // base + kT * R may pass 2^31
     }
-    return met;
+    // the bases of the chunks: base + kChunk may pass 2^31
+    __device__ __forceinline__ bool next(int& base) const {
+        if (base > pages - kChunk) return false;
+        base += kChunk;
+        return base < pages;
+    }
+    // counts until `most` are met (or all)
+    __device__ __forceinline__ int count(int most) {
+        int met = 0, base = 0;
+        do met += chunk(base); while (met < most && next(base));
+        return met;
+    }
+    template <class F>
+    __device__ __forceinline__ int all(int most, F f) {
+        int met = 0, base = 0;
+        do {
+            const int n = chunk(base);
+            each(base, met, f);
+            met += n;
+        } while (met < most && next(base));
+        return met;
+    }
+};
+template <class Pick>
+__device__ __forceinline__ Ranked<Pick> ranked(const int* refs, int pages, int* slots, Pick pick) {
+    return {refs, pages, slots, pick, {}, 0};
 }
 
 __global__ __launch_bounds__(kT) void k_reserve(int* tables, int* lens, int* refs, const int* counts, int* pairs,
@@ -164,11 +193,10 @@ __global__ __launch_bounds__(kT) void k_reserve(int* tables, int* lens, int* ref
             fresh[i] += cow[i];
         }
     }
-    int mine = 0, need = 0, overs = 0;
+    int mine = 0, need = 0;
 #pragma unroll
     for (int i = 0; i < R; ++i) mine += fresh[i];
     int at = group_scan(mine, slots, need);
-    group_scan(over, slots, overs);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         const int b = tid * per + i;
@@ -179,15 +207,17 @@ __global__ __launch_bounds__(kT) void k_reserve(int* tables, int* lens, int* ref
     }
     if (tid == 0) offset[B] = need;
     __syncthreads();
-    auto is_free = [](int, int r) { return r == 0; };
-    const int met = ranked(refs, pages, need, slots, is_free, [](int, int) {});
+    auto free_pages = ranked(refs, pages, slots, [](int, int r) { return r == 0; });
+    const int met = need > 0 ? free_pages.count(need) : 0;
+    int overs = 0;
+    group_scan(over, slots, overs);
     if (tid == 0) {
         status[0] = max(need - met, 0);
         status[1] = overs;
     }
     if (met < need || overs > 0) return;           // nothing changes
     // the page of rank r goes to the row whose fresh pages hold r
-    ranked(refs, pages, need, slots, is_free, [&](int p, int r) {
+    auto take = [&](int p, int r) {
         if (r >= need) return;
         int lo = 0, hi = B;                        // the last row with offset <= r; rows without fresh pages
         while (hi - lo > 1) {                      // share their offset with the next one and are passed over
@@ -203,7 +233,10 @@ __global__ __launch_bounds__(kT) void k_reserve(int* tables, int* lens, int* ref
             pairs[2 * lo] = src;
             pairs[2 * lo + 1] = p;
         }
-    });
+    };
+    if (need > 0) {
+        if (pages <= kChunk) free_pages.each(0, 0, take); else free_pages.all(need, take);
+    }
     __syncthreads();                               // every lens read, every free page ranked
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -220,11 +253,14 @@ __global__ __launch_bounds__(kT) void k_compact(int* refs, int* moves, int* coun
     __shared__ int slots[kWaves];
     const int tid = threadIdx.x;
     const int all = 0x7FFFFFFF;
-    const int used = ranked(refs, pages, all, slots, [](int, int r) { return r > 0; }, [](int, int) {});
-    const int holes = ranked(refs, used, all, slots, [](int, int r) { return r <= 0; },
-                             [&](int p, int k) { moves[2 * (size_t)k + 1] = p; });
-    ranked(refs + used, pages - used, all, slots, [](int, int r) { return r > 0; },
-           [&](int p, int k) { moves[2 * (size_t)k] = used + p; });
+    auto is_used = ranked(refs, pages, slots, [](int, int r) { return r > 0; });
+    const int used = is_used.count(all);
+    const int holes = ranked(refs, used, slots, [](int, int r) { return r <= 0; }).all(all, [&](int p, int k) {
+        moves[2 * (size_t)k + 1] = p;
+    });
+    ranked(refs + used, pages - used, slots, [](int, int r) { return r > 0; }).all(all, [&](int p, int k) {
+        moves[2 * (size_t)k] = used + p;
+    });
     if (tid == 0) *count = holes;
     for (int k = holes + tid; k < pages; k += kT) moves[2 * (size_t)k] = moves[2 * (size_t)k + 1] = -1;
     __threadfence();
@@ -252,31 +288,59 @@ __global__ __launch_bounds__(256) void k_remap(int* tables, const int* lens, con
 }
 
 // Copies of pages.  A unit is up to kSpan bytes of one page of one tensor and layer;
-// workgroups take units in turns.
-constexpr int kSpan = 16384;
+// workgroups take units in turns.  A short list that comes without a count is mostly
+// empty (a pair for each row of a batch): its valid pairs are gathered first.
+constexpr int kSpan = 8192, kGather = 4096;
 struct CopyArgs {
     CopyProblem p;
     int first[kMaxCopyTensors + 1];      // units of a page before each tensor's
 };
 
 __global__ __launch_bounds__(256) void k_copy_pages(CopyArgs a) {
+    __shared__ int gathered[kGather], count;
     const CopyProblem& p = a.p;
-    const int per = a.first[p.n];
-    const int n = p.count ? min(max(*p.count, 0), p.max_pairs) : p.max_pairs;
+    const int per = a.first[kMaxCopyTensors];
+    auto valid = [&](int src, int dst) { return (unsigned)src < (unsigned)p.pages && (unsigned)dst < (unsigned)p.pages; };
+    int n = p.count ? min(max(*p.count, 0), p.max_pairs) : p.max_pairs;
+    const bool gather = !p.count && n <= kGather;
+    if (gather) {                                  // in any order: the copies do not depend on one another
+        if (threadIdx.x == 0) count = 0;
+        __syncthreads();
+        for (int i = threadIdx.x; i < n; i += 256)
+            if (valid(p.pairs[2 * i], p.pairs[2 * i + 1])) gathered[atomicAdd(&count, 1)] = i;
+        __syncthreads();
+        n = count;
+    }
     const size_t units = (size_t)n * p.layers * per;
     for (size_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const int part = (int)(u % per);
-        const size_t rest = u / per;
-        const size_t pair = rest / p.layers;
-        const size_t layer = rest % p.layers;
+        size_t pair, layer;
+        int part;
+        if (units >> 32 == 0) {
+            const uint32_t rest = (uint32_t)u / (uint32_t)per;
+            part = (int)((uint32_t)u - rest * (uint32_t)per);
+            pair = rest / (uint32_t)p.layers;
+            layer = rest - (uint32_t)pair * (uint32_t)p.layers;
+        } else {
+            part = (int)(u % per);
+            pair = u / per / p.layers;
+            layer = u / per % p.layers;
+        }
+        if (gather) pair = gathered[pair];
         const int src = p.pairs[2 * pair], dst = p.pairs[2 * pair + 1];
-        if ((unsigned)src >= (unsigned)p.pages || (unsigned)dst >= (unsigned)p.pages) continue;
-        int t = 0;
-        while (part >= a.first[t + 1]) ++t;
-        const size_t bytes = p.page_bytes[t];
-        const size_t at = (size_t)(part - a.first[t]) * kSpan;
+        if (!valid(src, dst)) continue;
+        char* tensor = p.tensors[0];
+        size_t bytes = p.page_bytes[0];
+        int first = 0;
+#pragma unroll
+        for (int t = 1; t < kMaxCopyTensors; ++t)
+            if (part >= a.first[t]) {
+                tensor = p.tensors[t];
+                bytes = p.page_bytes[t];
+                first = a.first[t];
+            }
+        const size_t at = (size_t)(part - first) * kSpan;
         const size_t left = bytes - at < kSpan ? bytes - at : (size_t)kSpan;
-        char* base = p.tensors[t] + layer * (size_t)p.pages * bytes + at;
+        char* base = tensor + layer * (size_t)p.pages * bytes + at;
         const char* from = base + (size_t)src * bytes;
         char* to = base + (size_t)dst * bytes;
         if (bytes % 16 == 0) {
@@ -284,11 +348,11 @@ __global__ __launch_bounds__(256) void k_copy_pages(CopyArgs a) {
             uint4* d = (uint4*)to;
             const int words = (int)(left / 16);
             if (words == kSpan / 16) {
-                uint4 v[4];
+                uint4 v[kSpan / 4096];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = f[threadIdx.x + 256 * i];
+                for (int i = 0; i < kSpan / 4096; ++i) v[i] = f[threadIdx.x + 256 * i];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) d[threadIdx.x + 256 * i] = v[i];
+                for (int i = 0; i < kSpan / 4096; ++i) d[threadIdx.x + 256 * i] = v[i];
             } else {
                 for (int i = threadIdx.x; i < words; i += 256) d[i] = f[i];
             }
@@ -325,9 +389,13 @@ int launch_cache_compact(int* tables, const int* lens, int* refs, int* moves, in
 
 int launch_cache_copy_pages(const CopyProblem& p, hipStream_t st) {
     CopyArgs a{p, {0}};
-    for (int t = 0; t < p.n; ++t) a.first[t + 1] = a.first[t] + (int)((p.page_bytes[t] + kSpan - 1) / kSpan);
-    const size_t units = (size_t)p.max_pairs * p.layers * a.first[p.n];
-    const size_t most = (size_t)device_cu_count() * 8;
+    // tensors that are not there begin behind the last unit
+    for (int t = 0; t < kMaxCopyTensors; ++t)
+        a.first[t + 1] = a.first[t] + (t < p.n ? (int)((p.page_bytes[t] + kSpan - 1) / kSpan) : 0);
+    for (int t = p.n; t < kMaxCopyTensors; ++t) a.first[t] = 0x7FFFFFFF;
+    const size_t units = (size_t)p.max_pairs * p.layers * a.first[kMaxCopyTensors];
+    // 4 GB in copies of 8 KB: 517 us with 64 workgroups for each compute unit, 527 with 16
+    const size_t most = (size_t)device_cu_count() * 64;
     hipLaunchKernelGGL(k_copy_pages, dim3((unsigned)(units < most ? units : most)), dim3(256), 0, st, a);
     return (int)hipGetLastError();
 }

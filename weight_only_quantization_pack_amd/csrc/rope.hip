@@ -197,33 +197,40 @@ __device__ __forceinline__ void unit_codes(const float* v, float s, float inv, u
     *c1 = make_uint2(w[2], w[3]);
 }
 
-// U: units of 16 channels that a thread holds, kNT * U >= page * dim / 16
-template <class E, int U>
+// A block (a page's tokens of one head) by W waves, all four of a workgroup or one: then
+// four heads share the search for their page and the angles of its positions.  U: units of
+// 16 channels that a thread holds, 64 W U >= page * dim / 16.
+template <class E, int U, int W>
 __global__ __launch_bounds__(kNT) void k_append(AppendArgs a) {
-    __shared__ float2 table[kNT * 8];              // angles of kNT units; of kRows rows of queries
+    constexpr int BT = 64 * W;                     // threads of a block
+    __shared__ float2 table[kNT * 8];              // angles: of kRows rows of queries; of BT units (W = 4); of the page (W = 1)
     __shared__ int pos[kRows], live[kRows];
     __shared__ int2 item;
     __shared__ uint32_t slots[4];
     static_assert(kNT * 8 >= kRows * kMaxPairs / 2, "angles of a group's rows (dim at most 256)");
     const Sequences& s = a.seqs;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), bt = W == 4 ? tid : tid & 63;
     if ((int)blockIdx.x < a.row_groups) {          // queries
         const int t0 = blockIdx.x * kRows, n = min(s.T - t0, kRows);
-        if (tid < n) {
-            const int b = s.of_row(t0 + tid);
-            live[tid] = b >= 0;
-            pos[tid] = b >= 0 ? s.len(b) - s.rows(b) + (t0 + tid - s.start(b)) : 0;
+        static_assert(kRows == kNT / 64, "a wave finds a row's sequence");
+        if (wave < n) {
+            const int b = s.of_row_by_wave(t0 + wave);
+            if ((tid & 63) == 0) {
+                live[wave] = b >= 0;
+                pos[wave] = b >= 0 ? s.len(b) - s.rows(b) + (t0 + wave - s.start(b)) : 0;
+            }
         }
         __syncthreads();
         rotate_rows<E>(a.q, t0, n, pos, live, table);
         return;
     }
     const int kv = a.cache.kv, dim = a.cache.dim, page_log2 = a.cache.page_log2;
+    const int groups = W == 4 ? kv : (kv + 3) / 4;                   // of heads
     const int at = blockIdx.x - a.row_groups;
     const int which = at & 1;                      // keys, values
-    const int head = (at >> 1) % kv;
-    if (tid < 64) {
-        const int2 f = find_item(s, page_log2, (at >> 1) / kv);
+    const int head = W == 4 ? (at >> 1) % groups : (at >> 1) % groups * 4 + wave;
+    if (wave == 0) {
+        const int2 f = find_item(s, page_log2, (at >> 1) / groups);
         if (tid == 0) item = f;
     }
     __syncthreads();
@@ -240,7 +247,8 @@ __global__ __launch_bounds__(kNT) void k_append(AppendArgs a) {
     const uint16_t* x = a.in[which] + (size_t)row0 * a.stride[which] + (size_t)head * dim;
     Rotation rot = a.rot;
     if (which == 1) rot.inv_freq = nullptr;
-    const int per = dim / 16, units = n * per;
+    const int per = dim / 16;
+    const int units = W == 4 || head < kv ? n * per : 0;             // a wave without a head only helps with the angles
 
     float v[U][16];
     uint32_t top = 0;
@@ -248,15 +256,22 @@ __global__ __launch_bounds__(kNT) void k_append(AppendArgs a) {
         uint4 raw[U][2];
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            const int u = tid + kNT * i;
+            const int u = bt + BT * i;
             raw[i][0] = raw[i][1] = make_uint4(0, 0, 0, 0);
-            if (u < units) {
+            if (BT * i < units && u < units) {
                 const int t = u / per;
                 const Unit unit(rot, u - t * per);
                 const uint16_t* r = x + (size_t)t * a.stride[which];
                 raw[i][0] = *(const uint4*)(r + unit.c0);
                 raw[i][1] = *(const uint4*)(r + unit.c1);
             }
+        }
+        if (W == 1 && rot.inv_freq) {              // while the rows are on their way
+            for (int k = tid; k < n * rot.pairs; k += kNT) {
+                const int t = k / rot.pairs;
+                table[k] = angle(rot, lo + t, k - t * rot.pairs);
+            }
+            __syncthreads();
         }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
@@ -267,35 +282,41 @@ __global__ __launch_bounds__(kNT) void k_append(AppendArgs a) {
     if (rot.inv_freq) {
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            // the angles of this step's units, 8 pairs each, by all threads
-            const int u0 = kNT * i, count = min(max(units - u0, 0), kNT);
-            if (i) __syncthreads();
-            for (int k = tid; k < 8 * count; k += kNT) {
-                const int u = u0 + k / 8, t = u / per;
-                const Unit unit(rot, u - t * per);
-                if (unit.pair >= 0) table[k] = angle(rot, lo + t, unit.pair + (k & 7));
+            const int u0 = BT * i, count = min(units - u0, BT);
+            if (count <= 0) break;
+            if constexpr (W == 4) {
+                // the angles of this step's units, 8 pairs each, by all threads
+                if (i) __syncthreads();
+                for (int k = tid; k < 8 * count; k += kNT) {
+                    const int u = u0 + k / 8, t = u / per;
+                    const Unit unit(rot, u - t * per);
+                    if (unit.pair >= 0) table[k] = angle(rot, lo + t, unit.pair + (k & 7));
+                }
+                __syncthreads();
             }
-            __syncthreads();
-            const int u = u0 + tid;
-            if (u < units && Unit(rot, u % per).pair >= 0) rotate(v[i], table + 8 * tid, rot.interleaved);
+            const int u = u0 + bt, t = u / per;
+            const Unit unit(rot, u - t * per);
+            if (u < units && unit.pair >= 0)
+                rotate(v[i], table + (W == 4 ? 8 * tid : t * rot.pairs + unit.pair), rot.interleaved);
         }
     }
+    if (units == 0) return;                        // W = 1: no barrier from here on
 #pragma unroll
     for (int i = 0; i < U; ++i)
 #pragma unroll
         for (int e = 0; e < 16; ++e) top = max(top, abs_bits(v[i][e]));
-    const float amax = __builtin_bit_cast(float, group_reduce<4>(top, slots, MaxU32()));
+    const float amax = __builtin_bit_cast(float, group_reduce<W>(top, slots, MaxU32()));
 
     float* scale = a.cache.scales[which] + (size_t)page_id * kv + head;
     int8_t* block = a.cache.codes[which] + a.cache.block(page_id, head);
     const float before = slot0 > 0 ? *scale : 0.0f;
     const float after = fmaxf(before, amax / 127.0f);
-    __syncthreads();                               // everyone has read the old scale
-    if (tid == 0) *scale = after;
+    if (W == 4) __syncthreads();                   // everyone has read the old scale
+    if (bt == 0) *scale = after;
     if (after > before && slot0 > 0) {             // the codes that the block held, on the new scale
         const float shrink = before / after;
         uint4* held = (uint4*)block;
-        for (int i = tid; i < slot0 * dim / 16; i += kNT) {
+        for (int i = bt; i < slot0 * per; i += BT) {
             uint4 c = held[i];
             uint32_t* words = (uint32_t*)&c;
 #pragma unroll
@@ -312,7 +333,8 @@ __global__ __launch_bounds__(kNT) void k_append(AppendArgs a) {
     const float inv = after > 0.0f ? 1.0f / after : 0.0f;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-        const int u = tid + kNT * i;
+        const int u = bt + BT * i;
+        if (BT * i >= units) break;
         uint2 c0, c1;
         unit_codes(v[i], after, inv, &c0, &c1);
         if (u < units) {
@@ -340,16 +362,18 @@ __global__ __launch_bounds__(kNT) void k_read(ReadArgs a) {
     const int tid = threadIdx.x;
     const int t0 = blockIdx.x * kRows, n = min(s.T - t0, kRows);
     const int page_log2 = a.cache.page_log2, kv = a.cache.kv, dim = a.cache.dim;
-    if (tid < n) {
-        const int b = s.of_row(t0 + tid);
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);           // a row each
+    if (wave < n) {
+        const int b = s.of_row_by_wave(t0 + wave);
         int page = -2, pos = 0;
         if (b >= 0) {
-            const int len = s.len(b);
-            pos = len - s.rows(b) + (t0 + tid - s.start(b));
+            pos = s.len(b) - s.rows(b) + (t0 + wave - s.start(b));
             page = pos >= 0 ? s.page(b, pos >> page_log2, a.cache.pages) : -1;
         }
-        where[tid][0] = page;
-        where[tid][1] = pos & (a.cache.page() - 1);
+        if ((tid & 63) == 0) {
+            where[wave][0] = page;
+            where[wave][1] = pos & (a.cache.page() - 1);
+        }
     }
     __syncthreads();
     const int per = dim / 16, units = 2 * kv * per;
@@ -379,20 +403,25 @@ __global__ __launch_bounds__(kNT) void k_read(ReadArgs a) {
     }
 }
 
-template <class E, int U>
+template <class E, int U, int W>
 int launch_append_t(const AppendArgs& a, hipStream_t st) {
-    const unsigned groups = a.row_groups + 2u * a.items * a.cache.kv;
-    hipLaunchKernelGGL((k_append<E, U>), dim3(groups), dim3(kNT), 0, st, a);
+    const unsigned groups = a.row_groups + 2u * a.items * (W == 4 ? a.cache.kv : (a.cache.kv + 3) / 4);
+    hipLaunchKernelGGL((k_append<E, U, W>), dim3(groups), dim3(kNT), 0, st, a);
     return (int)hipGetLastError();
 }
 
+// A wave a block where a wave can hold it: four heads then share a page's search and its
+// angles (3374 rows of 3 sequences, 16-token pages of 8 heads of 128: 23 us with a
+// workgroup a block, 19 with a wave).  One row a sequence is one token a block.
 template <class E>
 int pick_append(const AppendArgs& a, hipStream_t st) {
+    if (!a.seqs.starts) return launch_append_t<E, 1, 1>(a, st);
     const int units = a.cache.page() * a.cache.dim / 16;
-    if (units <= kNT) return launch_append_t<E, 1>(a, st);
-    if (units <= 2 * kNT) return launch_append_t<E, 2>(a, st);
-    if (units <= 4 * kNT) return launch_append_t<E, 4>(a, st);
-    return launch_append_t<E, 8>(a, st);
+    if (units <= 128) return launch_append_t<E, 2, 1>(a, st);
+    if (units <= 256) return launch_append_t<E, 4, 1>(a, st);
+    if (units <= 512) return launch_append_t<E, 2, 4>(a, st);
+    if (units <= 1024) return launch_append_t<E, 4, 4>(a, st);
+    return launch_append_t<E, 8, 4>(a, st);
 }
 
 }  // namespace

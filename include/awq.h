@@ -545,7 +545,7 @@ awq_status awq_moe(const void* x, const float* inv_s, const void* router,
  *                  lens[b]) are not cached, attend to nothing and read as zeros.
  * A page may be in the rows of several sequences as long as no call writes to
  * it.  int32 and fp32 arrays need 4-byte alignment only.  T, B <= 2^20, and
- * kv_heads <= 65535, and
+ * heads <= 65535, and
  * what a launch cannot count (2^32 threads) is AWQ_ERR_SHAPE.
  * ------------------------------------------------------------------------ */
 
@@ -585,7 +585,8 @@ awq_status awq_rope_frequencies(int rotary_dim, double base, int scaling, double
  * (inverse = 1: by -t, the transposed map, which is also its gradient's); the
  * other channels are copied.
  *   x, out  dtype [T][heads][head_dim], heads and channels dense, rows x_stride
- *   and out_stride elements apart (multiples of 8, at least heads * head_dim);
+ *   and out_stride elements apart (multiples of 8, at least heads * head_dim; heads
+ *   <= 65535);
  *   out may be x; otherwise they do not overlap.  positions int32 [T],
  *   inv_freq fp32 [rotary_dim / 2].  head_dim a multiple of 16, at most 512,
  *   rotary_dim a multiple of 16, at most head_dim (else AWQ_ERR_SHAPE).
@@ -636,7 +637,7 @@ awq_status awq_cache_read(const void* k_codes, const float* k_scales, const void
  *   Query head h reads kv head h / (heads / kv_heads).  A query with no key has
  *   out 0 and lse -infinity.
  *   q dtype [T][heads][head_dim], rows q_stride elements apart as in awq_rope; out
- *   dtype [T][heads][head_dim] dense; lse fp32 [T][heads] or NULL.
+ *   dtype [T][heads][head_dim] dense and apart from q; lse fp32 [T][heads] or NULL.
  *   Scores, softmax and sums are fp32 over the exact codes; softmax weights
  *   (times the block's value scale, relative to the largest) are rounded to fp16
  *   for the product with the values.

@@ -64,7 +64,8 @@ def test_rope_validation(lib):
     for bad in (dict(x=MIS), dict(out=MIS), dict(pos=ODD), dict(f=ODD)):
         assert call(**bad) == ALIGN, bad
     for bad in (dict(T=-1), dict(heads=0), dict(dim=0), dict(dim=120), dict(dim=528), dict(rotary=0), dict(rotary=24),
-                dict(rotary=144), dict(xs=504), dict(xs=516), dict(os=500), dict(T=(1 << 31) - 1)):
+                dict(rotary=144), dict(xs=504), dict(xs=516), dict(os=500), dict(T=(1 << 31) - 1),
+                dict(heads=65536, xs=1 << 24, os=1 << 24)):
         assert call(**bad) == SHAPE, bad
     for bad in (dict(layout=2), dict(inverse=2), dict(dtype=2), dict(m=math.nan)):
         assert call(**bad) == UNSUP, bad
@@ -108,7 +109,7 @@ def test_cache_calls_validation(lib):
     for bad in (dict(q=MIS), dict(k=MIS), dict(v=MIS), dict(out=MIS), dict(f=ODD)):
         assert append(**bad) == ALIGN, bad
     for bad in (dict(qs=504), dict(ks=248), dict(vs=260), dict(rotary=0), dict(rotary=136), dict(rotary=144), dict(heads=0),
-                dict(T=1 << 20, kv=256, ks=1 << 15, vs=1 << 15)):
+                dict(T=1 << 20, kv=256, ks=1 << 15, vs=1 << 15), dict(heads=65536, qs=1 << 24)):
         assert append(**bad) == SHAPE, bad
     for bad in (dict(layout=2), dict(m=math.inf)):
         assert append(**bad) == UNSUP, bad

@@ -157,6 +157,12 @@ def test_long_context_and_many_sequences(gpu):
     announce("append long")
     run(Case([(1, 70000), (700, 65000)], 2, 1, 64, 64, seed=8))
     run(Case([((b * 7) % 5, (b * 37) % 150) for b in range(200)], 2, 1, 64, 16, seed=9))
+    run(Case([((b * 7) % 3, (b * 37) % 40) for b in range(5000)], 1, 1, 64, 16, seed=10))
+    run(Case([(40 * (b % 2), (b * 37) % 40) for b in range(300)], 1, 1, 64, 16, seed=11))
+    run(Case([(1, (b * 37) % 40) for b in range(9000)], 1, 1, 64, 32, seed=12), starts=False)
+    # more rows than tokens, row by row and page by page
+    run(Case([(5, 0), (3, 20), (40, 0)], 2, 2, 64, 16, seed=13, lens=[2, 23, 17]))
+    run(Case([(90, 0), (3, 20), (60, 0)], 2, 2, 64, 16, seed=14, lens=[33, 23, 1]))
 
 
 def test_refused(gpu):

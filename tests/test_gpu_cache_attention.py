@@ -161,16 +161,16 @@ def test_starts_that_make_no_sense(gpu):
             assert sentinel_intact(raw, n)
 
 
-@pytest.mark.parametrize("new", [1, 4, 200])
-def test_two_graphs_share_a_workspace(gpu, new):
+@pytest.mark.parametrize("new,dim", [(1, 128), (4, 128), (200, 128), (20, 256), (200, 256), (200, 192)])
+def test_two_graphs_share_a_workspace(gpu, new, dim):
     """Captured calls on one workspace full of something else, replayed in turns with eager work between."""
     import torch
-    announce("attention graphs", new)
+    announce("attention graphs", new, dim)
     calls = []
     for seed in (14, 15):
-        case = Case([(new, 900 + 50 * seed), (new, 31), (new, 0)], 8, 2, 128, 64, seed=seed)
+        case = Case([(new, 900 + 50 * seed), (new, 31), (new, 0)], 8, 2, dim, 64, seed=seed)
         calls.append((case, case.rows(8, 2.0), *case.on_gpu()))
-    sizes = [awq.cache_attention_workspace_bytes(3 * new, 3, 8, 2, 128, new, c[3].shape[1] * 64) for c in calls]
+    sizes = [awq.cache_attention_workspace_bytes(3 * new, 3, 8, 2, dim, new, c[3].shape[1] * 64) for c in calls]
     ws = torch.full((max(sizes) + 16,), 0xFF, dtype=torch.uint8, device="cuda")
     outs = [torch.empty_like(c[1]) for c in calls]
 
@@ -206,6 +206,16 @@ def test_many_ragged_sequences(gpu):
     announce("attention ragged")
     run(Case([((b * 5) % 4, (b * 61) % 400) for b in range(150)], 4, 1, 64, 32, seed=16))
     run(Case([(1, (b * 131) % 900) for b in range(90)], 8, 2, 128, 64, "bf16", seed=17), starts=False)
+
+
+def test_thousands_of_sequences(gpu):
+    """Sequences found by more than one look at the starts; most of them short, some without rows."""
+    announce("attention thousands")
+    for new, most in ((1, 60), (2, 60), (1, 4000), (3, 4000)):
+        pairs = [((b * 7) % (new + 1), (b * 13) % 50) for b in range(4500)]
+        run(Case(pairs, 2, 1, 64, 16, seed=new + most), max_new=new, max_len=most)
+    pairs = [((b * 7) % 5, (b * 13) % 50) for b in range(700)]
+    run(Case(pairs, 20, 1, 64, 16, seed=21), max_new=4)
 
 
 def test_one_long_sequence(gpu):

@@ -542,7 +542,7 @@ constexpr long long kMaxGroups = 1LL << 24;      // workgroups of 256 threads: a
 constexpr int kMaxCacheRows = 1 << 20;           // rows (tokens) and sequences of a call
 constexpr int kMaxBookRows = 65535;              // table rows are a launch's second dimension
 constexpr int kMaxPages = 1 << 30;
-constexpr int kMaxKvHeads = 65535;
+constexpr int kMaxHeads = 65535;
 constexpr int kMaxWindow = 1 << 30;              // positions less a window stay in 31 bits
 
 // index arrays are int32 and need no more than their own alignment
@@ -577,7 +577,7 @@ int check_cache(int kv_heads, int dim, int pages, int page_size) {
     if (int st = check_page(page_size)) return st;
     if (dim != 64 && dim != 96 && dim != 128 && dim != 192 && dim != 256) return AWQ_ERR_UNSUPPORTED;
     // a page of all heads stays below 2^31 codes
-    return kv_heads <= 0 || kv_heads > kMaxKvHeads || pages <= 0 || pages > kMaxPages ? AWQ_ERR_SHAPE : AWQ_OK;
+    return kv_heads <= 0 || kv_heads > kMaxHeads || pages <= 0 || pages > kMaxPages ? AWQ_ERR_SHAPE : AWQ_OK;
 }
 
 // T rows of B sequences with tables of W pages; without starts every sequence has one row
@@ -647,7 +647,8 @@ awq_status awq_rope(const void* x, long long x_stride, const int* positions, con
                     int inverse, int dtype, hipStream_t stream) {
     int st = check_dtype(dtype);
     if (st) return as_status(st);
-    if (T < 0 || heads <= 0 || head_dim <= 0 || head_dim % 16 != 0 || head_dim > kMaxRopeDim) return AWQ_ERR_SHAPE;
+    if (T < 0 || heads <= 0 || heads > kMaxHeads || head_dim <= 0 || head_dim % 16 != 0 || head_dim > kMaxRopeDim)
+        return AWQ_ERR_SHAPE;
     if (T / 4 + 1 >= kMaxGroups) return AWQ_ERR_SHAPE;
     if (inverse != 0 && inverse != 1) return AWQ_ERR_UNSUPPORTED;
     if (inv_freq == nullptr && T > 0) return AWQ_ERR_NULL;
@@ -670,7 +671,7 @@ awq_status awq_cache_append(const void* q, long long q_stride, const void* k, lo
     if (st) return as_status(st);
     if ((st = check_cache(kv_heads, head_dim, pages, page_size)) || (st = check_sequences(starts, T, B, W)))
         return as_status(st);
-    if (q != nullptr && heads <= 0) return AWQ_ERR_SHAPE;
+    if (q != nullptr && (heads <= 0 || heads > kMaxHeads)) return AWQ_ERR_SHAPE;
     if ((st = check_rotation(inv_freq, rotary_dim, head_dim, layout, magnitude))) return as_status(st);
     if (q != nullptr && (st = check_stride(q_stride, heads, head_dim))) return as_status(st);
     if ((st = check_stride(k_stride, kv_heads, head_dim)) || (st = check_stride(v_stride, kv_heads, head_dim)))

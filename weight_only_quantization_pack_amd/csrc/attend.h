@@ -27,7 +27,7 @@ struct AttendArgs {
     int split;                           // stretches may end inside a tile
     int groups;                          // workgroups of the first launch
     float* parts;                        // [groups][2][rows * (dim + 2)]
-    long long* line;                     // [B + 1]: units before each sequence; units of a stretch
+    long long* line;                     // [B + 1]: units before each sequence; units of a stretch (split, attend.hip)
 };
 
 // the steps of a sequence: the same for all its tiles of rows (their own first and
@@ -71,8 +71,8 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
     return (uint32_t)a / (uint32_t)b;
 }
 
-// The line of work, read by every wave for itself: sequence b in lane b % 64, the first
-// 64 kept in registers.  Units are steps (or, by tiles, whole tiles) of all heads.
+// The line of steps, read by every wave for itself: sequence b in lane b % 64, the first
+// 64 kept in registers.
 class LineWalk {
     struct Block {
         int start, n, len;
@@ -80,13 +80,12 @@ class LineWalk {
     };
     const AttendArgs& a;
     const int tile_rows;
-    const bool tiles;
     Block first;
     __device__ __forceinline__ Block block(int b) const {
         Block k{0, 0, 0, 0};
         if (b < a.seqs.B) {
             const Line l(a, b, tile_rows);
-            k = {l.start, l.n, l.len, tiles ? (long long)l.tiles * a.cache.kv : l.units(a.cache.kv)};
+            k = {l.start, l.n, l.len, l.units(a.cache.kv)};
         }
         return k;
     }
@@ -97,8 +96,8 @@ public:
         long long before;                // units before the sequence, or all
         Line line;
     };
-    __device__ __forceinline__ LineWalk(const AttendArgs& a_, int tile_rows_, bool tiles_)
-        : a(a_), tile_rows(tile_rows_), tiles(tiles_), first(block(threadIdx.x & 63)) {}
+    __device__ __forceinline__ LineWalk(const AttendArgs& a_, int tile_rows_)
+        : a(a_), tile_rows(tile_rows_), first(block(threadIdx.x & 63)) {}
     // Calls f(b, units, before) for the sequences, 64 at a time, until it is true for
     // one, and gives the first such.
     template <class F>
@@ -125,6 +124,25 @@ private:
                     __builtin_amdgcn_readlane(k.len, i), tile_rows);
     }
 };
+
+// Tiles without a line: sequence b has the places from start(b) * group / tile_rows + b on,
+// enough for its tiles, and finding it takes the starts alone.  The sequence and the
+// tile (counted from the place) of `place`; b = -1 where there is none.  By a wave.
+__device__ __forceinline__ long long first_place(const AttendArgs& a, int tile_rows, int b, int start) {
+    return (uint32_t)(start * a.group) / (uint32_t)tile_rows + b;
+}
+struct TilePlace {
+    int b, tile;
+    Line line;
+};
+__device__ __forceinline__ TilePlace find_tile(const AttendArgs& a, int tile_rows, long long place) {
+    const Sequences& s = a.seqs;
+    const int b = first_by_wave(s.B, [&](int k) { return first_place(a, tile_rows, k + 1, s.start(k + 1)) > place; });
+    if (b < 0) return {-1, 0, Line(a, 0, 0, 0, tile_rows)};
+    const Line l(a, b, tile_rows);
+    const long long tile = place - first_place(a, tile_rows, b, l.start);
+    return {tile >= 0 && tile < l.tiles ? b : -1, (int)tile, l};
+}
 
 __device__ __forceinline__ float lane_value(float v, int lane) {
     return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));

@@ -62,9 +62,12 @@ __global__ __launch_bounds__(64 * kW, D * C > 256 ? 1 : 2) void k_attend(AttendA
     const Sequences& s = a.seqs;
     const int kv = a.cache.kv, page_log2 = a.cache.page_log2;
 
-    // this workgroup's stretch [u, u_end), relative to sequence b
-    const LineWalk walk(a, R, !a.split);
-    long long u = blockIdx.x, u_end = 0;
+    // this workgroup's stretch [u, u_end) of the line of units, relative to sequence b: an even
+    // share of it, or just one tile's
+    long long u, u_end;
+    int b;
+    Line l(a, 0, 0, 0, R);
+    const LineWalk walk(a, R);
     if (a.split) {
         const bool note = blockIdx.x == 0;         // the join wants to know the line
         const long long total = walk([&](int b, long long, long long before) {
@@ -73,18 +76,21 @@ __global__ __launch_bounds__(64 * kW, D * C > 256 ? 1 : 2) void k_attend(AttendA
         }).before;
         const long long share = stretch(total, a.groups);
         if (note && threadIdx.x == 0) a.line[s.B] = share;
-        u *= share;
+        u = blockIdx.x * share;
         u_end = min(u + share, total);
         if (u >= u_end) return;
-    }
-    const auto p = walk([&](int, long long n, long long before) { return u < before + n; });
-    if (p.b < 0) return;
-    int b = p.b;
-    Line l = p.line;
-    u -= p.before;
-    u_end -= p.before;
-    if (!a.split) {
-        u *= l.tile_units();
+        const auto p = walk([&](int, long long n, long long before) { return u < before + n; });
+        if (p.b < 0) return;
+        b = p.b;
+        l = p.line;
+        u -= p.before;
+        u_end -= p.before;
+    } else {
+        const TilePlace p = find_tile(a, R, blockIdx.x / kv);
+        if (p.b < 0) return;
+        b = p.b;
+        l = p.line;
+        u = ((long long)(blockIdx.x % kv) * l.tiles + p.tile) * l.tile_units();
         u_end = u + l.tile_units();
     }
 
@@ -437,7 +443,7 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void k_attend_join(J
     if (t >= s.T) return;
     const int b = s.of_row_by_wave(t);
     if (b < 0) return;
-    const long long before = a.line[b], share = ja.tile_parts ? 1 : a.line[s.B];
+    const long long before = ja.tile_parts ? 0 : a.line[b], share = ja.tile_parts ? 1 : a.line[s.B];
     const Line l(a, b, R);
     const int head = h / a.group;
     const int row = (t - l.start) * a.group + (h - head * a.group);
@@ -449,7 +455,7 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void k_attend_join(J
     if (ja.tile_parts) {
         w1 = ja.tile_parts - 1;
         step = (size_t)a.cache.kv * size;
-        base = a.parts + (((size_t)before + (size_t)(l.tiles - 1 - tile) * a.cache.kv) * ja.tile_parts + head) * size;
+        base = a.parts + ((size_t)(first_place(a, R, b, l.start) + l.tiles - 1 - tile) * ja.tile_parts * a.cache.kv + head) * size;
     } else {
         const long long u0 = before + ((long long)head * l.tiles + tile) * l.tile_units();
         w0 = (int)quotient(u0 + kFixed, share);

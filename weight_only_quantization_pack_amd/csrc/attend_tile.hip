@@ -59,21 +59,12 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attend_tile(Atten
 
     // the tile: heads first (neighbouring workgroups, on different XCDs, read different
     // heads), long rows of keys before short ones
-    const LineWalk walk(a, R, true);
-    if (parts > 1 && blockIdx.x == 0)              // the join wants to know the line
-        walk([&](int b, long long, long long before) {
-            if (b < s.B) a.line[b] = before;
-            return false;
-        });
-    const long long unit = blockIdx.x / parts;
-    const auto mine = walk([&](int, long long u, long long before) { return unit < before + u; });
-    const int b = mine.b;
+    const int head = blockIdx.x % kv, part = blockIdx.x / kv % parts;
+    const TilePlace found = find_tile(a, R, blockIdx.x / kv / parts);
+    const int b = found.b;
     if (b < 0) return;
-    const Line& l = mine.line;
-    const int at = (int)(blockIdx.x - mine.before * parts);
-    const int head = at % kv;
-    const int part = at / kv % parts;
-    const int tile = l.tiles - 1 - at / kv / parts;
+    const Line& l = found.line;
+    const int tile = l.tiles - 1 - found.tile;
     const int pos0 = l.len - l.n;                                    // position of the sequence's first row
     const int pos_lo = pos0 + tile * R / a.group;
     const int pos_hi = pos0 + min(tile * R + R - 1, l.rows - 1) / a.group;

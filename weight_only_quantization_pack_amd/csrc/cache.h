@@ -19,6 +19,24 @@ struct Cache {
     }
 };
 
+// The first i in 0..n-1 with above(i), for an `above` that stays true once it is; -1 without
+// one.  By a whole wave, 64 places a load.  (Whatever `above` says, i is in 0..n-1.)
+template <class F>
+__device__ __forceinline__ int first_by_wave(int n, F above) {
+    const int lane = threadIdx.x & 63;
+    int lo = 0;
+    while (n > 64) {
+        const int step = (n + 63) / 64;            // lane i looks at the end of its stretch of `step` places
+        const uint64_t hit = __builtin_amdgcn_ballot_w64(above(lo + min((lane + 1) * step, n) - 1));
+        if (!hit) return -1;
+        const int i = __builtin_ctzll(hit);
+        lo += i * step;
+        n = min(step, n - i * step);
+    }
+    const uint64_t hit = __builtin_amdgcn_ballot_w64(lane < n && above(lo + min(lane, n - 1)));
+    return hit ? lo + __builtin_ctzll(hit) : -1;
+}
+
 // The sequences of a call.  Sequence b holds lens[b] tokens, the last starts[b + 1]
 // - starts[b] of which are rows starts[b].. of the call's T rows (starts null: one
 // row each).  All of it is device data that the host has not seen: an accessor
@@ -38,29 +56,11 @@ struct Sequences {
         const int p = (unsigned)w < (unsigned)W ? tables[(size_t)b * W + w] : -1;
         return (unsigned)p < (unsigned)pages ? p : -1;
     }
-    // the sequence of row t, or -1 behind the last one; by a whole wave, t the same in all
-    // lanes: 256 sequences a load
+    // the sequence of row t, or -1 behind the last one; by a whole wave, t the same in all lanes
     __device__ __forceinline__ int of_row_by_wave(int t) const {
         if (!starts) return t < B ? t : -1;
-        const int lane = threadIdx.x & 63;
-        for (int b0 = 0; b0 < B; b0 += 256) {
-            int from[4], to[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int b = min(b0 + 64 * k + lane, B - 1);
-                from[k] = starts[b];
-                to[k] = starts[b + 1];
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint64_t hit = __builtin_amdgcn_ballot_w64(to[k] > t);
-                if (hit) {
-                    const int i = __builtin_ctzll(hit), b = b0 + 64 * k + i;
-                    return b < B && __builtin_amdgcn_readlane(from[k], i) <= t ? b : -1;
-                }
-            }
-        }
-        return -1;
+        const int b = first_by_wave(B, [&](int i) { return starts[i + 1] > t; });
+        return b >= 0 && starts[b] <= t ? b : -1;
     }
 };
 

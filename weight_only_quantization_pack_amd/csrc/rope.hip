@@ -128,44 +128,32 @@ struct AppendArgs {
     Rotation rot;
     Cache cache;
     Sequences seqs;
-    int items;                           // (sequence, page) pairs at most
+    int items, by_rows;                  // of find_item
     int row_groups;                      // workgroups that rotate queries
 };
 
-// The i-th page that the call's rows reach, over the sequences in order: (sequence,
-// page of its table row), or sequence -1 past the last.  By one wave, 64 sequences
-// at a time.
-__device__ __forceinline__ int2 find_item(const Sequences& s, int page_log2, int i) {
-    if (!s.starts) {
-        if (i >= s.B) return make_int2(-1, 0);
-        return make_int2(i, (s.len(i) - 1) >> page_log2);     // -1 for an empty sequence
+// Item i of the call as (sequence, page of its table row), or sequence -1: by a wave.  With
+// by_rows an item is a row, and the first one of a sequence in a page stands for the page;
+// else sequence b has the items from start(b) / page + 2 b on, enough for its pages (n
+// rows reach at most n / page + 2), and finding it takes the starts alone.
+__device__ __forceinline__ int2 find_item(const Sequences& s, int page_log2, bool by_rows, int i) {
+    int b;
+    if (by_rows) {
+        b = s.of_row_by_wave(i);
+    } else {
+        b = first_by_wave(s.B, [&](int k) { return (s.start(k + 1) >> page_log2) + 2 * (k + 1) > i; });
+        if (b >= 0 && (s.start(b) >> page_log2) + 2 * b > i) b = -1;
     }
-    const int lane = threadIdx.x & 63;
-    for (int b0 = 0; b0 < s.B; b0 += 64) {
-        const int b = b0 + lane;
-        int w0 = 0, n = 0;
-        if (b < s.B) {
-            const int len = s.len(b), rows = s.rows(b);
-            const int first = max(len - rows, 0);
-            w0 = first >> page_log2;
-            n = len > first ? ((len - 1) >> page_log2) - w0 + 1 : 0;
-        }
-        int before = n;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(before, d);
-            if (lane >= d) before += o;
-        }
-        const int total = __shfl(before, 63);
-        before -= n;
-        if (i < total) {
-            const uint64_t hit = __builtin_amdgcn_ballot_w64(i >= before && i < before + n);
-            const int at = __builtin_ctzll(hit);
-            return make_int2(b0 + at, __shfl(w0, at) + i - __shfl(before, at));
-        }
-        i -= total;
+    if (b < 0) return make_int2(-1, 0);
+    const int len = s.len(b), rows = s.rows(b), start = s.start(b);
+    if (by_rows) {
+        const int pos = len - rows + (i - start);              // below 0: not cached
+        if (pos < 0 || ((pos & ((1 << page_log2) - 1)) != 0 && pos != max(len - rows, 0))) return make_int2(-1, 0);
+        return make_int2(b, pos >> page_log2);
     }
-    return make_int2(-1, 0);
+    const int first = max(len - rows, 0);
+    const int w = (first >> page_log2) + i - ((start >> page_log2) + 2 * b);
+    return len > first && w <= (len - 1) >> page_log2 ? make_int2(b, w) : make_int2(-1, 0);
 }
 
 // the codes of a unit's 16 values, rint(v / s), by multiplication where it decides
@@ -230,7 +218,7 @@ __global__ __launch_bounds__(kNT) void k_append(AppendArgs a) {
     const int which = at & 1;                      // keys, values
     const int head = W == 4 ? (at >> 1) % groups : (at >> 1) % groups * 4 + wave;
     if (wave == 0) {
-        const int2 f = find_item(s, page_log2, (at >> 1) / groups);
+        const int2 f = find_item(s, page_log2, a.by_rows, (at >> 1) / groups);
         if (tid == 0) item = f;
     }
     __syncthreads();
@@ -447,9 +435,9 @@ int launch_cache_append(const AppendProblem& p, hipStream_t st) {
     a.rot = p.rot;
     a.cache = p.cache;
     a.seqs = p.seqs;
-    // n rows of a sequence reach at most n / page + 2 pages, and at most n
-    const long long most = p.seqs.starts ? (long long)(p.seqs.T >> p.cache.page_log2) + 2LL * p.seqs.B : p.seqs.B;
-    a.items = (int)(most < p.seqs.T ? most : p.seqs.T);
+    const long long most = (p.seqs.T >> p.cache.page_log2) + 2LL * p.seqs.B;
+    a.by_rows = !p.seqs.starts || p.seqs.T <= most;
+    a.items = a.by_rows ? p.seqs.T : (int)most;
     a.row_groups = p.q ? (p.seqs.T + kRows - 1) / kRows : 0;
     return p.dtype == AWQ_BF16 ? pick_append<BF16>(a, st) : pick_append<F16>(a, st);
 }

@@ -159,6 +159,25 @@ def test_copy_pages(gpu, layers):
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("n,share", [(70, 0.5), (256, 1.0), (300, 0.3), (1000, 0.1), (4000, 0.9), (4096, 0.5), (4100, 0.2)])
+def test_copy_of_long_lists(gpu, n, share):
+    """Every valid pair of a list is copied, by many workgroups, wherever it stands."""
+    import torch
+    announce("copy long list", n, share)
+    g = np.random.default_rng(n)
+    pages = 2 * n + 10
+    t = [torch.randint(-100, 100, (3, pages, k), dtype=torch.int8, device="cuda") for k in (64, 12)]
+    order = g.permutation(pages)
+    pairs = np.where(g.random(n)[:, None] < share, np.stack([order[:n], order[n:2 * n]], 1), -1).astype(np.int32)
+    want = [a.clone() for a in t]
+    some = pairs[pairs[:, 0] >= 0]
+    for a in want:
+        a[:, put(some[:, 1].copy()).long()] = a[:, put(some[:, 0].copy()).long()]
+    awq.cache_copy_pages(t, put(pairs), layers=3)
+    for a, b in zip(t, want):
+        assert torch.equal(a, b)
+
+
 def test_copy_past_four_gigabytes(gpu):
     import torch
     announce("copy past 4 GB")

@@ -297,19 +297,37 @@ struct CopyArgs {
 };
 
 __global__ __launch_bounds__(256) void k_copy_pages(CopyArgs a) {
-    __shared__ int gathered[kGather], count;
+    __shared__ int gathered[kGather], counts[4];
     const CopyProblem& p = a.p;
     const int per = a.first[kMaxCopyTensors];
     auto valid = [&](int src, int dst) { return (unsigned)src < (unsigned)p.pages && (unsigned)dst < (unsigned)p.pages; };
     int n = p.count ? min(max(*p.count, 0), p.max_pairs) : p.max_pairs;
     const bool gather = !p.count && n <= kGather;
-    if (gather) {                                  // in any order: the copies do not depend on one another
-        if (threadIdx.x == 0) count = 0;
+    if (gather) {
+        // in the list's order, the same in every workgroup: a quarter of the list a wave,
+        // counted and then placed
+        const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const int quarter = (n + 255) / 256 * 64, end = min(n, (wave + 1) * quarter);
+        auto hits = [&](int i) {
+            return __builtin_amdgcn_ballot_w64(i + lane < end && valid(p.pairs[2 * (i + lane)], p.pairs[2 * (i + lane) + 1]));
+        };
+        int mine = 0;
+        for (int i = wave * quarter; i < end; i += 64) mine += __builtin_popcountll(hits(i));
+        if (lane == 0) counts[wave] = mine;
         __syncthreads();
-        for (int i = threadIdx.x; i < n; i += 256)
-            if (valid(p.pairs[2 * i], p.pairs[2 * i + 1])) gathered[atomicAdd(&count, 1)] = i;
+        int at = 0;
+        n = 0;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            if (w < wave) at += counts[w];
+            n += counts[w];
+        }
+        for (int i = wave * quarter; i < end; i += 64) {
+            const uint64_t hit = hits(i);
+            if (hit >> lane & 1) gathered[at + __builtin_popcountll(hit & ((1ull << lane) - 1))] = i + lane;
+            at += __builtin_popcountll(hit);
+        }
         __syncthreads();
-        n = count;
     }
     const size_t units = (size_t)n * p.layers * per;
     for (size_t u = blockIdx.x; u < units; u += gridDim.x) {

@@ -53,6 +53,9 @@ __device__ __forceinline__ uint32_t value_pair(uint32_t lo, uint32_t hi, int j) 
 template <int D, int C, bool SMALL>
 __global__ __launch_bounds__(64 * kW, D * C > 256 ? 1 : 2) void k_attend(AttendArgs a) {
     using K = Codes<D>;
+    // The next step's codes beside this one's, where the registers hold both: 16 sequences of
+    // 1000 to 4000 tokens, heads of 256, 38 us one step at a time and 62 with two (spilled).
+    constexpr bool kDeep = K::VD * C <= 192;
     constexpr int R = 16 * C, NK = K::NK, VB = K::VB, VW = K::VW;
     constexpr int JB = VB > 8 ? VB / 2 : VB;       // channels of a lane that one pass of the join takes
     __shared__ float join[kW][4][64][JB + 1];      // [wave][i][lane][j]; padded against bank conflicts
@@ -338,14 +341,21 @@ __global__ __launch_bounds__(64 * kW, D * C > 256 ? 1 : 2) void k_attend(AttendA
             }
         };
 
-        // loads under no condition, so that a wait counts only those before it: behind the
-        // last step they repeat it
-        K db;
-        for (int i = 0; i < mine; i += 2) {
-            load(db, min(i + 1, mine - 1));
-            compute(da, i);
-            load(da, min(i + 2, mine - 1));
-            if (i + 1 < mine) compute(db, i + 1);
+        if constexpr (kDeep) {
+            // loads under no condition, so that a wait counts only those before it: behind the
+            // last step they repeat it
+            K db;
+            for (int i = 0; i < mine; i += 2) {
+                load(db, min(i + 1, mine - 1));
+                compute(da, i);
+                load(da, min(i + 2, mine - 1));
+                if (i + 1 < mine) compute(db, i + 1);
+            }
+        } else {
+            for (int i = 0; i < mine; ++i) {
+                compute(da, i);
+                if (i + 1 < mine) load(da, i + 1);
+            }
         }
 
         // the four waves' results: one maximum, sums and outputs added in order

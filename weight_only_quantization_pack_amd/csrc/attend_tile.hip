@@ -6,28 +6,41 @@
 // and goes over the keys 64 at a time:
 //
 //   codes -> registers -> fp16 operands in LDS, two tiles of keys by turns
-//   scores  S^T = K Q^T          32 x 32 x 16 products, 32 rows (or 64) a wave
+//   scores  S^T = K Q^T          16 x 16 x 32 products, one or two columns of 16 rows a wave
 //   weights exp2(S - M)          stay in the lane that the next product wants them in
-//   output  O^T += V^T W         32 x 32 x 16 products
+//   output  O^T += V^T W         16 x 16 x 32 products
 //
 // Keys of a score tile are permuted so that a lane's registers hold 8 consecutive
-// keys of one row for each chunk of 16: the B operand of the second product.  Values
+// keys of one row for each chunk of 32: the B operand of the second product.  Values
 // are transposed on their way into LDS (four keys by four channels a thread).  Both
-// images are swizzled by 16 bytes so that the eight lanes that read together meet
-// eight different banks' quarters.
+// images are swizzled by 16 bytes so that lanes that read together meet different
+// banks.
+//
+// What bounds it: the instructions that a SIMD can issue.  A tile of 64 keys costs a
+// wave, with two columns and heads of 128, 64 products of 16 cycles and 280 other vector
+// instructions of 4 (weights, running maximum, conversion of the codes): 1024 and 1120
+// cycles, which overlap only across the two waves of a SIMD.  Counted on a prompt of
+// 8192 tokens, 32 heads over 8, heads of 128: products in 40 % of the SIMDs' cycles, vector
+// instructions in 44 %.  It takes 572 us, 960 TFLOP/s.  Tried and slower there:
+// 32 x 32 x 16 products 613, 64 rows a wave 944, tiles of 128 rows 662, waves in two
+// groups that take products and weights by turns 800.
+//
+// Eight waves: 256 rows in two columns a wave where the registers hold them, for heads to
+// 128.  Wider heads, and calls of fewer rows, take one column: heads of 256, 2048 tokens,
+// 114 us, and 190 with four waves of two columns (one wave a SIMD); 64 sequences of 500
+// tokens, 64 rows each, heads of 128, 37 us and 40.
 #include "attend.h"
 
 namespace awq {
 namespace {
 
-constexpr int kKeys = 64;                // keys of a tile
+constexpr int kKeys = 64, NW = 8;        // keys of a tile, waves of a workgroup
 
 template <int D>
 struct Image {
     static constexpr int KS = D == 96 ? 128 : D;            // halves of a key row (swizzled in blocks of 64)
     static constexpr int keys = kKeys * KS * 2, values = D * kKeys * 2;
 };
-
 
 // Row r of the A operand with the keys of score tile t (of two that make 32 keys), and
 // with the channels of output tile t (of two that make 32): a lane's results are then 8
@@ -44,9 +57,10 @@ __device__ __forceinline__ int swizzle(int row) {
     return ((row >> 1 & 1) | (row >> 3 & 3) << 1) ^ (row >> 2 & 1);
 }
 
-template <int D, int NW>
-__global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attend_tile(AttendArgs a, int parts) {
-    constexpr int NT = 64 * NW, CT = 2, R = 16 * CT * NW, NC = D / 32, ND = D / 16;
+// CT: columns of 16 rows a wave
+template <int D, int CT>
+__global__ __launch_bounds__(64 * NW, D <= 128 && CT == 1 ? 4 : 2) void k_attend_tile(AttendArgs a, int parts) {
+    constexpr int NT = 64 * NW, R = 16 * CT * NW, NC = D / 32, ND = D / 16;
     constexpr int KP = kKeys * D / 16, VP = kKeys / 4 * D / 4;       // pieces of a tile: 16 codes; 4 x 4 codes
     constexpr int KN = (KP + NT - 1) / NT, VN = (VP + NT - 1) / NT;
     using I = Image<D>;
@@ -398,10 +412,10 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attend_tile(Atten
     }
 }
 
-template <int D, int NW>
+template <int D, int CT>
 int launch_t(const AttendArgs& a, int parts, hipStream_t st) {
     constexpr int bytes = 2 * (Image<D>::keys + Image<D>::values);
-    auto kern = k_attend_tile<D, NW>;
+    auto kern = k_attend_tile<D, CT>;
     if (bytes > 65536)
         if (int e = (int)hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, bytes))
             return e;
@@ -412,8 +426,8 @@ int launch_t(const AttendArgs& a, int parts, hipStream_t st) {
 template <int D>
 int launch_d(const AttendArgs& a, const TilePlan& p, hipStream_t st) {
     if constexpr (D <= 128)
-        if (p.rows == 256) return launch_t<D, 8>(a, p.parts, st);
-    return launch_t<D, 4>(a, p.parts, st);
+        if (p.rows == 256) return launch_t<D, 2>(a, p.parts, st);
+    return launch_t<D, 1>(a, p.parts, st);
 }
 
 }  // namespace

@@ -544,9 +544,11 @@ awq_status awq_moe(const void* x, const float* inv_s, const void* router,
  *                  was.  Rows before a sequence's first token (more rows than
  *                  lens[b]) are not cached, attend to nothing and read as zeros.
  * A page may be in the rows of several sequences as long as no call writes to
- * it.  int32 and fp32 arrays need 4-byte alignment only.  T, B <= 2^20, and
- * heads <= 65535, and
- * what a launch cannot count (2^32 threads) is AWQ_ERR_SHAPE.
+ * it.  int32 and fp32 arrays need 4-byte alignment only.  T, B <= 2^20, heads <=
+ * 65535, and what a launch cannot count (2^32 threads) is AWQ_ERR_SHAPE.
+ * Scales are 0 or more.  A block (a page's tokens of one head) into which a token
+ * with an infinity or a NaN came has that as its scale until the page starts anew,
+ * and whoever sees one of its tokens reads NaN.
  * ------------------------------------------------------------------------ */
 
 typedef enum {
@@ -635,7 +637,8 @@ awq_status awq_cache_read(const void* k_codes, const float* k_scales, const void
  *         j > place - window with window > 0; from 2^30 on it counts as 2^30)
  *   lse = ln sum_j exp(s_j)
  *   Query head h reads kv head h / (heads / kv_heads).  A query with no key has
- *   out 0 and lse -infinity.
+ *   out 0 and lse -infinity; one that sees a block whose key or value scale is not
+ *   finite has NaN for both.
  *   q dtype [T][heads][head_dim], rows q_stride elements apart as in awq_rope; out
  *   dtype [T][heads][head_dim] dense and apart from q; lse fp32 [T][heads] or NULL.
  *   Scores, softmax and sums are fp32 over the exact codes; softmax weights

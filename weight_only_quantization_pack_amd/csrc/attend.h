@@ -164,6 +164,14 @@ __device__ __forceinline__ int query_exponent(float top) {
     const int e = top > 0.0f ? 13 - ((int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127) : 0;
     return min(max(e, -120), 120);
 }
+// What a block's scales make of a score's product (>= 0), and of its values.  A block whose
+// scale is not finite (a key or value was not) has a factor of NaN, which stands for it:
+// the value's scale is kept within what logarithm and reciprocal have.
+__device__ __forceinline__ float key_factor(float ks, float vs, float scale) {
+    return __builtin_fmaf(0.0f, ks + vs, ks * scale);
+}
+__device__ __forceinline__ float value_scale(float vs) { return fminf(fmaxf(vs, 0x1p-100f), 0x1p126f); }
+
 __device__ __forceinline__ float power_of_two(int e) { return __builtin_bit_cast(float, (uint32_t)(127 + e) << 23); }
 
 // rows of a tile, and into how many parts its keys are split

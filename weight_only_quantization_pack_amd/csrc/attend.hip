@@ -144,8 +144,9 @@ __global__ __launch_bounds__(64 * kW, D * C > 256 ? 1 : 2) void k_attend(AttendA
                 const int p = step < s1 ? s.page(b, (int)(key >> page_log2), a.cache.pages) : -1;
                 page_l[x] = p;
                 const size_t at = (size_t)max(p, 0) * kv + head;
-                c_l[x] = p >= 0 ? a.cache.scales[0][at] * a.scale : -1.0f;
-                const float vs = p >= 0 ? fmaxf(a.cache.scales[1][at], 0x1p-100f) : 1.0f;
+                const float ks = a.cache.scales[0][at], raw = a.cache.scales[1][at];
+                c_l[x] = p >= 0 ? key_factor(ks, raw, a.scale) : -1.0f;
+                const float vs = p >= 0 ? value_scale(raw) : 1.0f;
                 lv_l[x] = __builtin_amdgcn_logf(vs);
                 iv_l[x] = 1.0f / vs;
             }
@@ -270,7 +271,7 @@ __global__ __launch_bounds__(64 * kW, D * C > 256 ? 1 : 2) void k_attend(AttendA
             const float ks = SMALL && half ? d.c[1] : d.c[0];
             const float lv = SMALL && half ? d.lv[1] : d.lv[0];
             const float iv = SMALL && half ? d.iv[1] : d.iv[0];
-            const bool pages = SMALL ? d.c[0] >= 0.0f && d.c[1] >= 0.0f : d.c[0] >= 0.0f;
+            const bool pages = SMALL ? !(d.c[0] < 0.0f) && !(d.c[1] < 0.0f) : !(d.c[0] < 0.0f);
             const bool open = pages && key0 + kStep - 1 <= pos_lo && (a.window <= 0 || key0 > pos_hi - a.window);
             half8_t w[C];
 #pragma unroll
@@ -293,7 +294,7 @@ __global__ __launch_bounds__(64 * kW, D * C > 256 ? 1 : 2) void k_attend(AttendA
                     const int key = key0 + 8 * g;
 #pragma unroll
                     for (int y = 0; y < 8; ++y) {
-                        const bool seen = ks >= 0.0f && key + y <= pos[ct] && (a.window <= 0 || key + y > pos[ct] - a.window);
+                        const bool seen = !(ks < 0.0f) && key + y <= pos[ct] && (a.window <= 0 || key + y > pos[ct] - a.window);
                         t[y] = seen ? t[y] : -INFINITY;
                     }
                 }
@@ -385,7 +386,7 @@ __global__ __launch_bounds__(64 * kW, D * C > 256 ? 1 : 2) void k_attend(AttendA
             const int row = tile * R + 16 * ct + r;
             const bool live = row < l.rows;
             const int j = row / a.group, h = head * a.group + (row - j * a.group);
-            const float inv = all > 0.0f ? 1.0f / all : 0.0f;
+            const float inv = all == 0.0f ? 0.0f : 1.0f / all;
             const size_t at = (size_t)(l.start + j) * a.heads + h;
             for (int jb = 0; jb < VB; jb += JB) {
 #pragma unroll
@@ -425,7 +426,7 @@ __global__ __launch_bounds__(64 * kW, D * C > 256 ? 1 : 2) void k_attend(AttendA
                     part[16 * ct + r] = m;
                     part[R + 16 * ct + r] = all;
                 } else if (live && a.lse) {
-                    a.lse[at] = all > 0.0f ? (m + __builtin_amdgcn_logf(all)) * kLn2 : -INFINITY;
+                    a.lse[at] = all == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(all)) * kLn2;
                 }
             }
         }
@@ -530,12 +531,12 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void k_attend_join(J
             for (int x = 0; x < kMost; ++x) v[x] = __builtin_fmaf(acc[z][x][lane], f, v[x]);
         }
     }
-    const float inv = all > 0.0f ? 1.0f / all : 0.0f;
+    const float inv = all == 0.0f ? 0.0f : 1.0f / all;
     const size_t at = (size_t)t * a.heads + h;
 #pragma unroll
     for (int x = 0; x < kMost; ++x)
         if (lane + 64 * x < D) a.out[at * D + lane + 64 * x] = a.bf16 ? BF16::store(v[x] * inv) : F16::store(v[x] * inv);
-    if (lane == 0 && a.lse) a.lse[at] = all > 0.0f ? (m + __builtin_amdgcn_logf(all)) * kLn2 : -INFINITY;
+    if (lane == 0 && a.lse) a.lse[at] = all == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(all)) * kLn2;
 }
 
 // columns of 16 rows (0: attend_tile.hip's tiles), the workgroups and whether tiles

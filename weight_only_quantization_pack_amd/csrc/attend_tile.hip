@@ -159,6 +159,7 @@ __global__ __launch_bounds__(64 * NW, D <= 128 && CT == 1 ? 4 : 2) void k_attend
     };
     int page_l = -1, page_next = page_ids(t0);
     float ks_next = 0.0f, vs_next = 0.0f;
+    bool none = true;
     float c_l = -1.0f, lv_l = 0.0f, iv_l = 1.0f;
     // a tile's codes on their way
     const int mask = (1 << page_log2) - 1;
@@ -171,8 +172,9 @@ __global__ __launch_bounds__(64 * NW, D <= 128 && CT == 1 ? 4 : 2) void k_attend
             page_l = page_next;
             page_next = page_ids(t + 16);
             const size_t at = (size_t)max(page_l, 0) * kv + head;
-            ks_next = page_l >= 0 ? a.cache.scales[0][at] * a.scale : -1.0f;
-            vs_next = page_l >= 0 ? a.cache.scales[1][at] : 1.0f;
+            ks_next = a.cache.scales[0][at];
+            vs_next = a.cache.scales[1][at];
+            none = page_l < 0;
         }
         // tiles start at a page or in the middle of one: a key's slot is the tile's plus its own
         const uint32_t slot = (uint32_t)((t * kKeys) & mask) * D + head_bytes;
@@ -264,8 +266,8 @@ __global__ __launch_bounds__(64 * NW, D <= 128 && CT == 1 ? 4 : 2) void k_attend
     auto weights = [&](int t) {
         const int i = (t - t0) & 15, key0 = t * kKeys;
         if (i == 0) {
-            c_l = ks_next;
-            const float vs = fmaxf(vs_next, 0x1p-100f);
+            c_l = none ? -1.0f : key_factor(ks_next, vs_next, a.scale);
+            const float vs = none ? 1.0f : value_scale(vs_next);
             lv_l = __builtin_amdgcn_logf(vs);
             iv_l = 1.0f / vs;
         }
@@ -278,7 +280,7 @@ __global__ __launch_bounds__(64 * NW, D <= 128 && CT == 1 ? 4 : 2) void k_attend
             lv[kc] = __shfl(lv_l, from);
             iv[kc] = __shfl(iv_l, from);
         }
-        const bool closed = __builtin_amdgcn_ballot_w64(fminf(ks[0], ks[1]) < 0.0f) || key0 + kKeys - 1 > wave_lo ||
+        const bool closed = __builtin_amdgcn_ballot_w64(!(ks[0] >= 0.0f && ks[1] >= 0.0f)) || key0 + kKeys - 1 > wave_lo ||
                             (a.window > 0 && key0 <= wave_hi - a.window);
         float f[CT][2];                            // log2 weights are f * product + lv
 #pragma unroll
@@ -305,11 +307,12 @@ __global__ __launch_bounds__(64 * NW, D <= 128 && CT == 1 ? 4 : 2) void k_attend
 #pragma unroll
                 for (int kc = 0; kc < 2; ++kc) {
                     const int key = key0 + 32 * kc + 8 * g;
-                    const int hi = ks[kc] >= 0.0f ? pos[ct] - key : -1;                  // keys y <= hi, > lo are seen
+                    const int hi = ks[kc] < 0.0f ? -1 : pos[ct] - key;                   // keys y <= hi, > lo are seen
                     const int lo = a.window > 0 ? pos[ct] - a.window - key : -1;
 #pragma unroll
                     for (int y = 0; y < 8; ++y)
                         sc[ct][2 * kc + (y >> 2)][y & 3] = y <= hi && y > lo ? sc[ct][2 * kc + (y >> 2)][y & 3] : -INFINITY;
+                    if (ks[kc] != ks[kc] && hi >= 0 && lo < 7) sum[ct] = ks[kc];         // NaN for rows that see the block
                 }
             }
         }
@@ -400,7 +403,7 @@ __global__ __launch_bounds__(64 * NW, D <= 128 && CT == 1 ? 4 : 2) void k_attend
         }
         const int j = row / a.group, h = head * a.group + (row - j * a.group);
         const size_t out = (size_t)(l.start + j) * a.heads + h;
-        const float inv = all > 0.0f ? 1.0f / all : 0.0f;
+        const float inv = all == 0.0f ? 0.0f : 1.0f / all;
 #pragma unroll
         for (int d = 0; d < ND; d += 2) {
             float f[8];
@@ -408,7 +411,7 @@ __global__ __launch_bounds__(64 * NW, D <= 128 && CT == 1 ? 4 : 2) void k_attend
             for (int i = 0; i < 8; ++i) f[i] = o[ct][d + (i >> 2)][i & 3] * inv;
             *(uint4*)(a.out + out * D + 16 * d + 8 * g) = a.bf16 ? pack8<BF16>(f) : pack8<F16>(f);
         }
-        if (g == 0 && a.lse) a.lse[out] = all > 0.0f ? (M[ct] + __builtin_amdgcn_logf(all)) * kLn2 : -INFINITY;
+        if (g == 0 && a.lse) a.lse[out] = all == 0.0f ? -INFINITY : (M[ct] + __builtin_amdgcn_logf(all)) * kLn2;
     }
 }
 

@@ -157,7 +157,8 @@ __device__ __forceinline__ int2 find_item(const Sequences& s, int page_log2, boo
 }
 
 // the codes of a unit's 16 values, rint(v / s), by multiplication where it decides
-// (|v| <= 127 s): v * inv is within 127 * 2^-22 of the quotient
+// (|v| <= 127 s): v * inv is within 127 * 2^-22 of the quotient.  0 with a scale of 0 or
+// one that is not finite, which then stands for the whole block.
 __device__ __forceinline__ void unit_codes(const float* v, float s, float inv, uint2* c0, uint2* c1) {
     int k[16];
     float far = 0.0f;
@@ -167,11 +168,11 @@ __device__ __forceinline__ void unit_codes(const float* v, float s, float inv, u
         k[e] = (int)r;
         far = fmaxf(far, fabsf(t - r));
     }
-    const bool slow = !(far <= 0.5f - 0x1p-14f) || !(s >= 0x1p-100f);
+    const bool slow = !(far <= 0.5f - 0x1p-14f) || !(s >= 0x1p-100f && s < INFINITY);
     if (__builtin_amdgcn_ballot_w64(slow)) {
         if (slow) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) k[e] = s > 0.0f ? (int)__builtin_rintf(v[e] / s) : 0;
+            for (int e = 0; e < 16; ++e) k[e] = s > 0.0f && s < INFINITY ? (int)__builtin_rintf(v[e] / s) : 0;
         }
     }
     uint32_t w[4];
@@ -298,7 +299,9 @@ __global__ __launch_bounds__(kNT) void k_append(AppendArgs a) {
     float* scale = a.cache.scales[which] + (size_t)page_id * kv + head;
     int8_t* block = a.cache.codes[which] + a.cache.block(page_id, head);
     const float before = slot0 > 0 ? *scale : 0.0f;
-    const float after = fmaxf(before, amax / 127.0f);
+    // the larger one, and NaN if either is
+    const float top127 = amax / 127.0f;
+    const float after = before >= top127 || before != before ? before : top127;
     if (W == 4) __syncthreads();                   // everyone has read the old scale
     if (bt == 0) *scale = after;
     if (after > before && slot0 > 0) {             // the codes that the block held, on the new scale

@@ -572,8 +572,8 @@ typedef enum {
  * awq_rope_frequencies -- the rotary_dim / 2 inverse frequencies of a rotary
  * embedding and the magnitude of its rotations, on the HOST (both outputs are
  * HOST arrays).  rotary_dim even, at most 512; base > 1; factor >= 1 unless
- * AWQ_ROPE_PLAIN; original_length > 0 and high > low > 0 for AWQ_ROPE_YARN and
- * AWQ_ROPE_BANDS (ignored otherwise), else AWQ_ERR_UNSUPPORTED.
+ * AWQ_ROPE_PLAIN; original_length > 0 and high > low > 0, finite, for
+ * AWQ_ROPE_YARN and AWQ_ROPE_BANDS (ignored otherwise), else AWQ_ERR_UNSUPPORTED.
  */
 awq_status awq_rope_frequencies(int rotary_dim, double base, int scaling, double factor,
                                 double original_length, double low, double high,
@@ -589,7 +589,7 @@ awq_status awq_rope_frequencies(int rotary_dim, double base, int scaling, double
  *   x, out  dtype [T][heads][head_dim], heads and channels dense, rows x_stride
  *   and out_stride elements apart (multiples of 8, at least heads * head_dim; heads
  *   <= 65535);
- *   out may be x; otherwise they do not overlap.  positions int32 [T],
+ *   out may be x (with the same stride); otherwise they do not overlap.  positions int32 [T],
  *   inv_freq fp32 [rotary_dim / 2].  head_dim a multiple of 16, at most 512,
  *   rotary_dim a multiple of 16, at most head_dim (else AWQ_ERR_SHAPE).
  *   Angles are taken in 64 bits, rotations in 32, one rounding to dtype.
@@ -609,7 +609,7 @@ awq_status awq_rope(const void* x, long long x_stride, const int* positions, con
  *   q  dtype [T][heads][head_dim] or NULL, k, v dtype [T][kv_heads][head_dim]:
  *   rows q_stride, k_stride, v_stride elements apart as in awq_rope (parts of one
  *   fused projection's rows);  q_out dtype [T][heads][head_dim] dense, may be q
- *   where that is dense.
+ *   where that is dense, apart from all else otherwise.
  *   Every page that is written is in one sequence's row only.
  */
 awq_status awq_cache_append(const void* q, long long q_stride, const void* k, long long k_stride,
@@ -641,6 +641,8 @@ awq_status awq_cache_read(const void* k_codes, const float* k_scales, const void
  *   finite has NaN for both.
  *   q dtype [T][heads][head_dim], rows q_stride elements apart as in awq_rope; out
  *   dtype [T][heads][head_dim] dense and apart from q; lse fp32 [T][heads] or NULL.
+ *   scale finite; softcap 0 or 2^-10 .. 1024 (a capped score is right to softcap *
+ *   2^-21); |scale| times a key block's scale below 2^100 (both in fp32).
  *   Scores, softmax and sums are fp32 over the exact codes; softmax weights
  *   (times the block's value scale, relative to the largest) are rounded to fp16
  *   for the product with the values.

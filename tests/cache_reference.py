@@ -115,7 +115,9 @@ def attention(q, cache, tables, lens, starts, scale, window=0, softcap=0.0):
                 p = p / total
                 out[row, h], lse[row, h] = p @ v, m + math.log(total)
                 score = (D + 2) * 2.0 ** -24 * abs(scale) * np.abs(q[row, h]).sum() * 255.0 * sk.max()
-                score += 2.0 ** -20 * (1.0 + (softcap or 0.0) / 8.0)
+                # capped: cap - 2 cap r, r = 1 / (1 + z) near 1/2 with z rounded by 2^-23, the sum by 2^-24 and the
+                # reciprocal by 2^-23, and the cap's sum with a logarithm by 2^-24: cap (2^-24 + 2^-24 + 2^-23 + 2^-24) < cap 2^-21
+                score += 2.0 ** -20 * (1.0 + (softcap or 0.0) / 2.0)
                 weight = 2.0 ** -11 + 2.0 * math.expm1(score) + 2.0 ** -20 * (2.0 + abs(np.log2(np.maximum(sv, 2.0 ** -100))).max())
                 bound[row, h] = weight * (p @ np.abs(v)) + 2.0 ** -23 * (p * sv).max() * np.abs(codes).sum(0)
                 bound[row, h] += 2.0 ** -20 * 128.0 * (p @ sv)      # the bias of 128 leaves fp32 sums

@@ -173,3 +173,18 @@ def test_binding_refuses_tensors_off_the_gpu():
                  lambda: awq.cache_compact(t, i, i, 16), lambda: awq.cache_copy_pages(cache, t)):
         with pytest.raises(ValueError, match="GPU"):
             call()
+
+
+def test_refusals_of_what_cannot_be_right(lib):
+    """Overlapping rows of different strides, outputs over inputs, caps and lengths outside what is computed rightly."""
+    out, m = (ctypes.c_float * 256)(), ctypes.c_float()
+    for scaling in (3, 4):
+        for original, high in ((math.inf, 32.0), (4096.0, math.inf), (math.nan, 32.0), (4096.0, math.nan)):
+            assert lib.awq_rope_frequencies(64, 1e4, scaling, 2.0, original, 1.0, high, out, ctypes.byref(m)) == UNSUP
+    assert lib.awq_rope(P, 1024, P2, P3, 1.0, P, 512, 4, 4, 128, 128, 0, 0, 0, NUL) == UNSUP
+    append, _, attention = cache_calls(lib)
+    assert append(out=P, qs=1024) == UNSUP
+    assert attention(out=P) == UNSUP
+    for cap in (1e-30, 2.0 ** -11, 1025.0, 1e30, math.nan):
+        assert attention(cap=cap) == UNSUP, cap
+    assert lib.awq_cache_fork(P, P2, P3, P4, P5, P2, 4, 4, 2, 9, 16, NUL) == UNSUP

@@ -267,3 +267,19 @@ def test_refused(gpu):
                 dict(starts=None), dict(workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))):
         with pytest.raises(awq.AwqError):
             awq.cache_attention(**{**ok, **bad})
+
+
+@pytest.mark.parametrize("softcap", [2.0 ** -10, 0.5, 1024.0])
+def test_ends_of_the_caps(gpu, softcap):
+    announce("attention caps", softcap)
+    run(Case([(1, 77), (1, 700)], 4, 2, 64, 16, seed=61), softcap=softcap)
+    run(Case([(150, 20)], 4, 2, 64, 16, seed=62), softcap=softcap)
+
+
+@pytest.mark.parametrize("heads,kv", [(71, 1), (128, 1), (200, 2), (300, 1)])
+def test_many_heads_share_one(gpu, heads, kv):
+    """More rows than a tile's from single tokens."""
+    announce("attention shared heads", heads, kv)
+    for dim in (64, 192):
+        run(Case([(1, 400), (1, 0), (1, 2050)], heads, kv, dim, 32, seed=heads + dim), starts=False)
+    run(Case([(2, 90), (0, 3), (3, 0)], heads, kv, 128, 16, "bf16", seed=heads))

@@ -1016,7 +1016,7 @@ def cache_attention(q, cache, tables, lens, starts=None, scale=None, window: int
     if max_new is None:
         max_new = max(T, 1) if starts is not None else 1
     if max_len is None:
-        max_len = W * page
+        max_len = min(W * page, 0x7FFFFFFF)
     if out is None:
         out = q.new_empty((T, heads, dim))
         out_at = out.data_ptr()

@@ -543,6 +543,8 @@ constexpr int kMaxCacheRows = 1 << 20;           // rows (tokens) and sequences 
 constexpr int kMaxBookRows = 65535;              // table rows are a launch's second dimension
 constexpr int kMaxPages = 1 << 30;
 constexpr int kMaxHeads = 65535;
+// cap tanh(x / cap) comes from cap - 2 cap / (exp(2 x / cap) + 1): right to cap 2^-21
+constexpr float kMinCap = 0x1p-10f, kMaxCap = 1024.0f;
 constexpr int kMaxWindow = 1 << 30;              // positions less a window stay in 31 bits
 
 // index arrays are int32 and need no more than their own alignment
@@ -621,7 +623,8 @@ awq_status awq_rope_frequencies(int rotary_dim, double base, int scaling, double
     if (scaling != AWQ_ROPE_PLAIN && (!(factor >= 1.0) || !isfinite(factor))) return AWQ_ERR_UNSUPPORTED;
     if (scaling == AWQ_ROPE_BASE && rotary_dim <= 2) return AWQ_ERR_SHAPE;
     const bool parts = scaling == AWQ_ROPE_YARN || scaling == AWQ_ROPE_BANDS;
-    if (parts && (!(original_length > 0.0) || !(low > 0.0) || !(high > low))) return AWQ_ERR_UNSUPPORTED;
+    if (parts && (!(original_length > 0.0) || !isfinite(original_length) || !(low > 0.0) || !(high > low) || !isfinite(high)))
+        return AWQ_ERR_UNSUPPORTED;
     const int n = rotary_dim / 2;
     const double two_pi = 6.283185307179586476925;
     if (scaling == AWQ_ROPE_BASE) base *= pow(factor, (double)rotary_dim / (rotary_dim - 2));
@@ -656,6 +659,7 @@ awq_status awq_rope(const void* x, long long x_stride, const int* positions, con
     if ((st = check_stride(x_stride, heads, head_dim)) || (st = check_stride(out_stride, heads, head_dim)))
         return as_status(st);
     if (T == 0) return AWQ_OK;
+    if (x != nullptr && x == out && T > 1 && x_stride != out_stride) return AWQ_ERR_UNSUPPORTED;
     if ((st = check_ptrs({x, out})) || (st = check_index({positions}))) return as_status(st);
     const awq::RopeProblem p{x, x_stride, positions, out, out_stride,
                              rotation(inv_freq, rotary_dim, layout, magnitude, inverse), T, heads, head_dim, dtype};
@@ -683,6 +687,7 @@ awq_status awq_cache_append(const void* q, long long q_stride, const void* k, lo
     if ((st = check_ptrs({k, v, k_codes, v_codes})) || (st = check_index({k_scales, v_scales, tables, lens})))
         return as_status(st);
     if (q != nullptr && (st = check_ptrs({q, q_out}))) return as_status(st);
+    if (q != nullptr && q == q_out && T > 1 && q_stride != (long long)heads * head_dim) return AWQ_ERR_UNSUPPORTED;
     if (starts != nullptr && (st = check_index({starts}))) return as_status(st);
     const awq::AppendProblem p{q, k, v, q_stride, k_stride, v_stride, q_out,
                                rotation(inv_freq, rotary_dim, layout, magnitude, 0),
@@ -726,10 +731,12 @@ awq_status awq_cache_attention(const void* q, long long q_stride, const void* k_
     if ((st = check_attention(T, B, W, heads, kv_heads, head_dim, pages, page_size, max_new, max_len)) ||
         (st = check_sequences(starts, T, B, W)) || (st = check_stride(q_stride, heads, head_dim)))
         return as_status(st);
-    if (!isfinite(scale) || window < 0 || !(softcap >= 0.0f) || !isfinite(softcap)) return AWQ_ERR_UNSUPPORTED;
+    if (!isfinite(scale) || window < 0) return AWQ_ERR_UNSUPPORTED;
+    if (softcap != 0.0f && !(softcap >= kMinCap && softcap <= kMaxCap)) return AWQ_ERR_UNSUPPORTED;
     if (T == 0 || B == 0) return AWQ_OK;
     if ((st = check_ptrs({q, k_codes, v_codes, out})) || (st = check_index({k_scales, v_scales, tables, lens})))
         return as_status(st);
+    if (q == out) return AWQ_ERR_UNSUPPORTED;
     if (starts != nullptr && (st = check_index({starts}))) return as_status(st);
     if (lse != nullptr && (st = check_index({lse}))) return as_status(st);
     if ((st = check_workspace(workspace, workspace_bytes,
@@ -752,7 +759,7 @@ awq_status awq_cache_fork(const int* tables, const int* lens, int* refs, const i
     if ((st = check_index({refs}))) return as_status(st);
     if (B > 0 && (st = check_index({tables, lens}))) return as_status(st);
     if (B_out > 0 && (st = check_index({parents, out_tables, out_lens}))) return as_status(st);
-    if (out_tables != nullptr && out_tables == tables) return AWQ_ERR_UNSUPPORTED;
+    if (B > 0 && B_out > 0 && (out_tables == tables || out_lens == lens)) return AWQ_ERR_UNSUPPORTED;
     return hip_status(awq::launch_cache_fork(tables, lens, refs, parents, out_tables, out_lens, B, B_out, W, pages,
                                              log2_of(page_size), stream));
 }

@@ -23,6 +23,12 @@
 // keys form one line, and every workgroup takes an equal stretch of it.  Stretches
 // that end inside a tile leave (M, sum, o) in the workspace and a second launch
 // joins them in order.
+//
+// What bounds it is the read of the cache.  64 sequences of 200 to 8000 tokens, 64 heads
+// over 8 of 128 channels: 70 us, 4.1 TB/s, 6 us of it the join; one of 131072 tokens, 32
+// heads over 8: 61 us, 4.4 TB/s.  The vector instructions that turn codes into operands and
+// scores into weights take 25 % of the SIMDs' cycles, the products 7 %, and a wave waits
+// for its loads in most of the rest.  One token over 131 keys is latency: 8.5 us.
 #include "attend.h"
 
 namespace awq {

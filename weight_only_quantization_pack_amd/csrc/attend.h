@@ -21,6 +21,7 @@ struct AttendArgs {
     float* lse;
     Cache cache;
     Sequences seqs;
+    int piece;                           // of tiles of many rows: tiles of keys that a part takes (more where keys are)
     float scale, softcap;                // |scale| 2^24, for the operands' unit; its sign goes into q
     float sign;
     int heads, group, window, bf16;
@@ -131,6 +132,23 @@ private:
 __device__ __forceinline__ long long first_place(const AttendArgs& a, int tile_rows, int b, int start) {
     return (uint32_t)(start * a.group) / (uint32_t)tile_rows + b;
 }
+// The tiles of keys [t0, t1) that some of a tile's rows see, and into how many parts they go.
+constexpr int kTileKeys = 64;
+struct TileSpan {
+    int pos_lo, pos_hi, t0, t1, parts;             // positions of the first and last row
+    __device__ __forceinline__ TileSpan(const AttendArgs& a, const Line& l, int tile_rows, int tile, int most) {
+        const int pos0 = l.len - l.n;
+        pos_lo = pos0 + tile * tile_rows / a.group;
+        pos_hi = pos0 + min(tile * tile_rows + tile_rows - 1, l.rows - 1) / a.group;
+        const int span = a.seqs.span(l.len, a.cache.page_log2);
+        const int first = a.window > 0 ? max((int)max((long long)pos_lo + 1 - a.window, 0LL), 0) : 0;
+        const int last = min(pos_hi, span - 1);                      // -1: nothing
+        t0 = first / kTileKeys;
+        t1 = last >= first ? last / kTileKeys + 1 : t0;
+        parts = min(max((t1 - t0 + a.piece - 1) / a.piece, 1), most);
+    }
+};
+
 struct TilePlace {
     int b, tile;
     Line line;
@@ -174,7 +192,7 @@ __device__ __forceinline__ float value_scale(float vs) { return fminf(fmaxf(vs, 
 
 __device__ __forceinline__ float power_of_two(int e) { return __builtin_bit_cast(float, (uint32_t)(127 + e) << 23); }
 
-// rows of a tile, and into how many parts its keys are split
+// rows of a tile, into how many parts at most its keys are split
 struct TilePlan {
     int rows, parts;
 };

@@ -470,7 +470,8 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void k_attend_join(J
     int w0 = 0, w1;
     size_t second = 0, step;                       // what part w0's place is past base, and the others' distance
     if (ja.tile_parts) {
-        w1 = ja.tile_parts - 1;
+        w1 = TileSpan(a, l, R, tile, ja.tile_parts).parts - 1;
+        if (w1 == 0) return;                       // written by its workgroup
         step = (size_t)a.cache.kv * size;
         base = a.parts + ((size_t)(first_place(a, R, b, l.start) + l.tiles - 1 - tile) * ja.tile_parts * a.cache.kv + head) * size;
     } else {
@@ -620,6 +621,9 @@ int launch_cache_attention(const AttendProblem& p, void* workspace, hipStream_t 
     a.window = p.window;
     a.bf16 = p.dtype == AWQ_BF16;
     a.split = pl.split;
+    // tiles of keys that a part takes: the largest number of them, over the parts
+    const long long most = p.window > 0 ? min((long long)p.max_len, (long long)p.window + pl.tile.rows / a.group + kTileKeys) : p.max_len;
+    a.piece = (int)((most + kTileKeys - 1) / kTileKeys + pl.tile.parts - 1) / pl.tile.parts;
     a.groups = pl.groups;
     a.line = (long long*)workspace;
     a.parts = (float*)((char*)workspace + (pl.split ? line_bytes(p.seqs.B) : 0));

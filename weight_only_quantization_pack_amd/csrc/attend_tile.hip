@@ -34,7 +34,7 @@
 namespace awq {
 namespace {
 
-constexpr int kKeys = 64, NW = 8;        // keys of a tile, waves of a workgroup
+constexpr int kKeys = kTileKeys, NW = 8;        // keys of a tile, waves of a workgroup
 
 template <int D>
 struct Image {
@@ -79,19 +79,12 @@ __global__ __launch_bounds__(64 * NW, D <= 128 && CT == 1 ? 4 : 2) void k_attend
     if (b < 0) return;
     const Line& l = found.line;
     const int tile = l.tiles - 1 - found.tile;
+    const TileSpan keys(a, l, R, tile, parts);
+    if (part >= keys.parts) return;
     const int pos0 = l.len - l.n;                                    // position of the sequence's first row
-    const int pos_lo = pos0 + tile * R / a.group;
-    const int pos_hi = pos0 + min(tile * R + R - 1, l.rows - 1) / a.group;
-    // tiles of keys [t0, t1) that some row sees, and this part's share
+    const int t0 = keys.t0 + (int)((long long)(keys.t1 - keys.t0) * part / keys.parts);
+    const int t1 = keys.t0 + (int)((long long)(keys.t1 - keys.t0) * (part + 1) / keys.parts);
     const int span = s.span(l.len, page_log2);
-    const int first = a.window > 0 ? max((int)max((long long)pos_lo + 1 - a.window, 0LL), 0) : 0;
-    const int last = min(pos_hi, span - 1);                          // -1: nothing
-    int t0 = first / kKeys, t1 = last >= first ? last / kKeys + 1 : t0;
-    {
-        const int n = t1 - t0;
-        t1 = t0 + (int)((long long)n * (part + 1) / parts);
-        t0 = t0 + (int)((long long)n * part / parts);
-    }
 
     // rows of the wave: column col of column tile ct is row 16 (2 wave + ct) + col
     int pos[CT];
@@ -380,7 +373,7 @@ __global__ __launch_bounds__(64 * NW, D <= 128 && CT == 1 ? 4 : 2) void k_attend
         }
     }
 
-    float* slot = parts > 1 ? a.parts + (size_t)blockIdx.x * (size_t)(R * (D + 2)) : nullptr;
+    float* slot = keys.parts > 1 ? a.parts + (size_t)blockIdx.x * (size_t)(R * (D + 2)) : nullptr;
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
         float all = sum[ct];
@@ -388,7 +381,7 @@ __global__ __launch_bounds__(64 * NW, D <= 128 && CT == 1 ? 4 : 2) void k_attend
         all += __shfl_xor(all, 32);
         const int in = 16 * (CT * wave + ct) + col, row = tile * R + in;
         if (row >= l.rows) continue;
-        if (parts > 1) {
+        if (keys.parts > 1) {
             if (g == 0) {
                 slot[in] = M[ct];
                 slot[R + in] = all;
@@ -442,14 +435,24 @@ TilePlan tile_plan(int T, int B, int group, int kv, int dim, int max_new, int ma
     // tiles there will be, if the bounds hold
     const long long most_tiles = ((long long)T * group / p.rows + B) * kv;
     const long long tiles = min(most_tiles, B * ((rows + p.rows - 1) / p.rows) * kv);
-    // Parts that fill the workgroups that run at a time, of four tiles of keys at least.  512
-    // rows of 4 heads each over 30000 tokens, 8 kv heads: 301 us in 3 parts, 315 in 7 and 917 in
-    // one; 3 ragged chunks 192 us in one part and 223 in two (the parts' outputs are written
-    // and read again); 32 rows of 8 heads over 30000 tokens, one kv head: 36 us in 64 parts, 77 in 16.
-    const long long slots = (p.rows == 128 && dim <= 128 ? 2 : 1) * cus;
-    long long parts = min(slots / tiles, (long long)(max_len / (4 * kKeys)));
-    parts = min(parts, 2 * slots / most_tiles);    // the workspace holds for every T rows, whatever max_new says
-    p.parts = (int)max(1LL, min(parts, 64LL));
+    // As many parts as workgroups run at a time, if they pay.  A tile of keys takes 2.4 us, however
+    // few workgroups there are; the join about as much as 2.5 of them, and one more for each 4 MB that
+    // the parts leave to it.  1000 rows of 4 heads each behind 9000 tokens, 8 kv heads: 213 us in 2 parts
+    // and 329 in one; 300 behind 2000, 43 in 6, 48 in 3, 82 in one; a prompt of 1024, 58 in 2 and 48 in
+    // one; 32 rows of 8 heads over 30000 tokens, one kv head, 36 in 64 and 77 in 16.
+    const long long slots = (p.rows == 128 && dim <= 128 ? 2 : 1) * cus, steps = (max_len + kKeys - 1LL) / kKeys;
+    long long most = min(slots / tiles, 64LL);
+    most = min(most, 2 * slots / most_tiles);      // the workspace holds for every T rows, whatever max_new says
+    const double join = (double)T * group * kv * (dim + 2) * sizeof(float) / 4e6;
+    double best = (double)steps;
+    p.parts = 1;
+    for (int n = 2; n <= most; ++n) {
+        const double cost = (double)((steps + n - 1) / n) + 2.5 + n * join;
+        if (cost < best) {
+            best = cost;
+            p.parts = n;
+        }
+    }
     return p;
 }
 

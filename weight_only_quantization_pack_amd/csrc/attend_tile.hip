@@ -23,7 +23,8 @@
 // 8192 tokens, 32 heads over 8, heads of 128: products in 40 % of the SIMDs' cycles, vector
 // instructions in 44 %.  It takes 572 us, 960 TFLOP/s.  Tried and slower there:
 // 32 x 32 x 16 products 613, 64 rows a wave 944, tiles of 128 rows 662, waves in two
-// groups that take products and weights by turns 800.
+// groups that take products and weights by turns 800, exponentials of half of the keys between
+// the products of the other half 592.
 //
 // Eight waves: 256 rows in two columns a wave where the registers hold them, for heads to
 // 128.  Wider heads, and calls of fewer rows, take one column: heads of 256, 2048 tokens,

@@ -283,3 +283,18 @@ def test_many_heads_share_one(gpu, heads, kv):
     for dim in (64, 192):
         run(Case([(1, 400), (1, 0), (1, 2050)], heads, kv, dim, 32, seed=heads + dim), starts=False)
     run(Case([(2, 90), (0, 3), (3, 0)], heads, kv, 128, 16, "bf16", seed=heads))
+
+
+@pytest.mark.parametrize("window", [0, 700])
+@pytest.mark.parametrize("pairs,heads,kv,dim,page", [([(130, 6000)], 4, 2, 64, 64), ([(100, 5000), (100, 0), (64, 700)], 4, 1, 128, 16),
+                                                     ([(90, 4000), (0, 50), (200, 10)], 2, 2, 192, 32),
+                                                     ([(70, 9000), (1, 40)], 8, 1, 96, 128)], ids=str)
+def test_tiles_of_different_parts(gpu, pairs, heads, kv, dim, page, window):
+    """Long tiles in parts beside short ones in fewer or one; also with bounds that are smaller than the lengths."""
+    announce("attention parts", pairs, heads, kv, dim, page, window)
+    most = max(n + p for n, p in pairs)
+    need = awq.cache_attention_workspace_bytes(sum(n for n, _ in pairs), len(pairs), heads, kv, dim,
+                                               max(n for n, _ in pairs), most)
+    assert need > 0
+    run(Case(pairs, heads, kv, dim, page, seed=dim), window=window, max_new=max(n for n, _ in pairs), max_len=most)
+    run(Case(pairs, heads, kv, dim, page, "bf16", seed=dim + 1), window=window, max_new=40, max_len=most // 2)

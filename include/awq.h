@@ -644,8 +644,9 @@ awq_status awq_cache_read(const void* k_codes, const float* k_scales, const void
  *   scale finite; softcap 0 or 2^-10 .. 1024 (a capped score is right to softcap *
  *   2^-21); |scale| times a key block's scale below 2^100 (both in fp32).
  *   Scores, softmax and sums are fp32 over the exact codes; softmax weights
- *   (times the block's value scale, relative to the largest) are rounded to fp16
- *   for the product with the values.
+ *   (times the block's value scale, 2^-80 at least) are rounded to fp16 for the
+ *   product with the values: to 11 bits down to 2^-21 of the row's largest, to steps of
+ *   2^-31 of it below.
  *   max_new, max_len: bounds of a sequence's rows and tokens that the host knows;
  *   they choose among kernels, and larger sequences are still right.
  *   workspace / workspace_bytes: device scratch of at least

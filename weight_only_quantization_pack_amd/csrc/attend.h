@@ -11,7 +11,11 @@ constexpr int kStep = 32;                // keys of a step
 // tokens, 8 kv heads: 90 us of a workgroup's longest stretch without, 76 with 8, 71 with 16.
 constexpr int kFixed = 16;
 constexpr float kLow = -1e30f;           // below every score: the maximum before the first key
-constexpr float kSlack = 8.0f;           // the maximum may lag by 2^8: weights stay far below fp16's maximum
+// A weight is exp2(t - M).  M is set 2^7 below the largest score met and may lag by 2^8 more, so the row's largest
+// weight is 2^7 .. 2^15: below fp16's maximum, and with all the room below that fp16 has.  Weights keep their 11
+// bits down to 2^-21 of the largest and are lost from 2^-32 on (with M at the maximum itself 2^-14 and 2^-25, which the tail of
+// a softmax passes where one key, or one page's values, are far above the others).
+constexpr float kRoom = 7.0f, kSlack = 8.0f;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
 struct AttendArgs {
@@ -184,11 +188,12 @@ __device__ __forceinline__ int query_exponent(float top) {
 }
 // What a block's scales make of a score's product (>= 0), and of its values.  A block whose
 // scale is not finite (a key or value was not) has a factor of NaN, which stands for it:
-// the value's scale is kept within what logarithm and reciprocal have.
+// the value's scale is kept within what logarithm and reciprocal have: from 2^-80, so that the sum of 2^31 weights of
+// up to 2^15 over it is below 2^127.
 __device__ __forceinline__ float key_factor(float ks, float vs, float scale) {
     return __builtin_fmaf(0.0f, ks + vs, ks * scale);
 }
-__device__ __forceinline__ float value_scale(float vs) { return fminf(fmaxf(vs, 0x1p-100f), 0x1p126f); }
+__device__ __forceinline__ float value_scale(float vs) { return fminf(fmaxf(vs, 0x1p-80f), 0x1p126f); }
 
 __device__ __forceinline__ float power_of_two(int e) { return __builtin_bit_cast(float, (uint32_t)(127 + e) << 23); }
 

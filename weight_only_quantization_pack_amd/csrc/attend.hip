@@ -8,7 +8,8 @@
 // step of 32 keys has one key scale ks and one value scale vs (two with 16-token
 // pages).  The running maximum M is taken over t = log2(e) s + log2(vs): the weight
 // w = exp2(t - M) is then what multiplies a value's code, and the softmax's sum is
-// the sum of w / vs.  One fused multiply-add a score brings ks, scale and vs in.
+// the sum of w / vs.  (M stays a little below, so that fp16 holds more of the small
+// weights: attend.h.)  One fused multiply-add a score brings ks, scale and vs in.
 //
 // Queries are the columns and keys the rows of a 16 x 16 x 32 product, so that a
 // lane ends with 8 consecutive keys of one query: exactly the operand that the
@@ -307,10 +308,10 @@ __global__ __launch_bounds__(64 * kW, D * C > 256 ? 1 : 2) void k_attend(AttendA
                 float top = t[0];
 #pragma unroll
                 for (int y = 1; y < 8; ++y) top = fmaxf(top, t[y]);
-                if (__builtin_amdgcn_ballot_w64(top > M[ct] + kSlack)) {
+                if (__builtin_amdgcn_ballot_w64(top - M[ct] > kRoom + kSlack)) {
                     top = fmaxf(top, __shfl_xor(top, 16));
                     top = fmaxf(top, __shfl_xor(top, 32));
-                    const float m = fmaxf(M[ct], top);
+                    const float m = fmaxf(M[ct], top - kRoom);
                     const float down = __builtin_amdgcn_exp2f(M[ct] - m);
                     M[ct] = m;
                     sum[ct] *= down;

@@ -320,10 +320,10 @@ __global__ __launch_bounds__(64 * NW, D <= 128 && CT == 1 ? 4 : 2) void k_attend
                 for (int y = 1; y < 8; ++y) m = fmaxf(m, sc[ct][2 * kc + (y >> 2)][y & 3]);
                 top = fmaxf(top, __builtin_fmaf(m, f[ct][kc], lv[kc]));
             }
-            if (__builtin_amdgcn_ballot_w64(top > M[ct] + kSlack)) {
+            if (__builtin_amdgcn_ballot_w64(top - M[ct] > kRoom + kSlack)) {
                 top = fmaxf(top, __shfl_xor(top, 16));
                 top = fmaxf(top, __shfl_xor(top, 32));
-                const float m = fmaxf(M[ct], top);
+                const float m = fmaxf(M[ct], top - kRoom);
                 const float down = __builtin_amdgcn_exp2f(M[ct] - m);
                 M[ct] = m;
                 sum[ct] *= down;

@@ -1,0 +1,62 @@
+"""Attention at the ends of what numbers hold."""
+import numpy as np
+import pytest
+
+import weight_only_quantization_pack_amd as awq
+
+import block_reference as R
+from cache_util import Case, gpu as put
+from gpu_util import announce
+
+pytestmark = pytest.mark.gpu
+
+# rows a kv head: few, and many (tiles of 128 and 256)
+SHAPES = [([(1, 300), (1, 77)], 4, 2, 64, 16), ([(1, 2100)], 8, 2, 128, 64), ([(40, 200)], 4, 2, 64, 16),
+          ([(90, 300)], 4, 2, 128, 64), ([(70, 500)], 2, 1, 192, 128)]
+
+
+def one_key(case, codes, size):
+    """Queries of one channel, `size` by row and head, over keys of `codes`; the one key with the highest score takes all:
+    (got, lse, the key's values, its score)."""
+    import torch
+    x = np.zeros((case.T, case.heads, case.dim), np.float32)
+    x[..., 0] = size
+    case.cache[1][:] = 1.0
+    case.cache[3][:] = 2.0 ** -5                 # one value scale: its logarithm is rounded away beside such scores
+    case.cache[0][..., 0] = codes
+    q = put(x).to(case.dtype)
+    lse = torch.zeros(case.T, case.heads, device="cuda")
+    cache, tables, lens, st = case.on_gpu()
+    got = awq.cache_attention(q, cache, tables, lens, st, scale=1.0, max_new=max(case.new), lse=lse)
+    want, score = np.zeros(x.shape), np.zeros(x.shape[:2])
+    q = R.to_f64(q)
+    for b in range(len(case.lens)):
+        for row in range(case.starts[b], case.starts[b + 1]):
+            keys = np.arange(case.lens[b] - case.starts[b + 1] + row + 1)
+            p, slot = case.tables[b, keys // case.page], keys % case.page
+            for h in range(case.heads):
+                g = h // (case.heads // case.kv)
+                z = q[row, h, 0] * case.cache[0][p, g, slot, 0].astype(np.float64)
+                best = np.flatnonzero(z == z.max())
+                values = case.cache[2][p[best], g, slot[best]] * case.cache[3][p[best], g][:, None].astype(np.float64)
+                want[row, h], score[row, h] = values.mean(0), z.max()
+    return R.to_f64(got), R.to_f64(lse), want, score
+
+
+def near(case, got, lse, want, score):
+    """Keys of the highest score share it (their scores are the same numbers): a weight's and a scale's rounding, one to
+    the type, and the bias of 128 in fp32 sums; the logarithm is the score's rounding and 2^-23 of it."""
+    assert np.all(np.abs(got - want) <= 2.0 * R.unit(case.dtype) * np.abs(want) + (2.0 ** -11 + 2.0 ** -16) * 128.0 * 2.0 ** -5)
+    assert np.all(np.abs(lse - score) <= 2.0 ** -21 * np.abs(score) + 12.0)
+
+
+@pytest.mark.parametrize("exponent", [20, 24, 27, 30, 40, 70])
+@pytest.mark.parametrize("pairs,heads,kv,dim,page", SHAPES, ids=str)
+def test_large_scores(gpu, pairs, heads, kv, dim, page, exponent):
+    """Scores of up to 2^77: the softmax is all one key's (or all of those that share its score)."""
+    announce("attention large scores", pairs, heads, kv, dim, page, exponent)
+    case = Case(pairs, heads, kv, dim, page, "bf16", seed=dim + exponent)
+    g = np.random.default_rng(exponent)
+    codes = g.integers(20, 128, case.cache[0].shape[:3])
+    size = 2.0 ** exponent * (1.0 + g.integers(0, 100, (case.T, heads)) / 128.0)
+    near(case, *one_key(case, codes, size))

@@ -92,6 +92,7 @@ __global__ __launch_bounds__(64 * NW, D <= 128 && CT == 1 ? 4 : 2) void k_attend
     half8_t q[CT][NC];
     float qf[CT];
     float4_t bias[CT];
+    float reach = 0.0f;                            // of the wave's rows: no score's product times its qf is larger
     const int row0 = tile * R + 16 * CT * wave;
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
@@ -115,7 +116,7 @@ __global__ __launch_bounds__(64 * NW, D <= 128 && CT == 1 ? 4 : 2) void k_attend
         const int e2 = query_exponent(top);
         const float up = power_of_two(e2) * a.sign;
         qf[ct] = power_of_two(-e2) * kLog2e;
-        float sum = 0.0f;
+        float sum = 0.0f, all = 0.0f;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             float f[8];
@@ -124,12 +125,18 @@ __global__ __launch_bounds__(64 * NW, D <= 128 && CT == 1 ? 4 : 2) void k_attend
             for (int e = 0; e < 8; ++e) {
                 q[ct][c][e] = (_Float16)(f[e] * up);
                 sum += (float)q[ct][c][e];
+                all += fabsf((float)q[ct][c][e]);
             }
         }
         sum += __shfl_xor(sum, 16);
         sum += __shfl_xor(sum, 32);
+        all += __shfl_xor(all, 16);
+        all += __shfl_xor(all, 32);
+        reach = fmaxf(reach, all * 0x1p-15f * qf[ct]);       // codes of up to 255, and the bias's 128, of 2^-24
         bias[ct] = float4_t{1, 1, 1, 1} * (sum * -0x1p-17f);
     }
+#pragma unroll
+    for (int x = 1; x < 16; x *= 2) reach = fmaxf(reach, __shfl_xor(reach, x));
     // positions of the wave's rows; a wave without rows goes along with the last one
     const int wave_lo = pos0 + min(row0, l.rows - 1) / a.group;
     const int wave_hi = pos0 + min(row0 + 16 * CT - 1, l.rows - 1) / a.group;
@@ -237,6 +244,7 @@ __global__ __launch_bounds__(64 * NW, D <= 128 && CT == 1 ? 4 : 2) void k_attend
 
     float4_t sc[CT][4];
     half8_t w[CT][2];
+    bool large = false;                            // some score of the 16 tiles may pass 2^20
     auto scores = [&](const unsigned char* keys) {
 #pragma unroll
         for (int kt = 0; kt < 4; ++kt)
@@ -264,6 +272,7 @@ __global__ __launch_bounds__(64 * NW, D <= 128 && CT == 1 ? 4 : 2) void k_attend
             const float vs = none ? 1.0f : value_scale(vs_next);
             lv_l = __builtin_amdgcn_logf(vs);
             iv_l = 1.0f / vs;
+            large = a.softcap <= 0.0f && __builtin_amdgcn_ballot_w64(c_l * reach > 0x1p20f) != 0;
         }
         // scales of this lane's halves of the two 32 keys
         float ks[2], lv[2], iv[2];
@@ -275,7 +284,7 @@ __global__ __launch_bounds__(64 * NW, D <= 128 && CT == 1 ? 4 : 2) void k_attend
             iv[kc] = __shfl(iv_l, from);
         }
         const bool closed = __builtin_amdgcn_ballot_w64(!(ks[0] >= 0.0f && ks[1] >= 0.0f)) || key0 + kKeys - 1 > wave_lo ||
-                            (a.window > 0 && key0 <= wave_hi - a.window);
+                            (a.window > 0 && key0 <= wave_hi - a.window) || large;
         float f[CT][2];                            // log2 weights are f * product + lv
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
@@ -297,6 +306,19 @@ __global__ __launch_bounds__(64 * NW, D <= 128 && CT == 1 ? 4 : 2) void k_attend
                 }
             }
             if (closed) {
+                // The maximum is a rounded score, and f * product + lv - M below is not: beyond 2^20 they differ by more than
+                // the room that fp16 leaves, from 2^24 on by whole units.  Such scores are rounded here, as the
+                // maximum will be, and their difference is exact.
+                if (large) {
+#pragma unroll
+                    for (int kc = 0; kc < 2; ++kc) {
+#pragma unroll
+                        for (int y = 0; y < 8; ++y)
+                            sc[ct][2 * kc + (y >> 2)][y & 3] = __builtin_fmaf(sc[ct][2 * kc + (y >> 2)][y & 3], f[ct][kc], lv[kc]);
+                        f[ct][kc] = 1.0f;
+                        if (ct == CT - 1) lv[kc] = 0.0f;
+                    }
+                }
                 // the product of a key that the row does not see is -infinity (f > 0)
 #pragma unroll
                 for (int kc = 0; kc < 2; ++kc) {

@@ -60,3 +60,13 @@ def test_large_scores(gpu, pairs, heads, kv, dim, page, exponent):
     codes = g.integers(20, 128, case.cache[0].shape[:3])
     size = 2.0 ** exponent * (1.0 + g.integers(0, 100, (case.T, heads)) / 128.0)
     near(case, *one_key(case, codes, size))
+
+
+@pytest.mark.parametrize("pairs,heads,kv,dim,page", SHAPES, ids=str)
+def test_all_scores_far_below_zero(gpu, pairs, heads, kv, dim, page):
+    """Every score below -2^98 * 50: the least of them takes all, and no row counts as one without keys."""
+    announce("attention scores far below zero", pairs, heads, kv, dim, page)
+    case = Case(pairs, heads, kv, dim, page, "bf16", seed=dim)
+    g = np.random.default_rng(page)
+    codes = g.integers(50, 128, case.cache[0].shape[:3])
+    near(case, *one_key(case, codes, np.full((case.T, heads), -2.0 ** 98)))

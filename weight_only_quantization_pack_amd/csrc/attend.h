@@ -10,7 +10,7 @@ constexpr int kStep = 32;                // keys of a step
 // Steps that a tile's start and end take as long as.  64 ragged sequences of 200 to 8000
 // tokens, 8 kv heads: 90 us of a workgroup's longest stretch without, 76 with 8, 71 with 16.
 constexpr int kFixed = 16;
-constexpr float kLow = -1e30f;           // below every score: the maximum before the first key
+constexpr float kLow = -3e38f;           // below every finite score: the maximum before the first key
 // A weight is exp2(t - M).  M is set 2^7 below the largest score met and may lag by 2^8 more, so the row's largest
 // weight is 2^7 .. 2^15: below fp16's maximum, and with all the room below that fp16 has.  Weights keep their 11
 // bits down to 2^-21 of the largest and are lost from 2^-32 on (with M at the maximum itself 2^-14 and 2^-25, which the tail of

@@ -641,7 +641,7 @@ awq_status awq_cache_read(const void* k_codes, const float* k_scales, const void
  *   finite has NaN for both.
  *   q dtype [T][heads][head_dim], rows q_stride elements apart as in awq_rope; out
  *   dtype [T][heads][head_dim] dense and apart from q; lse fp32 [T][heads] or NULL.
- *   scale finite; softcap 0 or 2^-10 .. 1024 (a capped score is right to softcap *
+ *   |scale| below 2^100; softcap 0 or 2^-10 .. 1024 (a capped score is right to softcap *
  *   2^-21); |scale| times a key block's scale, and that times any |q|, below 2^100.
  *   Scores, softmax and sums are fp32 over the exact codes; softmax weights
  *   (times the block's value scale, 2^-80 at least) are rounded to fp16 for the

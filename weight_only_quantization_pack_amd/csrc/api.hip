@@ -545,6 +545,7 @@ constexpr int kMaxPages = 1 << 30;
 constexpr int kMaxHeads = 65535;
 // cap tanh(x / cap) comes from cap - 2 cap / (exp(2 x / cap) + 1): right to cap 2^-21
 constexpr float kMinCap = 0x1p-10f, kMaxCap = 1024.0f;
+constexpr float kMaxScale = 0x1p100f;            // times 2^24, the unit of a product's operands, it stays in fp32
 constexpr int kMaxWindow = 1 << 30;              // positions less a window stay in 31 bits
 
 // index arrays are int32 and need no more than their own alignment
@@ -731,7 +732,7 @@ awq_status awq_cache_attention(const void* q, long long q_stride, const void* k_
     if ((st = check_attention(T, B, W, heads, kv_heads, head_dim, pages, page_size, max_new, max_len)) ||
         (st = check_sequences(starts, T, B, W)) || (st = check_stride(q_stride, heads, head_dim)))
         return as_status(st);
-    if (!isfinite(scale) || window < 0) return AWQ_ERR_UNSUPPORTED;
+    if (!(fabsf(scale) < kMaxScale) || window < 0) return AWQ_ERR_UNSUPPORTED;
     if (softcap != 0.0f && !(softcap >= kMinCap && softcap <= kMaxCap)) return AWQ_ERR_UNSUPPORTED;
     if (T == 0 || B == 0) return AWQ_OK;
     if ((st = check_ptrs({q, k_codes, v_codes, out})) || (st = check_index({k_scales, v_scales, tables, lens})))

@@ -5,7 +5,7 @@ import pytest
 import weight_only_quantization_pack_amd as awq
 
 import block_reference as R
-from cache_util import Case, gpu as put
+from cache_util import Case, gpu as put, ints
 from gpu_util import announce
 
 pytestmark = pytest.mark.gpu
@@ -70,3 +70,21 @@ def test_all_scores_far_below_zero(gpu, pairs, heads, kv, dim, page):
     g = np.random.default_rng(page)
     codes = g.integers(50, 128, case.cache[0].shape[:3])
     near(case, *one_key(case, codes, np.full((case.T, heads), -2.0 ** 98)))
+
+
+def test_a_length_near_two_to_the_31(gpu):
+    """2^31 - 1 tokens, all of them in one page: the first 32 tokens of each 128 say -100, the others 100, all with
+    the same score.  A wave adds 2^15 steps in fp32, which round one way at worst: 2^-9 of (100 + the bias of 128)."""
+    import torch
+    announce("attention 2^31 - 1 tokens")
+    page, dim, n = 128, 64, (1 << 31) - 1
+    codes = torch.zeros(1, 1, page, dim, dtype=torch.int8, device="cuda")
+    values = torch.full_like(codes, 100)
+    values[:, :, :32] = -100
+    one = torch.ones(1, 1, device="cuda")
+    q = torch.randn(1, 1, dim, device="cuda").half()
+    tables = torch.zeros(1, 1 << 24, dtype=torch.int32, device="cuda")
+    lse = torch.zeros(1, 1, device="cuda")
+    out = awq.cache_attention(q, (codes, one, values, one), tables, ints([n]), lse=lse)
+    assert float((out.float() - 50.0).abs().max()) <= 2.0 ** -9 * 228 + 2.0 ** -11 * 50
+    assert abs(float(lse) - np.log(n)) <= 2.0 ** -9

@@ -50,7 +50,7 @@ struct Line {
         int first = 0;
         if (a.window > 0) first = max((int)max((long long)len - n + 1 - a.window, 0LL), 0);
         step0 = first / kStep;
-        steps = max((span + kStep - 1) / kStep - step0, 1);
+        steps = max((int)(((uint32_t)span + (kStep - 1)) / kStep) - step0, 1);       // a span may end at 2^31 - 1
     }
     // a tile's units: its steps behind a few that stand for its start and end
     __device__ __forceinline__ int tile_units() const { return kFixed + steps; }

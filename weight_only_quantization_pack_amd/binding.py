@@ -1026,8 +1026,8 @@ def cache_attention(q, cache, tables, lens, starts=None, scale=None, window: int
     need = lib.awq_cache_attention_workspace_bytes(T, B, heads, kv, dim, max_new, max_len)
     keep, ws, ws_bytes = _workspace(workspace, need, q)
     st = lib.awq_cache_attention(q_at, q_stride, *codes, *seqs, out_at, lse_at,
-                                 dim ** -0.5 if scale is None else scale, window, softcap, T, B, W, heads, kv, dim,
-                                 pages, page, max_new, max_len, code, ws, ws_bytes, _raw_stream(dev))
+                                 dim ** -0.5 if scale is None else scale, max(min(window, 1 << 30), -1), softcap, T, B, W,
+                                 heads, kv, dim, pages, page, max_new, max_len, code, ws, ws_bytes, _raw_stream(dev))
     if st:
         _check(st, "awq_cache_attention")
     return out

@@ -552,6 +552,7 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void k_attend_join(J
 struct Plan {
     int columns, split, groups;
     TilePlan tile;
+    long long keys;                                // of tiles: keys that one's rows see at most
     int rows() const { return columns ? 16 * columns : tile.rows; }
     int places() const { return columns ? 2 : 1; }           // parts that a workgroup may leave
 };
@@ -564,14 +565,22 @@ size_t line_bytes(int B) { return ((size_t)B + 1) * sizeof(long long) / 16 * 16 
 // sequences of 400 to 7800 tokens, 3 kv heads: 55 us here, 89 in tiles; 64 rows, 64
 // sequences of 250 to 1000, 8 kv heads: 70 here, 49 in tiles; 128 rows, 16 of 500 to 2000:
 // 53 here, 44 in tiles.
-Plan plan(int T, int B, int heads, int kv, int dim, int max_new, int max_len) {
+Plan plan(int T, int B, int heads, int kv, int dim, int max_new, int max_len, int window) {
     Plan p;
+    p.keys = max_len;
     const int group = heads / kv, cus = device_cu_count();
     const long long rows = (long long)max_new * group;
     p.tile = TilePlan{0, 1};
     if (rows > 64 || (rows > 32 && (long long)B * kv >= 2 * cus)) {
         p.columns = 0;
         p.tile = tile_plan(T, B, group, kv, dim, max_new, max_len, cus);
+        // With a window a tile has few keys however long the sequence is: parts by these, and by the length where it
+        // is shorter (the workspace's size knows no window).  512 rows of 32 heads over 8 behind 100000 tokens, window 128:
+        // 20 us, and 37 in the 4 parts that the length would give; window 4096: 72, in parts either way.
+        if (window > 0 && window + (long long)p.tile.rows / group + kTileKeys < max_len) {
+            p.keys = window + (long long)p.tile.rows / group + kTileKeys;
+            p.tile.parts = min(p.tile.parts, tile_plan(T, B, group, kv, dim, max_new, (int)p.keys, cus).parts);
+        }
         p.split = p.tile.parts > 1;
         p.groups = (int)(((long long)T * group / p.tile.rows + B) * kv * p.tile.parts);
         return p;
@@ -600,13 +609,14 @@ void launch_d(const AttendArgs& a, int columns, hipStream_t st) {
 }  // namespace
 
 size_t attend_workspace_bytes(int T, int B, int heads, int kv, int dim, int max_new, int max_len) {
-    const Plan p = plan(T, B, heads, kv, dim, max_new, max_len);
+    const Plan p = plan(T, B, heads, kv, dim, max_new, max_len, 0);
     if (!p.split) return 0;
     return line_bytes(B) + (size_t)p.groups * p.places() * p.rows() * (dim + 2) * sizeof(float);
 }
 
 int launch_cache_attention(const AttendProblem& p, void* workspace, hipStream_t st) {
-    const Plan pl = plan(p.seqs.T, p.seqs.B, p.heads, p.cache.kv, p.cache.dim, p.max_new, p.max_len);
+    const Plan pl = plan(p.seqs.T, p.seqs.B, p.heads, p.cache.kv, p.cache.dim, p.max_new, p.max_len,
+                         p.window);
     AttendArgs a{};
     a.q = (const uint16_t*)p.q;
     a.q_stride = p.q_stride;
@@ -622,9 +632,8 @@ int launch_cache_attention(const AttendProblem& p, void* workspace, hipStream_t 
     a.window = p.window;
     a.bf16 = p.dtype == AWQ_BF16;
     a.split = pl.split;
-    // tiles of keys that a part takes: the largest number of them, over the parts
-    const long long most = p.window > 0 ? min((long long)p.max_len, (long long)p.window + pl.tile.rows / a.group + kTileKeys) : p.max_len;
-    a.piece = (int)((most + kTileKeys - 1) / kTileKeys + pl.tile.parts - 1) / pl.tile.parts;
+    // tiles of keys that a part takes: a tile's largest number of them, over the parts
+    a.piece = (int)((pl.keys + kTileKeys - 1) / kTileKeys + pl.tile.parts - 1) / pl.tile.parts;
     a.groups = pl.groups;
     a.line = (long long*)workspace;
     a.parts = (float*)((char*)workspace + (pl.split ? line_bytes(p.seqs.B) : 0));

@@ -699,7 +699,8 @@ awq_status awq_cache_attention(const void* q, long long q_stride, const void* k_
  * 0..pages-1 are passed over.  count: device int32, how many pairs there are, or
  * NULL: max_pairs.  No dst may be another pair's src or dst.
  *   tensors  HOST array of n_tensors (1..8) device pointers, each [layers][pages]
- *   pages of page_bytes[t] (HOST array; multiples of 4, at most 2^30) bytes.
+ *   pages of page_bytes[t] (HOST array; multiples of 4, at most 2^30) bytes, aligned to
+ *   16 bytes where page_bytes[t] is a multiple of 16 and to 4 where it is not.
  */
 awq_status awq_cache_fork(const int* tables, const int* lens, int* refs, const int* parents,
                           int* out_tables, int* out_lens, int B, int B_out, int W, int pages,

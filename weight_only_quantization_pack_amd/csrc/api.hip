@@ -799,7 +799,9 @@ awq_status awq_cache_copy_pages(void* const* tensors, const size_t* page_bytes, 
     if (max_pairs == 0) return AWQ_OK;
     int st = AWQ_OK;
     for (int t = 0; t < n_tensors; ++t) if (tensors[t] == nullptr) return AWQ_ERR_NULL;
-    for (int t = 0; t < n_tensors; ++t) if ((st = check_ptr(tensors[t]))) return as_status(st);
+    // pages of whole 16 bytes are copied in these, others (scales, in layers of any number) in words of 4
+    for (int t = 0; t < n_tensors; ++t)
+        if ((st = page_bytes[t] % 16 == 0 ? check_ptr(tensors[t]) : check_index({tensors[t]}))) return as_status(st);
     if ((st = check_index({pairs}))) return as_status(st);
     if (count != nullptr && (st = check_index({count}))) return as_status(st);
     p.n = n_tensors;

@@ -564,8 +564,15 @@ typedef enum {
                                * in original_length, divided by factor for those that
                                * turn `low` times or fewer, a ramp over i between; the
                                * magnitude is 0.1 ln(factor) + 1                      */
-    AWQ_ROPE_BANDS = 4        /* the same ends, a ramp over the number of turns
+    AWQ_ROPE_BANDS = 4,       /* the same ends, a ramp over the number of turns
                                * (original_length * f / 2 pi); magnitude 1            */
+    AWQ_ROPE_YARN_ROUNDED = AWQ_ROPE_YARN | 16
+                              /* AWQ_ROPE_YARN with the ramp's ends rounded, the lower
+                               * one down and the upper one up, and kept in 0 ..
+                               * rotary_dim - 1: what YaRN's released code computes and
+                               * its checkpoints expect unless they ask not to round.
+                               * (AWQ_ROPE_YARN's ends are not rounded; the two differ
+                               * by up to a third in the channels of the ramp.)       */
 } awq_rope_scaling;
 
 /*
@@ -573,7 +580,7 @@ typedef enum {
  * embedding and the magnitude of its rotations, on the HOST (both outputs are
  * HOST arrays).  rotary_dim even, at most 512; base > 1; factor >= 1 unless
  * AWQ_ROPE_PLAIN; original_length > 0 and high > low > 0, finite, for
- * AWQ_ROPE_YARN and AWQ_ROPE_BANDS (ignored otherwise), else AWQ_ERR_UNSUPPORTED.
+ * AWQ_ROPE_YARN, AWQ_ROPE_YARN_ROUNDED and AWQ_ROPE_BANDS (ignored otherwise), else AWQ_ERR_UNSUPPORTED.
  */
 awq_status awq_rope_frequencies(int rotary_dim, double base, int scaling, double factor,
                                 double original_length, double low, double high,

@@ -761,16 +761,19 @@ def moe(x, router, gate, up, down, inter: int, top_k: int, bits: int = 4, group_
 # lens int32 [B] and starts int32 [B + 1] (or None: one row each), as in awq.h.
 # ---------------------------------------------------------------------------
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
-ROPE_SCALINGS = {None: 0, "linear": 1, "base": 2, "yarn": 3, "bands": 4}
+ROPE_SCALINGS = {None: 0, "linear": 1, "base": 2, "yarn": 3, "bands": 4, "yarn_rounded": 3 | 16}
 
 
 def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling=None, factor: float = 1.0,
                      original_length: float = 0.0, low: float = 1.0, high: float = 32.0, device="cuda"):
     """(inv_freq fp32 [rotary_dim / 2] on `device`, magnitude) of a rotary
     embedding (awq_rope_frequencies): scaling None, "linear", "base" (a larger
-    base), "yarn" or "bands" (frequencies that turn `high` times or more in
+    base), "yarn_rounded", "yarn" or "bands" (frequencies that turn `high` times or more in
     original_length are kept, those that turn `low` times or fewer are divided by
-    factor; a ramp over the channels, or over the number of turns)."""
+    factor; a ramp over the channels, or over the number of turns).  The channels'
+    ramp begins and ends at whole channels in "yarn_rounded", as in YaRN's released
+    code: it is the one for a checkpoint that does not say otherwise; "yarn" does
+    not round its ends."""
     torch = _torch()
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"scaling must be one of {list(ROPE_SCALINGS)}, got {scaling!r}")

@@ -620,6 +620,8 @@ awq_status awq_rope_frequencies(int rotary_dim, double base, int scaling, double
     if (inv_freq == nullptr || magnitude == nullptr) return AWQ_ERR_NULL;
     if (rotary_dim <= 0 || rotary_dim % 2 != 0 || rotary_dim > kMaxRopeDim) return AWQ_ERR_SHAPE;
     if (!(base > 1.0) || !isfinite(base)) return AWQ_ERR_UNSUPPORTED;
+    const bool rounded = scaling == AWQ_ROPE_YARN_ROUNDED;
+    if (rounded) scaling = AWQ_ROPE_YARN;
     if (scaling < AWQ_ROPE_PLAIN || scaling > AWQ_ROPE_BANDS) return AWQ_ERR_UNSUPPORTED;
     if (scaling != AWQ_ROPE_PLAIN && (!(factor >= 1.0) || !isfinite(factor))) return AWQ_ERR_UNSUPPORTED;
     if (scaling == AWQ_ROPE_BASE && rotary_dim <= 2) return AWQ_ERR_SHAPE;
@@ -636,8 +638,13 @@ awq_status awq_rope_frequencies(int rotary_dim, double base, int scaling, double
         if (scaling == AWQ_ROPE_LINEAR) keep = 0.0;
         if (scaling == AWQ_ROPE_BANDS) keep = (original_length * f / two_pi - low) / (high - low);
         if (scaling == AWQ_ROPE_YARN) {          // a ramp over the channels between those that turn high and low times
-            const double from = n * log(original_length / (high * two_pi)) / log(base);
-            const double to = n * log(original_length / (low * two_pi)) / log(base);
+            double from = n * log(original_length / (high * two_pi)) / log(base);
+            double to = n * log(original_length / (low * two_pi)) / log(base);
+            if (rounded) {
+                from = fmin(fmax(floor(from), 0.0), rotary_dim - 1.0);
+                to = fmin(fmax(ceil(to), 0.0), rotary_dim - 1.0);
+                if (to <= from) to = from + 0.5;           // no channel between: a step behind `from`
+            }
             keep = 1.0 - (i - from) / (to - from);
         }
         keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;

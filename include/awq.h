@@ -545,7 +545,8 @@ awq_status awq_moe(const void* x, const float* inv_s, const void* router,
  *                  lens[b]) are not cached, attend to nothing and read as zeros.
  * A page may be in the rows of several sequences as long as no call writes to
  * it.  int32 and fp32 arrays need 4-byte alignment only.  T, B <= 2^20, heads <=
- * 65535, and what a launch cannot count (2^32 threads) is AWQ_ERR_SHAPE.
+ * 65535, T * heads below 2^24 for the attention, and what a launch cannot count (2^32
+ * threads) is AWQ_ERR_SHAPE.
  * Scales are 0 or more.  A block (a page's tokens of one head) into which a token
  * with an infinity or a NaN came has that as its scale until the page starts anew,
  * and whoever sees one of its tokens reads NaN.
@@ -655,7 +656,8 @@ awq_status awq_cache_read(const void* k_codes, const float* k_scales, const void
  *   product with the values: to 11 bits down to 2^-21 of the row's largest, to steps of
  *   2^-31 of it below.
  *   max_new, max_len: bounds of a sequence's rows and tokens that the host knows;
- *   they choose among kernels, and larger sequences are still right.
+ *   they choose among kernels, and larger sequences are still right.  A max_new far
+ *   above the rows that come takes the kernel for prompts, which single rows fill badly.
  *   workspace / workspace_bytes: device scratch of at least
  *   awq_cache_attention_workspace_bytes(T, B, heads, kv_heads, head_dim, max_new,
  *   max_len) bytes on the current device, 16-byte aligned (may be NULL when that is 0).

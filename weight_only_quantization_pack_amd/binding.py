@@ -999,8 +999,9 @@ def cache_attention(q, cache, tables, lens, starts=None, scale=None, window: int
     (awq_cache_attention): q fp16 or bf16 [T][heads][dim], causal, within `window`
     keys (0: all), scores scale * q.k (default dim^-1/2) capped by softcap (0:
     not).  max_new, max_len: the most rows and tokens of a sequence, if known (they
-    choose the kernel; default T, or 1 without starts, and the table's).  lse: fp32
-    [T][heads] to write, or None.  Returns out, [T][heads][dim] like q."""
+    choose the kernel; default T, or 1 without starts, and the table's).  Give max_new
+    with starts: 63 single rows over up to 8000 tokens take 107 us with max_new=1 and 432
+    as what could be one prompt of 63.  lse: fp32 [T][heads] to write, or None.  Returns out, [T][heads][dim] like q."""
     torch = _torch()
     dev = _gpu_of(q, "q")
     if torch._C._cuda_getDevice() != dev:

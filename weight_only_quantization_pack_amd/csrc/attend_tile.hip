@@ -87,7 +87,7 @@ __global__ __launch_bounds__(64 * NW, D <= 128 && CT == 1 ? 4 : 2) void k_attend
     const int t1 = keys.t0 + (int)((long long)(keys.t1 - keys.t0) * (part + 1) / keys.parts);
     const int span = s.span(l.len, page_log2);
 
-    // rows of the wave: column col of column tile ct is row 16 (2 wave + ct) + col
+    // rows of the wave: column col of column tile ct is row 16 (CT wave + ct) + col
     int pos[CT];
     half8_t q[CT][NC];
     float qf[CT];

@@ -16,8 +16,9 @@
 // All of it is one pass over the rows and bound by memory: 4099 rows of 64 heads of 128,
 // half of each turned, 29 us (4.6 TB/s); 16384 rows of 64 + 8 + 8 heads into the
 // cache 154 us, half of them for the queries (4.2 TB/s with the read back, 19 us).  One row
-// is a launch: 2.4 us for the kernel.  32 single tokens into pages that hold some: 7.8 us,
-// three dependent loads (place, old scale and codes) behind the launch.
+// is a launch: 2.4 us for the kernel.  64 single tokens into pages that hold some: 7.4 us,
+// three dependent loads (place, old scale and codes) behind the launch, and 9.3 where all
+// held codes go to a new scale.
 #include "cache.h"
 
 namespace awq {

@@ -88,3 +88,41 @@ def test_a_length_near_two_to_the_31(gpu):
     out = awq.cache_attention(q, (codes, one, values, one), tables, ints([n]), lse=lse)
     assert float((out.float() - 50.0).abs().max()) <= 2.0 ** -9 * 228 + 2.0 ** -11 * 50
     assert abs(float(lse) - np.log(n)) <= 2.0 ** -9
+
+
+@pytest.mark.parametrize("window", [0, 200])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("pairs,heads,kv,dim,page", SHAPES + [([(130, 4000)], 4, 2, 64, 64), ([(200, 0), (90, 1500)], 2, 1, 128, 32)],
+                         ids=str)
+def test_large_scores_in_one_page(gpu, pairs, heads, kv, dim, page, sign, window):
+    """One page's scores are 2^33 and more, or as far below zero, among ordinary ones: it takes all of every row that sees it,
+    or nothing unless the row sees nothing else.  Its codes differ (but two of 128), so one of its tokens is the largest.  Ordinary scores are sums of one
+    product, right to 2^-22, so what is left is the weights' 2^-11 and what fp32 sums lose to the bias of 128."""
+    announce("attention one large page", pairs, heads, kv, dim, page, sign, window)
+    case = Case(pairs, heads, kv, dim, page, "bf16", seed=dim + page)
+    g = np.random.default_rng(page + window)
+    case.cache[0][..., 0] = g.integers(-127, 128, case.cache[0].shape[:3])
+    case.cache[1][:], case.cache[3][:] = 2.0 ** -7, 2.0 ** -5
+    for b, n in enumerate(case.lens):
+        p = case.tables[b, (n - 1) // (2 * page)]
+        case.cache[1][p] = 2.0 ** 33
+        case.cache[0][p, :, :, 0] = sign * np.resize(1 + g.permutation(127), page)
+    x = np.zeros((case.T, heads, dim), np.float32)
+    x[..., 0] = 1.0 + g.integers(0, 128, (case.T, heads)) / 128.0
+    q = put(x).to(case.dtype)
+    cache, tables, lens, st = case.on_gpu()
+    got = R.to_f64(awq.cache_attention(q, cache, tables, lens, st, scale=1.0, window=window, max_new=max(case.new)))
+    x = R.to_f64(q)
+    for b in range(len(case.lens)):
+        for row in range(case.starts[b], case.starts[b + 1]):
+            pos = case.lens[b] - case.starts[b + 1] + row
+            keys = np.arange(max(0, pos - window + 1) if window else 0, pos + 1)
+            p, slot = case.tables[b, keys // page], keys % page
+            for h in range(heads):
+                k = h // (heads // kv)
+                z = x[row, h, 0] * case.cache[0][p, k, slot, 0] * case.cache[1][p, k].astype(np.float64)
+                share = np.exp(z - z.max())
+                v = case.cache[2][p, k, slot] * 2.0 ** -5
+                want = share @ v / share.sum()
+                size = share @ np.abs(v) / share.sum()
+                assert np.all(np.abs(got[row, h] - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -10 * size + 2.0 ** -16 * 4.0), (row, h)

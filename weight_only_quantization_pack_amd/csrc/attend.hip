@@ -313,7 +313,8 @@ __global__ __launch_bounds__(64 * kW, D * C > 256 ? 1 : 2) void k_attend(AttendA
                 if (__builtin_amdgcn_ballot_w64(top - M[ct] > kRoom + kSlack)) {
                     top = fmaxf(top, __shfl_xor(top, 16));
                     top = fmaxf(top, __shfl_xor(top, 32));
-                    const float m = fmaxf(M[ct], top - kRoom);
+                    // a row by its own scores only: its bits do not depend on the rows beside it
+                    const float m = top - M[ct] > kRoom + kSlack ? top - kRoom : M[ct];
                     const float down = __builtin_amdgcn_exp2f(M[ct] - m);
                     M[ct] = m;
                     sum[ct] *= down;

@@ -21,7 +21,8 @@
 // instructions of 4 (weights, running maximum, conversion of the codes): 1024 and 1120
 // cycles, which overlap only across the two waves of a SIMD.  Counted on a prompt of
 // 8192 tokens, 32 heads over 8, heads of 128: products in 40 % of the SIMDs' cycles, vector
-// instructions in 44 %.  It takes 572 us, 960 TFLOP/s.  Tried and slower there:
+// instructions in 44 %.  It takes 578 us, 950 TFLOP/s (572 where all rows of a wave raise their
+// maximum together, which made a row's bits depend on its neighbours).  Tried and slower there:
 // 32 x 32 x 16 products 613, 64 rows a wave 944, tiles of 128 rows 662, waves in two
 // groups that take products and weights by turns 800, exponentials of half of the keys between
 // the products of the other half 592.
@@ -342,10 +343,12 @@ __global__ __launch_bounds__(64 * NW, D <= 128 && CT == 1 ? 4 : 2) void k_attend
                 for (int y = 1; y < 8; ++y) m = fmaxf(m, sc[ct][2 * kc + (y >> 2)][y & 3]);
                 top = fmaxf(top, __builtin_fmaf(m, f[ct][kc], lv[kc]));
             }
-            if (__builtin_amdgcn_ballot_w64(top - M[ct] > kRoom + kSlack)) {
+            // (rare, and laid out of the way: the prompt of 8192 tokens 578 us, 582 where it is not)
+            if (__builtin_expect(__builtin_amdgcn_ballot_w64(top - M[ct] > kRoom + kSlack) != 0, 0)) {
                 top = fmaxf(top, __shfl_xor(top, 16));
                 top = fmaxf(top, __shfl_xor(top, 32));
-                const float m = fmaxf(M[ct], top - kRoom);
+                // a row by its own scores only: its bits do not depend on the rows beside it
+                const float m = top - M[ct] > kRoom + kSlack ? top - kRoom : M[ct];
                 const float down = __builtin_amdgcn_exp2f(M[ct] - m);
                 M[ct] = m;
                 sum[ct] *= down;

@@ -8,7 +8,8 @@ All of that is a relative error e[j] of a key's share.
 
 A weight goes to fp16 in a unit in which the largest of the row is 2^7 at least (the running maximum never passes
 the row's own): half a step is 2^-11 of it, or 2^-25 below 2^-14, which is 2^-32 of the largest.  Products of it with codes
-are summed in fp32: 2^-24 of the magnitudes for each step of 32 keys, and for the join.  Few rows' codes carry a bias of
+are summed in fp32: 2^-24 of the magnitudes for each step of 32 keys, and for the join and what an instruction rounds
+within its own sum 8 more.  Few rows' codes carry a bias of
 128, and so does the sum that takes it off again.
 """
 import math

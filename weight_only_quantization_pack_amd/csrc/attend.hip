@@ -30,8 +30,8 @@
 // What bounds it is the read of the cache.  64 sequences of 200 to 8000 tokens, 64 heads
 // over 8 of 128 channels: 70 us, 4.1 TB/s, 6 us of it the join; one of 131072 tokens, 32
 // heads over 8: 61 us, 4.4 TB/s.  The vector instructions that turn codes into operands and
-// scores into weights take 25 % of the SIMDs' cycles, the products 7 %; waves wait
-// for 32 % of their time.  One token over 131 keys is latency: 8.5 us.
+// scores into weights take 25 % of the SIMDs' cycles, the products 8 %; waves wait
+// for 26 % of their time.  One token over 131 keys is latency: 8.5 us.
 #include "attend.h"
 
 namespace awq {

@@ -96,8 +96,8 @@ def test_a_length_near_two_to_the_31(gpu):
                          ids=str)
 def test_large_scores_in_one_page(gpu, pairs, heads, kv, dim, page, sign, window):
     """One page's scores are 2^33 and more, or as far below zero, among ordinary ones: it takes all of every row that sees it,
-    or nothing unless the row sees nothing else.  Its codes differ (but two of 128), so one of its tokens is the largest.  Ordinary scores are sums of one
-    product, right to 2^-22, so what is left is the weights' 2^-11 and what fp32 sums lose to the bias of 128."""
+    or nothing unless the row sees nothing else.  Its codes differ (but two of 128), so one of its
+    tokens is the largest.  Ordinary scores are one product, right to 2^-22, so what is left is the weights' 2^-11 and what fp32 sums lose to the bias of 128."""
     announce("attention one large page", pairs, heads, kv, dim, page, sign, window)
     case = Case(pairs, heads, kv, dim, page, "bf16", seed=dim + page)
     g = np.random.default_rng(page + window)

@@ -93,7 +93,7 @@ __global__ __launch_bounds__(64 * NW, D <= 128 && CT == 1 ? 4 : 2) void k_attend
     half8_t q[CT][NC];
     float qf[CT];
     float4_t bias[CT];
-    float reach = 0.0f;                            // of the wave's rows: no score's product times its qf is larger
+    float reach = 0.0f;
     const int row0 = tile * R + 16 * CT * wave;
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
@@ -117,7 +117,7 @@ __global__ __launch_bounds__(64 * NW, D <= 128 && CT == 1 ? 4 : 2) void k_attend
         const int e2 = query_exponent(top);
         const float up = power_of_two(e2) * a.sign;
         qf[ct] = power_of_two(-e2) * kLog2e;
-        float sum = 0.0f, all = 0.0f;
+        float sum = 0.0f;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             float f[8];
@@ -126,18 +126,16 @@ __global__ __launch_bounds__(64 * NW, D <= 128 && CT == 1 ? 4 : 2) void k_attend
             for (int e = 0; e < 8; ++e) {
                 q[ct][c][e] = (_Float16)(f[e] * up);
                 sum += (float)q[ct][c][e];
-                all += fabsf((float)q[ct][c][e]);
             }
         }
         sum += __shfl_xor(sum, 16);
         sum += __shfl_xor(sum, 32);
-        all += __shfl_xor(all, 16);
-        all += __shfl_xor(all, 32);
-        reach = fmaxf(reach, all * 0x1p-15f * qf[ct]);       // codes of up to 255, and the bias's 128, of 2^-24
+        reach = fmaxf(reach, qf[ct]);
         bias[ct] = float4_t{1, 1, 1, 1} * (sum * -0x1p-17f);
     }
-#pragma unroll
-    for (int x = 1; x < 16; x *= 2) reach = fmaxf(reach, __shfl_xor(reach, x));
+    // What no product of the wave's rows passes, qf taken in: D channels below 2^14, codes of up to 255 and the bias's
+    // 128 in units of 2^-24.
+    reach = __builtin_bit_cast(float, wave_reduce(__builtin_bit_cast(uint32_t, reach), MaxU32())) * (0.5f * D);
     // positions of the wave's rows; a wave without rows goes along with the last one
     const int wave_lo = pos0 + min(row0, l.rows - 1) / a.group;
     const int wave_hi = pos0 + min(row0 + 16 * CT - 1, l.rows - 1) / a.group;
